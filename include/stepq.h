@@ -57,6 +57,10 @@ enum { STEPQ_ORDER_DELTA_FIRST = 0, STEPQ_ORDER_DECAY_FIRST = 1 };
 #define STEPQ_FLAG_SCALE_OVF 2u /* a row or column factor overflowed binary16             */
 #define STEPQ_FLAG_PIVOT_OVF 4u /* an FP16 pivot entry overflowed binary16                */
 #define STEPQ_FLAG_BAD_SLOT 8u  /* a slot index outside [0, n_slots) other than -1          */
+#define STEPQ_FLAG_BAD_SEQ 16u  /* token offsets that are not 0 <= cu[s] <= cu[s+1] <= n_tokens */
+
+/* element types of the sequence calls' q, k, v and out, and of stepq_read_slots' values */
+enum { STEPQ_DTYPE_F32 = 0, STEPQ_DTYPE_BF16 = 1, STEPQ_DTYPE_F16 = 2 };
 
 /*
  * Plan description (Method 1: the offline precision map, pivots and impact scores).
@@ -198,6 +202,103 @@ int stepq_debug_side_delay(stepq_plan_t plan, long long cycles);
 
 /* Thread-local message describing the last failed call on this thread ("" if none). */
 const char* stepq_last_error(void);
+
+/* ---------------------------------------------------------------------------------------- */
+/* The delta rule over sequences: FP32 states, prompts into packed pools, gradients.        */
+/* ---------------------------------------------------------------------------------------- */
+
+/*
+ * What a sequence call works on.
+ *   kind, order  as for a plan.  KDA: n_qk_heads == n_heads is usual but not required.
+ *   dtype        type of q, k, v, out and their gradients (STEPQ_DTYPE_*); gates, strengths and
+ *                states are fp32.
+ *   n_qk_heads, n_heads  heads of q and k, heads of v, alpha, beta, the state and out;
+ *                n_heads is a multiple, and value head h reads key head
+ *                h / (n_heads / n_qk_heads).
+ *   d            d_k = d_v, 64 or 128.
+ *   n_seqs, n_tokens  sequences, and rows of q, k, v, alpha, beta and out.
+ *   cu_seqlens   device int32 [n_seqs + 1]: sequence s is rows cu[s] .. cu[s+1] - 1 (0 <= cu[s] <=
+ *                cu[s+1] <= n_tokens; lengths of zero are fine; the ranges must not meet).  Rows
+ *                of no sequence are not read, and out is left as it was there.  A sequence whose
+ *                offsets break the rule is skipped and raises STEPQ_FLAG_BAD_SEQ.  NULL: n_seqs
+ *                sequences of n_tokens / n_seqs rows each (must divide).
+ *   q_stride .. out_stride  elements from one token's row to the next (heads of a token are d
+ *                elements apart); 0 = packed (heads * d).  A multiple of 16 bytes.
+ *   device       HIP device ordinal of every pointer and of the stream.
+ *   status       device uint32 that the kernels OR their STEPQ_FLAG_* bits into, or NULL.
+ */
+typedef struct {
+  int kind, order, dtype;
+  int n_qk_heads, n_heads, d;
+  int n_seqs, n_tokens;
+  int device;
+  long long q_stride, k_stride, v_stride, out_stride;
+  const int32_t* cu_seqlens;
+  uint32_t* status;
+} stepq_delta_desc;
+
+/* Bytes of workspace (device memory, 256-byte aligned) that a call with this description needs:
+   stepq_delta_forward, stepq_delta_backward.  May be 0.  The workspace belongs to the call until
+   its work on the stream is done; two calls that may run at the same time (two streams, two
+   captured graphs) need one each. */
+int stepq_delta_forward_workspace(const stepq_delta_desc* desc, size_t* bytes);
+int stepq_delta_backward_workspace(const stepq_delta_desc* desc, size_t* bytes);
+
+/*
+ * Runs every sequence from its state (Background's recurrence, without quantization):
+ *   S_t = A_t S_{t-1} + beta_t k_t v_t^T,  out_t = S_t^T q_t.
+ *   q, k [n_tokens, n_qk_heads, d], v, out [n_tokens, n_heads, d] of `dtype`, 16-byte aligned;
+ *   alpha [n_tokens, n_heads] (GDN) or [n_tokens, n_heads, d] (KDA), beta [n_tokens, n_heads];
+ *   S_in [.., n_heads, d, d] first states, NULL = zero;  S_out last states, NULL = not kept; may be
+ *   S_in (in place), but must not overlap it otherwise.
+ *   slots  device int32 [n_seqs]: sequence s uses state slots[s] of n_slots (S_in and S_out
+ *   alike), -1 = skip the sequence (its out rows and state are left as they were), any other
+ *   index outside [0, n_slots) is skipped too and raises STEPQ_FLAG_BAD_SLOT.  Two sequences must
+ *   not name one slot.  NULL: sequence s uses state s.
+ * GDN sequences of 16 tokens and more on average run in chunks of 64 tokens on the matrix cores
+ * (sums and states in binary32, operands in pairs of binary16 with power-of-two scales: 22 bits);
+ * there a non-finite input makes its head's outputs from its chunk's first token on non-finite.
+ * Otherwise tokens are taken one by one in binary32.  Only enqueues kernels: may be captured.
+ */
+int stepq_delta_forward(const stepq_delta_desc* desc, const void* q, const void* k, const void* v,
+                        const float* alpha, const float* beta, const float* S_in, float* S_out,
+                        int n_slots, const int32_t* slots, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of stepq_delta_forward (GDN; no slots): from d_out [n_tokens, n_heads, d] (dtype, out's
+ * stride) and dS_out [n_seqs, n_heads, d, d] fp32 (NULL = zero) to
+ *   dq, dk [n_tokens, n_qk_heads, d] and dv [n_tokens, n_heads, d] of `dtype`, packed;
+ *   dalpha, dbeta [n_tokens, n_heads] fp32;  dS_in [n_seqs, n_heads, d, d] fp32 (NULL = not wanted).
+ * All are written, not added to; rows of no sequence are left as they were.  Value heads that share
+ * a key head add up in index order in binary32, so results do not depend on scheduling.  No
+ * division by a gate: gates of zero have their gradient.  KDA: STEPQ_ERR_UNSUPPORTED.
+ */
+int stepq_delta_backward(const stepq_delta_desc* desc, const void* q, const void* k, const void* v,
+                         const float* alpha, const float* beta, const float* S_in,
+                         const void* d_out, const float* dS_out, void* dq, void* dk, void* dv,
+                         float* dalpha, float* dbeta, float* dS_in, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Prompts through a packed pool: every sequence's state is read from its slot (values r c z), run over
+ * its tokens as by stepq_delta_forward, and written back by the refit of stepq_encode_state -- once
+ * for all its tokens, not once a token.  A slot of zero bytes is the zero state: clear a slot to
+ * start a request.  desc's kind, order, n_heads, d and device are the plan's; its status is not
+ * used (the plan's is).  slots as for stepq_decode_step_slots; a sequence without tokens leaves its
+ * slot as it was.  Ordering and capture are as for stepq_encode_state_slots.
+ */
+int stepq_prefill_workspace(stepq_plan_t plan, const stepq_delta_desc* desc, size_t* bytes);
+int stepq_prefill_slots(stepq_plan_t plan, const stepq_delta_desc* desc, void* pool, int n_slots,
+                        const int32_t* slots, const void* q, const void* k, const void* v,
+                        const float* alpha, const float* beta, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Values of packed states: S [B, n_heads, d, d] of `dtype` (16-byte aligned), row b = the state in
+   slot slots[b] (r c z rounded once to binary32, then to dtype; FP16 pivots as stored).  -1 leaves
+   row b as it was; other indices outside [0, n_slots) do too and raise STEPQ_FLAG_BAD_SLOT. */
+int stepq_read_slots(stepq_plan_t plan, const void* pool, int n_slots, const int32_t* slots, int B,
+                     void* S, int dtype, void* stream);
 
 /* ---------------------------------------------------------------------------------------- */
 /* Offline planning on the host (Method 1, Method 2).  binary64, host pointers.            */

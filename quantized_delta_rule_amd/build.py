@@ -26,7 +26,9 @@ HIPCC_FLAGS = [
 
 
 SOURCES = ("stepq_k128_gdn.hip", "stepq_k128_kda.hip", "stepq_k64.hip", "stepq_calib.hip",
-           "stepq_noalloc.hip", "stepq_api.cpp", "stepq_offline.cpp")
+           "stepq_noalloc.hip", "stepq_delta_step.hip", "stepq_delta_chunk.hip",
+           "stepq_delta_grad.hip", "stepq_read.hip", "stepq_api.cpp", "stepq_delta_api.cpp",
+           "stepq_offline.cpp")
 OBJDIR = os.path.join(HERE, "_build")
 
 

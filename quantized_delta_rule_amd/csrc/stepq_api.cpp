@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "stepq.h"
+#include "stepq_delta.h"
 #include "stepq_internal.h"
 
 using namespace stepq;
@@ -59,28 +60,6 @@ float tree_sum(const float* x, int n) {
   if (n == 1) return x[0];
   return tree_sum(x, n / 2) + tree_sum(x + n / 2, n - n / 2);
 }
-
-// Makes the plan's device current and restores the caller's on scope exit; when it is already
-// current (the usual case) no device switch is made either way.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok_ = false;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) {
-      prev = -1;
-      return;
-    }
-    if (prev == dev) {
-      prev = -1;
-      ok_ = true;
-      return;
-    }
-    if (hipSetDevice(dev) == hipSuccess) ok_ = true;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) (void)hipSetDevice(prev);
-  }
-};
 
 }  // namespace
 
@@ -556,6 +535,85 @@ int stepq_unpack_debug(stepq_plan_t p, const void* pool, int B, float* S_hat, ui
   HIP_TRY(wait_writeback(p, s));
   HIP_TRY(launch_unpack(p->dp, (const uint8_t*)pool, B, S_hat, r, c, z, s));
   return ok();
+}
+
+int stepq_read_slots(stepq_plan_t p, const void* pool, int n_slots, const int32_t* slots, int B,
+                     void* S, int dtype, void* stream) {
+  if (int rc = check_plan(p)) return rc;
+  if (int rc = check_slots(pool, n_slots, slots, B)) return rc;
+  if (dtype != STEPQ_DTYPE_F32 && dtype != STEPQ_DTYPE_BF16 && dtype != STEPQ_DTYPE_F16)
+    return fail(STEPQ_ERR_INVALID_ARG, "dtype must be STEPQ_DTYPE_F32, _BF16 or _F16");
+  if (B > 0 && !S) return fail(STEPQ_ERR_INVALID_ARG, "S is NULL");
+  if (((uintptr_t)S & 15u) != 0) return fail(STEPQ_ERR_INVALID_ARG, "S must be 16-byte aligned");
+  if (int rc = check_grid(p, B)) return rc;
+  DeviceGuard dg(p->device);
+  hipStream_t s = (hipStream_t)stream;
+  if (int rc = refuse_capture(p, s, "read_slots")) return rc;
+  HIP_TRY(wait_writeback(p, s));
+  HIP_TRY(launch_read(p->dp, (const uint8_t*)pool, n_slots, slots, B, S, dtype, nullptr, nullptr,
+                      nullptr, s));
+  return ok();
+}
+
+// Workspace of a prompt pass: the states [N, H, d, d], the resolved slots and rows, then the
+// sequence pass's own.
+static size_t prefill_bytes(const stepq_plan* p, const SeqArgs& a) {
+  const size_t n = (size_t)a.N;
+  return n * p->H * p->D * p->D * sizeof(float) + 2 * ((n * sizeof(int) + 255) / 256 * 256) +
+         (uses_chunks(a) ? chunk_forward_bytes(a) : 0);
+}
+
+// The plan fixes the kind, the gate order, the heads, d and the device of the description.
+static int prefill_args(stepq_plan_t p, const stepq_delta_desc* d, SeqArgs* a) {
+  if (int rc = check_plan(p)) return rc;
+  if (!d) return fail(STEPQ_ERR_INVALID_ARG, "desc is NULL");
+  if (d->kind != p->kind || d->order != p->dp.order || d->n_heads != p->H || d->d != p->D ||
+      d->device != p->device)
+    return fail(STEPQ_ERR_INVALID_ARG, "desc's kind, order, n_heads, d and device must be the plan's");
+  if (int rc = seq_args(d, a)) return rc;
+  if (p->mode == STEPQ_MODE_SPLIT && d->n_seqs > p->max_batch)
+    return fail(STEPQ_ERR_INVALID_ARG, "n_seqs = %d exceeds max_batch %d", d->n_seqs, p->max_batch);
+  a->status = p->status;
+  return check_grid(p, d->n_seqs);
+}
+
+int stepq_prefill_workspace(stepq_plan_t p, const stepq_delta_desc* d, size_t* bytes) {
+  SeqArgs a;
+  if (int rc = prefill_args(p, d, &a)) return rc;
+  if (!bytes) return fail(STEPQ_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = prefill_bytes(p, a);
+  return ok();
+}
+
+int stepq_prefill_slots(stepq_plan_t p, const stepq_delta_desc* d, void* pool, int n_slots,
+                        const int32_t* slots, const void* q, const void* k, const void* v,
+                        const float* alpha, const float* beta, void* out, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  SeqArgs a;
+  if (int rc = prefill_args(p, d, &a)) return rc;
+  if (int rc = check_slots(pool, n_slots, slots, a.N)) return rc;
+  if (int rc = seq_inputs(&a, q, k, v, alpha, beta, out)) return rc;
+  if (int rc = seq_workspace(workspace, workspace_bytes, prefill_bytes(p, a))) return rc;
+  if (a.N == 0 || a.T == 0) return ok();
+  DeviceGuard dg(p->device);
+  hipStream_t s = (hipStream_t)stream;
+  if (int rc = refuse_capture(p, s, "prefill_slots")) return rc;
+  HIP_TRY(wait_writeback(p, s));
+  char* w = (char*)workspace;
+  float* S = (float*)w;
+  w += (size_t)a.N * p->H * p->D * p->D * sizeof(float);
+  int* slot_of = (int*)w;
+  w += ((size_t)a.N * sizeof(int) + 255) / 256 * 256;
+  int* row_of = (int*)w;
+  w += ((size_t)a.N * sizeof(int) + 255) / 256 * 256;
+  HIP_TRY(launch_read(p->dp, (const uint8_t*)pool, n_slots, slots, a.N, S, kF32, &a, slot_of, row_of, s));
+  a.S_in = a.S_out = S;
+  a.slots = row_of;
+  a.n_slots = a.N;
+  a.ws = w;
+  a.status = nullptr;  // the read has reported bad slots and offsets
+  HIP_TRY(uses_chunks(a) ? launch_chunk_forward(a, s) : launch_recurrent(a, s));
+  return encode_impl(p, S, pool, n_slots, slot_of, a.N, stream);
 }
 
 int stepq_sync(stepq_plan_t p) {

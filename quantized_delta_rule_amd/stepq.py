@@ -19,6 +19,7 @@ GDN, KDA = 0, 1
 FUSED, SPLIT = 0, 1
 DELTA_FIRST, DECAY_FIRST = 0, 1   # gate order: A = Diag(a)(I - b k k^T) or (I - b k k^T) Diag(a)
 FLAG_NONFINITE, FLAG_SCALE_OVF, FLAG_PIVOT_OVF, FLAG_BAD_SLOT = 1, 2, 4, 8
+FLAG_BAD_SEQ = 16
 
 _lib = None
 
@@ -56,6 +57,13 @@ def lib() -> ctypes.CDLL:
         "stepq_encode_state_slots": (i, [P, P, P, i, P, i, P]),
         "stepq_decode_step_slots": (i, [P, P, i, P, i, P, P, P, P, P, P, P]),
         "stepq_unpack_debug": (i, [P, P, i, P, P, P, P, P]),
+        "stepq_delta_forward_workspace": (i, [P, ctypes.POINTER(sz)]),
+        "stepq_delta_backward_workspace": (i, [P, ctypes.POINTER(sz)]),
+        "stepq_delta_forward": (i, [P] * 8 + [i, P, P, P, sz, P]),
+        "stepq_delta_backward": (i, [P] * 16 + [sz, P]),
+        "stepq_prefill_workspace": (i, [P, P, ctypes.POINTER(sz)]),
+        "stepq_prefill_slots": (i, [P, P, P, i] + [P] * 8 + [sz, P]),
+        "stepq_read_slots": (i, [P, P, i, P, i, P, i, P]),
         "stepq_get_status": (i, [P, ctypes.POINTER(ctypes.c_uint32), i]),
         "stepq_sync": (i, [P]),
         "stepq_debug_side_delay": (i, [P, ctypes.c_longlong]),
@@ -221,6 +229,36 @@ class Plan:
         _check(lib().stepq_decode_step_slots(self._h, self._pool(pool, n_slots), int(n_slots),
                                              self._slots(slots, B), int(B), *args,
                                              _stream_ptr(stream)), "decode_step_slots")
+
+    # -- prompts into the pool, and its values -------------------------------------------------
+    def prefill_slots(self, pool, n_slots, slots, q, k, v, alpha, beta, out, *, cu_seqlens=None,
+                      n_seqs=None, workspace=None, stream=None):
+        """Runs each sequence's tokens from the packed state in its slot and packs the last state
+        back (tensors and offsets as for delta.forward)."""
+        from . import delta
+        a = delta._Sequences(q, k, v, alpha, beta, out, "out", cu_seqlens, n_seqs, self.kind,
+                             self.order, None, stream)
+        if a.device != self.device:
+            raise ValueError(f"q must live on cuda:{self.device} (got cuda:{a.device})")
+        if (a.H, a.d) != (self.H, self.d):
+            raise ValueError(f"v must have the plan's heads [{self.H}, {self.d}] (got [{a.H}, {a.d}])")
+        L, d = lib(), ctypes.byref(a.desc)
+        ws, size, keep = a.workspace(workspace, delta._need(L.stepq_prefill_workspace,
+                                                            "prefill_workspace", self._h, d))
+        _check(L.stepq_prefill_slots(self._h, d, self._pool(pool, n_slots), int(n_slots),
+                                     self._slots(slots, a.N), a.q, a.k, a.v, a.alpha, a.beta, a.out,
+                                     ws, size, a.ptr()), "prefill_slots")
+
+    def read_slots(self, pool, n_slots, slots, B, S, stream=None):
+        """Values r c z of B slots into S [B, H, d, d] (float32, bfloat16 or float16)."""
+        import torch
+        from . import delta
+        sp = _dev_tensor(S, "S", S.dtype, B * self.H * self.d * self.d, self.device)
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        _check(lib().stepq_read_slots(self._h, self._pool(pool, n_slots), int(n_slots),
+                                      self._slots(slots, B), int(B), sp, delta.dtype_code(S.dtype),
+                                      _stream_ptr(stream)), "read_slots")
 
     def unpack(self, pool, B, stream=None):
         """Returns S_hat [B,H,d,d] f32, r [B,H,d] u16 bits, c [B,H,d] u16 bits, z [B,H,d,d] i8."""
