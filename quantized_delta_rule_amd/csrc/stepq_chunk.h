@@ -38,22 +38,52 @@ template <int DT> constexpr int kOutPlanes = DT == kBF16 ? 1 : 2; // operands of
 
 // Workspace of the forward pass.  Key block (chunk slot, key head): K, K^T and Q fragments.  Head block
 // (chunk slot, value head): T and P fragments and the row tables.
-template <int D, int DT> struct Lay {
+template <int D, int DT> struct LayF {
+  static constexpr bool grad = false;
   static constexpr int NF = D / 8;                       // fragments of K, K^T or Q (one plane)
   static constexpr int NPI = kInPlanes<DT>, NPO = kOutPlanes<DT>;
   static constexpr int offK = 0, offKT = NPI * NF * kFrag, offQ = 2 * NPI * NF * kFrag;
   static constexpr int key = 3 * NPI * NF * kFrag;
   static constexpr int offT = 0, offP = 2 * kTri * kFrag, offTab = offP + NPO * kTri * kFrag;
+  static constexpr int offTt = offTab;  // none
   static constexpr int head = offTab + 2048;
+};
+// Workspace of the gradient.  Q^T in Q's place, K K^T and Q K^T (binary32, row-major, lower tiles) behind
+// the fragments; T, T^T, P^T (two planes each).  Then, per chunk slot and value head in binary32: the
+// states before and the states' gradients behind every chunk, W and Y.
+template <int D, int DT> struct LayB {
+  static constexpr bool grad = true;
+  static constexpr int NF = D / 8, NPI = kInPlanes<DT>, NPO = 2;
+  static constexpr int offK = 0, offKT = NPI * NF * kFrag, offQ = 2 * NPI * NF * kFrag;
+  static constexpr int offKK = 3 * NPI * NF * kFrag, offQK = offKK + 64 * 64 * 4;
+  static constexpr int key = offQK + 64 * 64 * 4;
+  static constexpr int offT = 0, offTt = 2 * kTri * kFrag, offP = 4 * kTri * kFrag, offTab = 6 * kTri * kFrag;
+  static constexpr int head = offTab + 4096;
 };
 // Row tables (64 floats each); inverse operand scales are folded in.
 constexpr int kTabU = 0;     // beta G / scale of K's row
 constexpr int kTabB = 64;    // beta (0 behind the sequence's end)
 constexpr int kTabT = 128;   // 1 / scale of T's row
 constexpr int kTabQ = 192;   // G / scale of Q's row
-constexpr int kTabP = 256;   // 1 / scale of P's row
+constexpr int kTabP = 256;   // 1 / scale of P's (gradient: P^T's) row
 constexpr int kTabD = 320;   // L[C, s] / scale of K's row (K^T's column)
-constexpr int kTabG = 384;   // [0] = G_C
+constexpr int kTabG = 384;   // G; [63] = G_C
+constexpr int kTabTt = 448;  // 1 / scale of T^T's row            (gradient from here on)
+constexpr int kTabL = 512;   // L[C, s]
+constexpr int kTabIK = 576;  // 1 / scale of K's row
+constexpr int kTabIQ = 640;  // 1 / scale of Q's row
+
+// Fragment of a 64 x 64 upper-triangular matrix: row tile rt = 2 b + p, k-step ks >= b.
+__host__ __device__ constexpr int up_frag(int rt, int ks) { return rt < 2 ? 2 * rt + ks : 2 + rt; }
+
+template <class Y>
+__host__ __device__ inline long long key_bytes(const SeqArgs& a) {
+  return chunk_slots(a.T, a.N) * a.Hq * Y::key;
+}
+template <class Y>
+__host__ __device__ inline long long head_bytes(const SeqArgs& a) {
+  return chunk_slots(a.T, a.N) * a.H * Y::head;
+}
 
 // Power of two that brings magnitude m into [2^11, 2^12), and its inverse.  Zero, subnormal and
 // non-finite m get the nearest scale whose inverse is normal too.
