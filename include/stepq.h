@@ -223,7 +223,8 @@ const char* stepq_last_error(void);
  *                offsets break the rule is skipped and raises STEPQ_FLAG_BAD_SEQ.  NULL: n_seqs
  *                sequences of n_tokens / n_seqs rows each (must divide).
  *   q_stride .. out_stride  elements from one token's row to the next (heads of a token are d
- *                elements apart); 0 = packed (heads * d).  A multiple of 16 bytes.
+ *                elements apart); 0 = packed (heads * d).  A multiple of 16 bytes, below
+ *                2^23 elements.
  *   device       HIP device ordinal of every pointer and of the stream.
  *   status       device uint32 that the kernels OR their STEPQ_FLAG_* bits into, or NULL.
  */

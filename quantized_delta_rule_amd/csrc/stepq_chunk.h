@@ -131,6 +131,74 @@ __device__ __forceinline__ float to_operand(const f4* x, h8* hi, h8* lo) {
   return inv;
 }
 
+// Copies 1 KiB (16 bytes a lane) from memory straight into LDS, without registers and without a wait: the
+// reader waits for vmcnt 0 and then for a barrier.  In assembly because the compiler would otherwise wait
+// before the next LDS read of any buffer; there is no output register that could be reused too early.
+// src and at (an LDS byte offset) are uniform, lane16 = 16 * lane.
+__device__ __forceinline__ void copy_to_lds(const char* src, unsigned at, unsigned lane16) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(lane16), "s"(src) : "memory", "m0");
+}
+__device__ __forceinline__ unsigned lds_offset(const void* p) {
+  return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
+}
+// `bytes` (a multiple of 1 KiB) from src to LDS offset `at`, the pieces over NW waves.
+template <int NW>
+__device__ __forceinline__ void copy_block(const char* src, unsigned at, int bytes, int w, unsigned lane16) {
+  src += w * kFrag;
+  at += w * kFrag;
+#pragma unroll
+  for (int i = 0; i < bytes; i += NW * kFrag)
+    if (i + NW * kFrag <= bytes || i + w * kFrag < bytes) copy_to_lds(src + i, at + i, lane16);
+}
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Keeps the LDS reads above it above the arithmetic below it: fragments are read one product ahead.
+__device__ __forceinline__ void ahead() { __builtin_amdgcn_sched_barrier(0); }
+
+// Rows of a chunk in accumulator order: x[rt][i] = row 32 (rt >> 1) + 8 g + 4 (rt & 1) + i of `base` (the
+// chunk's first row, this head's first column), this lane's CT columns as they lie in memory.  Rows
+// behind the end (len <= r) read the last row instead and are dropped by the caller: no load sits in a
+// branch of its own, and none is converted before it is used, so all are in flight at once.
+template <int DT, int CT> struct Raw;
+template <> struct Raw<kF32, 1> { float x; };
+template <> struct Raw<kF32, 2> { f2 x; };
+template <> struct Raw<kBF16, 1> { unsigned x; };  // a register each: pairs would be packed on arrival
+template <> struct Raw<kBF16, 2> { us2 x; };
+template <> struct Raw<kF16, 1> { unsigned x; };  // a register each: pairs would be packed on arrival
+template <> struct Raw<kF16, 2> { us2 x; };
+template <int DT, int CT>
+__device__ __forceinline__ float raw_value(const Raw<DT, CT>& r, int ct) {
+  if constexpr (DT == kF32 && CT == 1) return r.x;
+  else if constexpr (DT == kF32) return r.x[ct];
+  else if constexpr (CT == 1) return e_f<DT>((unsigned short)r.x);
+  else return e_f<DT>(r.x[ct]);
+}
+template <int DT, int CT>
+__device__ __forceinline__ void rows_acc(const char* base, int stride, int len, int col, int g, Raw<DT, CT> (*x)[4]) {
+  constexpr int es = DT == kF32 ? 4 : 2;
+#pragma unroll
+  for (int rt = 0; rt < 4; rt++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int r = min(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i, len - 1);
+      const char* const p = base + (__umul24(r, stride) + col) * es;
+      if constexpr (DT != kF32 && CT == 1) x[rt][i].x = *(const unsigned short*)p;
+      else x[rt][i] = *(const Raw<DT, CT>*)p;
+    }
+}
+template <int DT, int CT>
+__device__ __forceinline__ void rows_store(char* base, int stride, int len, int col, int g, const float (*x)[4][CT]) {
+  constexpr int es = DT == kF32 ? 4 : 2;
+  const unsigned lane_off = (unsigned)(8 * g * stride + col) * es;
+#pragma unroll
+  for (int rt = 0; rt < 4; rt++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const int r = 32 * (rt >> 1) + 4 * (rt & 1) + i;
+      if (len >= kChunk || r + 8 * g < len)
+        storen<DT, CT>(base + (long long)r * stride * es + lane_off, 0, x[rt][i]);
+    }
+}
+
 // The chunk of chunk slot j: sequence, first token, tokens (<= 64).  False: the slot is empty.
 struct ChunkAt {
   int s, t0, len, c;

@@ -330,7 +330,9 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   // staged: K, K^T (and Q), then T (and P), then the tables
   constexpr int keyN = Y::grad ? Y::offQ : Y::key, triN = Y::grad ? Y::offTt : Y::offTab;
   constexpr int offT = keyN, offP = keyN + Y::offP, offTab = keyN + triN;
-  __shared__ __attribute__((aligned(16))) char lds[offTab + 2048];
+  constexpr int part = offTab + 2048;
+  constexpr int NBUF = 2 * part <= 160 * 1024 ? 2 : 1;  // binary32 inputs have room for one
+  __shared__ __attribute__((aligned(16))) char buf[NBUF * part];
   const long long tile = blockIdx.x;
   const int s = (int)(tile / A.H), h = (int)(tile - (long long)s * A.H);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -356,13 +358,47 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   const char* const heads = A.ws + key_bytes<Y>(A);
   const int hq = h / A.grp;
   const int nc = (t1 - t0 + kChunk - 1) / kChunk;
-  for (int c = 0; c < nc; c++) {
+  // chunk c's pieces on their way into LDS, 1 KiB a wave at a time
+  const unsigned lds0 = lds_offset(buf), lane16 = 16 * lane;
+  auto fetch = [&](int c) {
     const char* const key = A.ws + ((j0 + c) * A.Hq + hq) * Y::key;
     const char* const head = heads + ((j0 + c) * A.H + h) * Y::head;
-    __syncthreads();
-    for (int i = tid * 16; i < keyN; i += 64 * NW * 16) *(f4*)(lds + i) = *(const f4*)(key + i);
-    for (int i = tid * 16; i < triN; i += 64 * NW * 16) *(f4*)(lds + offT + i) = *(const f4*)(head + i);
-    for (int i = tid * 16; i < 2048; i += 64 * NW * 16) *(f4*)(lds + offTab + i) = *(const f4*)(head + Y::offTab + i);
+    const unsigned at = lds0 + (NBUF == 2 ? (c & 1) * part : 0);
+    copy_block<NW>(key, at, keyN, w, lane16);
+    if constexpr (Y::grad) {
+      copy_block<NW>(head, at + offT, triN, w, lane16);
+      copy_block<NW>(head + Y::offTab, at + offTab, 2048, w, lane16);
+    } else {
+      copy_block<NW>(head, at + offT, Y::head, w, lane16);
+    }
+  };
+  // V of chunk c in accumulator order
+  Raw<DT, CT> v[4][4];
+  auto fetch_v = [&](int c) {
+    const int tc = t0 + c * kChunk;
+    rows_acc<DT, CT>((const char*)A.v + (tc * A.vs + (long long)h * D) * (DT == kF32 ? 4 : 2), (int)A.vs, t1 - tc, col, g, v);
+  };
+  if (nc) {
+    fetch(0);
+    fetch_v(0);
+  }
+  for (int c = 0; c < nc; c++) {
+    const char* const lds = buf + (NBUF == 2 ? (c & 1) * part : 0);
+    const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
+    wait_copies();
+    __syncthreads();  // chunk c is there, and every wave is done with chunk c - 1
+    f4 R[CT][4];
+#pragma unroll
+    for (int rt = 0; rt < 4; rt++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+#pragma unroll
+        for (int ct = 0; ct < CT; ct++)
+          R[ct][rt][i] = 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i < len ? raw_value<DT, CT>(v[rt][i], ct) : 0.0f;
+    if (c + 1 < nc) {
+      if (NBUF == 2) fetch(c + 1);
+      fetch_v(c + 1);
+    }
     if constexpr (Y::grad) {
       float* const dst = keepS + ((j0 + c) * A.H + h) * D * D + col;
 #pragma unroll
@@ -375,67 +411,83 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
           storen<kF32, CT>(dst, (long long)(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i) * D, x);
         }
     }
-    const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
-    // V in accumulator order (zero behind the end)
-    f4 R[CT][4];
-#pragma unroll
-    for (int rt = 0; rt < 4; rt++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int t = 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i;
-        float x[CT] = {};
-        if (t < len) loadn<DT, CT>(A.v, (tc + (long long)t) * A.vs + (long long)h * D + col, x);
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) R[ct][rt][i] = x[ct];
-      }
-    __syncthreads();
     const float* const tab = (const float*)(lds + offTab);
     auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane * 16); };
     auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
-    h8 Sh[CT][NB], Sl[CT][NB];
-    float iS[CT];
+    // Every product's fragments are read while its other operand is formed.
+    h8 f[Y::NF], fl[NPI == 2 ? Y::NF : 1];
+    auto read = [&](int off) {
+#pragma unroll
+      for (int n = 0; n < Y::NF; n++) {
+        f[n] = frag(off, Y::NF, 0, n);
+        if constexpr (NPI == 2) fl[n] = frag(off, Y::NF, 1, n);
+      }
+    };
+    h8 Sh[CT][NB], Sl[CT][NB], xh[CT][2], xl[CT][2];
+    float iS[CT], ix[CT];
+    read(Y::offK);
+    ahead();
 #pragma unroll
     for (int ct = 0; ct < CT; ct++) iS[ct] = to_operand<NB, 2>(S[ct], Sh[ct], Sl[ct]);
     // R = beta V - beta G K S0
+    f4 z[CT][2 * NB > 4 ? 2 * NB : 4];
+    auto times_state = [&](bool low) {
 #pragma unroll
-    for (int rt = 0; rt < 4; rt++) {
-      f4 u[CT] = {};
+      for (int rt = 0; rt < 4; rt++) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ks++) {
-        const h8 a = frag(Y::offK, Y::NF, 0, rt * KS + ks);
+        for (int ct = 0; ct < CT; ct++) z[ct][rt] = f4{0, 0, 0, 0};
 #pragma unroll
-        for (int ct = 0; ct < CT; ct++) u[ct] = mfma(a, Sl[ct][ks], mfma(a, Sh[ct][ks], u[ct]));
-        if constexpr (NPI == 2) {
-          const h8 al = frag(Y::offK, Y::NF, 1, rt * KS + ks);
+        for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-          for (int ct = 0; ct < CT; ct++) u[ct] = mfma(al, Sh[ct][ks], u[ct]);
-        }
+          for (int ct = 0; ct < CT; ct++) {
+            z[ct][rt] = mfma(f[rt * KS + ks], Sh[ct][ks], z[ct][rt]);
+            if (low) z[ct][rt] = mfma(f[rt * KS + ks], Sl[ct][ks], z[ct][rt]);
+            if constexpr (NPI == 2) z[ct][rt] = mfma(fl[rt * KS + ks], Sh[ct][ks], z[ct][rt]);
+          }
       }
-      const f4 cu = rows(kTabU, rt), be = rows(kTabB, rt);
+    };
+    times_state(true);
+    ahead();
+    h8 ft[2][kTri];
 #pragma unroll
-      for (int ct = 0; ct < CT; ct++)
+    for (int n = 0; n < kTri; n++) {
+      ft[0][n] = frag(offT, kTri, 0, n);
+      ft[1][n] = frag(offT, kTri, 1, n);
+    }
+    ahead();
 #pragma unroll
-        for (int i = 0; i < 4; i++) R[ct][rt][i] = fmaf(-cu[i] * iS[ct], u[ct][i], be[i] * R[ct][rt][i]);
+    for (int ct = 0; ct < CT; ct++) {
+#pragma unroll
+      for (int rt = 0; rt < 4; rt++) {
+        const f4 cu = rows(kTabU, rt), be = rows(kTabB, rt);
+#pragma unroll
+        for (int i = 0; i < 4; i++) R[ct][rt][i] = fmaf(-cu[i] * iS[ct], z[ct][rt][i], be[i] * R[ct][rt][i]);
+      }
+      ix[ct] = to_operand<2, 2>(R[ct], xh[ct], xl[ct]);
     }
     // W = T R (in R's place)
-    h8 xh[CT][2], xl[CT][2];
-    float ix[CT];
 #pragma unroll
-    for (int ct = 0; ct < CT; ct++) ix[ct] = to_operand<2, 2>(R[ct], xh[ct], xl[ct]);
+    for (int rt = 0; rt < 4; rt++)
+#pragma unroll
+      for (int ct = 0; ct < CT; ct++) {
+        z[ct][rt] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks <= rt >> 1; ks++) {
+          const int n = tri_frag(rt, ks);
+          z[ct][rt] = mfma(ft[1][n], xh[ct][ks], mfma(ft[0][n], xl[ct][ks], mfma(ft[0][n], xh[ct][ks], z[ct][rt])));
+        }
+      }
+    ahead();
+    if constexpr (!Y::grad) read(Y::offQ);
+    else read(Y::offKT);
+    ahead();
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) {
-      f4 y[CT] = {};
-#pragma unroll
-      for (int ks = 0; ks <= rt >> 1; ks++) {
-        const h8 a = frag(offT, kTri, 0, tri_frag(rt, ks)), al = frag(offT, kTri, 1, tri_frag(rt, ks));
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) y[ct] = mfma(al, xh[ct][ks], mfma(a, xl[ct][ks], mfma(a, xh[ct][ks], y[ct])));
-      }
       const f4 it = rows(kTabT, rt);
 #pragma unroll
       for (int ct = 0; ct < CT; ct++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) R[ct][rt][i] = y[ct][i] * (it[i] * ix[ct]);
+        for (int i = 0; i < 4; i++) R[ct][rt][i] = z[ct][rt][i] * (it[i] * ix[ct]);
     }
     if constexpr (Y::grad) {
       float* const dst = keepW + ((j0 + c) * A.H + h) * 64 * D + col;
@@ -452,44 +504,37 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
       // O = G Q S0 + P W
 #pragma unroll
       for (int ct = 0; ct < CT; ct++) ix[ct] = to_operand<2, NPO>(R[ct], xh[ct], xl[ct]);
+      times_state(NPO == 2);
+      ahead();
+      h8 fp[NPO][kTri];
+#pragma unroll
+      for (int p = 0; p < NPO; p++)
+#pragma unroll
+        for (int n = 0; n < kTri; n++) fp[p][n] = frag(offP, kTri, p, n);
+      ahead();
+      float o[4][4][CT];
 #pragma unroll
       for (int rt = 0; rt < 4; rt++) {
-        f4 y[CT] = {}, z[CT] = {};
-#pragma unroll
-        for (int ks = 0; ks < KS; ks++) {
-          const h8 a = frag(Y::offQ, Y::NF, 0, rt * KS + ks);
-#pragma unroll
-          for (int ct = 0; ct < CT; ct++) {
-            y[ct] = mfma(a, Sh[ct][ks], y[ct]);
-            if constexpr (NPO == 2) y[ct] = mfma(a, Sl[ct][ks], y[ct]);
-          }
-          if constexpr (NPI == 2) {
-            const h8 al = frag(Y::offQ, Y::NF, 1, rt * KS + ks);
-#pragma unroll
-            for (int ct = 0; ct < CT; ct++) y[ct] = mfma(al, Sh[ct][ks], y[ct]);
-          }
-        }
+        f4 y[CT] = {};
 #pragma unroll
         for (int ks = 0; ks <= rt >> 1; ks++) {
-          const h8 a = frag(offP, kTri, 0, tri_frag(rt, ks));
+          const int n = tri_frag(rt, ks);
 #pragma unroll
-          for (int ct = 0; ct < CT; ct++) z[ct] = mfma(a, xh[ct][ks], z[ct]);
-          if constexpr (NPO == 2) {
-            const h8 al = frag(offP, kTri, 1, tri_frag(rt, ks));
-#pragma unroll
-            for (int ct = 0; ct < CT; ct++) z[ct] = mfma(al, xh[ct][ks], mfma(a, xl[ct][ks], z[ct]));
+          for (int ct = 0; ct < CT; ct++) {
+            y[ct] = mfma(fp[0][n], xh[ct][ks], y[ct]);
+            if constexpr (NPO == 2) y[ct] = mfma(fp[NPO - 1][n], xh[ct][ks], mfma(fp[0][n], xl[ct][ks], y[ct]));
           }
         }
         const f4 cq = rows(kTabQ, rt), ip = rows(kTabP, rt);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int t = 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i;
-          float o[CT];
+        for (int i = 0; i < 4; i++)
 #pragma unroll
-          for (int ct = 0; ct < CT; ct++) o[ct] = fmaf(cq[i] * iS[ct], y[ct][i], (ip[i] * ix[ct]) * z[ct][i]);
-          if (t < len) storen<DT, CT>(A.out, (tc + (long long)t) * A.os + (long long)h * D + col, o);
-        }
+          for (int ct = 0; ct < CT; ct++) o[rt][i][ct] = fmaf(cq[i] * iS[ct], z[ct][rt][i], (ip[i] * ix[ct]) * y[ct][i]);
       }
+      ahead();
+      read(Y::offKT);
+      ahead();
+      rows_store<DT, CT>((char*)A.out + (tc * A.os + (long long)h * D) * (DT == kF32 ? 4 : 2), (int)A.os, len, col, g, o);
     }
     // S1 = G_C S0 + K^T diag(L[C, .]) W
 #pragma unroll
@@ -500,23 +545,21 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     }
     const float G = tab[kTabG + 63];
 #pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++) {
-      f4 y[CT] = {};
+    for (int rt = 0; rt < 2 * NB; rt++)
 #pragma unroll
-      for (int ks = 0; ks < 2; ks++) {
-        const h8 a = frag(Y::offKT, Y::NF, 0, 2 * rt + ks);
+      for (int ct = 0; ct < CT; ct++) {
+        f4 y = {0, 0, 0, 0};
 #pragma unroll
-        for (int ct = 0; ct < CT; ct++) y[ct] = mfma(a, xl[ct][ks], mfma(a, xh[ct][ks], y[ct]));
-        if constexpr (NPI == 2) {
-          const h8 al = frag(Y::offKT, Y::NF, 1, 2 * rt + ks);
-#pragma unroll
-          for (int ct = 0; ct < CT; ct++) y[ct] = mfma(al, xh[ct][ks], y[ct]);
+        for (int ks = 0; ks < 2; ks++) {
+          y = mfma(f[2 * rt + ks], xl[ct][ks], mfma(f[2 * rt + ks], xh[ct][ks], y));
+          if constexpr (NPI == 2) y = mfma(fl[2 * rt + ks], xh[ct][ks], y);
         }
+#pragma unroll
+        for (int i = 0; i < 4; i++) S[ct][rt][i] = fmaf(G, S[ct][rt][i], ix[ct] * y[i]);
       }
-#pragma unroll
-      for (int ct = 0; ct < CT; ct++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) S[ct][rt][i] = fmaf(G, S[ct][rt][i], ix[ct] * y[ct][i]);
+    if (NBUF == 1 && c + 1 < nc) {
+      __syncthreads();
+      fetch(c + 1);
     }
   }
   if (!Y::grad && A.S_out) {

@@ -48,9 +48,9 @@ int seq_args(const void* desc, SeqArgs* a) {
   long long st[4];
   for (int i = 0; i < 4; i++) {
     st[i] = given[i] ? given[i] : packed[i];
-    if (st[i] < packed[i] || st[i] % unit || st[i] > (1LL << 40))
-      return fail(STEPQ_ERR_INVALID_ARG, "%s_stride %lld must be at least %lld and a multiple of 16 bytes",
-                  i == 0 ? "q" : i == 1 ? "k" : i == 2 ? "v" : "out", given[i], packed[i]);
+    if (st[i] < packed[i] || st[i] % unit || st[i] >= (1LL << 23))  // 64 rows within 31 bits of bytes
+      return fail(STEPQ_ERR_INVALID_ARG, "%s_stride %lld must be %lld .. 2^23 - 1 and a multiple of 16 bytes",
+                  i == 0 ? "q" : i == 1 ? "k" : i == 2 ? "v" : "out", st[i], packed[i]);
   }
   int ndev = 0;
   if (hipGetDeviceCount(&ndev) != hipSuccess || d->device < 0 || d->device >= ndev)
