@@ -3,7 +3,7 @@
 //
 // Mathematics of a chunk of C = 64 tokens (GDN; a_t gates, L[t,s] = prod_{s<r<=t} a_r, G_t = L[t,-1]):
 //   A = strict-lower(diag(beta) (L o K K^T)),  T = (I + A)^-1,  P = lower(L o Q K^T)
-//   R = diag(beta) (V - diag(G) K S0),  W = T R        (W_t = beta_t e_t, the weighted errors)
+//   R = V - diag(G) K S0,  W = T diag(beta) R            (W_t = beta_t e_t, the weighted errors)
 //   O = diag(G) Q S0 + P W,             S1 = G_C S0 + K^T diag(L[C,.]) W
 // L is formed by running products, never by quotients or logarithms, so a gate may be zero, negative
 // or above one.
@@ -37,19 +37,19 @@ template <int DT> constexpr int kInPlanes = DT == kF32 ? 2 : 1;   // q, k, v, d_
 template <int DT> constexpr int kOutPlanes = DT == kBF16 ? 1 : 2; // operands of 16-bit outputs only
 
 // Workspace of the forward pass.  Key block (chunk slot, key head): K, K^T and Q fragments.  Head block
-// (chunk slot, value head): T and P fragments and the row tables.
+// (chunk slot, value head): T diag(beta) and P fragments and the row tables.
 template <int D, int DT> struct LayF {
   static constexpr bool grad = false;
   static constexpr int NF = D / 8;                       // fragments of K, K^T or Q (one plane)
   static constexpr int NPI = kInPlanes<DT>, NPO = kOutPlanes<DT>;
   static constexpr int offK = 0, offKT = NPI * NF * kFrag, offQ = 2 * NPI * NF * kFrag;
-  static constexpr int key = 3 * NPI * NF * kFrag;
+  static constexpr int key = 3 * NPI * NF * kFrag, offKK = 0, offQK = 0;  // none
   static constexpr int offT = 0, offP = 2 * kTri * kFrag, offTab = offP + NPO * kTri * kFrag;
   static constexpr int offTt = offTab;  // none
   static constexpr int head = offTab + 2048;
 };
-// Workspace of the gradient.  Q^T in Q's place, K K^T and Q K^T (binary32, row-major, lower tiles) behind
-// the fragments; T, T^T, P^T (two planes each).  Then, per chunk slot and value head in binary32: the
+// Workspace of the gradient.  Q^T in Q's place, K K^T [t][s] and Q K^T [s][t] (binary32, t >= s within 32-row
+// blocks) behind the fragments; T, T^T, P^T (two planes each).  Then, per chunk slot and value head in binary32: the
 // states before and the states' gradients behind every chunk, W and Y.
 template <int D, int DT> struct LayB {
   static constexpr bool grad = true;
@@ -61,9 +61,9 @@ template <int D, int DT> struct LayB {
   static constexpr int head = offTab + 4096;
 };
 // Row tables (64 floats each); inverse operand scales are folded in.
-constexpr int kTabU = 0;     // beta G / scale of K's row
+constexpr int kTabU = 0;     // G / scale of K's row (gradient: times beta)
 constexpr int kTabB = 64;    // beta (0 behind the sequence's end)
-constexpr int kTabT = 128;   // 1 / scale of T's row
+constexpr int kTabT = 128;   // [0] = 1 / scale of T (gradient: of T's rows)
 constexpr int kTabQ = 192;   // G / scale of Q's row
 constexpr int kTabP = 256;   // 1 / scale of P's (gradient: P^T's) row
 constexpr int kTabD = 320;   // L[C, s] / scale of K's row (K^T's column)
@@ -98,36 +98,56 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// Maximum over the four lanes of a column (lanes that differ in bits 4 and 5), without LDS.
+__device__ __forceinline__ float col_max(float x) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
+}
+
 // 8 binary32 values times s as hi (and lo) planes.
 template <int NP>
 __device__ __forceinline__ void split8(const float* x, float s, h8& hi, h8& lo) {
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const float y = x[i] * s;
-    hi[i] = (_Float16)y;
-    if constexpr (NP == 2) lo[i] = (_Float16)(y - (float)hi[i]);
+    hi[i] = (_Float16)(x[i] * s);
+    if constexpr (NP == 2) lo[i] = (_Float16)fmaf(x[i], s, -(float)hi[i]);  // one mixed-precision fma
   }
 }
 
-// Accumulator row tiles x[0 .. 2 NB - 1] (16 rows each, one column a lane) -> B operands of NB 32-row
-// steps, with the column's scale; returns the inverse scale.
-template <int NB, int NP>
-__device__ __forceinline__ float to_operand(const f4* x, h8* hi, h8* lo) {
+// Largest magnitude of a column's accumulator tiles.
+template <int NT>
+__device__ __forceinline__ float tiles_max(const f4* x) {
   float m = 0.0f;
 #pragma unroll
-  for (int t = 0; t < 2 * NB; t++)
+  for (int t = 0; t < NT; t++)
 #pragma unroll
     for (int i = 0; i < 4; i++) m = fmaxf(m, fabsf(x[t][i]));
-  m = fmaxf(m, __shfl_xor(m, 16));
-  m = fmaxf(m, __shfl_xor(m, 32));
-  float inv;
-  const float s = scale_of(m, inv);
+  return col_max(m);
+}
+// Accumulator row tiles x[0 .. 2 NB - 1] (16 rows each, one column a lane) times s -> B operands of NB
+// 32-row steps.  SCALED: s is 1.
+template <int NB, int NP, bool SCALED = false>
+__device__ __forceinline__ void to_planes(const f4* x, float s, h8* hi, h8* lo) {
 #pragma unroll
   for (int b = 0; b < NB; b++) {
+    if (SCALED) asm("" : "+v"(s));  // an opaque 1: keeps the fma below, which rounds to binary16 by itself
     const float y[8] = {x[2 * b][0], x[2 * b][1], x[2 * b][2], x[2 * b][3],
                         x[2 * b + 1][0], x[2 * b + 1][1], x[2 * b + 1][2], x[2 * b + 1][3]};
-    split8<NP>(y, s, hi[b], lo[b]);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      hi[b][i] = (_Float16)(SCALED ? y[i] : y[i] * s);
+      if constexpr (NP == 2) lo[b][i] = (_Float16)fmaf(y[i], s, -(float)hi[b][i]);
+    }
   }
+}
+// The same with the column's own scale; returns the inverse scale.
+template <int NB, int NP>
+__device__ __forceinline__ float to_operand(const f4* x, h8* hi, h8* lo) {
+  float inv;
+  const float s = scale_of(tiles_max<2 * NB>(x), inv);
+  to_planes<NB, NP>(x, s, hi, lo);
   return inv;
 }
 
@@ -154,50 +174,39 @@ __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)
 // Keeps the LDS reads above it above the arithmetic below it: fragments are read one product ahead.
 __device__ __forceinline__ void ahead() { __builtin_amdgcn_sched_barrier(0); }
 
-// Rows of a chunk in accumulator order: x[rt][i] = row 32 (rt >> 1) + 8 g + 4 (rt & 1) + i of `base` (the
-// chunk's first row, this head's first column), this lane's CT columns as they lie in memory.  Rows
-// behind the end (len <= r) read the last row instead and are dropped by the caller: no load sits in a
-// branch of its own, and none is converted before it is used, so all are in flight at once.
-template <int DT, int CT> struct Raw;
-template <> struct Raw<kF32, 1> { float x; };
-template <> struct Raw<kF32, 2> { f2 x; };
-template <> struct Raw<kBF16, 1> { unsigned x; };  // a register each: pairs would be packed on arrival
-template <> struct Raw<kBF16, 2> { us2 x; };
-template <> struct Raw<kF16, 1> { unsigned x; };  // a register each: pairs would be packed on arrival
-template <> struct Raw<kF16, 2> { us2 x; };
-template <int DT, int CT>
-__device__ __forceinline__ float raw_value(const Raw<DT, CT>& r, int ct) {
-  if constexpr (DT == kF32 && CT == 1) return r.x;
-  else if constexpr (DT == kF32) return r.x[ct];
-  else if constexpr (CT == 1) return e_f<DT>((unsigned short)r.x);
-  else return e_f<DT>(r.x[ct]);
-}
-template <int DT, int CT>
-__device__ __forceinline__ void rows_acc(const char* base, int stride, int len, int col, int g, Raw<DT, CT> (*x)[4]) {
-  constexpr int es = DT == kF32 ? 4 : 2;
+// Rows of a chunk in accumulator order: x[rt][i] = row 32 (rt >> 1) + 8 g + 4 (rt & 1) + i, this lane's
+// column.  Through a buffer descriptor that ends behind the chunk's last token: rows behind it read as
+// zero and are not written, without a branch or a comparison, and nothing is converted before it is used,
+// so all loads are in flight at once.
+template <int DT>
+struct Rows {
+  static constexpr int es = DT == kF32 ? 4 : 2;
+  unsigned first;  // byte offset of row 8 g
+  int step;        // bytes from row to row
+  __device__ Rows(long long stride, int col, int g) : first((unsigned)((8 * g * (int)stride + col) * es)), step((int)stride * es) {}
+  __device__ static __amdgpu_buffer_rsrc_t at(const void* p, long long row, long long stride, int head_col, int D, int len) {
+    return __builtin_amdgcn_make_buffer_rsrc((char*)p + (row * stride + head_col) * es, 0,
+                                             (int)((unsigned)(len - 1) * (unsigned)stride * es + D * es), 0x00020000);
+  }
+  __device__ unsigned off(int rt, int i) const { return first + (unsigned)((32 * (rt >> 1) + 4 * (rt & 1) + i) * step); }
+  __device__ void load(__amdgpu_buffer_rsrc_t r, unsigned (*x)[4]) const {
 #pragma unroll
-  for (int rt = 0; rt < 4; rt++)
+    for (int rt = 0; rt < 4; rt++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int r = min(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i, len - 1);
-      const char* const p = base + (__umul24(r, stride) + col) * es;
-      if constexpr (DT != kF32 && CT == 1) x[rt][i].x = *(const unsigned short*)p;
-      else x[rt][i] = *(const Raw<DT, CT>*)p;
-    }
-}
-template <int DT, int CT>
-__device__ __forceinline__ void rows_store(char* base, int stride, int len, int col, int g, const float (*x)[4][CT]) {
-  constexpr int es = DT == kF32 ? 4 : 2;
-  const unsigned lane_off = (unsigned)(8 * g * stride + col) * es;
-#pragma unroll
-  for (int rt = 0; rt < 4; rt++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int r = 32 * (rt >> 1) + 4 * (rt & 1) + i;
-      if (len >= kChunk || r + 8 * g < len)
-        storen<DT, CT>(base + (long long)r * stride * es + lane_off, 0, x[rt][i]);
-    }
-}
+      for (int i = 0; i < 4; i++) {
+        if constexpr (DT == kF32) x[rt][i] = __builtin_amdgcn_raw_buffer_load_b32(r, off(rt, i), 0, 0);
+        else x[rt][i] = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, off(rt, i), 0, 0);
+      }
+  }
+  __device__ static float value(unsigned x) {
+    if constexpr (DT == kF32) return __uint_as_float(x);
+    else return e_f<DT>((unsigned short)x);
+  }
+  __device__ void store(__amdgpu_buffer_rsrc_t r, int rt, int i, float x) const {
+    if constexpr (DT == kF32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off(rt, i), 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(f_e<DT>(x), r, off(rt, i), 0, 0);
+  }
+};
 
 // The chunk of chunk slot j: sequence, first token, tokens (<= 64).  False: the slot is empty.
 struct ChunkAt {

@@ -12,305 +12,448 @@ constexpr int kPitch = 68;  // floats of a row of the 64 x 64 matrices in LDS
 // local matrices
 // ---------------------------------------------------------------------------------------------
 
-template <int D, int DT>
+// One workgroup per (chunk, key head): K and Q once, then the value heads that share them.  Wave w owns the 16
+// tokens of row tile w (32 (w >> 1) + perm(lane & 15, w & 1)) as columns of K K^T and K Q^T: with K's row
+// tiles as the A side the accumulators of a pair hold 8 consecutive tokens s of a lane's token t, which is
+// P's fragment as it is and two 16-byte stores of A.  (The gradient wants P^T: Q on the A side, s as columns.)
+//
+// Products of gates between two tokens come from running products inside groups of 8 and blocks of 32:
+//   L[t,s] = pre32[t] suf32[s] across blocks, pre8[t] mid suf8[s] across groups of a block,
+// pre = from the group's start to t, suf = behind s to the group's end; inside a group one by one.
+template <int D, int DT, bool QT>
 struct PrepSmem {
-  static constexpr int NPI = kInPlanes<DT>, KP = D + 8;  // 16-byte aligned rows, 4 banks apart
-  union {
-    struct {
-      _Float16 K[NPI][64][KP], Q[NPI][64][KP];
-    } in;
-    struct {
-      float L[64][kPitch], A[64][kPitch], P[64][kPitch];  // L becomes T once A and P are formed
-    } m;
-  };
-  float isk[64], isq[64], al[64], be[64], sT[64], sP[64], sU[64];
+  static constexpr int NPI = kInPlanes<DT>;
+  _Float16 K[NPI][64][D + 8], Q[QT ? NPI : 1][QT ? 64 : 1][D + 8];
+  float X[64][kPitch];   // A, then T but for its lower left quarter
+  float Z[32][36];       // T's lower left quarter
+  float gate[4][5][64];  // a wave's copies: a, pre8, suf8, pre32, suf32
+  float isk[64], isq[64], be[64], most[4];
 };
 
-// Rows of q or k (tokens behind the end repeat the last one: their W is zero) as scaled planes.
+// The wave's 16 rows of q or k as scaled planes (a lane: row `row`, elements 32 ks + 8 g ..); returns the
+// inverse scale.
 template <int D, int DT>
-__device__ __forceinline__ void load_rows(const void* src, long long stride, long long head, int t0,
-                                          int len, _Float16 (*dst)[64][D + 8], float* is) {
-  constexpr int E = D / 4;
-  const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
-  const long long at = (t0 + (long long)(row < len ? row : len - 1)) * stride + head + part * E;
-  float x[E];
-  float m = 0.0f;
+__device__ __forceinline__ float load_rows(const void* src, long long at, int g, h8 (*f)[kInPlanes<DT>]) {
+  constexpr int KS = D / 32, NPI = kInPlanes<DT>;
+  float x[KS][8], m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E; i += 8) {
-    load8<DT>(src, at + i, x + i);
+  for (int ks = 0; ks < KS; ks++) load8<DT>(src, at + 32 * ks + 8 * g, x[ks]);
 #pragma unroll
-    for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(x[i + j]));
-  }
-  m = fmaxf(m, __shfl_xor(m, 1));
-  m = fmaxf(m, __shfl_xor(m, 2));
+  for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+    for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[ks][e]));
   float inv;
-  const float s = scale_of(m, inv);
-  if (part == 0) is[row] = inv;
+  const float s = scale_of(col_max(m), inv);
 #pragma unroll
-  for (int i = 0; i < E; i += 8) {
-    h8 hi, lo;
-    split8<kInPlanes<DT>>(x + i, s, hi, lo);
-    *(h8*)&dst[0][row][part * E + i] = hi;
-    if constexpr (kInPlanes<DT> == 2) *(h8*)&dst[1][row][part * E + i] = lo;
+  for (int ks = 0; ks < KS; ks++) {
+    h8 lo;
+    split8<NPI>(x[ks], s, f[ks][0], lo);
+    if constexpr (NPI == 2) f[ks][1] = lo;
   }
+  return inv;
 }
 
-// T = (I + A)^-1 in place of X: 16 x 16 diagonal blocks by forward substitution (a wave each, a column a
-// lane), then X21 = -X22 (A21 X11) for 16- and 32-row halves on binary32 matrix instructions.
-__device__ __forceinline__ void invert(const float (*A)[kPitch], float (*X)[kPitch], int w, int lane) {
+// Inverses of the two 32 x 32 diagonal blocks I + A (strictly lower A in X), one wave each: the 16 x 16
+// blocks by forward substitution (a column a lane, both blocks at once), then X10 = -X11 (A10 X00) on
+// binary32 matrix instructions.  Substitution, not a power series: keys that repeat make A's powers large.
+// Returns the largest magnitude written, columns times be.
+__device__ __forceinline__ float invert_block(float (*X)[kPitch], const float* be, int r0, int lane) {
   const int c = lane & 15, g = lane >> 4;
-  if (lane < 16) {
+  float m = 0.0f;
+  if (lane < 32) {
+    const int b = r0 + 16 * g;
     float x[16];
 #pragma unroll
     for (int t = 0; t < 16; t++) {
       float acc = t == c ? 1.0f : 0.0f;
 #pragma unroll
-      for (int s = 0; s < t; s++) acc = fmaf(-A[16 * w + t][16 * w + s], x[s], acc);
+      for (int s = 0; s < t; s += 4) {
+        const f4 a = *(const f4*)&X[b + t][b + s];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          if (s + i < t) acc = fmaf(-a[i], x[s + i], acc);
+      }
       x[t] = acc;
     }
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int t = 0; t < 16; t++) X[16 * w + t][16 * w + c] = x[t];
-  } else if (lane < 32 && !(w & 1)) {  // the block right of an even diagonal block
+    for (int t = 0; t < 16; t++) {
+      X[b + t][b + c] = x[t];
+      m = fmaxf(m, fabsf(x[t]));
+    }
+    m *= fabsf(be[b + c]);
+  } else if (lane < 48) {
 #pragma unroll
-    for (int t = 0; t < 16; t++) X[16 * w + t][16 * w + 16 + c] = 0.0f;
+    for (int t = 0; t < 16; t++) X[r0 + t][r0 + 16 + c] = 0.0f;
   }
-  __syncthreads();
-  auto dot = [&](const float (*M)[kPitch], int r, int m, const float (*B)[kPitch], int cb, f4 y) {
+  __builtin_amdgcn_wave_barrier();
+  f4 y = {0, 0, 0, 0}, x = {0, 0, 0, 0};
 #pragma unroll
-    for (int kk = 0; kk < 4; kk++)
-      y = __builtin_amdgcn_mfma_f32_16x16x4f32(M[16 * r + c][16 * m + 4 * kk + g],
-                                               B[16 * m + 4 * kk + g][16 * cb + c], y, 0, 0, 0);
+  for (int k = 0; k < 4; k++)
+    y = __builtin_amdgcn_mfma_f32_16x16x4f32(X[r0 + 16 + c][r0 + 4 * k + g], X[r0 + 4 * k + g][r0 + c], y, 0, 0, 0);
+#pragma unroll
+  for (int k = 0; k < 4; k++)
+    x = __builtin_amdgcn_mfma_f32_16x16x4f32(X[r0 + 16 + c][r0 + 16 + 4 * g + k], y[k], x, 0, 0, 0);
+  __builtin_amdgcn_wave_barrier();
+  float n = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    X[r0 + 16 + 4 * g + i][r0 + c] = -x[i];
+    n = fmaxf(n, fabsf(x[i]));
+  }
+  return fmaxf(m, n * fabsf(be[r0 + c]));
+}
+
+// T's lower left 32 x 32 quarter, -X11 (A10 X00) with 32 x 32 blocks, one 16 x 16 tile a wave, into Z.
+__device__ __forceinline__ float invert_corner(const float (*X)[kPitch], float (*Z)[36], const float* be, int w, int lane) {
+  const int c = lane & 15, g = lane >> 4, cb = w & 1, r = 2 + (w >> 1);
+  auto half = [&](int row) {
+    f4 y = {0, 0, 0, 0};
+    for (int m = cb; m < 2; m++)
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        y = __builtin_amdgcn_mfma_f32_16x16x4f32(X[16 * row + c][16 * m + 4 * k + g], X[16 * m + 4 * k + g][16 * cb + c], y, 0, 0, 0);
     return y;
   };
-  auto dot_acc = [&](int r, int m, f4 y, f4 x) {  // x += X[r][m] y, y an accumulator tile
+  auto add = [&](int m, f4 y, f4 x) {
 #pragma unroll
-    for (int kk = 0; kk < 4; kk++)
-      x = __builtin_amdgcn_mfma_f32_16x16x4f32(X[16 * r + c][16 * m + 4 * g + kk], y[kk], x, 0, 0, 0);
+    for (int k = 0; k < 4; k++)
+      x = __builtin_amdgcn_mfma_f32_16x16x4f32(X[16 * r + c][16 * m + 4 * g + k], y[k], x, 0, 0, 0);
     return x;
   };
-  const f4 zero = {0, 0, 0, 0};
-  if (w < 2) {
-    const int r = 2 * w + 1;
-    const f4 y = dot(A, r, r - 1, X, r - 1, zero);
-    const f4 x = dot_acc(r, r, y, zero);
+  f4 x = add(2, half(2), f4{0, 0, 0, 0});
+  if (r == 3) x = add(3, half(3), x);
+  float n = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; i++) X[16 * r + 4 * g + i][16 * (r - 1) + c] = -x[i];
+  for (int i = 0; i < 4; i++) {
+    Z[16 * (r - 2) + 4 * g + i][16 * cb + c] = -x[i];
+    n = fmaxf(n, fabsf(x[i]));
   }
-  __syncthreads();
-  {
-    const int cb = w & 1, r = 2 + (w >> 1);
-    auto half = [&](int row) {
-      f4 y = zero;
-      for (int m = cb; m < 2; m++) y = dot(A, row, m, X, cb, y);
-      return y;
-    };
-    f4 x = dot_acc(r, 2, half(2), zero);
-    if (r == 3) x = dot_acc(3, 3, half(3), x);
-#pragma unroll
-    for (int i = 0; i < 4; i++) X[16 * r + 4 * g + i][16 * cb + c] = -x[i];
-  }
-  __syncthreads();
+  return n * fabsf(be[16 * cb + c]);
 }
 
 // Y: the workspace's layout (LayF, or LayB: with the gradient's extra pieces).
 template <int D, int DT, class Y>
-__global__ __launch_bounds__(256) void k_chunk_prep(SeqArgs A) {
+__global__ __launch_bounds__(256, DT == kF32 ? 2 : 3) void k_chunk_prep(SeqArgs A) {
   constexpr int KS = D / 32, NPI = Y::NPI, NPO = Y::NPO;
-  __shared__ PrepSmem<D, DT> sm;
+  __shared__ PrepSmem<D, DT, Y::grad> sm;
   const long long j = blockIdx.x;
   const int hq = blockIdx.y;
   ChunkAt at;
   if (!chunk_at(A, j, at)) return;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c16 = lane & 15, g = lane >> 4;
-  load_rows<D, DT>(A.k, A.ks, (long long)hq * D, at.t0, at.len, sm.in.K, sm.isk);
-  load_rows<D, DT>(A.q, A.qs, (long long)hq * D, at.t0, at.len, sm.in.Q, sm.isq);
-  __syncthreads();
-  // fragments of K, Q (rows = tokens) and K^T (rows = key dimensions)
+  const int c16 = lane & 15, g = lane >> 4, wb = w >> 1, wp = w & 1;
+  const int own = 32 * wb + perm_row(c16, wp);  // the lane's token
   char* const key = A.ws + (j * A.Hq + hq) * Y::key;
+  float* const KK = (float*)(key + (Y::grad ? Y::offKK : 0));
+  float* const QK = (float*)(key + (Y::grad ? Y::offQK : 0));
+  // K and Q: fragments of row tile w, K (gradient: and Q) into LDS.  Tokens behind the end repeat the
+  // last one: their W is zero.
+  h8 kf[KS][NPI], qf[KS][NPI];
+  float ik, iq;
+  {
+    const long long t = at.t0 + (long long)min(own, at.len - 1);
+    ik = load_rows<D, DT>(A.k, t * A.ks + (long long)hq * D, g, kf);
+    iq = load_rows<D, DT>(A.q, t * A.qs + (long long)hq * D, g, qf);
+    if (g == 0) {
+      sm.isk[own] = ik;
+      sm.isq[own] = iq;
+    }
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+      for (int p = 0; p < NPI; p++) {
+        const int o = (p * Y::NF + w * KS + ks) * kFrag + lane * 16;
+        *(h8*)(key + Y::offK + o) = kf[ks][p];
+        *(h8*)&sm.K[p][own][32 * ks + 8 * g] = kf[ks][p];
+        if constexpr (Y::grad) *(h8*)&sm.Q[p][own][32 * ks + 8 * g] = qf[ks][p];
+        else *(h8*)(key + Y::offQ + o) = qf[ks][p];
+      }
+  }
+  __syncthreads();
+  // K K^T, columns = this wave's tokens, rows up to their block; K Q^T likewise (gradient: Q K^T, rows from
+  // their block on).  Block nb of both runs over tiles 2 nb, 2 nb + 1.
+  float kk[2][8], qk[2][8];
+#pragma unroll
+  for (int nb = 0; nb < 2; nb++) {
+    const bool kk_on = nb <= wb, qk_on = Y::grad ? nb >= wb : nb <= wb;
+    f4 a[2], b[2];
+#pragma unroll
+    for (int p = 0; p < 2; p++) {
+      a[p] = b[p] = f4{0, 0, 0, 0};
+      const int row = 32 * nb + perm_row(c16, p);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) {
+        h8 fk[NPI], fq[NPI];
+#pragma unroll
+        for (int n = 0; n < NPI; n++) {
+          if (kk_on) fk[n] = *(const h8*)&sm.K[n][row][32 * ks + 8 * g];
+          if (Y::grad && qk_on) fq[n] = *(const h8*)&sm.Q[Y::grad ? n : 0][Y::grad ? row : 0][32 * ks + 8 * g];
+        }
+        if (kk_on) {
+          a[p] = mfma(fk[0], kf[ks][0], a[p]);
+          if constexpr (NPI == 2) a[p] = mfma(fk[0], kf[ks][1], mfma(fk[1], kf[ks][0], a[p]));
+        }
+        if (qk_on) {
+          if constexpr (Y::grad) {
+            b[p] = mfma(fq[0], kf[ks][0], b[p]);
+            if constexpr (NPI == 2) b[p] = mfma(fq[0], kf[ks][1], mfma(fq[1], kf[ks][0], b[p]));
+          } else {
+            b[p] = mfma(fk[0], qf[ks][0], b[p]);
+            if constexpr (NPI == 2) b[p] = mfma(fk[0], qf[ks][1], mfma(fk[1], qf[ks][0], b[p]));
+          }
+        }
+      }
+    }
+    const float* const isr = Y::grad ? sm.isq : sm.isk;
+    const float io = Y::grad ? ik : iq;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      const int r = 32 * nb + 8 * g + e;
+      kk[nb][e] = kk_on ? a[e >> 2][e & 3] * (sm.isk[r] * ik) : 0.0f;
+      qk[nb][e] = qk_on ? b[e >> 2][e & 3] * (isr[r] * io) : 0.0f;
+    }
+    if constexpr (Y::grad) {
+      if (kk_on) store8<kF32>(KK, own * 64 + 32 * nb + 8 * g, kk[nb]);  // [t][s], t own
+      if (qk_on) store8<kF32>(QK, own * 64 + 32 * nb + 8 * g, qk[nb]);  // [s][t], s own
+    }
+  }
+  // K^T (and Q^T): rows = key dimensions
+#pragma unroll
   for (int f = w; f < Y::NF; f += 4) {
-    const int rt = f / KS, ks = f - rt * KS;
-    const int row = 32 * (rt >> 1) + perm_row(c16, rt & 1), col = 32 * ks + 8 * g;
     const int kr = 32 * (f >> 2) + perm_row(c16, (f >> 1) & 1), kc = 32 * (f & 1) + 8 * g;
 #pragma unroll
     for (int p = 0; p < NPI; p++) {
       const int o = (p * Y::NF + f) * kFrag + lane * 16;
-      *(h8*)(key + Y::offK + o) = *(const h8*)&sm.in.K[p][row][col];
       h8 t;
 #pragma unroll
-      for (int i = 0; i < 8; i++) t[i] = sm.in.K[p][kc + i][kr];
+      for (int i = 0; i < 8; i++) t[i] = sm.K[p][kc + i][kr];
       *(h8*)(key + Y::offKT + o) = t;
       if constexpr (Y::grad) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) t[i] = sm.in.Q[p][kc + i][kr];
+        for (int i = 0; i < 8; i++) t[i] = sm.Q[p][kc + i][kr];
         *(h8*)(key + Y::offQ + o) = t;
-      } else {
-        *(h8*)(key + Y::offQ + o) = *(const h8*)&sm.in.Q[p][row][col];
       }
     }
   }
-  // K K^T and Q K^T, row tile w (plain row order), lower tiles only
-  f4 kk[4], qk[4];
-#pragma unroll
-  for (int c = 0; c < 4; c++) {
-    kk[c] = qk[c] = f4{0, 0, 0, 0};
-    if (c > w) continue;
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++) {
-      h8 a[NPI], q[NPI], b[NPI];
-#pragma unroll
-      for (int p = 0; p < NPI; p++) {
-        a[p] = *(const h8*)&sm.in.K[p][16 * w + c16][32 * ks + 8 * g];
-        q[p] = *(const h8*)&sm.in.Q[p][16 * w + c16][32 * ks + 8 * g];
-        b[p] = *(const h8*)&sm.in.K[p][16 * c + c16][32 * ks + 8 * g];
-      }
-      kk[c] = mfma(a[0], b[0], kk[c]);
-      qk[c] = mfma(q[0], b[0], qk[c]);
-      if constexpr (NPI == 2) {
-        kk[c] = mfma(a[0], b[1], mfma(a[1], b[0], kk[c]));
-        qk[c] = mfma(q[0], b[1], mfma(q[1], b[0], qk[c]));
-      }
+  float al_next = 1.0f, be_next = 0.0f;  // gates of the next head, token `lane`
+  auto gates = [&](int hh) {
+    if (lane < at.len) {
+      const long long th = (at.t0 + (long long)lane) * A.H + hq * A.grp + hh;
+      al_next = A.alpha[th];
+      be_next = A.beta[th];
     }
-  }
-  if constexpr (Y::grad) {
-#pragma unroll
-    for (int c = 0; c < 4; c++) {
-      if (c > w) continue;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int t = 16 * w + 4 * g + i, s = 16 * c + c16;
-        ((float*)(key + Y::offKK))[t * 64 + s] = kk[c][i] * (sm.isk[t] * sm.isk[s]);
-        ((float*)(key + Y::offQK))[t * 64 + s] = qk[c][i] * (sm.isq[t] * sm.isk[s]);
-      }
-    }
-  }
+  };
+  gates(0);
   for (int hh = 0; hh < A.grp; hh++) {
     const int h = hq * A.grp + hh;
     char* const head = A.ws + key_bytes<Y>(A) + (j * A.H + h) * Y::head;
     float* const tab = (float*)(head + Y::offTab);
-    __syncthreads();  // the operand planes (first head) or the last head's matrices are free
-    if (tid < 64) {
-      const long long th = (at.t0 + (long long)(tid < at.len ? tid : 0)) * A.H + h;
-      sm.al[tid] = tid < at.len ? A.alpha[th] : 1.0f;
-      sm.be[tid] = tid < at.len ? A.beta[th] : 0.0f;
+    const float al = al_next, be = be_next;
+    if (hh + 1 < A.grp) gates(hh + 1);
+    // running products, token = lane
+    float(*const gt)[64] = sm.gate[w];
+    float p8 = al, s8 = 1.0f;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const float x = __shfl_up(p8, o);
+      if ((lane & 7) >= o) p8 *= x;
     }
-    __syncthreads();
-    // L[t][s], rows 16 w .. 16 w + 15, column s = lane: a running product down the column
     {
-      int ln = lane;  // opaque: the 64 comparisons are not kept in scalar registers across heads
-      asm("" : "+v"(ln));
-      float l = 1.0f;
-      for (int t = 0; t < 16 * w; t++) l = t > ln ? l * sm.al[t] : 1.0f;
+      float x = __shfl_down(al, 1);
+      s8 = (lane & 7) < 7 ? x : 1.0f;
 #pragma unroll
-      for (int i = 0; i < 16; i++) {
-        const int t = 16 * w + i;
-        l = t > ln ? l * sm.al[t] : 1.0f;
-        sm.m.L[t][ln] = t >= ln ? l : 0.0f;
+      for (int o = 1; o < 8; o <<= 1) {
+        x = __shfl_down(s8, o);
+        if ((lane & 7) + o < 8) s8 *= x;
       }
     }
-    __syncthreads();
+    float B[8];  // whole groups of 8
 #pragma unroll
-    for (int c = 0; c < 4; c++) {
-      const int s = 16 * c + c16;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int t = 16 * w + 4 * g + i;
-        float a = 0.0f, p = 0.0f;
-        if (s <= t) {
-          const float l = sm.m.L[t][s] * sm.isk[s];
-          p = qk[c][i] * sm.isq[t] * l;
-          if (s < t) a = sm.be[t] * (kk[c][i] * sm.isk[t] * l);
-        }
-        sm.m.A[t][s] = a;
-        sm.m.P[t][s] = p;
-      }
-    }
-    if (tid < 64) {
-      const float G = sm.al[0] * sm.m.L[tid][0];
-      tab[kTabU + tid] = sm.be[tid] * G * sm.isk[tid];
-      tab[kTabB + tid] = sm.be[tid];
-      tab[kTabQ + tid] = G * sm.isq[tid];
-      tab[kTabD + tid] = sm.m.L[63][tid] * sm.isk[tid];
-      tab[kTabG + tid] = G;
-      if constexpr (Y::grad) {
-        tab[kTabL + tid] = sm.m.L[63][tid];
-        tab[kTabIK + tid] = sm.isk[tid];
-        tab[kTabIQ + tid] = sm.isq[tid];
-      }
-    }
-    __syncthreads();
-    float(*const X)[kPitch] = sm.m.L;
-    invert(sm.m.A, X, w, lane);
-    // row scales of T and P (gradient: of T, and of the columns of T and P)
+    for (int n = 0; n < 8; n++) B[n] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p8), 8 * n + 7));
+    float p32 = p8, s32 = s8;
     {
-      const int row = tid >> 2, part = tid & 3;
-      float mt = 0.0f, mp = 0.0f, mu = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        if (row >= 32 || part < 2) {
-          const f4 x = *(const f4*)&X[row][16 * part + i], p = *(const f4*)&sm.m.P[row][16 * part + i];
-#pragma unroll
-          for (int e = 0; e < 4; e++) mt = fmaxf(mt, fabsf(x[e])), mp = fmaxf(mp, fabsf(p[e]));
-        }
-      }
+      const int n = (lane >> 3) & 3;
+      const bool up = lane >= 32;
+      const float b0 = up ? B[4] : B[0], b1 = up ? B[5] : B[1], b2 = up ? B[6] : B[2], b3 = up ? B[7] : B[3];
+      if (n > 0) p32 *= b0;
+      if (n > 1) p32 *= b1;
+      if (n > 2) p32 *= b2;
+      if (n < 3) s32 *= b3;
+      if (n < 2) s32 *= b2;
+      if (n < 1) s32 *= b1;
+    }
+    gt[0][lane] = al;
+    gt[1][lane] = p8;
+    gt[2][lane] = s8;
+    gt[3][lane] = p32;
+    gt[4][lane] = s32;
+    __builtin_amdgcn_wave_barrier();
+    const float BL = B[0] * B[1] * B[2] * B[3], BU = B[4] * B[5] * B[6] * B[7];
+    if (w == 0) {
+      const float G = lane < 32 ? p32 : BL * p32, L63 = lane < 32 ? s32 * BU : s32;
+      const float ik0 = sm.isk[lane], iq0 = sm.isq[lane];
+      tab[kTabU + lane] = (Y::grad ? be * G : G) * ik0;
+      tab[kTabB + lane] = be;
+      tab[kTabQ + lane] = G * iq0;
+      tab[kTabD + lane] = L63 * ik0;
+      tab[kTabG + lane] = G;
       if constexpr (Y::grad) {
-        mp = 0.0f;
-        if (row < 32 || part >= 2)
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            mu = fmaxf(mu, fabsf(X[16 * part + i][row]));
-            mp = fmaxf(mp, fabsf(sm.m.P[16 * part + i][row]));
-          }
-        mu = fmaxf(mu, __shfl_xor(mu, 1));
-        mu = fmaxf(mu, __shfl_xor(mu, 2));
+        tab[kTabL + lane] = L63;
+        tab[kTabIK + lane] = ik0;
+        tab[kTabIQ + lane] = iq0;
       }
-      mt = fmaxf(mt, __shfl_xor(mt, 1));
-      mt = fmaxf(mt, __shfl_xor(mt, 2));
-      mp = fmaxf(mp, __shfl_xor(mp, 1));
-      mp = fmaxf(mp, __shfl_xor(mp, 2));
-      if (part == 0) {
-        float it, ip;
-        sm.sT[row] = scale_of(mt, it);
-        sm.sP[row] = scale_of(mp, ip);
-        tab[kTabT + row] = it;
-        tab[kTabP + row] = ip;
-        if constexpr (Y::grad) {
-          sm.sU[row] = scale_of(mu, it);
-          tab[kTabTt + row] = it;
+    }
+    const float be_own = __shfl(be, own);
+    const int og = c16 >> 2, oi = 4 * wp + (c16 & 3);  // own token: group of the block, place in the group
+    // L between `own` and the 8 tokens 8 g + e of its own block: down: own is the later one
+    float Lo[8];
+    auto in_block = [&](bool down) {
+      const float *a = &gt[0][32 * wb + 8 * g], *pre = &gt[1][32 * wb + 8 * g], *suf = &gt[2][32 * wb + 8 * g];
+      const int lo = down ? g : og, hi = down ? og : g;  // earlier and later group
+      const float b1 = wb ? B[5] : B[1], b2 = wb ? B[6] : B[2];
+      float mid = gt[down ? 1 : 2][own];
+      if (lo == 0 && hi > 1) mid *= b1;
+      if (lo <= 1 && hi == 3) mid *= b2;
+      float c = 1.0f;
+      if (down) {
+#pragma unroll
+        for (int e = 7; e >= 0; e--) {
+          Lo[e] = g < og ? mid * suf[e] : g == og && e <= oi ? c : 0.0f;
+          if (e <= oi) c *= a[e];
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          if (e > oi) c *= a[e];
+          Lo[e] = g > og ? mid * pre[e] : g == og && e >= oi ? c : 0.0f;
+        }
+      }
+    };
+    in_block(true);
+    float pv[2][8];
+    __syncthreads();  // the last head's T has been read
+    if (w == 0) sm.be[lane] = be;
+#pragma unroll
+    for (int nb = 0; nb < 2; nb++) {
+      if (nb > wb) continue;
+      float av[8];
+      const float pre = gt[3][own];
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const float l = nb == wb ? Lo[e] : pre * gt[4][8 * g + e];
+        const bool strict = nb < wb || g < og || e < oi;
+        av[e] = strict ? be_own * (kk[nb][e] * l) : 0.0f;
+        if constexpr (!Y::grad) pv[nb][e] = qk[nb][e] * l;
+      }
+      store8<kF32>(&sm.X[own][0], 32 * nb + 8 * g, av);
+    }
+    if constexpr (Y::grad) {
+      in_block(false);
+#pragma unroll
+      for (int nb = 0; nb < 2; nb++) {
+        if (nb < wb) continue;
+        const float suf = gt[4][own];
+#pragma unroll
+        for (int e = 0; e < 8; e++) pv[nb][e] = qk[nb][e] * (nb == wb ? Lo[e] : suf * gt[3][32 + 8 * g + e]);
       }
     }
     __syncthreads();
-    // 6 fragments each of T and P: three a wave; gradient: T, T^T and P^T, 18 over the waves
+    float m = 0.0f;
+    if (wp == 0) m = invert_block(sm.X, sm.be, 32 * wb, lane);
+    // P's (gradient: P^T's) fragments meanwhile
+    {
+      float mp = 0.0f;
+#pragma unroll
+      for (int nb = 0; nb < 2; nb++)
+        if (Y::grad ? nb >= wb : nb <= wb)
+#pragma unroll
+          for (int e = 0; e < 8; e++) mp = fmaxf(mp, fabsf(pv[nb][e]));
+      float ip;
+      const float sp = scale_of(col_max(mp), ip);
+      if (g == 0) tab[kTabP + own] = ip;
+#pragma unroll
+      for (int nb = 0; nb < 2; nb++)
+        if (Y::grad ? nb >= wb : nb <= wb) {
+          h8 hi, lo;
+          split8<2>(pv[nb], sp, hi, lo);
+          char* const dst = head + Y::offP + (Y::grad ? up_frag(w, nb) : tri_frag(w, nb)) * kFrag + lane * 16;
+          *(h8*)dst = hi;
+          if constexpr (NPO == 2) *(h8*)(dst + kTri * kFrag) = lo;
+        }
+    }
+    __syncthreads();
+    m = fmaxf(m, invert_corner(sm.X, sm.Z, sm.be, w, lane));
+    m = fmaxf(m, __shfl_xor(m, 1));
+    m = fmaxf(m, __shfl_xor(m, 2));
+    m = fmaxf(m, __shfl_xor(m, 4));
+    m = fmaxf(m, __shfl_xor(m, 8));
+    m = col_max(m);
+    if (lane == 0) sm.most[w] = m;
+    __syncthreads();
+    // T's fragments of row tile w
+    auto T_row = [&](int ks, float* x) {
+      const float* src = wb && !ks ? &sm.Z[own - 32][8 * g] : &sm.X[own][32 * ks + 8 * g];
+      const f4 x0 = *(const f4*)src, x1 = *(const f4*)(src + 4);
+#pragma unroll
+      for (int e = 0; e < 4; e++) x[e] = x0[e], x[4 + e] = x1[e];
+    };
     if constexpr (!Y::grad) {
+      float iT;
+      const float sT = scale_of(fmaxf(fmaxf(sm.most[0], sm.most[1]), fmaxf(sm.most[2], sm.most[3])), iT);
+      if (tid == 0) tab[kTabT] = iT;
 #pragma unroll
-      for (int n = 0; n < 3; n++) {
-        const int f = 3 * (w & 1) + n;
-        const int rt = f < 2 ? f : 2 + ((f - 2) >> 1), ks = f < 2 ? 0 : (f - 2) & 1;
-        const int row = 32 * (rt >> 1) + perm_row(c16, rt & 1), col = 32 * ks + 8 * g;
-        const float* src = w < 2 ? &X[row][col] : &sm.m.P[row][col];
-        const f4 x0 = *(const f4*)src, x1 = *(const f4*)(src + 4);
-        const float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-        h8 hi, lo;
-        split8<2>(x, w < 2 ? sm.sT[row] : sm.sP[row], hi, lo);
-        char* const dst = head + (w < 2 ? Y::offT : Y::offP) + f * kFrag + lane * 16;
-        *(h8*)dst = hi;
-        if (w < 2 || NPO == 2) *(h8*)(dst + kTri * kFrag) = lo;
-      }
-    } else {
-      for (int n = w; n < 18; n += 4) {
-        const int m = n / 6, f = n - 6 * m;  // 0 T, 1 T^T, 2 P^T
-        const int rt = m ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : 2 + ((f - 2) >> 1));
-        const int ks = m ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : (f - 2) & 1);
-        const int row = 32 * (rt >> 1) + perm_row(c16, rt & 1), col = 32 * ks + 8 * g;
+      for (int ks = 0; ks < 2; ks++) {
+        if (ks > wb) continue;
         float x[8];
+        T_row(ks, x);
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = m == 0 ? X[row][col + i] : m == 1 ? X[col + i][row] : sm.m.P[col + i][row];
+        for (int e = 0; e < 8; e++) x[e] *= sm.be[32 * ks + 8 * g + e];
         h8 hi, lo;
-        split8<2>(x, m == 0 ? sm.sT[row] : m == 1 ? sm.sU[row] : sm.sP[row], hi, lo);
-        char* const dst = head + (2 * m * kTri + f) * kFrag + lane * 16;
+        split8<2>(x, sT, hi, lo);
+        char* const dst = head + Y::offT + tri_frag(w, ks) * kFrag + lane * 16;
         *(h8*)dst = hi;
         *(h8*)(dst + kTri * kFrag) = lo;
+      }
+    } else {
+      // T and T^T, rows scaled
+      float x[2][8], y[2][8], mt = 0.0f, mu = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < 2; ks++) {
+        if (ks <= wb) {
+          T_row(ks, x[ks]);
+#pragma unroll
+          for (int e = 0; e < 8; e++) mt = fmaxf(mt, fabsf(x[ks][e]));
+        }
+        if (ks >= wb) {
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            y[ks][e] = !wb && ks ? sm.Z[8 * g + e][own] : sm.X[32 * ks + 8 * g + e][own];
+            mu = fmaxf(mu, fabsf(y[ks][e]));
+          }
+        }
+      }
+      float it, iu;
+      const float st = scale_of(col_max(mt), it), su = scale_of(col_max(mu), iu);
+      if (g == 0) {
+        tab[kTabT + own] = it;
+        tab[kTabTt + own] = iu;
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ks++) {
+        h8 hi, lo;
+        if (ks <= wb) {
+          split8<2>(x[ks], st, hi, lo);
+          char* const dst = head + Y::offT + tri_frag(w, ks) * kFrag + lane * 16;
+          *(h8*)dst = hi;
+          *(h8*)(dst + kTri * kFrag) = lo;
+        }
+        if (ks >= wb) {
+          split8<2>(y[ks], su, hi, lo);
+          char* const dst = head + Y::offTt + up_frag(w, ks) * kFrag + lane * 16;
+          *(h8*)dst = hi;
+          *(h8*)(dst + kTri * kFrag) = lo;
+        }
       }
     }
   }
@@ -320,11 +463,13 @@ __global__ __launch_bounds__(256) void k_chunk_prep(SeqArgs A) {
 // the pass over the chunks
 // ---------------------------------------------------------------------------------------------
 
-// A wave owns 16 CT columns of one (sequence, head) state for the whole sequence: lane l holds columns
-// CT (l & 15) .. + CT - 1 (column tile ct = column CT (l & 15) + ct), rows in accumulator order.  All
-// waves of a workgroup read the same fragments, staged in LDS once a chunk.
-// For the gradient (LayB) nothing is read out: the states before every chunk and W are kept.
-template <int D, int DT, int CT, int NW, class Y>
+// A wave owns 16 columns of one (sequence, head) state for the whole sequence (lane l: column l & 15, rows in
+// accumulator order) and never needs another wave's: all waves of a workgroup read the same fragments,
+// staged in LDS one chunk ahead.  The state is held in units of a power of two per column (S = unit * St,
+// St within binary16's range, checked every chunk), so that it turns into an operand without a product and
+// the update accumulates on it directly.  For the gradient (LayB) nothing is read out: the states before
+// every chunk and W are kept.
+template <int D, int DT, int NW, class Y>
 __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS, float* keepW) {
   constexpr int KS = D / 32, NPI = Y::NPI, NPO = Y::NPO, NB = D / 32;
   // staged: K, K^T (and Q), then T (and P), then the tables
@@ -342,18 +487,27 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   const int slot = seq_slot(A, s, valid, h == 0 && blockIdx.y == 0 && tid == 0);
   if (slot < 0) return;
   if (t0 == t1 && (Y::grad || !A.S_out || A.S_out == A.S_in)) return;
-  const int col = 16 * CT * ((int)blockIdx.y * NW + w) + CT * c16;
+  const int col = 16 * ((int)blockIdx.y * NW + w) + c16;
   const long long so = ((long long)slot * A.H + h) * D * D + col;
-  f4 S[CT][2 * NB];
+  auto state_row = [&](int rt, int i) { return 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i; };
+  f4 St[2 * NB];
 #pragma unroll
   for (int rt = 0; rt < 2 * NB; rt++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      float x[CT] = {};
-      if (A.S_in) loadn<kF32, CT>(A.S_in, so + (long long)(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i) * D, x);
+    for (int i = 0; i < 4; i++) St[rt][i] = A.S_in ? A.S_in[so + (long long)state_row(rt, i) * D] : 0.0f;
+  float unit = 0x1p-10f;  // an empty state takes its unit from the first W
+  auto rescale = [&](float m) {  // largest magnitude into [2^11, 2^12)
+    float inv;
+    const float f = m > 0.0f ? scale_of(m, inv) : (inv = 1.0f);
+    unit *= inv;
 #pragma unroll
-      for (int ct = 0; ct < CT; ct++) S[ct][rt][i] = x[ct];
-    }
+    for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= f;
+  };
+  {
+    const float m = tiles_max<2 * NB>(St);
+    if (m > 0.0f) unit = 1.0f;
+    rescale(m);
+  }
   const long long j0 = first_slot(A, s);
   const char* const heads = A.ws + key_bytes<Y>(A);
   const int hq = h / A.grp;
@@ -372,47 +526,33 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
       copy_block<NW>(head, at + offT, Y::head, w, lane16);
     }
   };
-  // V of chunk c in accumulator order
-  Raw<DT, CT> v[4][4];
+  const Rows<DT> vrows(A.vs, col, g), orows(A.os, col, g);
+  unsigned v[4][4];  // V of the next chunk, as it lies in memory
   auto fetch_v = [&](int c) {
     const int tc = t0 + c * kChunk;
-    rows_acc<DT, CT>((const char*)A.v + (tc * A.vs + (long long)h * D) * (DT == kF32 ? 4 : 2), (int)A.vs, t1 - tc, col, g, v);
+    vrows.load(vrows.at(A.v, tc, A.vs, h * D, D, t1 - tc < kChunk ? t1 - tc : kChunk), v);
   };
   if (nc) {
     fetch(0);
     fetch_v(0);
   }
+  const f4 zero = {0, 0, 0, 0};
   for (int c = 0; c < nc; c++) {
     const char* const lds = buf + (NBUF == 2 ? (c & 1) * part : 0);
     const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
     wait_copies();
     __syncthreads();  // chunk c is there, and every wave is done with chunk c - 1
-    f4 R[CT][4];
+    f4 R[4];
 #pragma unroll
     for (int rt = 0; rt < 4; rt++)
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++)
-          R[ct][rt][i] = 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i < len ? raw_value<DT, CT>(v[rt][i], ct) : 0.0f;
+      for (int i = 0; i < 4; i++) R[rt][i] = vrows.value(v[rt][i]);
     if (c + 1 < nc) {
       if (NBUF == 2) fetch(c + 1);
       fetch_v(c + 1);
     }
-    if constexpr (Y::grad) {
-      float* const dst = keepS + ((j0 + c) * A.H + h) * D * D + col;
-#pragma unroll
-      for (int rt = 0; rt < 2 * NB; rt++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          float x[CT];
-#pragma unroll
-          for (int ct = 0; ct < CT; ct++) x[ct] = S[ct][rt][i];
-          storen<kF32, CT>(dst, (long long)(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i) * D, x);
-        }
-    }
     const float* const tab = (const float*)(lds + offTab);
-    auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane * 16); };
+    auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane16); };
     auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
     // Every product's fragments are read while its other operand is formed.
     h8 f[Y::NF], fl[NPI == 2 ? Y::NF : 1];
@@ -423,28 +563,37 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
         if constexpr (NPI == 2) fl[n] = frag(off, Y::NF, 1, n);
       }
     };
-    h8 Sh[CT][NB], Sl[CT][NB], xh[CT][2], xl[CT][2];
-    float iS[CT], ix[CT];
+    h8 Sh[NB], Sl[NB], xh[2], xl[2];
+    f4 z[2 * NB > 4 ? 2 * NB : 4];
     read(Y::offK);
     ahead();
+    {
+      const float m = tiles_max<2 * NB>(St);
+      if (__any(m > 0x1p14f || (m < 1.0f && m > 0.0f))) rescale(m);
+    }
+    if constexpr (Y::grad) {
+      float* const dst = keepS + ((j0 + c) * A.H + h) * D * D + col;
 #pragma unroll
-    for (int ct = 0; ct < CT; ct++) iS[ct] = to_operand<NB, 2>(S[ct], Sh[ct], Sl[ct]);
-    // R = beta V - beta G K S0
-    f4 z[CT][2 * NB > 4 ? 2 * NB : 4];
+      for (int rt = 0; rt < 2 * NB; rt++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) dst[(long long)state_row(rt, i) * D] = St[rt][i] * unit;
+    }
+    to_planes<NB, 2, true>(St, 1.0f, Sh, Sl);
     auto times_state = [&](bool low) {
 #pragma unroll
-      for (int rt = 0; rt < 4; rt++) {
+      for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-        for (int ct = 0; ct < CT; ct++) z[ct][rt] = f4{0, 0, 0, 0};
+        for (int rt = 0; rt < 4; rt++) z[rt] = mfma(f[rt * KS + ks], Sh[ks], ks ? z[rt] : zero);
+      if (low)
 #pragma unroll
         for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-          for (int ct = 0; ct < CT; ct++) {
-            z[ct][rt] = mfma(f[rt * KS + ks], Sh[ct][ks], z[ct][rt]);
-            if (low) z[ct][rt] = mfma(f[rt * KS + ks], Sl[ct][ks], z[ct][rt]);
-            if constexpr (NPI == 2) z[ct][rt] = mfma(fl[rt * KS + ks], Sh[ct][ks], z[ct][rt]);
-          }
-      }
+          for (int rt = 0; rt < 4; rt++) z[rt] = mfma(f[rt * KS + ks], Sl[ks], z[rt]);
+      if constexpr (NPI == 2)
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+          for (int rt = 0; rt < 4; rt++) z[rt] = mfma(fl[rt * KS + ks], Sh[ks], z[rt]);
     };
     times_state(true);
     ahead();
@@ -455,55 +604,42 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
       ft[1][n] = frag(offT, kTri, 1, n);
     }
     ahead();
+    // R = V - G K S0 (gradient: times beta)
+    float ix, w1;
 #pragma unroll
-    for (int ct = 0; ct < CT; ct++) {
+    for (int rt = 0; rt < 4; rt++) {
+      const f4 cu = rows(kTabU, rt), be = Y::grad ? rows(kTabB, rt) : zero;
 #pragma unroll
-      for (int rt = 0; rt < 4; rt++) {
-        const f4 cu = rows(kTabU, rt), be = rows(kTabB, rt);
-#pragma unroll
-        for (int i = 0; i < 4; i++) R[ct][rt][i] = fmaf(-cu[i] * iS[ct], z[ct][rt][i], be[i] * R[ct][rt][i]);
-      }
-      ix[ct] = to_operand<2, 2>(R[ct], xh[ct], xl[ct]);
+      for (int i = 0; i < 4; i++) R[rt][i] = fmaf(-cu[i] * unit, z[rt][i], Y::grad ? be[i] * R[rt][i] : R[rt][i]);
     }
-    // W = T R (in R's place)
+    ix = to_operand<2, 2>(R, xh, xl);
+    // W = w1 z, z = T R (gradient: T's rows have scales of their own)
+    w1 = (Y::grad ? 1.0f : tab[kTabT]) * ix;
+    auto tri = [&](auto&& a, int p, const h8* b, bool first) {
 #pragma unroll
-    for (int rt = 0; rt < 4; rt++)
+      for (int ks = 0; ks < 2; ks++)
 #pragma unroll
-      for (int ct = 0; ct < CT; ct++) {
-        z[ct][rt] = f4{0, 0, 0, 0};
-#pragma unroll
-        for (int ks = 0; ks <= rt >> 1; ks++) {
-          const int n = tri_frag(rt, ks);
-          z[ct][rt] = mfma(ft[1][n], xh[ct][ks], mfma(ft[0][n], xl[ct][ks], mfma(ft[0][n], xh[ct][ks], z[ct][rt])));
-        }
-      }
+        for (int rt = 0; rt < 4; rt++)
+          if (ks <= rt >> 1) z[rt] = mfma(a[p][tri_frag(rt, ks)], b[ks], first && !ks ? zero : z[rt]);
+    };
+    tri(ft, 0, xh, true);
+    tri(ft, 0, xl, false);
+    tri(ft, 1, xh, false);
     ahead();
     if constexpr (!Y::grad) read(Y::offQ);
     else read(Y::offKT);
     ahead();
 #pragma unroll
-    for (int rt = 0; rt < 4; rt++) {
-      const f4 it = rows(kTabT, rt);
-#pragma unroll
-      for (int ct = 0; ct < CT; ct++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) R[ct][rt][i] = z[ct][rt][i] * (it[i] * ix[ct]);
-    }
+    for (int rt = 0; rt < 4; rt++) R[rt] = Y::grad ? z[rt] * rows(kTabT, rt) : z[rt];
     if constexpr (Y::grad) {
       float* const dst = keepW + ((j0 + c) * A.H + h) * 64 * D + col;
 #pragma unroll
       for (int rt = 0; rt < 4; rt++)
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          float x[CT];
-#pragma unroll
-          for (int ct = 0; ct < CT; ct++) x[ct] = R[ct][rt][i];
-          storen<kF32, CT>(dst, (long long)(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i) * D, x);
-        }
+        for (int i = 0; i < 4; i++) dst[(long long)state_row(rt, i) * D] = R[rt][i] * w1;
     } else {
       // O = G Q S0 + P W
-#pragma unroll
-      for (int ct = 0; ct < CT; ct++) ix[ct] = to_operand<2, NPO>(R[ct], xh[ct], xl[ct]);
+      const float iw = to_operand<2, NPO>(R, xh, xl) * w1;
       times_state(NPO == 2);
       ahead();
       h8 fp[NPO][kTri];
@@ -512,51 +648,56 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
 #pragma unroll
         for (int n = 0; n < kTri; n++) fp[p][n] = frag(offP, kTri, p, n);
       ahead();
-      float o[4][4][CT];
+      f4 y[4];
 #pragma unroll
-      for (int rt = 0; rt < 4; rt++) {
-        f4 y[CT] = {};
-#pragma unroll
-        for (int ks = 0; ks <= rt >> 1; ks++) {
-          const int n = tri_frag(rt, ks);
-#pragma unroll
-          for (int ct = 0; ct < CT; ct++) {
-            y[ct] = mfma(fp[0][n], xh[ct][ks], y[ct]);
-            if constexpr (NPO == 2) y[ct] = mfma(fp[NPO - 1][n], xh[ct][ks], mfma(fp[0][n], xl[ct][ks], y[ct]));
-          }
-        }
-        const f4 cq = rows(kTabQ, rt), ip = rows(kTabP, rt);
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-          for (int ct = 0; ct < CT; ct++) o[rt][i][ct] = fmaf(cq[i] * iS[ct], z[ct][rt][i], (ip[i] * ix[ct]) * y[ct][i]);
+      for (int rt = 0; rt < 4; rt++) y[rt] = z[rt];
+      tri(fp, 0, xh, true);
+      if constexpr (NPO == 2) {
+        tri(fp, 0, xl, false);
+        tri(fp, 1, xh, false);
       }
       ahead();
       read(Y::offKT);
       ahead();
-      rows_store<DT, CT>((char*)A.out + (tc * A.os + (long long)h * D) * (DT == kF32 ? 4 : 2), (int)A.os, len, col, g, o);
+      const __amdgpu_buffer_rsrc_t out = orows.at(A.out, tc, A.os, h * D, D, len);
+#pragma unroll
+      for (int rt = 0; rt < 4; rt++) {
+        const f4 cq = rows(kTabQ, rt), ip = rows(kTabP, rt);
+#pragma unroll
+        for (int i = 0; i < 4; i++) orows.store(out, rt, i, fmaf(cq[i] * unit, y[rt][i], (ip[i] * iw) * z[rt][i]));
+      }
     }
-    // S1 = G_C S0 + K^T diag(L[C, .]) W
+    // S1 = G_C S0 + K^T diag(L[C, .]) W, in the state's units
 #pragma unroll
-    for (int ct = 0; ct < CT; ct++) {
+    for (int rt = 0; rt < 4; rt++) R[rt] *= rows(kTabD, rt);
+    {
+      const float m = tiles_max<4>(R) * w1;
+      if (__any(m > unit * 0x1p14f)) {  // W outgrows the units: they become W's
+        float inv, to = unit;
+        if (m > unit * 0x1p14f) {
+          (void)scale_of(m, inv);
+          to = inv;
+        }
+        const float f = unit / to;  // both powers of two
 #pragma unroll
-      for (int rt = 0; rt < 4; rt++) R[ct][rt] *= rows(kTabD, rt);
-      ix[ct] = to_operand<2, 2>(R[ct], xh[ct], xl[ct]);
+        for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= f;
+        unit = to;
+      }
+      to_planes<2, 2>(R, w1 / unit, xh, xl);
     }
     const float G = tab[kTabG + 63];
 #pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++)
+    for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= G;
 #pragma unroll
-      for (int ct = 0; ct < CT; ct++) {
-        f4 y = {0, 0, 0, 0};
+    for (int ks = 0; ks < 2; ks++) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ks++) {
-          y = mfma(f[2 * rt + ks], xl[ct][ks], mfma(f[2 * rt + ks], xh[ct][ks], y));
-          if constexpr (NPI == 2) y = mfma(fl[2 * rt + ks], xh[ct][ks], y);
-        }
+      for (int rt = 0; rt < 2 * NB; rt++) St[rt] = mfma(f[2 * rt + ks], xh[ks], St[rt]);
 #pragma unroll
-        for (int i = 0; i < 4; i++) S[ct][rt][i] = fmaf(G, S[ct][rt][i], ix[ct] * y[i]);
-      }
+      for (int rt = 0; rt < 2 * NB; rt++) St[rt] = mfma(f[2 * rt + ks], xl[ks], St[rt]);
+      if constexpr (NPI == 2)
+#pragma unroll
+        for (int rt = 0; rt < 2 * NB; rt++) St[rt] = mfma(fl[2 * rt + ks], xh[ks], St[rt]);
+    }
     if (NBUF == 1 && c + 1 < nc) {
       __syncthreads();
       fetch(c + 1);
@@ -566,12 +707,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
 #pragma unroll
     for (int rt = 0; rt < 2 * NB; rt++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        float x[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) x[ct] = S[ct][rt][i];
-        storen<kF32, CT>(A.S_out, so + (long long)(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i) * D, x);
-      }
+      for (int i = 0; i < 4; i++) A.S_out[so + (long long)state_row(rt, i) * D] = St[rt][i] * unit;
   }
 }
 

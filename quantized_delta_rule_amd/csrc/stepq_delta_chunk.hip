@@ -19,8 +19,8 @@ hipError_t launch(const SeqArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_chunk_prep<D, DT, LayF<D, DT>>), dim3((unsigned)chunk_slots(a.T, a.N), a.Hq), dim3(256), 0, s, a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  constexpr int CT = 1, NW = D / 16;
-  hipLaunchKernelGGL((k_chunk_state<D, DT, CT, NW, LayF<D, DT>>), dim3((unsigned)((long long)a.N * a.H), 1), dim3(64 * NW), 0, s,
+  constexpr int NW = D / 16;
+  hipLaunchKernelGGL((k_chunk_state<D, DT, NW, LayF<D, DT>>), dim3((unsigned)((long long)a.N * a.H), 1), dim3(64 * NW), 0, s,
                      a, nullptr, nullptr);
   return hipGetLastError();
 }

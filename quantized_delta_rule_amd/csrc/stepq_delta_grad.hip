@@ -441,7 +441,7 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
           if (s <= t) {
             const float l = sm.m.L[t][s], p = dp[n][i] * (sm.isO[t] * sm.isW[s]);
             nv = p * l;
-            x = p * QK[t * 64 + s];
+            x = p * QK[s * 64 + t];
             if (s < t) {
               const float y = dx[n][i] * (sm.isY[t] * sm.isW[s]), kk = KK[t * 64 + s], b = sm.be[t] * y;
               zv = -b * l;
@@ -614,7 +614,7 @@ hipError_t launch(GradArgs b, hipStream_t s) {
   a.status = nullptr;  // reported once, by the reverse pass
   if (a.T > 0) {
     hipLaunchKernelGGL((k_chunk_prep<D, DT, LayB<D, DT>>), slots, dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_chunk_state<D, DT, 1, D / 16, LayB<D, DT>>), dim3(tiles.x, 1), dim3(4 * D), 0, s, a, keep.S, keep.W);
+    hipLaunchKernelGGL((k_chunk_state<D, DT, D / 16, LayB<D, DT>>), dim3(tiles.x, 1), dim3(4 * D), 0, s, a, keep.S, keep.W);
   }
   a.status = status;
   hipLaunchKernelGGL((k_chunk_reverse<D, DT, CT, 4>), tiles, dim3(256), 0, s, b, keep);
