@@ -28,16 +28,18 @@ struct Keep {  // per chunk slot and value head, binary32
   float* Y;    // [64][D]
 };
 
-// The reverse pass: like k_chunk_state a wave owns 16 CT columns of one state's gradient for the whole
-// sequence.
-template <int D, int DT, int CT, int NW>
+// The reverse pass: like k_chunk_state a wave owns 16 columns of one state's gradient for the whole sequence
+// and holds it in units of a power of two per column.
+template <int D, int DT, int NW>
 __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep) {
   using L = LayB<D, DT>;
   constexpr int KS = D / 32, NPI = L::NPI, NB = D / 32;
   constexpr int keyN = L::offKK, triN = 4 * kTri * kFrag;  // K, K^T, Q^T; T^T, P^T
   constexpr int offTt = keyN, offP = keyN + 2 * kTri * kFrag, offTab = keyN + triN;
+  constexpr int part = offTab + 2048;
+  constexpr int NBUF = 2 * part <= 160 * 1024 ? 2 : 1;
   const SeqArgs& A = B.f;
-  __shared__ __attribute__((aligned(16))) char lds[offTab + 2048];
+  __shared__ __attribute__((aligned(16))) char buf[NBUF * part];
   const long long tile = blockIdx.x;
   const int s = (int)(tile / A.H), h = (int)(tile - (long long)s * A.H);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -45,161 +47,207 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
   if (seq_slot(A, s, valid, h == 0 && blockIdx.y == 0 && tid == 0) < 0) return;
-  const int col = 16 * CT * ((int)blockIdx.y * NW + w) + CT * c16;
+  const int col = 16 * ((int)blockIdx.y * NW + w) + c16;
   const long long so = ((long long)s * A.H + h) * D * D + col;
   auto state_row = [&](int rt, int i) { return 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i; };
-  f4 G[CT][2 * NB];
+  f4 Gt[2 * NB];
 #pragma unroll
   for (int rt = 0; rt < 2 * NB; rt++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      float x[CT] = {};
-      if (B.dS_out) loadn<kF32, CT>(B.dS_out, so + (long long)state_row(rt, i) * D, x);
+    for (int i = 0; i < 4; i++) Gt[rt][i] = B.dS_out ? B.dS_out[so + (long long)state_row(rt, i) * D] : 0.0f;
+  float unit = 0x1p-10f;
+  auto rescale = [&](float m) {
+    float inv;
+    const float f = m > 0.0f ? scale_of(m, inv) : (inv = 1.0f);
+    unit *= inv;
 #pragma unroll
-      for (int ct = 0; ct < CT; ct++) G[ct][rt][i] = x[ct];
-    }
+    for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] *= f;
+  };
+  {
+    const float m = tiles_max<2 * NB>(Gt);
+    if (m > 0.0f) unit = 1.0f;
+    rescale(m);
+  }
   auto store_G = [&](float* dst) {
 #pragma unroll
     for (int rt = 0; rt < 2 * NB; rt++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        float x[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) x[ct] = G[ct][rt][i];
-        storen<kF32, CT>(dst, (long long)state_row(rt, i) * D, x);
-      }
+      for (int i = 0; i < 4; i++) dst[(long long)state_row(rt, i) * D] = Gt[rt][i] * unit;
   };
   const long long j0 = first_slot(A, s);
   const char* const heads = A.ws + key_bytes<L>(A);
   const int hq = h / A.grp;
-  for (int c = (t1 - t0 + kChunk - 1) / kChunk - 1; c >= 0; c--) {
+  const int nc = (t1 - t0 + kChunk - 1) / kChunk;
+  const unsigned lds0 = lds_offset(buf), lane16 = 16 * lane;
+  auto fetch = [&](int c) {
     const char* const key = A.ws + ((j0 + c) * A.Hq + hq) * L::key;
     const char* const head = heads + ((j0 + c) * A.H + h) * L::head;
-    __syncthreads();
-    for (int i = tid * 16; i < keyN; i += 64 * NW * 16) *(f4*)(lds + i) = *(const f4*)(key + i);
-    for (int i = tid * 16; i < triN; i += 64 * NW * 16) *(f4*)(lds + offTt + i) = *(const f4*)(head + L::offTt + i);
-    for (int i = tid * 16; i < 2048; i += 64 * NW * 16) *(f4*)(lds + offTab + i) = *(const f4*)(head + L::offTab + i);
-    store_G(keep.G + ((j0 + c) * A.H + h) * D * D + col);
+    const unsigned at = lds0 + (NBUF == 2 ? (c & 1) * part : 0);
+    copy_block<NW>(key, at, keyN, w, lane16);
+    copy_block<NW>(head + L::offTt, at + offTt, triN, w, lane16);
+    copy_block<NW>(head + L::offTab, at + offTab, 2048, w, lane16);
+  };
+  const Rows<DT> orows(A.os, col, g), vrows((long long)A.H * D, col, g);
+  unsigned o[4][4];
+  auto fetch_o = [&](int c) {
+    const int tc = t0 + c * kChunk;
+    orows.load(orows.at(B.d_out, tc, A.os, h * D, D, t1 - tc < kChunk ? t1 - tc : kChunk), o);
+  };
+  if (nc) {
+    fetch(nc - 1);
+    fetch_o(nc - 1);
+  }
+  const f4 zero = {0, 0, 0, 0};
+  for (int c = nc - 1; c >= 0; c--) {
+    const char* const lds = buf + (NBUF == 2 ? (c & 1) * part : 0);
     const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
-    f4 dO[CT][4];  // accumulator order, zero behind the end
+    wait_copies();
+    __syncthreads();
+    f4 dO[4];
 #pragma unroll
     for (int rt = 0; rt < 4; rt++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int t = state_row(rt, i);
-        float x[CT] = {};
-        if (t < len) loadn<DT, CT>(B.d_out, (tc + (long long)t) * A.os + (long long)h * D + col, x);
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) dO[ct][rt][i] = x[ct];
-      }
-    __syncthreads();
-    const float* const tab = (const float*)(lds + offTab);
-    auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane * 16); };
-    auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
-    // dW = P^T dO + D K dS1
-    h8 Gh[CT][NB], Gl[CT][NB], xh[CT][2], xl[CT][2];
-    float iG[CT], ix[CT];
-    f4 Y[CT][4];
-#pragma unroll
-    for (int ct = 0; ct < CT; ct++) {
-      iG[ct] = to_operand<NB, 2>(G[ct], Gh[ct], Gl[ct]);
-      ix[ct] = to_operand<2, NPI>(dO[ct], xh[ct], xl[ct]);
+      for (int i = 0; i < 4; i++) dO[rt][i] = orows.value(o[rt][i]);
+    if (c) {
+      if (NBUF == 2) fetch(c - 1);
+      fetch_o(c - 1);
     }
+    const float* const tab = (const float*)(lds + offTab);
+    auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane16); };
+    auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
+    h8 f[L::NF], fl[NPI == 2 ? L::NF : 1];
+    auto read = [&](int off) {
+#pragma unroll
+      for (int n = 0; n < L::NF; n++) {
+        f[n] = frag(off, L::NF, 0, n);
+        if constexpr (NPI == 2) fl[n] = frag(off, L::NF, 1, n);
+      }
+    };
+    h8 ft[2][kTri];
+    auto read_tri = [&](int off) {
+#pragma unroll
+      for (int n = 0; n < kTri; n++) {
+        ft[0][n] = frag(off, kTri, 0, n);
+        ft[1][n] = frag(off, kTri, 1, n);
+      }
+    };
+    read(L::offK);
+    ahead();
+    {
+      const float m = tiles_max<2 * NB>(Gt);
+      if (__any(m > 0x1p14f || (m < 1.0f && m > 0.0f))) rescale(m);
+    }
+    store_G(keep.G + ((j0 + c) * A.H + h) * D * D + col);
+    h8 xh[2], xl[2];
+    f4 z[4], y[4];
+    {  // z = K dS1
+      h8 Gh[NB], Gl[NB];
+      to_planes<NB, 2, true>(Gt, 1.0f, Gh, Gl);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+        for (int rt = 0; rt < 4; rt++) z[rt] = mfma(f[rt * KS + ks], Gh[ks], ks ? z[rt] : zero);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+        for (int rt = 0; rt < 4; rt++) z[rt] = mfma(f[rt * KS + ks], Gl[ks], z[rt]);
+      if constexpr (NPI == 2)
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+          for (int rt = 0; rt < 4; rt++) z[rt] = mfma(fl[rt * KS + ks], Gh[ks], z[rt]);
+    }
+    ahead();
+    read_tri(offP);
+    ahead();
+    auto tri = [&](int p, const h8* b, bool first) {
+#pragma unroll
+      for (int ks = 1; ks >= 0; ks--)
+#pragma unroll
+        for (int rt = 0; rt < 4; rt++)
+          if (ks >= rt >> 1) y[rt] = mfma(ft[p][up_frag(rt, ks)], b[ks], first && ks ? zero : y[rt]);
+    };
+    float ix = to_operand<2, NPI>(dO, xh, xl);
+    tri(0, xh, true);
+    tri(1, xh, false);
+    if constexpr (NPI == 2) tri(0, xl, false);
+    ahead();
+    read_tri(offTt);
+    ahead();
+    // dW = P^T dO + D K dS1, then Y = T^T dW
+    f4 Y[4];
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) {
-      f4 u[CT] = {}, y[CT] = {};
-#pragma unroll
-      for (int ks = 0; ks < KS; ks++) {
-        const h8 a = frag(L::offK, L::NF, 0, rt * KS + ks);
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) u[ct] = mfma(a, Gl[ct][ks], mfma(a, Gh[ct][ks], u[ct]));
-        if constexpr (NPI == 2) {
-          const h8 al = frag(L::offK, L::NF, 1, rt * KS + ks);
-#pragma unroll
-          for (int ct = 0; ct < CT; ct++) u[ct] = mfma(al, Gh[ct][ks], u[ct]);
-        }
-      }
-#pragma unroll
-      for (int ks = rt >> 1; ks < 2; ks++) {
-        const h8 a = frag(offP, kTri, 0, up_frag(rt, ks)), al = frag(offP, kTri, 1, up_frag(rt, ks));
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) {
-          y[ct] = mfma(al, xh[ct][ks], mfma(a, xh[ct][ks], y[ct]));
-          if constexpr (NPI == 2) y[ct] = mfma(a, xl[ct][ks], y[ct]);
-        }
-      }
       const f4 cd = rows(kTabD, rt), ip = rows(kTabP, rt);
 #pragma unroll
-      for (int ct = 0; ct < CT; ct++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) Y[ct][rt][i] = fmaf(cd[i] * iG[ct], u[ct][i], (ip[i] * ix[ct]) * y[ct][i]);
+      for (int i = 0; i < 4; i++) Y[rt][i] = fmaf(cd[i] * unit, z[rt][i], (ip[i] * ix) * y[rt][i]);
     }
-    // Y = T^T dW
-#pragma unroll
-    for (int ct = 0; ct < CT; ct++) ix[ct] = to_operand<2, 2>(Y[ct], xh[ct], xl[ct]);
-    float* const dstY = keep.Y + ((j0 + c) * A.H + h) * 64 * D + col;
-#pragma unroll
-    for (int rt = 0; rt < 4; rt++) {
-      f4 y[CT] = {};
-#pragma unroll
-      for (int ks = rt >> 1; ks < 2; ks++) {
-        const h8 a = frag(offTt, kTri, 0, up_frag(rt, ks)), al = frag(offTt, kTri, 1, up_frag(rt, ks));
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) y[ct] = mfma(al, xh[ct][ks], mfma(a, xl[ct][ks], mfma(a, xh[ct][ks], y[ct])));
-      }
-      const f4 it = rows(kTabTt, rt), be = rows(kTabB, rt);
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int t = state_row(rt, i);
-        float x[CT], v[CT];
-#pragma unroll
-        for (int ct = 0; ct < CT; ct++) {
-          Y[ct][rt][i] = x[ct] = y[ct][i] * (it[i] * ix[ct]);
-          v[ct] = be[i] * x[ct];
-        }
-        storen<kF32, CT>(dstY, (long long)t * D, x);
-        if (t < len) storen<DT, CT>(B.dv, ((tc + (long long)t) * A.H + h) * D + col, v);
-      }
-    }
-    // dS0 = G_C dS1 + Q^T G dO - K^T G diag(beta) Y
-    h8 qh[CT][2], ql[CT][2];
-    float iq[CT];
-#pragma unroll
-    for (int ct = 0; ct < CT; ct++) {
+    ix = to_operand<2, 2>(Y, xh, xl);
+    tri(0, xh, true);
+    tri(0, xl, false);
+    tri(1, xh, false);
+    ahead();
+    read(L::offQ);
+    ahead();
+    {
+      float* const dst = keep.Y + ((j0 + c) * A.H + h) * 64 * D + col;
+      const __amdgpu_buffer_rsrc_t dv = vrows.at(B.dv, tc, (long long)A.H * D, h * D, D, len);
 #pragma unroll
       for (int rt = 0; rt < 4; rt++) {
-        dO[ct][rt] *= rows(kTabQ, rt);
-        Y[ct][rt] *= -rows(kTabU, rt);
-      }
-      iq[ct] = to_operand<2, 2>(dO[ct], qh[ct], ql[ct]);
-      ix[ct] = to_operand<2, 2>(Y[ct], xh[ct], xl[ct]);
-    }
-    const float GC = tab[kTabG + 63];
+        const f4 it = rows(kTabTt, rt), be = rows(kTabB, rt);
 #pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++) {
-      f4 y[CT] = {}, z[CT] = {};
+        for (int i = 0; i < 4; i++) {
+          Y[rt][i] = y[rt][i] * (it[i] * ix);
+          dst[(long long)state_row(rt, i) * D] = Y[rt][i];
+          vrows.store(dv, rt, i, be[i] * Y[rt][i]);
+        }
+      }
+    }
+    // dS0 = G_C dS1 + Q^T G dO - K^T G diag(beta) Y, in the gradient's units
+#pragma unroll
+    for (int rt = 0; rt < 4; rt++) {
+      dO[rt] *= rows(kTabQ, rt);
+      Y[rt] *= -rows(kTabU, rt);
+    }
+    {
+      const float m = fmaxf(tiles_max<4>(dO), tiles_max<4>(Y));
+      if (__any(m > unit * 0x1p14f)) {
+        float inv, to = unit;
+        if (m > unit * 0x1p14f) {
+          (void)scale_of(m, inv);
+          to = inv;
+        }
+        const float r = unit / to;
+#pragma unroll
+        for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] *= r;
+        unit = to;
+      }
+    }
+    const float GC = tab[kTabG + 63], iu = 1.0f / unit;
+#pragma unroll
+    for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] *= GC;
+    auto update = [&]() {
 #pragma unroll
       for (int ks = 0; ks < 2; ks++) {
-        const h8 a = frag(L::offKT, L::NF, 0, 2 * rt + ks), b = frag(L::offQ, L::NF, 0, 2 * rt + ks);
 #pragma unroll
-        for (int ct = 0; ct < CT; ct++) {
-          y[ct] = mfma(a, xl[ct][ks], mfma(a, xh[ct][ks], y[ct]));
-          z[ct] = mfma(b, ql[ct][ks], mfma(b, qh[ct][ks], z[ct]));
-        }
-        if constexpr (NPI == 2) {
-          const h8 al = frag(L::offKT, L::NF, 1, 2 * rt + ks), bl = frag(L::offQ, L::NF, 1, 2 * rt + ks);
+        for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] = mfma(f[2 * rt + ks], xh[ks], Gt[rt]);
 #pragma unroll
-          for (int ct = 0; ct < CT; ct++) {
-            y[ct] = mfma(al, xh[ct][ks], y[ct]);
-            z[ct] = mfma(bl, qh[ct][ks], z[ct]);
-          }
-        }
+        for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] = mfma(f[2 * rt + ks], xl[ks], Gt[rt]);
+        if constexpr (NPI == 2)
+#pragma unroll
+          for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] = mfma(fl[2 * rt + ks], xh[ks], Gt[rt]);
       }
-#pragma unroll
-      for (int ct = 0; ct < CT; ct++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-          G[ct][rt][i] = fmaf(GC, G[ct][rt][i], fmaf(ix[ct], y[ct][i], iq[ct] * z[ct][i]));
+    };
+    to_planes<2, 2>(dO, iu, xh, xl);
+    update();
+    ahead();
+    read(L::offKT);
+    ahead();
+    to_planes<2, 2>(Y, iu, xh, xl);
+    update();
+    if (NBUF == 1 && c) {
+      __syncthreads();
+      fetch(c - 1);
     }
   }
   if (B.dS_in) store_G(B.dS_in + so);
@@ -209,13 +257,18 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
 // every chunk's gradients
 // ---------------------------------------------------------------------------------------------
 
-// Sum over the 16 lanes of a row.
-__device__ __forceinline__ float sum16(float x) {
-  x += __shfl_xor(x, 1);
-  x += __shfl_xor(x, 2);
-  x += __shfl_xor(x, 4);
-  x += __shfl_xor(x, 8);
-  return x;
+// Sum over the 16 lanes of a row, without LDS.
+template <int N>
+__device__ __forceinline__ float add_ror(float x) {
+  return x + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum16(float x) { return add_ror<1>(add_ror<2>(add_ror<4>(add_ror<8>(x)))); }
+// Sum over the four rows of 16 lanes.
+__device__ __forceinline__ float sum_rows(float x) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
 template <int D, int DT>
@@ -226,22 +279,22 @@ struct GradSmem {
       _Float16 O[NPI][64][D + 8], Y[2][64][D + 8], W[2][64][D + 8];
     } in;
     struct {  // N, N^T and Z + Z^T with K's or Q's scales folded into their columns; xT[s][t] the pairs
-      float L[64][kPitch], N[64][kPitch], Nt[64][kPitch], Z[64][kPitch], xT[64][kPitch];
+      float L[64][kPitch], N[64][kPitch], Nt[64][kPitch], Z[64][kPitch], xT[64][kPitch];  // xT[s][t]
     } m;
     float out[64][D + 4];
   };
   char fr[20 * 2 * kFrag];  // fragments of N (6), N^T (6) and Z (8)
   float isO[64], isY[64], isW[64], sN[3][64], iN[3][64];
-  float al[64], be[64], yv[64], rowx[2][64], dot[3][NW][64], corner[NW], z[64], y[64], extra[64];
+  float al[64], be[64], yv[64], rowx[2][64], dot[3][NW][64], corner[NW], z[64], y[64], da[64];
 };
 
 // Rows of a 64-row operand as planes, TPR threads a row; zero from row `len` on.  vrow: adds the row's
 // product with a row of v (the strengths' gradient).
 template <int D, int DT, int ET, int NP, int TPR>
-__device__ __forceinline__ void rows_in(const void* src, long long at, bool live, _Float16 (*dst)[64][D + 8],
+__device__ __forceinline__ void rows_in(int tid, const void* src, long long at, bool live, _Float16 (*dst)[64][D + 8],
                                         float* is, const void* vsrc, long long vat, float* dot) {
   constexpr int E = D / TPR;
-  const int row = threadIdx.x / TPR, part = threadIdx.x % TPR;
+  const int row = tid / TPR, part = tid % TPR;
   float x[E], m = 0.0f, p = 0.0f;
 #pragma unroll
   for (int i = 0; i < E; i += 8) {
@@ -289,19 +342,46 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   const int hq = blockIdx.y;
   ChunkAt at;
   if (!chunk_at(A, j, at)) return;
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int c16 = lane & 15, g = lane >> 4;
+  int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int c16 = lane & 15, g = lane >> 4;
   const int dk = 32 * (w >> 1) + perm_row(c16, w & 1);
   const char* const key = A.ws + (j * A.Hq + hq) * Y::key;
-  const float* const KK = (const float*)(key + Y::offKK);
-  const float* const QK = (const float*)(key + Y::offQK);
-  const int row = tid / TPR;
+  // dO W^T and Y W^T: lower tiles, row tile rt with the columns of one parity (D = 128), or all (64)
+  constexpr int NC = NW == 8 ? 2 : 4, step = NW == 8 ? 2 : 1;
+  const int rt = NW == 8 ? w >> 1 : w, c0 = NW == 8 ? w & 1 : 0;
+  // what all heads share: k_t.k_s and q_t.k_s of this wave's pairs, this lane's column of Q and K
+  f4 kk[NC], qk[NC];
+#pragma unroll
+  for (int n = 0; n < NC; n++) {
+    const int c = min(c0 + step * n, rt), s = 16 * c + c16;
+#pragma unroll
+    for (int i = 0; i < 4; i++) kk[n][i] = ((const float*)(key + Y::offKK))[(16 * rt + 4 * g + i) * 64 + s];
+    qk[n] = *(const f4*)((const float*)(key + Y::offQK) + s * 64 + 16 * rt + 4 * g);
+  }
+  float qv[4][4], kv[4][4];
+#pragma unroll
+  for (int r = 0; r < 4; r++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const long long t = at.t0 + (long long)min(16 * r + 4 * g + i, at.len - 1);
+      loadn<DT, 1>(A.q, t * A.qs + (long long)hq * D + dk, &qv[r][i]);
+      loadn<DT, 1>(A.k, t * A.ks + (long long)hq * D + dk, &kv[r][i]);
+    }
+  int row = tid / TPR;
   const f4 zero = {0, 0, 0, 0};
   f4 dQ[4] = {zero, zero, zero, zero}, dK[4] = {zero, zero, zero, zero};
   for (int hh = 0; hh < A.grp; hh++) {
     const int h = hq * A.grp + hh;
     const float* const tab = (const float*)(A.ws + key_bytes<Y>(A) + (j * A.H + h) * Y::head + Y::offTab);
     const long long jh = j * A.H + h;
+    // opaque per head: the addresses and predicates made from them are not kept across heads, where
+    // they would spill
+    asm("" : "+v"(tid));
+    lane = tid & 63;
+    c16 = lane & 15;
+    g = lane >> 4;
+    row = tid / TPR;
     __syncthreads();
     if (tid < 64) {
       const long long th = (at.t0 + (long long)(tid < at.len ? tid : 0)) * A.H + h;
@@ -309,42 +389,44 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       sm.be[tid] = tid < at.len ? A.beta[th] : 0.0f;
     }
     const long long tok = at.t0 + (long long)row;
-    rows_in<D, DT, DT, NPI, TPR>(B.d_out, tok * A.os + (long long)h * D, row < at.len, sm.in.O, sm.isO, nullptr, 0, nullptr);
-    rows_in<D, DT, kF32, 2, TPR>(keep.Y, (jh * 64 + row) * D, row < at.len, sm.in.Y, sm.isY, A.v, tok * A.vs + (long long)h * D, sm.yv);
-    rows_in<D, DT, kF32, 2, TPR>(keep.W, (jh * 64 + row) * D, row < at.len, sm.in.W, sm.isW, nullptr, 0, nullptr);
+    rows_in<D, DT, DT, NPI, TPR>(tid, B.d_out, tok * A.os + (long long)h * D, row < at.len, sm.in.O, sm.isO, nullptr, 0, nullptr);
+    rows_in<D, DT, kF32, 2, TPR>(tid, keep.Y, (jh * 64 + row) * D, row < at.len, sm.in.Y, sm.isY, A.v, tok * A.vs + (long long)h * D, sm.yv);
+    rows_in<D, DT, kF32, 2, TPR>(tid, keep.W, (jh * 64 + row) * D, row < at.len, sm.in.W, sm.isW, nullptr, 0, nullptr);
+    ahead();
     __syncthreads();
-    // products with the states: this wave's 16 rows of S0 and dS1 as column operands
+    // products with the states: this wave's 16 rows of S0, then of dS1, as column operands
     {
       h8 Sh[KS], Sl[KS], Gh[KS], Gl[KS];
       float iS, iG;
       {
-        float x[KS][8], y[KS][8], m = 0.0f, n = 0.0f, cn = 0.0f;
+        float x[KS][8], m = 0.0f, cn = 0.0f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ks++) {
-          load8<kF32>(keep.S, (jh * D + dk) * D + 32 * ks + 8 * g, x[ks]);
-          load8<kF32>(keep.G, (jh * D + dk) * D + 32 * ks + 8 * g, y[ks]);
+        for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.S, (jh * D + dk) * D + 32 * ks + 8 * g, x[ks]);
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+          for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[ks][e]));
+        float s = scale_of(col_max(m), iS);
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++) split8<2>(x[ks], s, Sh[ks], Sl[ks]);
+        ahead();
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.G, (jh * D + dk) * D + 32 * ks + 8 * g, x[ks]);
+        m = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
 #pragma unroll
           for (int e = 0; e < 8; e++) {
             m = fmaxf(m, fabsf(x[ks][e]));
-            n = fmaxf(n, fabsf(y[ks][e]));
-            cn = fmaf(x[ks][e], y[ks][e], cn);
+            cn = fmaf(x[ks][e], (float)Sh[ks][e] + (float)Sl[ks][e], cn);
           }
-        }
-        m = fmaxf(m, __shfl_xor(m, 16));
-        m = fmaxf(m, __shfl_xor(m, 32));
-        n = fmaxf(n, __shfl_xor(n, 16));
-        n = fmaxf(n, __shfl_xor(n, 32));
-        cn = sum16(cn);
-        cn += __shfl_xor(cn, 16);
-        cn += __shfl_xor(cn, 32);
+        cn = sum_rows(sum16(cn * iS));
         if (lane == 0) sm.corner[w] = cn;
-        const float s = scale_of(m, iS), r = scale_of(n, iG);
+        s = scale_of(col_max(m), iG);
 #pragma unroll
-        for (int ks = 0; ks < KS; ks++) {
-          split8<2>(x[ks], s, Sh[ks], Sl[ks]);
-          split8<2>(y[ks], r, Gh[ks], Gl[ks]);
-        }
+        for (int ks = 0; ks < KS; ks++) split8<2>(x[ks], s, Gh[ks], Gl[ks]);
       }
+      ahead();
 #pragma unroll
       for (int rt = 0; rt < 4; rt++) {
         f4 e1 = zero, e2 = zero, e3 = zero;
@@ -352,37 +434,36 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
         for (int ks = 0; ks < KS; ks++) {
           const int r = 16 * rt + c16, k = 32 * ks + 8 * g;
           const h8 o = *(const h8*)&sm.in.O[0][r][k];
-          e1 = mfma(o, Sl[ks], mfma(o, Sh[ks], e1));
-          if constexpr (NPI == 2) e1 = mfma(*(const h8*)&sm.in.O[1][r][k], Sh[ks], e1);
           const h8 yh = *(const h8*)&sm.in.Y[0][r][k], yl = *(const h8*)&sm.in.Y[1][r][k];
-          e2 = mfma(yl, Sh[ks], mfma(yh, Sl[ks], mfma(yh, Sh[ks], e2)));
           const h8 wh = *(const h8*)&sm.in.W[0][r][k], wl = *(const h8*)&sm.in.W[1][r][k];
-          e3 = mfma(wl, Gh[ks], mfma(wh, Gl[ks], mfma(wh, Gh[ks], e3)));
+          e1 = mfma(o, Sh[ks], e1);
+          e2 = mfma(yh, Sh[ks], e2);
+          e3 = mfma(wh, Gh[ks], e3);
+          e1 = mfma(o, Sl[ks], e1);
+          e2 = mfma(yh, Sl[ks], e2);
+          e3 = mfma(wh, Gl[ks], e3);
+          if constexpr (NPI == 2) e1 = mfma(*(const h8*)&sm.in.O[1][r][k], Sh[ks], e1);
+          e2 = mfma(yl, Sh[ks], e2);
+          e3 = mfma(wl, Gh[ks], e3);
         }
+        const int t0 = 16 * rt + 4 * g;
+        const f4 io = *(const f4*)&sm.isO[t0], iy = *(const f4*)&sm.isY[t0], iw = *(const f4*)&sm.isW[t0];
+        const f4 G = *(const f4*)&tab[kTabG + t0], lc = *(const f4*)&tab[kTabL + t0], be = *(const f4*)&sm.be[t0];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const int t = 16 * rt + 4 * g + i;
-          const float a = e1[i] * (sm.isO[t] * iS), b = e2[i] * (sm.isY[t] * iS), c = e3[i] * (sm.isW[t] * iG);
-          const float G = tab[kTabG + t];
-          dQ[rt][i] = fmaf(G, a, dQ[rt][i]);
-          dK[rt][i] = fmaf(-G * sm.be[t], b, fmaf(tab[kTabL + t], c, dK[rt][i]));
-          float q = 0.0f, k = 0.0f;
-          if (t < at.len) {
-            loadn<DT, 1>(A.q, (at.t0 + (long long)t) * A.qs + (long long)hq * D + dk, &q);
-            loadn<DT, 1>(A.k, (at.t0 + (long long)t) * A.ks + (long long)hq * D + dk, &k);
-          }
-          const float zq = sum16(q * a), zk = sum16(k * b), yk = sum16(k * c);
+          const float a = e1[i] * (io[i] * iS), b = e2[i] * (iy[i] * iS), c = e3[i] * (iw[i] * iG);
+          dQ[rt][i] = fmaf(G[i], a, dQ[rt][i]);
+          dK[rt][i] = fmaf(-G[i] * be[i], b, fmaf(lc[i], c, dK[rt][i]));
+          const float zq = sum16(qv[rt][i] * a), zk = sum16(kv[rt][i] * b), yk = sum16(kv[rt][i] * c);
           if (c16 == 0) {
-            sm.dot[0][w][t] = zq;
-            sm.dot[1][w][t] = zk;
-            sm.dot[2][w][t] = yk;
+            sm.dot[0][w][t0 + i] = zq;
+            sm.dot[1][w][t0 + i] = zk;
+            sm.dot[2][w][t0 + i] = yk;
           }
         }
+        ahead();
       }
     }
-    // dO W^T and Y W^T: lower tiles, row tile rt with the columns of one parity (D = 128), or all (64)
-    constexpr int NC = NW == 8 ? 2 : 4, step = NW == 8 ? 2 : 1;
-    const int rt = NW == 8 ? w >> 1 : w, c0 = NW == 8 ? w & 1 : 0;
     f4 dp[NC], dx[NC];
 #pragma unroll
     for (int n = 0; n < NC; n++) {
@@ -441,12 +522,12 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
           if (s <= t) {
             const float l = sm.m.L[t][s], p = dp[n][i] * (sm.isO[t] * sm.isW[s]);
             nv = p * l;
-            x = p * QK[s * 64 + t];
+            x = p * qk[n][i];
             if (s < t) {
-              const float y = dx[n][i] * (sm.isY[t] * sm.isW[s]), kk = KK[t * 64 + s], b = sm.be[t] * y;
+              const float y = dx[n][i] * (sm.isY[t] * sm.isW[s]), b = sm.be[t] * y;
               zv = -b * l;
-              x = fmaf(-b, kk, x);
-              rx[i] = fmaf(y, l * kk, rx[i]);
+              x = fmaf(-b, kk[n][i], x);
+              rx[i] = fmaf(y, l * kk[n][i], rx[i]);
             }
           }
           sm.m.N[t][s] = nv * ik;
@@ -502,20 +583,36 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       *(h8*)(sm.fr + 2 * f * kFrag + lane * 16) = hi;
       *(h8*)(sm.fr + (2 * f + 1) * kFrag + lane * 16) = lo;
     }
-    // gates: lane t follows F_r = sum over s < r of x[t,s] L[r-1,s]; xT[r][t] becomes L[t,r] F_r
-    if (w == NW - 1) {
-      float F = sm.z[lane], C = 0.0f, mine = 0.0f;
+    // gates: dalpha_r = sum over t >= r of L[t,r] F_r[t] with F_r[t] = sum over s < r of x[t,s] L[r-1,s]
+    // (the state before the chunk as s = -1, the state behind it as one more t).  Lane t; a wave takes
+    // 64 / NW gates: F at its first by a sum, then F_{r+1} = a_r F_r + x[t,r].
+    {
+      constexpr int RW = 64 / NW;
+      const int r0 = RW * w;
+      float F = sm.z[lane], C = 0.0f;
 #pragma unroll
       for (int v = 0; v < NW; v++) C += sm.corner[v];
+      if (w) {
+        const float* const lr = sm.m.L[r0 - 1];
+        const float G = sm.al[0] * lr[0];
+        const float y = lane < r0 ? sm.y[lane] * lr[lane] : 0.0f;
+        C = fmaf(C, G, sum_rows(sum16(y)));
+        float f0 = F * G, f1 = 0.0f;
 #pragma unroll 8
-      for (int r = 0; r < 64; r++) {
-        const float x = sm.m.xT[r][lane], a = sm.al[r];
-        sm.m.xT[r][lane] = lane >= r ? sm.m.L[lane][r] * F : 0.0f;
-        mine = lane == r ? C : mine;
-        F = fmaf(a, F, x);
-        C = fmaf(a, C, sm.y[r]);
+        for (int s = 0; s < r0; s += 2) {
+          f0 = fmaf(lr[s], sm.m.xT[s][lane], f0);
+          f1 = fmaf(lr[s + 1], sm.m.xT[s + 1][lane], f1);
+        }
+        F = f0 + f1;
       }
-      sm.extra[lane] = sm.m.L[63][lane] * mine;
+#pragma unroll
+      for (int i = 0; i < RW; i++) {
+        const int r = r0 + i;
+        const float v = sum_rows(sum16(lane >= r ? sm.m.L[lane][r] * F : 0.0f));
+        if (lane == 0) sm.da[r] = fmaf(sm.m.L[63][r], C, v);
+        F = fmaf(sm.al[r], F, sm.m.xT[r][lane]);
+        C = fmaf(sm.al[r], C, sm.y[r]);
+      }
     }
     __syncthreads();
     {
@@ -556,19 +653,10 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
           dK[r][i] = fmaf(sm.iN[1][tt], t[r][i], fmaf(sm.iN[2][tt], z[r][i], dK[r][i]));
         }
     }
-    {
-      constexpr int E = 64 / TPR;
-      const int part = tid % TPR;
-      float a = 0.0f;
-#pragma unroll
-      for (int i = 0; i < E; i++) a += sm.m.xT[row][part * E + i];
-#pragma unroll
-      for (int o = 1; o < TPR; o <<= 1) a += __shfl_xor(a, o);
-      if (part == 0 && row < at.len) {
-        const long long th = (at.t0 + (long long)row) * A.H + h;
-        B.dalpha[th] = a + sm.extra[row];
-        B.dbeta[th] = sm.yv[row] - (sm.rowx[0][row] + (NW == 8 ? sm.rowx[1][row] : 0.0f));
-      }
+    if (tid < at.len) {
+      const long long th = (at.t0 + (long long)tid) * A.H + h;
+      B.dalpha[th] = sm.da[tid];
+      B.dbeta[th] = sm.yv[tid] - (sm.rowx[0][tid] + (NW == 8 ? sm.rowx[1][tid] : 0.0f));
     }
   }
   // dQ and dK to rows through LDS
@@ -608,16 +696,15 @@ hipError_t launch(GradArgs b, hipStream_t s) {
   keep.G = keep.S + n * D * D;
   keep.W = keep.G + n * D * D;
   keep.Y = keep.W + n * 64 * D;
-  constexpr int CT = D == 128 ? 2 : 1;
-  const dim3 slots((unsigned)chunk_slots(a.T, a.N), a.Hq), tiles((unsigned)((long long)a.N * a.H), D / (64 * CT));
+  const dim3 slots((unsigned)chunk_slots(a.T, a.N), a.Hq), tiles((unsigned)((long long)a.N * a.H));
   unsigned* const status = a.status;
   a.status = nullptr;  // reported once, by the reverse pass
   if (a.T > 0) {
     hipLaunchKernelGGL((k_chunk_prep<D, DT, LayB<D, DT>>), slots, dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_chunk_state<D, DT, D / 16, LayB<D, DT>>), dim3(tiles.x, 1), dim3(4 * D), 0, s, a, keep.S, keep.W);
+    hipLaunchKernelGGL((k_chunk_state<D, DT, D / 16, LayB<D, DT>>), tiles, dim3(4 * D), 0, s, a, keep.S, keep.W);
   }
   a.status = status;
-  hipLaunchKernelGGL((k_chunk_reverse<D, DT, CT, 4>), tiles, dim3(256), 0, s, b, keep);
+  hipLaunchKernelGGL((k_chunk_reverse<D, DT, D / 16>), tiles, dim3(4 * D), 0, s, b, keep);
   if (a.T > 0) hipLaunchKernelGGL((k_chunk_grad<D, DT>), slots, dim3(4 * D), 0, s, b, keep);
   return hipGetLastError();
 }
