@@ -278,17 +278,19 @@ struct GradSmem {
     struct {
       _Float16 O[NPI][64][D + 8], Y[2][64][D + 8], W[2][64][D + 8];
     } in;
-    struct {  // N, N^T and Z + Z^T with K's or Q's scales folded into their columns; xT[s][t] the pairs
-      float L[64][kPitch], N[64][kPitch], Nt[64][kPitch], Z[64][kPitch], xT[64][kPitch];  // xT[s][t]
+    struct {
+      char fr[24 * 2 * kFrag];  // fragments of N, Zd (lower, 6 each), N^T, Zu (upper)
+      float xT[64][66];         // xT[s][t]: the pairs' values without their gates
+      float iF[4][64];          // inverse row scales of the four
     } m;
     float out[64][D + 4];
   };
-  char fr[20 * 2 * kFrag];  // fragments of N (6), N^T (6) and Z (8)
-  float isO[64], isY[64], isW[64], sN[3][64], iN[3][64];
-  float al[64], be[64], yv[64], rowx[2][64], dot[3][NW][64], corner[NW], z[64], y[64], da[64];
+  float isO[64], isY[64], isW[64], isk[64], isq[64];
+  float gate[7][64];            // a, pre8, suf8, pre32, suf32, G, L[C,.]
+  float be[64], yv[64], rowx[64], dot[3][NW][64], corner[NW], z[64], y[64], da[64];
 };
 
-// Rows of a 64-row operand as planes, TPR threads a row; zero from row `len` on.  vrow: adds the row's
+// Rows of a 64-row operand as planes, TPR threads a row; zero where not `live`.  dot: adds the row's
 // product with a row of v (the strengths' gradient).
 template <int D, int DT, int ET, int NP, int TPR>
 __device__ __forceinline__ void rows_in(int tid, const void* src, long long at, bool live, _Float16 (*dst)[64][D + 8],
@@ -297,18 +299,18 @@ __device__ __forceinline__ void rows_in(int tid, const void* src, long long at, 
   const int row = tid / TPR, part = tid % TPR;
   float x[E], m = 0.0f, p = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E; i += 8) {
+  for (int i = 0; i < E; i += 8) load8<ET>(src, at + part * E + i, x + i);
+  if (dot) {
+    float v[E];
 #pragma unroll
-    for (int e = 0; e < 8; e++) x[i + e] = 0.0f;
-    if (live) load8<ET>(src, at + part * E + i, x + i);
+    for (int i = 0; i < E; i += 8) load8<DT>(vsrc, vat + part * E + i, v + i);
 #pragma unroll
-    for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[i + e]));
-    if (dot && live) {
-      float v[8];
-      load8<DT>(vsrc, vat + part * E + i, v);
+    for (int i = 0; i < E; i++) p = fmaf(x[i], v[i], p);
+  }
 #pragma unroll
-      for (int e = 0; e < 8; e++) p = fmaf(x[i + e], v[e], p);
-    }
+  for (int i = 0; i < E; i++) {
+    x[i] = live ? x[i] : 0.0f;
+    m = fmaxf(m, fabsf(x[i]));
   }
 #pragma unroll
   for (int o = 1; o < TPR; o <<= 1) {
@@ -331,7 +333,10 @@ __device__ __forceinline__ void rows_in(int tid, const void* src, long long at, 
 }
 
 // One workgroup of D / 16 waves per (chunk, key head); the value heads that share the key head one after
-// another, dQ and dK summed in registers.  Wave w owns the 16 key dimensions 32 (w >> 1) + perm(., w & 1).
+// another, dQ and dK summed in registers.  Wave w owns the 16 key dimensions 32 (w >> 1) + perm(., w & 1) of
+// all products with the states and of dQ and dK.  The pairs of tokens are formed twice, with the later
+// token and with the earlier one as the lane's own (a wave each where there are eight): a lane then holds 8
+// consecutive partners (their row tiles permuted), which is the fragment of N, N^T and either half of Z + Z^T as it is.
 template <int D, int DT>
 __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   using Y = LayB<D, DT>;
@@ -347,319 +352,491 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   int c16 = lane & 15, g = lane >> 4;
   const int dk = 32 * (w >> 1) + perm_row(c16, w & 1);
   const char* const key = A.ws + (j * A.Hq + hq) * Y::key;
-  // dO W^T and Y W^T: lower tiles, row tile rt with the columns of one parity (D = 128), or all (64)
-  constexpr int NC = NW == 8 ? 2 : 4, step = NW == 8 ? 2 : 1;
-  const int rt = NW == 8 ? w >> 1 : w, c0 = NW == 8 ? w & 1 : 0;
-  // what all heads share: k_t.k_s and q_t.k_s of this wave's pairs, this lane's column of Q and K
-  f4 kk[NC], qk[NC];
+  // pairs: row tile pt, own token; down: own is the later token
+  const int pt = w & 3, pb = pt >> 1;
+  const bool down = NW == 4 || w < 4, up = NW == 4 || w >= 4;
+  // this lane's column of Q and K, rows 16 rt + 4 g + i (zero behind the end)
+  using Col = Rows<DT, true>;
+  const Col qrows(A.qs, dk, g), krows(A.ks, dk, g);
+  constexpr int NV = DT == kF32 ? 4 : 2;  // 16-bit types: two rows a register
+  unsigned qv[4][NV], kv[4][NV];
+  {
+    unsigned q[4][4], k[4][4];
+    qrows.load(qrows.at(A.q, at.t0, A.qs, hq * D, D, at.len), q);
+    krows.load(krows.at(A.k, at.t0, A.ks, hq * D, D, at.len), k);
 #pragma unroll
-  for (int n = 0; n < NC; n++) {
-    const int c = min(c0 + step * n, rt), s = 16 * c + c16;
+    for (int rt = 0; rt < 4; rt++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) kk[n][i] = ((const float*)(key + Y::offKK))[(16 * rt + 4 * g + i) * 64 + s];
-    qk[n] = *(const f4*)((const float*)(key + Y::offQK) + s * 64 + 16 * rt + 4 * g);
+      for (int i = 0; i < NV; i++) {
+        qv[rt][i] = NV == 4 ? q[rt][i] : q[rt][2 * i & 3] | q[rt][(2 * i + 1) & 3] << 16;
+        kv[rt][i] = NV == 4 ? k[rt][i] : k[rt][2 * i & 3] | k[rt][(2 * i + 1) & 3] << 16;
+      }
   }
-  float qv[4][4], kv[4][4];
-#pragma unroll
-  for (int r = 0; r < 4; r++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const long long t = at.t0 + (long long)min(16 * r + 4 * g + i, at.len - 1);
-      loadn<DT, 1>(A.q, t * A.qs + (long long)hq * D + dk, &qv[r][i]);
-      loadn<DT, 1>(A.k, t * A.ks + (long long)hq * D + dk, &kv[r][i]);
-    }
+  auto column = [&](unsigned (*v)[NV], int rt, int i) {
+    if constexpr (NV == 4) return Col::value(v[rt][i]);
+    else return Col::value(i & 1 ? v[rt][i >> 1] >> 16 : v[rt][i >> 1]);
+  };
+  if (tid < 64) {
+    const float* const tab = (const float*)(A.ws + key_bytes<Y>(A) + (j * A.H + hq * A.grp) * Y::head + Y::offTab);
+    sm.isk[tid] = tab[kTabIK + tid];
+    sm.isq[tid] = tab[kTabIQ + tid];
+  }
   int row = tid / TPR;
   const f4 zero = {0, 0, 0, 0};
   f4 dQ[4] = {zero, zero, zero, zero}, dK[4] = {zero, zero, zero, zero};
+  // the sums are taken where they stand: left to the end they would hold every term in registers
+  auto settle = [](f4& x) { asm volatile("" : "+v"(x)); };
   for (int hh = 0; hh < A.grp; hh++) {
     const int h = hq * A.grp + hh;
-    const float* const tab = (const float*)(A.ws + key_bytes<Y>(A) + (j * A.H + h) * Y::head + Y::offTab);
     const long long jh = j * A.H + h;
-    // opaque per head: the addresses and predicates made from them are not kept across heads, where
-    // they would spill
-    asm("" : "+v"(tid));
-    lane = tid & 63;
-    c16 = lane & 15;
-    g = lane >> 4;
-    row = tid / TPR;
-    __syncthreads();
-    if (tid < 64) {
-      const long long th = (at.t0 + (long long)(tid < at.len ? tid : 0)) * A.H + h;
-      sm.al[tid] = tid < at.len ? A.alpha[th] : 1.0f;
-      sm.be[tid] = tid < at.len ? A.beta[th] : 0.0f;
+    int own;
+    // opaque again at every phase: addresses and predicates made from the lane are not kept across phases
+    // and heads, where they would spill
+    auto fresh = [&]() {
+      asm("" : "+v"(tid));
+      lane = tid & 63;
+      c16 = lane & 15;
+      g = lane >> 4;
+      row = tid / TPR;
+      own = 16 * pt + c16;
+    };
+    fresh();
+#pragma unroll
+    for (int rt = 0; rt < 4; rt++)
+#pragma unroll
+      for (int i = 0; i < NV; i++) asm volatile("" : "+v"(qv[rt][i]), "+v"(kv[rt][i]));  // stay as they are packed
+    // S0 is on its way while the rows become operands, dS1 while S0's products run
+    float x[KS][8];
+    const long long sat = (jh * D + dk) * D + 8 * g;
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.S, sat + 32 * ks, x[ks]);
+    float al = 1.0f, be = 0.0f;
+    if (w == NW - 1 && lane < at.len) {
+      const long long th = (at.t0 + (long long)lane) * A.H + h;
+      al = A.alpha[th];
+      be = A.beta[th];
     }
-    const long long tok = at.t0 + (long long)row;
-    rows_in<D, DT, DT, NPI, TPR>(tid, B.d_out, tok * A.os + (long long)h * D, row < at.len, sm.in.O, sm.isO, nullptr, 0, nullptr);
-    rows_in<D, DT, kF32, 2, TPR>(tid, keep.Y, (jh * 64 + row) * D, row < at.len, sm.in.Y, sm.isY, A.v, tok * A.vs + (long long)h * D, sm.yv);
-    rows_in<D, DT, kF32, 2, TPR>(tid, keep.W, (jh * 64 + row) * D, row < at.len, sm.in.W, sm.isW, nullptr, 0, nullptr);
+    ahead();
+    __syncthreads();  // the last head's fragments have been read
+    const bool live = row < at.len;
+    const long long tok = at.t0 + (long long)min(row, at.len - 1);
+    rows_in<D, DT, DT, NPI, TPR>(tid, B.d_out, tok * A.os + (long long)h * D, live, sm.in.O, sm.isO, nullptr, 0, nullptr);
+    rows_in<D, DT, kF32, 2, TPR>(tid, keep.Y, (jh * 64 + row) * D, live, sm.in.Y, sm.isY, A.v, tok * A.vs + (long long)h * D, sm.yv);
+    rows_in<D, DT, kF32, 2, TPR>(tid, keep.W, (jh * 64 + row) * D, live, sm.in.W, sm.isW, nullptr, 0, nullptr);
+    if (w == NW - 1) {
+      float p8 = al, s8 = __shfl_down(al, 1);
+      s8 = (lane & 7) < 7 ? s8 : 1.0f;
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        const float u = __shfl_up(p8, o), d = __shfl_down(s8, o);
+        if ((lane & 7) >= o) p8 *= u;
+        if ((lane & 7) + o < 8) s8 *= d;
+      }
+      float p32 = p8, s32 = s8, G = 1.0f, lc = 1.0f;
+#pragma unroll
+      for (int n = 0; n < 8; n++) {
+        const float b = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p8), 8 * n + 7));
+        const int m = lane >> 3;
+        if (n < m) G *= b;
+        if (n > m) lc *= b;
+        if (n < m && (n >> 2) == (m >> 2)) p32 *= b;
+        if (n > m && (n >> 2) == (m >> 2)) s32 *= b;
+      }
+      sm.gate[0][lane] = al;
+      sm.gate[1][lane] = p8;
+      sm.gate[2][lane] = s8;
+      sm.gate[3][lane] = p32;
+      sm.gate[4][lane] = s32;
+      sm.gate[5][lane] = G * p8;
+      sm.gate[6][lane] = lc * s8;
+      sm.be[lane] = be;
+    }
+    // this wave's 16 rows of S0 as column operands
+    h8 Sh[KS], Sl[KS];
+    float iS;
+    {
+      float m = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[ks][e]));
+      const float s = scale_of(col_max(m), iS);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) split8<2>(x[ks], s, Sh[ks], Sl[ks]);
+    }
+    ahead();
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.G, sat + 32 * ks, x[ks]);
     ahead();
     __syncthreads();
-    // products with the states: this wave's 16 rows of S0, then of dS1, as column operands
-    {
-      h8 Sh[KS], Sl[KS], Gh[KS], Gl[KS];
-      float iS, iG;
-      {
-        float x[KS][8], m = 0.0f, cn = 0.0f;
+    fresh();
+    // dQ += G dO S0^T, dK -= G beta Y S0^T; and their products with q_t and k_t
 #pragma unroll
-        for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.S, (jh * D + dk) * D + 32 * ks + 8 * g, x[ks]);
+    for (int rt = 0; rt < 4; rt++) {
+      f4 e1 = zero, e2 = zero;
+      const int r = 16 * rt + c16;
 #pragma unroll
-        for (int ks = 0; ks < KS; ks++)
-#pragma unroll
-          for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[ks][e]));
-        float s = scale_of(col_max(m), iS);
-#pragma unroll
-        for (int ks = 0; ks < KS; ks++) split8<2>(x[ks], s, Sh[ks], Sl[ks]);
-        ahead();
-#pragma unroll
-        for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.G, (jh * D + dk) * D + 32 * ks + 8 * g, x[ks]);
-        m = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ks++)
-#pragma unroll
-          for (int e = 0; e < 8; e++) {
-            m = fmaxf(m, fabsf(x[ks][e]));
-            cn = fmaf(x[ks][e], (float)Sh[ks][e] + (float)Sl[ks][e], cn);
-          }
-        cn = sum_rows(sum16(cn * iS));
-        if (lane == 0) sm.corner[w] = cn;
-        s = scale_of(col_max(m), iG);
-#pragma unroll
-        for (int ks = 0; ks < KS; ks++) split8<2>(x[ks], s, Gh[ks], Gl[ks]);
+      for (int ks = 0; ks < KS; ks++) {
+        const int k = 32 * ks + 8 * g;
+        const h8 o = *(const h8*)&sm.in.O[0][r][k];
+        const h8 yh = *(const h8*)&sm.in.Y[0][r][k], yl = *(const h8*)&sm.in.Y[1][r][k];
+        e1 = mfma(o, Sh[ks], e1);
+        e2 = mfma(yh, Sh[ks], e2);
+        e1 = mfma(o, Sl[ks], e1);
+        e2 = mfma(yh, Sl[ks], e2);
+        if constexpr (NPI == 2) e1 = mfma(*(const h8*)&sm.in.O[1][r][k], Sh[ks], e1);
+        e2 = mfma(yl, Sh[ks], e2);
       }
+      const int t0 = 16 * rt + 4 * g;
+      const f4 io = *(const f4*)&sm.isO[t0] * iS, iy = *(const f4*)&sm.isY[t0] * iS;
+      const f4 G = *(const f4*)&sm.gate[5][t0], be4 = *(const f4*)&sm.be[t0];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float a = e1[i] * io[i], b = e2[i] * iy[i];
+        dQ[rt][i] = fmaf(G[i], a, dQ[rt][i]);
+        dK[rt][i] = fmaf(-G[i] * be4[i], b, dK[rt][i]);
+        const float zq = sum16(column(qv, rt, i) * a), zk = sum16(column(kv, rt, i) * b);
+        if (c16 == 0) {
+          sm.dot[0][w][t0 + i] = zq;
+          sm.dot[1][w][t0 + i] = zk;
+        }
+      }
+      settle(dQ[rt]);
+      settle(dK[rt]);
+      ahead();
+    }
+    fresh();
+    // dK += D W dS1^T; <S0, dS1>
+    {
+      h8 Gh[KS], Gl[KS];
+      float m = 0.0f, cn = 0.0f, iG;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          m = fmaxf(m, fabsf(x[ks][e]));
+          cn = fmaf(x[ks][e], (float)Sh[ks][e] + (float)Sl[ks][e], cn);
+        }
+      cn = sum_rows(sum16(cn * iS));
+      if (lane == 0) sm.corner[w] = cn;
+      const float s = scale_of(col_max(m), iG);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) split8<2>(x[ks], s, Gh[ks], Gl[ks]);
       ahead();
 #pragma unroll
       for (int rt = 0; rt < 4; rt++) {
-        f4 e1 = zero, e2 = zero, e3 = zero;
+        f4 e3 = zero;
+        const int r = 16 * rt + c16;
 #pragma unroll
         for (int ks = 0; ks < KS; ks++) {
-          const int r = 16 * rt + c16, k = 32 * ks + 8 * g;
-          const h8 o = *(const h8*)&sm.in.O[0][r][k];
-          const h8 yh = *(const h8*)&sm.in.Y[0][r][k], yl = *(const h8*)&sm.in.Y[1][r][k];
+          const int k = 32 * ks + 8 * g;
           const h8 wh = *(const h8*)&sm.in.W[0][r][k], wl = *(const h8*)&sm.in.W[1][r][k];
-          e1 = mfma(o, Sh[ks], e1);
-          e2 = mfma(yh, Sh[ks], e2);
-          e3 = mfma(wh, Gh[ks], e3);
-          e1 = mfma(o, Sl[ks], e1);
-          e2 = mfma(yh, Sl[ks], e2);
-          e3 = mfma(wh, Gl[ks], e3);
-          if constexpr (NPI == 2) e1 = mfma(*(const h8*)&sm.in.O[1][r][k], Sh[ks], e1);
-          e2 = mfma(yl, Sh[ks], e2);
-          e3 = mfma(wl, Gh[ks], e3);
+          e3 = mfma(wl, Gh[ks], mfma(wh, Gl[ks], mfma(wh, Gh[ks], e3)));
         }
         const int t0 = 16 * rt + 4 * g;
-        const f4 io = *(const f4*)&sm.isO[t0], iy = *(const f4*)&sm.isY[t0], iw = *(const f4*)&sm.isW[t0];
-        const f4 G = *(const f4*)&tab[kTabG + t0], lc = *(const f4*)&tab[kTabL + t0], be = *(const f4*)&sm.be[t0];
+        const f4 iw = *(const f4*)&sm.isW[t0] * iG, lc = *(const f4*)&sm.gate[6][t0];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const float a = e1[i] * (io[i] * iS), b = e2[i] * (iy[i] * iS), c = e3[i] * (iw[i] * iG);
-          dQ[rt][i] = fmaf(G[i], a, dQ[rt][i]);
-          dK[rt][i] = fmaf(-G[i] * be[i], b, fmaf(lc[i], c, dK[rt][i]));
-          const float zq = sum16(qv[rt][i] * a), zk = sum16(kv[rt][i] * b), yk = sum16(kv[rt][i] * c);
-          if (c16 == 0) {
-            sm.dot[0][w][t0 + i] = zq;
-            sm.dot[1][w][t0 + i] = zk;
-            sm.dot[2][w][t0 + i] = yk;
-          }
+          const float c = e3[i] * iw[i];
+          dK[rt][i] = fmaf(lc[i], c, dK[rt][i]);
+          const float yk = sum16(column(kv, rt, i) * c);
+          if (c16 == 0) sm.dot[2][w][t0 + i] = yk;
         }
-        ahead();
+        settle(dK[rt]);
       }
+      ahead();
     }
-    f4 dp[NC], dx[NC];
+    fresh();
+    // pairs: dO W^T and Y W^T (down: [own t][8 s], up: [own s][8 t])
+    float pd[2][8], xd[2][8], p1[NW == 4 ? 2 : 1][8], x1[NW == 4 ? 2 : 1][8];
+    float(*const pu)[8] = NW == 4 ? p1 : pd;
+    float(*const xu)[8] = NW == 4 ? x1 : xd;
+    float kk[2][8], qk[2][8];  // k_t.k_s and q_t.k_s of the down pairs
+    if (down)
 #pragma unroll
-    for (int n = 0; n < NC; n++) {
-      dp[n] = dx[n] = zero;
-      const int c = c0 + step * n;
-      if (c > rt) continue;
+      for (int nb = 0; nb < 2; nb++) {
+        if (nb > pb) continue;
+        load8<kF32>(key + Y::offKK, own * 64 + 32 * nb + 8 * g, kk[nb]);
+#pragma unroll
+        for (int e = 0; e < 8; e++) qk[nb][e] = ((const float*)(key + Y::offQK))[(32 * nb + 8 * g + e) * 64 + own];
+      }
+    if (down) {
+      h8 o[KS][NPI], yh[KS], yl[KS];
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
-        const int r = 16 * rt + c16, q = 16 * c + c16, k = 32 * ks + 8 * g;
-        const h8 wh = *(const h8*)&sm.in.W[0][q][k], wl = *(const h8*)&sm.in.W[1][q][k];
-        const h8 o = *(const h8*)&sm.in.O[0][r][k];
-        dp[n] = mfma(o, wl, mfma(o, wh, dp[n]));
-        if constexpr (NPI == 2) dp[n] = mfma(*(const h8*)&sm.in.O[1][r][k], wh, dp[n]);
-        const h8 yh = *(const h8*)&sm.in.Y[0][r][k], yl = *(const h8*)&sm.in.Y[1][r][k];
-        dx[n] = mfma(yl, wh, mfma(yh, wl, mfma(yh, wh, dx[n])));
+        const int k = 32 * ks + 8 * g;
+#pragma unroll
+        for (int p = 0; p < NPI; p++) o[ks][p] = *(const h8*)&sm.in.O[p][own][k];
+        yh[ks] = *(const h8*)&sm.in.Y[0][own][k];
+        yl[ks] = *(const h8*)&sm.in.Y[1][own][k];
+      }
+      const float io = sm.isO[own], iy = sm.isY[own];
+#pragma unroll
+      for (int nb = 0; nb < 2; nb++) {
+        if (nb > pb) continue;
+        f4 a[2] = {zero, zero}, b[2] = {zero, zero};
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+          for (int p = 0; p < 2; p++) {
+            const int r = 32 * nb + perm_row(c16, p), k = 32 * ks + 8 * g;
+            const h8 wh = *(const h8*)&sm.in.W[0][r][k], wl = *(const h8*)&sm.in.W[1][r][k];
+            a[p] = mfma(wl, o[ks][0], mfma(wh, o[ks][0], a[p]));
+            if constexpr (NPI == 2) a[p] = mfma(wh, o[ks][NPI - 1], a[p]);
+            b[p] = mfma(wl, yh[ks], mfma(wh, yl[ks], mfma(wh, yh[ks], b[p])));
+          }
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float iw = sm.isW[32 * nb + 8 * g + e];
+          pd[nb][e] = a[e >> 2][e & 3] * (iw * io);
+          xd[nb][e] = b[e >> 2][e & 3] * (iw * iy);
+        }
       }
     }
-    __syncthreads();  // the planes are free: matrices in their place
-    {
-      constexpr int RW = 64 / NW;  // rows of L a wave
-      int ln = lane;
-      asm("" : "+v"(ln));
-      float l = 1.0f;
-      for (int t = 0; t < RW * w; t++) l = t > ln ? l * sm.al[t] : 1.0f;
+    if (up) {
+      h8 wh[KS], wl[KS];
 #pragma unroll
-      for (int i = 0; i < RW; i++) {
-        const int t = RW * w + i;
-        l = t > ln ? l * sm.al[t] : 1.0f;
-        sm.m.L[t][ln] = t >= ln ? l : 0.0f;
+      for (int ks = 0; ks < KS; ks++) {
+        wh[ks] = *(const h8*)&sm.in.W[0][own][32 * ks + 8 * g];
+        wl[ks] = *(const h8*)&sm.in.W[1][own][32 * ks + 8 * g];
       }
-      if (tid < 64) {
+      const float iw = sm.isW[own];
+#pragma unroll
+      for (int nb = 0; nb < 2; nb++) {
+        if (nb < pb) continue;
+        f4 a[2] = {zero, zero}, b[2] = {zero, zero};
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+          for (int p = 0; p < 2; p++) {
+            const int r = 32 * nb + perm_row(c16, p), k = 32 * ks + 8 * g;
+            const h8 o = *(const h8*)&sm.in.O[0][r][k];
+            const h8 yh = *(const h8*)&sm.in.Y[0][r][k], yl = *(const h8*)&sm.in.Y[1][r][k];
+            a[p] = mfma(o, wl[ks], mfma(o, wh[ks], a[p]));
+            if constexpr (NPI == 2) a[p] = mfma(*(const h8*)&sm.in.O[NPI - 1][r][k], wh[ks], a[p]);
+            b[p] = mfma(yl, wh[ks], mfma(yh, wl[ks], mfma(yh, wh[ks], b[p])));
+          }
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const int t = 32 * nb + 8 * g + e;
+          pu[nb][e] = a[e >> 2][e & 3] * (sm.isO[t] * iw);
+          xu[nb][e] = b[e >> 2][e & 3] * (sm.isY[t] * iw);
+        }
+      }
+    }
+    __syncthreads();  // the planes are free: fragments and pairs in their place
+    fresh();
+    {
+      const int po = own & 31, og = po >> 3, oi = po & 7;  // own token: place in its block, group, place in that
+      const float* const ga = &sm.gate[0][32 * pb + 8 * g];
+      auto mid = [&](bool dn) {
+        const int lo = dn ? g : og, hi = dn ? og : g;
+        float m = sm.gate[dn ? 1 : 2][own];
+        if (lo == 0 && hi > 1) m *= sm.gate[1][32 * pb + 15];
+        if (lo <= 1 && hi == 3) m *= sm.gate[1][32 * pb + 23];
+        return m;
+      };
+      // a fragment pair and its rows' scale
+      auto put = [&](float (*v)[8], int which, bool lower) {
+        float m = 0.0f, inv;
+#pragma unroll
+        for (int nb = 0; nb < 2; nb++)
+          if (lower ? nb <= pb : nb >= pb)
+#pragma unroll
+            for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(v[nb][e]));
+        const float s = scale_of(col_max(m), inv);
+        if (g == 0) sm.m.iF[which][own] = inv;
+#pragma unroll
+        for (int nb = 0; nb < 2; nb++)
+          if (lower ? nb <= pb : nb >= pb) {
+            h8 hi, lo;
+            split8<2>(v[nb], s, hi, lo);
+            char* const dst = sm.m.fr + 2 * (6 * which + (lower ? tri_frag(pt, nb) : up_frag(pt, nb))) * kFrag + lane * 16;
+            *(h8*)dst = hi;
+            *(h8*)(dst + kFrag) = lo;
+          }
+      };
+      if (down) {
+        const float be_own = sm.be[own], m = mid(true), pre = sm.gate[3][own];
+        float rx = 0.0f;
+#pragma unroll
+        for (int nb = 0; nb < 2; nb++) {
+          if (nb > pb) continue;
+          float c = 1.0f;
+#pragma unroll
+          for (int e = 7; e >= 0; e--) {
+            const int s = 32 * nb + 8 * g + e;
+            float l;
+            bool on = true, strict = true;  // s <= t, s < t
+            if (nb < pb) {
+              l = pre * sm.gate[4][s];
+            } else {
+              on = 8 * g + e <= po;
+              strict = 8 * g + e < po;
+              l = g < og ? m * sm.gate[2][s] : c;
+              if (e <= oi) c *= ga[e];
+            }
+            const float p = on ? pd[nb][e] : 0.0f, y = strict ? xd[nb][e] : 0.0f, ik = sm.isk[s];
+            l = on ? l : 0.0f;
+            const float by = be_own * y;
+            sm.m.xT[s][own] = fmaf(p, qk[nb][e], -by * kk[nb][e]);
+            rx = fmaf(y, l * kk[nb][e], rx);
+            pd[nb][e] = p * l * ik;
+            xd[nb][e] = -by * l * ik;
+          }
+        }
+        rx = sum_rows(rx);
+        if (g == 0) sm.rowx[own] = rx;
+        put(pd, 0, true);
+        put(xd, 1, true);
+      }
+      if (up) {
+        const float m = mid(false), suf = sm.gate[4][own];
+#pragma unroll
+        for (int nb = 0; nb < 2; nb++) {
+          if (nb < pb) continue;
+          float c = 1.0f;
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const int t = 32 * nb + 8 * g + e;
+            float l;
+            bool on = true, strict = true;  // t >= s, t > s
+            if (nb > pb) {
+              l = suf * sm.gate[3][t];
+            } else {
+              on = 8 * g + e >= po;
+              strict = 8 * g + e > po;
+              if (e > oi) c *= ga[e];
+              l = g > og ? m * sm.gate[1][t] : c;
+            }
+            l = on ? l : 0.0f;
+            const float p = on ? pu[nb][e] : 0.0f, y = strict ? xu[nb][e] : 0.0f;
+            pu[nb][e] = p * l * sm.isq[t];
+            xu[nb][e] = -sm.be[t] * y * l * sm.isk[t];
+          }
+        }
+        put(pu, 2, false);
+        put(xu, 3, false);
+      }
+      if (w == 0) {
         float zq = 0.0f, zk = 0.0f, yk = 0.0f;
 #pragma unroll
-        for (int v = 0; v < NW; v++) zq += sm.dot[0][v][tid], zk += sm.dot[1][v][tid], yk += sm.dot[2][v][tid];
-        sm.z[tid] = fmaf(-sm.be[tid], zk, zq);
-        sm.y[tid] = yk;
-        sm.yv[tid] = fmaf(-tab[kTabG + tid], zk, sm.yv[tid]);
+        for (int v = 0; v < NW; v++) zq += sm.dot[0][v][lane], zk += sm.dot[1][v][lane], yk += sm.dot[2][v][lane];
+        sm.z[lane] = fmaf(-sm.be[lane], zk, zq);
+        sm.y[lane] = yk;
+        sm.yv[lane] = fmaf(-sm.gate[5][lane], zk, sm.yv[lane]);
       }
     }
     __syncthreads();
+    fresh();
+    // dQ += N K, dK += (Zd + Zu) K + N^T Q
     {
-      float rx[4] = {};
+      f4 n[4], d[4], t[4], u[4];
 #pragma unroll
-      for (int n = 0; n < NC; n++) {
-        const int c = c0 + step * n, s = 16 * c + c16;
-        const float ik = tab[kTabIK + s];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int t = 16 * rt + 4 * g + i;
-          if (c > rt) {
-            sm.m.N[t][s] = 0.0f;
-            sm.m.Nt[s][t] = 0.0f;
-            continue;
-          }
-          float nv = 0.0f, zv = 0.0f, x = 0.0f;
-          if (s <= t) {
-            const float l = sm.m.L[t][s], p = dp[n][i] * (sm.isO[t] * sm.isW[s]);
-            nv = p * l;
-            x = p * qk[n][i];
-            if (s < t) {
-              const float y = dx[n][i] * (sm.isY[t] * sm.isW[s]), b = sm.be[t] * y;
-              zv = -b * l;
-              x = fmaf(-b, kk[n][i], x);
-              rx[i] = fmaf(y, l * kk[n][i], rx[i]);
-            }
-          }
-          sm.m.N[t][s] = nv * ik;
-          sm.m.Nt[s][t] = nv * tab[kTabIQ + t];
-          if (s <= t) {
-            sm.m.Z[t][s] = zv * ik;
-            sm.m.Z[s][t] = zv * tab[kTabIK + t];
-          }
-          sm.m.xT[s][t] = x;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float v = sum16(rx[i]);
-        if (c16 == 0) sm.rowx[NW == 8 ? w & 1 : 0][16 * rt + 4 * g + i] = v;
-      }
-    }
-    __syncthreads();
-    // row scales of N, N^T and Z
-    {
-      constexpr int E = 64 / TPR;
-      const int part = tid % TPR;
-      float m[3] = {};
-#pragma unroll
-      for (int i = 0; i < E; i++) {
-        m[0] = fmaxf(m[0], fabsf(sm.m.N[row][part * E + i]));
-        m[1] = fmaxf(m[1], fabsf(sm.m.Nt[row][part * E + i]));
-        m[2] = fmaxf(m[2], fabsf(sm.m.Z[row][part * E + i]));
-      }
-#pragma unroll
-      for (int v = 0; v < 3; v++) {
-#pragma unroll
-        for (int o = 1; o < TPR; o <<= 1) m[v] = fmaxf(m[v], __shfl_xor(m[v], o));
-        if (part == 0) {
-          float inv;
-          sm.sN[v][row] = scale_of(m[v], inv);
-          sm.iN[v][row] = inv;
-        }
-      }
-    }
-    __syncthreads();
-    // fragments: N row tile rt, k-steps ks <= rt / 2; N^T ks >= rt / 2; Z all
-    for (int f = w; f < 20; f += NW) {
-      const int v = f < 6 ? 0 : f < 12 ? 1 : 2, e = f - 6 * v;
-      const int r = v == 0 ? (e < 2 ? e : 2 + ((e - 2) >> 1)) : v == 1 ? (e < 4 ? e >> 1 : e - 2) : e >> 1;
-      const int ks = v == 0 ? (e < 2 ? 0 : (e - 2) & 1) : v == 1 ? (e < 4 ? e & 1 : 1) : e & 1;
-      const float* src = v == 0 ? &sm.m.N[16 * r + c16][32 * ks + 8 * g]
-                                : v == 1 ? &sm.m.Nt[16 * r + c16][32 * ks + 8 * g] : &sm.m.Z[16 * r + c16][32 * ks + 8 * g];
-      const f4 x0 = *(const f4*)src, x1 = *(const f4*)(src + 4);
-      const float x[8] = {x0[0], x0[1], x0[2], x0[3], x1[0], x1[1], x1[2], x1[3]};
-      h8 hi, lo;
-      split8<2>(x, sm.sN[v][16 * r + c16], hi, lo);
-      *(h8*)(sm.fr + 2 * f * kFrag + lane * 16) = hi;
-      *(h8*)(sm.fr + (2 * f + 1) * kFrag + lane * 16) = lo;
-    }
-    // gates: dalpha_r = sum over t >= r of L[t,r] F_r[t] with F_r[t] = sum over s < r of x[t,s] L[r-1,s]
-    // (the state before the chunk as s = -1, the state behind it as one more t).  Lane t; a wave takes
-    // 64 / NW gates: F at its first by a sum, then F_{r+1} = a_r F_r + x[t,r].
-    {
-      constexpr int RW = 64 / NW;
-      const int r0 = RW * w;
-      float F = sm.z[lane], C = 0.0f;
-#pragma unroll
-      for (int v = 0; v < NW; v++) C += sm.corner[v];
-      if (w) {
-        const float* const lr = sm.m.L[r0 - 1];
-        const float G = sm.al[0] * lr[0];
-        const float y = lane < r0 ? sm.y[lane] * lr[lane] : 0.0f;
-        C = fmaf(C, G, sum_rows(sum16(y)));
-        float f0 = F * G, f1 = 0.0f;
-#pragma unroll 8
-        for (int s = 0; s < r0; s += 2) {
-          f0 = fmaf(lr[s], sm.m.xT[s][lane], f0);
-          f1 = fmaf(lr[s + 1], sm.m.xT[s + 1][lane], f1);
-        }
-        F = f0 + f1;
-      }
-#pragma unroll
-      for (int i = 0; i < RW; i++) {
-        const int r = r0 + i;
-        const float v = sum_rows(sum16(lane >= r ? sm.m.L[lane][r] * F : 0.0f));
-        if (lane == 0) sm.da[r] = fmaf(sm.m.L[63][r], C, v);
-        F = fmaf(sm.al[r], F, sm.m.xT[r][lane]);
-        C = fmaf(sm.al[r], C, sm.y[r]);
-      }
-    }
-    __syncthreads();
-    {
-      f4 n[4] = {zero, zero, zero, zero}, t[4] = {zero, zero, zero, zero}, z[4] = {zero, zero, zero, zero};
-      auto fr = [&](int f, int p) { return *(const h8*)(sm.fr + (2 * f + p) * kFrag + lane * 16); };
+      for (int r = 0; r < 4; r++) n[r] = d[r] = t[r] = u[r] = zero;
+      auto fr = [&](int which, int f, int p) { return *(const h8*)(sm.m.fr + (2 * (6 * which + f) + p) * kFrag + lane * 16); };
 #pragma unroll
       for (int ks = 0; ks < 2; ks++) {
-        const h8 k = *(const h8*)(key + Y::offKT + (2 * w + ks) * kFrag + lane * 16);
-        const h8 q = *(const h8*)(key + Y::offQ + (2 * w + ks) * kFrag + lane * 16);
-        h8 kl, ql;
-        if constexpr (NPI == 2) {
-          kl = *(const h8*)(key + Y::offKT + (Y::NF + 2 * w + ks) * kFrag + lane * 16);
-          ql = *(const h8*)(key + Y::offQ + (Y::NF + 2 * w + ks) * kFrag + lane * 16);
+        h8 k[NPI], q[NPI];
+#pragma unroll
+        for (int p = 0; p < NPI; p++) {
+          k[p] = *(const h8*)(key + Y::offKT + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
+          q[p] = *(const h8*)(key + Y::offQ + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
         }
 #pragma unroll
         for (int r = 0; r < 4; r++) {
           if (ks <= r >> 1) {
-            const h8 a = fr(tri_frag(r, ks), 0);
-            n[r] = mfma(fr(tri_frag(r, ks), 1), k, mfma(a, k, n[r]));
-            if constexpr (NPI == 2) n[r] = mfma(a, kl, n[r]);
+            const int f = tri_frag(r, ks);
+            const h8 a = fr(0, f, 0), b = fr(1, f, 0);
+            n[r] = mfma(fr(0, f, 1), k[0], mfma(a, k[0], n[r]));
+            d[r] = mfma(fr(1, f, 1), k[0], mfma(b, k[0], d[r]));
+            if constexpr (NPI == 2) {
+              n[r] = mfma(a, k[NPI - 1], n[r]);
+              d[r] = mfma(b, k[NPI - 1], d[r]);
+            }
           }
           if (ks >= r >> 1) {
-            const h8 a = fr(6 + up_frag(r, ks), 0);
-            t[r] = mfma(fr(6 + up_frag(r, ks), 1), q, mfma(a, q, t[r]));
-            if constexpr (NPI == 2) t[r] = mfma(a, ql, t[r]);
+            const int f = up_frag(r, ks);
+            const h8 a = fr(2, f, 0), b = fr(3, f, 0);
+            t[r] = mfma(fr(2, f, 1), q[0], mfma(a, q[0], t[r]));
+            u[r] = mfma(fr(3, f, 1), k[0], mfma(b, k[0], u[r]));
+            if constexpr (NPI == 2) {
+              t[r] = mfma(a, q[NPI - 1], t[r]);
+              u[r] = mfma(b, k[NPI - 1], u[r]);
+            }
           }
-          const h8 a = fr(12 + 2 * r + ks, 0);
-          z[r] = mfma(fr(12 + 2 * r + ks, 1), k, mfma(a, k, z[r]));
-          if constexpr (NPI == 2) z[r] = mfma(a, kl, z[r]);
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; r++)
+      for (int r = 0; r < 4; r++) {
+        const int t0 = 16 * r + 4 * g;
+        const f4 i0 = *(const f4*)&sm.m.iF[0][t0], i1 = *(const f4*)&sm.m.iF[1][t0];
+        const f4 i2 = *(const f4*)&sm.m.iF[2][t0], i3 = *(const f4*)&sm.m.iF[3][t0];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const int tt = 16 * r + 4 * g + i;
-          dQ[r][i] = fmaf(sm.iN[0][tt], n[r][i], dQ[r][i]);
-          dK[r][i] = fmaf(sm.iN[1][tt], t[r][i], fmaf(sm.iN[2][tt], z[r][i], dK[r][i]));
+          dQ[r][i] = fmaf(i0[i], n[r][i], dQ[r][i]);
+          dK[r][i] = fmaf(i1[i], d[r][i], fmaf(i3[i], u[r][i], fmaf(i2[i], t[r][i], dK[r][i])));
         }
+        settle(dQ[r]);
+        settle(dK[r]);
+      }
     }
+    fresh();
+    // gates: dalpha_r = sum over t >= r of L[t,r] F_r[t] with F_r[t] = sum over s < r of x[t,s] L[r-1,s]
+    // (the state before the chunk as s = -1, the state behind it as one more t).  Lane t; a wave takes groups
+    // of 8 gates: F at a group's first by a sum, then F_{r+1} = a_r F_r + x[t,r].
+    {
+      const int tg = lane >> 3;
+      float corner = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NW; v++) corner += sm.corner[v];
+      const float zl = sm.z[lane], yl = sm.y[lane], p8 = sm.gate[1][lane], s8 = sm.gate[2][lane];
+#pragma unroll
+      for (int q = 0; q < 8 / NW; q++) {
+        const int n = (8 / NW) * w + q, r0 = 8 * n;
+        float v = lane < r0 ? s8 : 0.0f, u = tg > n ? p8 : 0.0f;  // L[r0 - 1, s] and L[t, r0 + 7]
+#pragma unroll
+        for (int m = 1; m < 7; m++) {
+          const float b = sm.gate[1][8 * m + 7];
+          if (m > tg && m < n) v *= b;
+          if (m > n && m < tg) u *= b;
+        }
+        const float G = n ? sm.gate[5][n ? r0 - 1 : 0] : 1.0f;
+        float C = fmaf(corner, G, sum_rows(sum16(lane < r0 ? yl * v : 0.0f)));
+        float f0 = zl * G, f1 = 0.0f;
+#pragma unroll 4
+        for (int s = 0; s < r0; s += 2) {
+          f0 = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), s)), sm.m.xT[s][lane], f0);
+          f1 = fmaf(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), s + 1)), sm.m.xT[s + 1][lane], f1);
+        }
+        float F = f0 + f1;
+        float l[8], c = 1.0f;  // L[lane, r0 + e]
+#pragma unroll
+        for (int e = 7; e >= 0; e--) {
+          const bool in = tg == n && e <= (lane & 7);
+          l[e] = tg > n ? u * sm.gate[2][r0 + e] : in ? c : 0.0f;
+          if (in) c *= sm.gate[0][r0 + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const int r = r0 + e;
+          const float a = sm.gate[0][r];
+          const float d = sum_rows(sum16(lane >= r ? l[e] * F : 0.0f));
+          if (lane == 0) sm.da[r] = fmaf(sm.gate[6][r], C, d);
+          F = fmaf(a, F, sm.m.xT[r][lane]);
+          C = fmaf(a, C, sm.y[r]);
+        }
+      }
+    }
+    __syncthreads();
     if (tid < at.len) {
       const long long th = (at.t0 + (long long)tid) * A.H + h;
       B.dalpha[th] = sm.da[tid];
-      B.dbeta[th] = sm.yv[tid] - (sm.rowx[0][tid] + (NW == 8 ? sm.rowx[1][tid] : 0.0f));
+      B.dbeta[th] = sm.yv[tid] - sm.rowx[tid];
     }
   }
   // dQ and dK to rows through LDS
+  row = tid / TPR;
 #pragma unroll
   for (int which = 0; which < 2; which++) {
     __syncthreads();
