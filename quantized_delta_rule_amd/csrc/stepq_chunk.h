@@ -178,21 +178,17 @@ __device__ __forceinline__ void ahead() { __builtin_amdgcn_sched_barrier(0); }
 // column.  Through a buffer descriptor that ends behind the chunk's last token: rows behind it read as
 // zero and are not written, without a branch or a comparison, and nothing is converted before it is used,
 // so all loads are in flight at once.
-// PLAIN: row 16 rt + 4 g + i instead.
-template <int DT, bool PLAIN = false>
+template <int DT>
 struct Rows {
   static constexpr int es = DT == kF32 ? 4 : 2;
-  unsigned first;  // byte offset of row 8 g (4 g)
+  unsigned first;  // byte offset of row 8 g
   int step;        // bytes from row to row
-  __device__ Rows(long long stride, int col, int g)
-      : first((unsigned)(((PLAIN ? 4 : 8) * g * (int)stride + col) * es)), step((int)stride * es) {}
+  __device__ Rows(long long stride, int col, int g) : first((unsigned)((8 * g * (int)stride + col) * es)), step((int)stride * es) {}
   __device__ static __amdgpu_buffer_rsrc_t at(const void* p, long long row, long long stride, int head_col, int D, int len) {
     return __builtin_amdgcn_make_buffer_rsrc((char*)p + (row * stride + head_col) * es, 0,
                                              (int)((unsigned)(len - 1) * (unsigned)stride * es + D * es), 0x00020000);
   }
-  __device__ unsigned off(int rt, int i) const {
-    return first + (unsigned)((PLAIN ? 16 * rt + i : 32 * (rt >> 1) + 4 * (rt & 1) + i) * step);
-  }
+  __device__ unsigned off(int rt, int i) const { return first + (unsigned)((32 * (rt >> 1) + 4 * (rt & 1) + i) * step); }
   __device__ void load(__amdgpu_buffer_rsrc_t r, unsigned (*x)[4]) const {
 #pragma unroll
     for (int rt = 0; rt < 4; rt++)

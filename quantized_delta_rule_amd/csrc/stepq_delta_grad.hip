@@ -275,8 +275,8 @@ template <int D, int DT>
 struct GradSmem {
   static constexpr int NPI = kInPlanes<DT>, NW = D / 16;
   union {
-    struct {
-      _Float16 O[NPI][64][D + 8], Y[2][64][D + 8], W[2][64][D + 8];
+    struct {  // fragments: row tiles in accumulator order, D / 32 steps each
+      char O[NPI][4 * (D / 32) * kFrag], Y[2][4 * (D / 32) * kFrag], W[2][4 * (D / 32) * kFrag];
     } in;
     struct {
       char fr[24 * 2 * kFrag];  // fragments of N, Zd (lower, 6 each), N^T, Zu (upper)
@@ -290,45 +290,46 @@ struct GradSmem {
   float be[64], yv[64], rowx[64], dot[3][NW][64], corner[NW], z[64], y[64], da[64];
 };
 
-// Rows of a 64-row operand as planes, TPR threads a row; zero where not `live`.  dot: adds the row's
-// product with a row of v (the strengths' gradient).
-template <int D, int DT, int ET, int NP, int TPR>
-__device__ __forceinline__ void rows_in(int tid, const void* src, long long at, bool live, _Float16 (*dst)[64][D + 8],
-                                        float* is, const void* vsrc, long long vat, float* dot) {
-  constexpr int E = D / TPR;
-  const int row = tid / TPR, part = tid % TPR;
-  float x[E], m = 0.0f, p = 0.0f;
+// Row tile rt of a 64-row operand as fragments; zero where not `live` (the lane's row, at element `at`).
+// dot: also the row's product with a row of v (the strengths' gradient).
+template <int D, int DT, int ET, int NP>
+__device__ __forceinline__ void rows_in(const void* src, long long at, bool live, int rt, int lane, int row,
+                                        char (*dst)[4 * (D / 32) * kFrag], float* is, const void* vsrc, long long vat,
+                                        float* dot) {
+  constexpr int KS = D / 32;
+  const int g = lane >> 4;
+  float x[KS][8], m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E; i += 8) load8<ET>(src, at + part * E + i, x + i);
+  for (int ks = 0; ks < KS; ks++) load8<ET>(src, at + 32 * ks + 8 * g, x[ks]);
   if (dot) {
-    float v[E];
+    float p = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; i += 8) load8<DT>(vsrc, vat + part * E + i, v + i);
+    for (int ks = 0; ks < KS; ks++) {
+      float v[8];
+      load8<DT>(vsrc, vat + 32 * ks + 8 * g, v);
 #pragma unroll
-    for (int i = 0; i < E; i++) p = fmaf(x[i], v[i], p);
+      for (int e = 0; e < 8; e++) p = fmaf(x[ks][e], v[e], p);
+    }
+    p = sum_rows(p);
+    if (g == 0) dot[row] = p;
   }
 #pragma unroll
-  for (int i = 0; i < E; i++) {
-    x[i] = live ? x[i] : 0.0f;
-    m = fmaxf(m, fabsf(x[i]));
-  }
+  for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-  for (int o = 1; o < TPR; o <<= 1) {
-    m = fmaxf(m, __shfl_xor(m, o));
-    if (dot) p += __shfl_xor(p, o);
-  }
+    for (int e = 0; e < 8; e++) {
+      x[ks][e] = live ? x[ks][e] : 0.0f;
+      m = fmaxf(m, fabsf(x[ks][e]));
+    }
   float inv;
-  const float s = scale_of(m, inv);
-  if (part == 0) {
-    is[row] = inv;
-    if (dot) dot[row] = p;
-  }
+  const float s = scale_of(col_max(m), inv);
+  if (g == 0) is[row] = inv;
 #pragma unroll
-  for (int i = 0; i < E; i += 8) {
+  for (int ks = 0; ks < KS; ks++) {
     h8 hi, lo;
-    split8<NP>(x + i, s, hi, lo);
-    *(h8*)&dst[0][row][part * E + i] = hi;
-    if constexpr (NP == 2) *(h8*)&dst[1][row][part * E + i] = lo;
+    split8<NP>(x[ks], s, hi, lo);
+    char* const o = &dst[0][(rt * KS + ks) * kFrag + lane * 16];
+    *(h8*)o = hi;
+    if constexpr (NP == 2) *(h8*)(o + 4 * KS * kFrag) = lo;
   }
 }
 
@@ -355,8 +356,8 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   // pairs: row tile pt, own token; down: own is the later token
   const int pt = w & 3, pb = pt >> 1;
   const bool down = NW == 4 || w < 4, up = NW == 4 || w >= 4;
-  // this lane's column of Q and K, rows 16 rt + 4 g + i (zero behind the end)
-  using Col = Rows<DT, true>;
+  // this lane's column of Q and K, rows in accumulator order (zero behind the end)
+  using Col = Rows<DT>;
   const Col qrows(A.qs, dk, g), krows(A.ks, dk, g);
   constexpr int NV = DT == kF32 ? 4 : 2;  // 16-bit types: two rows a register
   unsigned qv[4][NV], kv[4][NV];
@@ -392,13 +393,14 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
     int own;
     // opaque again at every phase: addresses and predicates made from the lane are not kept across phases
     // and heads, where they would spill
+    auto rd = [&](const char* plane, int rt, int ks) { return *(const h8*)(plane + (rt * KS + ks) * kFrag + lane * 16); };
     auto fresh = [&]() {
       asm("" : "+v"(tid));
       lane = tid & 63;
       c16 = lane & 15;
       g = lane >> 4;
       row = tid / TPR;
-      own = 16 * pt + c16;
+      own = 32 * pb + perm_row(c16, pt & 1);
     };
     fresh();
 #pragma unroll
@@ -418,11 +420,15 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
     }
     ahead();
     __syncthreads();  // the last head's fragments have been read
-    const bool live = row < at.len;
-    const long long tok = at.t0 + (long long)min(row, at.len - 1);
-    rows_in<D, DT, DT, NPI, TPR>(tid, B.d_out, tok * A.os + (long long)h * D, live, sm.in.O, sm.isO, nullptr, 0, nullptr);
-    rows_in<D, DT, kF32, 2, TPR>(tid, keep.Y, (jh * 64 + row) * D, live, sm.in.Y, sm.isY, A.v, tok * A.vs + (long long)h * D, sm.yv);
-    rows_in<D, DT, kF32, 2, TPR>(tid, keep.W, (jh * 64 + row) * D, live, sm.in.W, sm.isW, nullptr, 0, nullptr);
+    {  // Y (with V) and then, or in the other four waves, W and dO: row tile pt
+      const bool live = own < at.len;
+      const long long tok = at.t0 + (long long)min(own, at.len - 1);
+      if (down) rows_in<D, DT, kF32, 2>(keep.Y, (jh * 64 + own) * D, live, pt, lane, own, sm.in.Y, sm.isY, A.v, tok * A.vs + (long long)h * D, sm.yv);
+      if (up) {
+        rows_in<D, DT, kF32, 2>(keep.W, (jh * 64 + own) * D, live, pt, lane, own, sm.in.W, sm.isW, nullptr, 0, nullptr);
+        rows_in<D, DT, DT, NPI>(B.d_out, tok * A.os + (long long)h * D, live, pt, lane, own, sm.in.O, sm.isO, nullptr, 0, nullptr);
+      }
+    }
     if (w == NW - 1) {
       float p8 = al, s8 = __shfl_down(al, 1);
       s8 = (lane & 7) < 7 ? s8 : 1.0f;
@@ -474,20 +480,17 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) {
       f4 e1 = zero, e2 = zero;
-      const int r = 16 * rt + c16;
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
-        const int k = 32 * ks + 8 * g;
-        const h8 o = *(const h8*)&sm.in.O[0][r][k];
-        const h8 yh = *(const h8*)&sm.in.Y[0][r][k], yl = *(const h8*)&sm.in.Y[1][r][k];
+        const h8 o = rd(sm.in.O[0], rt, ks), yh = rd(sm.in.Y[0], rt, ks), yl = rd(sm.in.Y[1], rt, ks);
         e1 = mfma(o, Sh[ks], e1);
         e2 = mfma(yh, Sh[ks], e2);
         e1 = mfma(o, Sl[ks], e1);
         e2 = mfma(yh, Sl[ks], e2);
-        if constexpr (NPI == 2) e1 = mfma(*(const h8*)&sm.in.O[1][r][k], Sh[ks], e1);
+        if constexpr (NPI == 2) e1 = mfma(rd(sm.in.O[NPI - 1], rt, ks), Sh[ks], e1);
         e2 = mfma(yl, Sh[ks], e2);
       }
-      const int t0 = 16 * rt + 4 * g;
+      const int t0 = 32 * (rt >> 1) + 8 * g + 4 * (rt & 1);
       const f4 io = *(const f4*)&sm.isO[t0] * iS, iy = *(const f4*)&sm.isY[t0] * iS;
       const f4 G = *(const f4*)&sm.gate[5][t0], be4 = *(const f4*)&sm.be[t0];
 #pragma unroll
@@ -526,14 +529,12 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
 #pragma unroll
       for (int rt = 0; rt < 4; rt++) {
         f4 e3 = zero;
-        const int r = 16 * rt + c16;
 #pragma unroll
         for (int ks = 0; ks < KS; ks++) {
-          const int k = 32 * ks + 8 * g;
-          const h8 wh = *(const h8*)&sm.in.W[0][r][k], wl = *(const h8*)&sm.in.W[1][r][k];
+          const h8 wh = rd(sm.in.W[0], rt, ks), wl = rd(sm.in.W[1], rt, ks);
           e3 = mfma(wl, Gh[ks], mfma(wh, Gl[ks], mfma(wh, Gh[ks], e3)));
         }
-        const int t0 = 16 * rt + 4 * g;
+        const int t0 = 32 * (rt >> 1) + 8 * g + 4 * (rt & 1);
         const f4 iw = *(const f4*)&sm.isW[t0] * iG, lc = *(const f4*)&sm.gate[6][t0];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
@@ -564,11 +565,10 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       h8 o[KS][NPI], yh[KS], yl[KS];
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
-        const int k = 32 * ks + 8 * g;
 #pragma unroll
-        for (int p = 0; p < NPI; p++) o[ks][p] = *(const h8*)&sm.in.O[p][own][k];
-        yh[ks] = *(const h8*)&sm.in.Y[0][own][k];
-        yl[ks] = *(const h8*)&sm.in.Y[1][own][k];
+        for (int p = 0; p < NPI; p++) o[ks][p] = rd(sm.in.O[p], pt, ks);
+        yh[ks] = rd(sm.in.Y[0], pt, ks);
+        yl[ks] = rd(sm.in.Y[1], pt, ks);
       }
       const float io = sm.isO[own], iy = sm.isY[own];
 #pragma unroll
@@ -579,8 +579,7 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
         for (int ks = 0; ks < KS; ks++)
 #pragma unroll
           for (int p = 0; p < 2; p++) {
-            const int r = 32 * nb + perm_row(c16, p), k = 32 * ks + 8 * g;
-            const h8 wh = *(const h8*)&sm.in.W[0][r][k], wl = *(const h8*)&sm.in.W[1][r][k];
+            const h8 wh = rd(sm.in.W[0], 2 * nb + p, ks), wl = rd(sm.in.W[1], 2 * nb + p, ks);
             a[p] = mfma(wl, o[ks][0], mfma(wh, o[ks][0], a[p]));
             if constexpr (NPI == 2) a[p] = mfma(wh, o[ks][NPI - 1], a[p]);
             b[p] = mfma(wl, yh[ks], mfma(wh, yl[ks], mfma(wh, yh[ks], b[p])));
@@ -597,8 +596,8 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       h8 wh[KS], wl[KS];
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
-        wh[ks] = *(const h8*)&sm.in.W[0][own][32 * ks + 8 * g];
-        wl[ks] = *(const h8*)&sm.in.W[1][own][32 * ks + 8 * g];
+        wh[ks] = rd(sm.in.W[0], pt, ks);
+        wl[ks] = rd(sm.in.W[1], pt, ks);
       }
       const float iw = sm.isW[own];
 #pragma unroll
@@ -609,11 +608,10 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
         for (int ks = 0; ks < KS; ks++)
 #pragma unroll
           for (int p = 0; p < 2; p++) {
-            const int r = 32 * nb + perm_row(c16, p), k = 32 * ks + 8 * g;
-            const h8 o = *(const h8*)&sm.in.O[0][r][k];
-            const h8 yh = *(const h8*)&sm.in.Y[0][r][k], yl = *(const h8*)&sm.in.Y[1][r][k];
+            const h8 o = rd(sm.in.O[0], 2 * nb + p, ks);
+            const h8 yh = rd(sm.in.Y[0], 2 * nb + p, ks), yl = rd(sm.in.Y[1], 2 * nb + p, ks);
             a[p] = mfma(o, wl[ks], mfma(o, wh[ks], a[p]));
-            if constexpr (NPI == 2) a[p] = mfma(*(const h8*)&sm.in.O[NPI - 1][r][k], wh[ks], a[p]);
+            if constexpr (NPI == 2) a[p] = mfma(rd(sm.in.O[NPI - 1], 2 * nb + p, ks), wh[ks], a[p]);
             b[p] = mfma(yl, wh[ks], mfma(yh, wl[ks], mfma(yh, wh[ks], b[p])));
           }
 #pragma unroll
@@ -624,6 +622,15 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
         }
       }
     }
+    h8 fk[2][NPI], fq[2][NPI];  // this wave's rows of K^T and Q^T, for the products after the next barrier
+#pragma unroll
+    for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+      for (int p = 0; p < NPI; p++) {
+        fk[ks][p] = *(const h8*)(key + Y::offKT + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
+        fq[ks][p] = *(const h8*)(key + Y::offQ + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
+      }
+    ahead();
     __syncthreads();  // the planes are free: fragments and pairs in their place
     fresh();
     {
@@ -737,12 +744,7 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       auto fr = [&](int which, int f, int p) { return *(const h8*)(sm.m.fr + (2 * (6 * which + f) + p) * kFrag + lane * 16); };
 #pragma unroll
       for (int ks = 0; ks < 2; ks++) {
-        h8 k[NPI], q[NPI];
-#pragma unroll
-        for (int p = 0; p < NPI; p++) {
-          k[p] = *(const h8*)(key + Y::offKT + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
-          q[p] = *(const h8*)(key + Y::offQ + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
-        }
+        const h8 *k = fk[ks], *q = fq[ks];
 #pragma unroll
         for (int r = 0; r < 4; r++) {
           if (ks <= r >> 1) {
@@ -769,7 +771,7 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       }
 #pragma unroll
       for (int r = 0; r < 4; r++) {
-        const int t0 = 16 * r + 4 * g;
+        const int t0 = 32 * (r >> 1) + 8 * g + 4 * (r & 1);
         const f4 i0 = *(const f4*)&sm.m.iF[0][t0], i1 = *(const f4*)&sm.m.iF[1][t0];
         const f4 i2 = *(const f4*)&sm.m.iF[2][t0], i3 = *(const f4*)&sm.m.iF[3][t0];
 #pragma unroll
@@ -843,7 +845,7 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
 #pragma unroll
     for (int r = 0; r < 4; r++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) sm.out[16 * r + 4 * g + i][dk] = which ? dK[r][i] : dQ[r][i];
+      for (int i = 0; i < 4; i++) sm.out[32 * (r >> 1) + 8 * g + 4 * (r & 1) + i][dk] = which ? dK[r][i] : dQ[r][i];
     __syncthreads();
     constexpr int E = D / TPR;
     if (row < at.len) {
