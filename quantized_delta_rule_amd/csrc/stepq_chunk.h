@@ -161,14 +161,14 @@ __device__ __forceinline__ void copy_to_lds(const char* src, unsigned at, unsign
 __device__ __forceinline__ unsigned lds_offset(const void* p) {
   return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(__attribute__((address_space(3))) const char*)p);
 }
-// `bytes` (a multiple of 1 KiB) from src to LDS offset `at`, the pieces over NW waves.
+// Bytes [from, to) (multiples of 1 KiB) of src to LDS offset `at` + from, the pieces over NW waves.
 template <int NW>
-__device__ __forceinline__ void copy_block(const char* src, unsigned at, int bytes, int w, unsigned lane16) {
-  src += w * kFrag;
-  at += w * kFrag;
+__device__ __forceinline__ void copy_block(const char* src, unsigned at, int from, int to, int w, unsigned lane16) {
+  src += from + w * kFrag;
+  at += from + w * kFrag;
 #pragma unroll
-  for (int i = 0; i < bytes; i += NW * kFrag)
-    if (i + NW * kFrag <= bytes || i + w * kFrag < bytes) copy_to_lds(src + i, at + i, lane16);
+  for (int i = 0; i < to - from; i += NW * kFrag)
+    if (i + NW * kFrag <= to - from || i + w * kFrag < to - from) copy_to_lds(src + i, at + i, lane16);
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // Keeps the LDS reads above it above the arithmetic below it: fragments are read one product ahead.
@@ -179,15 +179,22 @@ __device__ __forceinline__ void ahead() { __builtin_amdgcn_sched_barrier(0); }
 // zero and are not written, without a branch or a comparison, and nothing is converted before it is used,
 // so all loads are in flight at once.
 template <int DT>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p, long long row, long long stride, int head_col, int D, int len) {
+  constexpr int es = DT == kF32 ? 4 : 2;
+  return __builtin_amdgcn_make_buffer_rsrc((char*)p + (row * stride + head_col) * es, 0,
+                                           (int)((unsigned)(len - 1) * (unsigned)stride * es + D * es), 0x00020000);
+}
+template <int DT>
+__device__ __forceinline__ float raw_value(unsigned x) {
+  if constexpr (DT == kF32) return __uint_as_float(x);
+  else return e_f<DT>((unsigned short)x);
+}
+template <int DT>
 struct Rows {
   static constexpr int es = DT == kF32 ? 4 : 2;
   unsigned first;  // byte offset of row 8 g
   int step;        // bytes from row to row
   __device__ Rows(long long stride, int col, int g) : first((unsigned)((8 * g * (int)stride + col) * es)), step((int)stride * es) {}
-  __device__ static __amdgpu_buffer_rsrc_t at(const void* p, long long row, long long stride, int head_col, int D, int len) {
-    return __builtin_amdgcn_make_buffer_rsrc((char*)p + (row * stride + head_col) * es, 0,
-                                             (int)((unsigned)(len - 1) * (unsigned)stride * es + D * es), 0x00020000);
-  }
   __device__ unsigned off(int rt, int i) const { return first + (unsigned)((32 * (rt >> 1) + 4 * (rt & 1) + i) * step); }
   __device__ void load(__amdgpu_buffer_rsrc_t r, unsigned (*x)[4]) const {
 #pragma unroll
@@ -198,13 +205,77 @@ struct Rows {
         else x[rt][i] = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, off(rt, i), 0, 0);
       }
   }
-  __device__ static float value(unsigned x) {
-    if constexpr (DT == kF32) return __uint_as_float(x);
-    else return e_f<DT>((unsigned short)x);
+};
+
+// The same for a wave's 16 neighbouring columns, 16 bytes a lane: memory instructions that move 2 bytes a
+// lane keep the address unit busy for as long as ones that move 16 (16 loads of V and 16 stores of O a chunk
+// took 3,000 of the chunk pass's 11,600 cycles).  Rows and lanes change places through a piece of LDS of
+// the wave's own, a pass of 32 rows (16-bit types) or one 16-row tile (binary32) at a time; pitches keep the
+// four lane groups on different banks.
+template <int DT>
+struct Slice {
+  static constexpr bool F = DT == kF32;
+  static constexpr int es = F ? 4 : 2, NL = F ? 4 : 2, lr = F ? 4 : 2;  // passes of 64 rows, lanes a row
+  static constexpr int pitch = F ? 80 : 40, bytes = 1280, TP = F ? 1 : 2;  // tiles a pass
+  typedef unsigned u4 __attribute__((ext_vector_type(4)));
+  typedef unsigned u2 __attribute__((ext_vector_type(2)));
+  unsigned first;   // byte offset of the lane's place in a pass
+  int row;          // bytes of a row
+  char *put, *get;  // the lane's places in the piece: 16 bytes of a row; its column in its first row
+  // col0: the wave's first column
+  __device__ Slice(char* piece, long long stride, int col0, int lane)
+      : first((unsigned)(((F ? perm_row(lane / lr, 0) : lane / lr) * (int)stride + col0) * es + (lane % lr) * 16)),
+        row((int)stride * es),
+        put(piece + (lane / lr) * pitch + (lane % lr) * 16),
+        get(piece + (F ? 4 : 8) * (lane >> 4) * pitch + (lane & 15) * es) {}
+  __device__ unsigned off(int n) const { return first + (unsigned)((F ? 32 * (n >> 1) + 4 * (n & 1) : 32 * n) * row); }
+  __device__ void load(__amdgpu_buffer_rsrc_t r, u4* x) const {
+#pragma unroll
+    for (int n = 0; n < NL; n++) x[n] = __builtin_amdgcn_raw_buffer_load_b128(r, off(n), 0, 0);
   }
-  __device__ void store(__amdgpu_buffer_rsrc_t r, int rt, int i, float x) const {
-    if constexpr (DT == kF32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off(rt, i), 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b16(f_e<DT>(x), r, off(rt, i), 0, 0);
+  __device__ void to_acc(const u4* x, f4* y) const {
+#pragma unroll
+    for (int n = 0; n < NL; n++) {
+      *(u2*)put = u2{x[n][0], x[n][1]};
+      *(u2*)(put + 8) = u2{x[n][2], x[n][3]};
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int p = 0; p < TP; p++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          if constexpr (F) y[n][i] = *(const float*)(get + i * pitch);
+          else y[TP * n + p][i] = e_f<DT>(*(const unsigned short*)(get + (4 * p + i) * pitch));
+        }
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  // a pass: TP tiles into the piece, then 16 bytes a lane
+  __device__ u4 gather(const f4* y) const {
+#pragma unroll
+    for (int p = 0; p < TP; p++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        if constexpr (F) *(float*)(get + i * pitch) = y[p][i];
+        else *(unsigned short*)(get + (4 * p + i) * pitch) = f_e<DT>(y[p][i]);
+      }
+    __builtin_amdgcn_wave_barrier();
+    const u2 a = *(const u2*)put, b = *(const u2*)(put + 8);
+    __builtin_amdgcn_wave_barrier();
+    return u4{a[0], a[1], b[0], b[1]};
+  }
+  __device__ void store(__amdgpu_buffer_rsrc_t r, const f4* y) const {  // 64 rows
+#pragma unroll
+    for (int n = 0; n < NL; n++) __builtin_amdgcn_raw_buffer_store_b128(gather(y + TP * n), r, off(n), 0, 0);
+  }
+  // NT row tiles times s to the rows of a packed binary32 matrix (this slice made with its stride), all rows
+  template <int NT>
+  __device__ void store_all(float* dst, const f4* y, float s) const {
+    static_assert(F);
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      const f4 z = y[n] * s;
+      *(u4*)((char*)dst + off(n)) = gather(&z);
+    }
   }
 };
 

@@ -476,8 +476,11 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   constexpr int keyN = Y::grad ? Y::offQ : Y::key, triN = Y::grad ? Y::offTt : Y::offTab;
   constexpr int offT = keyN, offP = keyN + Y::offP, offTab = keyN + triN;
   constexpr int part = offTab + 2048;
-  constexpr int NBUF = 2 * part <= 160 * 1024 ? 2 : 1;  // binary32 inputs have room for one
-  __shared__ __attribute__((aligned(16))) char buf[NBUF * part];
+  constexpr int NBUF = 2 * part + NW * Slice<DT>::bytes <= 160 * 1024 ? 2 : 1;  // binary32 inputs: one
+  using Tr = Slice<DT>;
+  using TrF = Slice<kF32>;
+  constexpr int trN = Tr::bytes;
+  __shared__ __attribute__((aligned(16))) char buf[NBUF * part + NW * trN];
   const long long tile = blockIdx.x;
   const int s = (int)(tile / A.H), h = (int)(tile - (long long)s * A.H);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -512,28 +515,34 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   const char* const heads = A.ws + key_bytes<Y>(A);
   const int hq = h / A.grp;
   const int nc = (t1 - t0 + kChunk - 1) / kChunk;
-  // chunk c's pieces on their way into LDS, 1 KiB a wave at a time
+  // chunk c's pieces on their way into LDS, 1 KiB a wave at a time: the key block's three parts and the head
+  // block's, so that they can be issued between products
   const unsigned lds0 = lds_offset(buf), lane16 = 16 * lane;
-  auto fetch = [&](int c) {
+  auto fetch = [&](int c, int n) {
     const char* const key = A.ws + ((j0 + c) * A.Hq + hq) * Y::key;
     const char* const head = heads + ((j0 + c) * A.H + h) * Y::head;
     const unsigned at = lds0 + (NBUF == 2 ? (c & 1) * part : 0);
-    copy_block<NW>(key, at, keyN, w, lane16);
-    if constexpr (Y::grad) {
-      copy_block<NW>(head, at + offT, triN, w, lane16);
-      copy_block<NW>(head + Y::offTab, at + offTab, 2048, w, lane16);
+    if (n < 3) {
+      copy_block<NW>(key, at, min(n * Y::offKT, keyN), min((n + 1) * Y::offKT, keyN), w, lane16);
+    } else if constexpr (Y::grad) {
+      copy_block<NW>(head, at + offT, 0, triN, w, lane16);
+      copy_block<NW>(head + Y::offTab, at + offTab, 0, 2048, w, lane16);
     } else {
-      copy_block<NW>(head, at + offT, Y::head, w, lane16);
+      copy_block<NW>(head, at + offT, 0, Y::head, w, lane16);
     }
   };
-  const Rows<DT> vrows(A.vs, col, g), orows(A.os, col, g);
-  unsigned v[4][4];  // V of the next chunk, as it lies in memory
+  char* const piece = buf + NBUF * part + w * trN;
+  const int col0 = 16 * ((int)blockIdx.y * NW + w);
+  const Tr vrows(piece, A.vs, col0, lane), orows(piece, A.os, col0, lane);
+  const TrF krows(piece, D, col0, lane);
+  typename Tr::u4 v[Tr::NL];  // V of the next chunk, as it lies in memory
   auto fetch_v = [&](int c) {
     const int tc = t0 + c * kChunk;
-    vrows.load(vrows.at(A.v, tc, A.vs, h * D, D, t1 - tc < kChunk ? t1 - tc : kChunk), v);
+    vrows.load(rows_at<DT>(A.v, tc, A.vs, h * D, D, t1 - tc < kChunk ? t1 - tc : kChunk), v);
   };
   if (nc) {
-    fetch(0);
+#pragma unroll
+    for (int n = 0; n < 4; n++) fetch(0, n);
     fetch_v(0);
   }
   const f4 zero = {0, 0, 0, 0};
@@ -542,15 +551,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
     wait_copies();
     __syncthreads();  // chunk c is there, and every wave is done with chunk c - 1
-    f4 R[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; rt++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) R[rt][i] = vrows.value(v[rt][i]);
-    if (c + 1 < nc) {
-      if (NBUF == 2) fetch(c + 1);
-      fetch_v(c + 1);
-    }
+    const bool more = NBUF == 2 && c + 1 < nc;
     const float* const tab = (const float*)(lds + offTab);
     auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane16); };
     auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
@@ -566,18 +567,16 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     h8 Sh[NB], Sl[NB], xh[2], xl[2];
     f4 z[2 * NB > 4 ? 2 * NB : 4];
     read(Y::offK);
+    f4 R[4];
+    vrows.to_acc(v, R);
+    if (more) fetch(c + 1, 0);
+    if (c + 1 < nc) fetch_v(c + 1);
     ahead();
     {
       const float m = tiles_max<2 * NB>(St);
       if (__any(m > 0x1p14f || (m < 1.0f && m > 0.0f))) rescale(m);
     }
-    if constexpr (Y::grad) {
-      float* const dst = keepS + ((j0 + c) * A.H + h) * D * D + col;
-#pragma unroll
-      for (int rt = 0; rt < 2 * NB; rt++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) dst[(long long)state_row(rt, i) * D] = St[rt][i] * unit;
-    }
+    if constexpr (Y::grad) krows.template store_all<2 * NB>(keepS + ((j0 + c) * A.H + h) * D * D, St, unit);
     to_planes<NB, 2, true>(St, 1.0f, Sh, Sl);
     auto times_state = [&](bool low) {
 #pragma unroll
@@ -604,6 +603,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
       ft[1][n] = frag(offT, kTri, 1, n);
     }
     ahead();
+    if (more) fetch(c + 1, 1);
     // R = V - G K S0 (gradient: times beta)
     float ix, w1;
 #pragma unroll
@@ -628,15 +628,12 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     ahead();
     if constexpr (!Y::grad) read(Y::offQ);
     else read(Y::offKT);
+    if (more) fetch(c + 1, 2);
     ahead();
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) R[rt] = Y::grad ? z[rt] * rows(kTabT, rt) : z[rt];
     if constexpr (Y::grad) {
-      float* const dst = keepW + ((j0 + c) * A.H + h) * 64 * D + col;
-#pragma unroll
-      for (int rt = 0; rt < 4; rt++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) dst[(long long)state_row(rt, i) * D] = R[rt][i] * w1;
+      krows.template store_all<4>(keepW + ((j0 + c) * A.H + h) * 64 * D, R, w1);
     } else {
       // O = G Q S0 + P W
       const float iw = to_operand<2, NPO>(R, xh, xl) * w1;
@@ -659,14 +656,15 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
       ahead();
       read(Y::offKT);
       ahead();
-      const __amdgpu_buffer_rsrc_t out = orows.at(A.out, tc, A.os, h * D, D, len);
 #pragma unroll
       for (int rt = 0; rt < 4; rt++) {
         const f4 cq = rows(kTabQ, rt), ip = rows(kTabP, rt);
 #pragma unroll
-        for (int i = 0; i < 4; i++) orows.store(out, rt, i, fmaf(cq[i] * unit, y[rt][i], (ip[i] * iw) * z[rt][i]));
+        for (int i = 0; i < 4; i++) y[rt][i] = fmaf(cq[i] * unit, y[rt][i], (ip[i] * iw) * z[rt][i]);
       }
+      orows.store(rows_at<DT>(A.out, tc, A.os, h * D, D, len), y);
     }
+    if (more) fetch(c + 1, 3);
     // S1 = G_C S0 + K^T diag(L[C, .]) W, in the state's units
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) R[rt] *= rows(kTabD, rt);
@@ -700,7 +698,8 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     }
     if (NBUF == 1 && c + 1 < nc) {
       __syncthreads();
-      fetch(c + 1);
+#pragma unroll
+      for (int n = 0; n < 4; n++) fetch(c + 1, n);
     }
   }
   if (!Y::grad && A.S_out) {

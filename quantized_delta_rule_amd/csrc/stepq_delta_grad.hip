@@ -37,9 +37,13 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
   constexpr int keyN = L::offKK, triN = 4 * kTri * kFrag;  // K, K^T, Q^T; T^T, P^T
   constexpr int offTt = keyN, offP = keyN + 2 * kTri * kFrag, offTab = keyN + triN;
   constexpr int part = offTab + 2048;
-  constexpr int NBUF = 2 * part <= 160 * 1024 ? 2 : 1;
+  constexpr int NBUF = 2 * part + NW * Slice<kF32>::bytes <= 160 * 1024 ? 2 : 1;
   const SeqArgs& A = B.f;
-  __shared__ __attribute__((aligned(16))) char buf[NBUF * part];
+  using Tr = Slice<DT>;
+  using TrF = Slice<kF32>;
+  constexpr int trN = TrF::bytes;
+  static_assert(NBUF * part + NW * trN <= 160 * 1024);
+  __shared__ __attribute__((aligned(16))) char buf[NBUF * part + NW * trN];
   const long long tile = blockIdx.x;
   const int s = (int)(tile / A.H), h = (int)(tile - (long long)s * A.H);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -68,33 +72,34 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     if (m > 0.0f) unit = 1.0f;
     rescale(m);
   }
-  auto store_G = [&](float* dst) {
-#pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) dst[(long long)state_row(rt, i) * D] = Gt[rt][i] * unit;
-  };
   const long long j0 = first_slot(A, s);
   const char* const heads = A.ws + key_bytes<L>(A);
   const int hq = h / A.grp;
   const int nc = (t1 - t0 + kChunk - 1) / kChunk;
   const unsigned lds0 = lds_offset(buf), lane16 = 16 * lane;
-  auto fetch = [&](int c) {
+  auto fetch = [&](int c, int n) {
     const char* const key = A.ws + ((j0 + c) * A.Hq + hq) * L::key;
     const char* const head = heads + ((j0 + c) * A.H + h) * L::head;
     const unsigned at = lds0 + (NBUF == 2 ? (c & 1) * part : 0);
-    copy_block<NW>(key, at, keyN, w, lane16);
-    copy_block<NW>(head + L::offTt, at + offTt, triN, w, lane16);
-    copy_block<NW>(head + L::offTab, at + offTab, 2048, w, lane16);
+    if (n < 3) {
+      copy_block<NW>(key, at, n * L::offKT, (n + 1) * L::offKT, w, lane16);
+    } else {
+      copy_block<NW>(head + L::offTt, at + offTt, 0, triN, w, lane16);
+      copy_block<NW>(head + L::offTab, at + offTab, 0, 2048, w, lane16);
+    }
   };
-  const Rows<DT> orows(A.os, col, g), vrows((long long)A.H * D, col, g);
-  unsigned o[4][4];
+  char* const piece = buf + NBUF * part + w * trN;
+  const int col0 = 16 * ((int)blockIdx.y * NW + w);
+  const Tr orows(piece, A.os, col0, lane), vrows(piece, (long long)A.H * D, col0, lane);
+  const TrF krows(piece, D, col0, lane);
+  typename Tr::u4 o[Tr::NL];
   auto fetch_o = [&](int c) {
     const int tc = t0 + c * kChunk;
-    orows.load(orows.at(B.d_out, tc, A.os, h * D, D, t1 - tc < kChunk ? t1 - tc : kChunk), o);
+    orows.load(rows_at<DT>(B.d_out, tc, A.os, h * D, D, t1 - tc < kChunk ? t1 - tc : kChunk), o);
   };
   if (nc) {
-    fetch(nc - 1);
+#pragma unroll
+    for (int n = 0; n < 4; n++) fetch(nc - 1, n);
     fetch_o(nc - 1);
   }
   const f4 zero = {0, 0, 0, 0};
@@ -103,15 +108,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
     wait_copies();
     __syncthreads();
-    f4 dO[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; rt++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) dO[rt][i] = orows.value(o[rt][i]);
-    if (c) {
-      if (NBUF == 2) fetch(c - 1);
-      fetch_o(c - 1);
-    }
+    const bool more = NBUF == 2 && c;
     const float* const tab = (const float*)(lds + offTab);
     auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane16); };
     auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
@@ -132,12 +129,16 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
       }
     };
     read(L::offK);
+    f4 dO[4];
+    orows.to_acc(o, dO);
+    if (more) fetch(c - 1, 0);
+    if (c) fetch_o(c - 1);
     ahead();
     {
       const float m = tiles_max<2 * NB>(Gt);
       if (__any(m > 0x1p14f || (m < 1.0f && m > 0.0f))) rescale(m);
     }
-    store_G(keep.G + ((j0 + c) * A.H + h) * D * D + col);
+    krows.template store_all<2 * NB>(keep.G + ((j0 + c) * A.H + h) * D * D, Gt, unit);
     h8 xh[2], xl[2];
     f4 z[4], y[4];
     {  // z = K dS1
@@ -159,6 +160,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     }
     ahead();
     read_tri(offP);
+    if (more) fetch(c - 1, 1);
     ahead();
     auto tri = [&](int p, const h8* b, bool first) {
 #pragma unroll
@@ -173,6 +175,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     if constexpr (NPI == 2) tri(0, xl, false);
     ahead();
     read_tri(offTt);
+    if (more) fetch(c - 1, 2);
     ahead();
     // dW = P^T dO + D K dS1, then Y = T^T dW
     f4 Y[4];
@@ -190,19 +193,16 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     read(L::offQ);
     ahead();
     {
-      float* const dst = keep.Y + ((j0 + c) * A.H + h) * 64 * D + col;
-      const __amdgpu_buffer_rsrc_t dv = vrows.at(B.dv, tc, (long long)A.H * D, h * D, D, len);
+      f4 dv[4];
 #pragma unroll
       for (int rt = 0; rt < 4; rt++) {
-        const f4 it = rows(kTabTt, rt), be = rows(kTabB, rt);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          Y[rt][i] = y[rt][i] * (it[i] * ix);
-          dst[(long long)state_row(rt, i) * D] = Y[rt][i];
-          vrows.store(dv, rt, i, be[i] * Y[rt][i]);
-        }
+        Y[rt] = y[rt] * (rows(kTabTt, rt) * ix);
+        dv[rt] = rows(kTabB, rt) * Y[rt];
       }
+      krows.template store_all<4>(keep.Y + ((j0 + c) * A.H + h) * 64 * D, Y, 1.0f);
+      vrows.store(rows_at<DT>(B.dv, tc, (long long)A.H * D, h * D, D, len), dv);
     }
+    if (more) fetch(c - 1, 3);
     // dS0 = G_C dS1 + Q^T G dO - K^T G diag(beta) Y, in the gradient's units
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) {
@@ -247,10 +247,11 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     update();
     if (NBUF == 1 && c) {
       __syncthreads();
-      fetch(c - 1);
+#pragma unroll
+      for (int n = 0; n < 4; n++) fetch(c - 1, n);
     }
   }
-  if (B.dS_in) store_G(B.dS_in + so);
+  if (B.dS_in) krows.template store_all<2 * NB>(B.dS_in + ((long long)s * A.H + h) * D * D, Gt, unit);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -357,14 +358,13 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   const int pt = w & 3, pb = pt >> 1;
   const bool down = NW == 4 || w < 4, up = NW == 4 || w >= 4;
   // this lane's column of Q and K, rows in accumulator order (zero behind the end)
-  using Col = Rows<DT>;
-  const Col qrows(A.qs, dk, g), krows(A.ks, dk, g);
+  const Rows<DT> qrows(A.qs, dk, g), krows(A.ks, dk, g);
   constexpr int NV = DT == kF32 ? 4 : 2;  // 16-bit types: two rows a register
   unsigned qv[4][NV], kv[4][NV];
   {
     unsigned q[4][4], k[4][4];
-    qrows.load(qrows.at(A.q, at.t0, A.qs, hq * D, D, at.len), q);
-    krows.load(krows.at(A.k, at.t0, A.ks, hq * D, D, at.len), k);
+    qrows.load(rows_at<DT>(A.q, at.t0, A.qs, hq * D, D, at.len), q);
+    krows.load(rows_at<DT>(A.k, at.t0, A.ks, hq * D, D, at.len), k);
 #pragma unroll
     for (int rt = 0; rt < 4; rt++)
 #pragma unroll
@@ -374,8 +374,8 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       }
   }
   auto column = [&](unsigned (*v)[NV], int rt, int i) {
-    if constexpr (NV == 4) return Col::value(v[rt][i]);
-    else return Col::value(i & 1 ? v[rt][i >> 1] >> 16 : v[rt][i >> 1]);
+    if constexpr (NV == 4) return raw_value<DT>(v[rt][i]);
+    else return raw_value<DT>(i & 1 ? v[rt][i >> 1] >> 16 : v[rt][i >> 1]);
   };
   if (tid < 64) {
     const float* const tab = (const float*)(A.ws + key_bytes<Y>(A) + (j * A.H + hq * A.grp) * Y::head + Y::offTab);
@@ -552,15 +552,6 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
     float pd[2][8], xd[2][8], p1[NW == 4 ? 2 : 1][8], x1[NW == 4 ? 2 : 1][8];
     float(*const pu)[8] = NW == 4 ? p1 : pd;
     float(*const xu)[8] = NW == 4 ? x1 : xd;
-    float kk[2][8], qk[2][8];  // k_t.k_s and q_t.k_s of the down pairs
-    if (down)
-#pragma unroll
-      for (int nb = 0; nb < 2; nb++) {
-        if (nb > pb) continue;
-        load8<kF32>(key + Y::offKK, own * 64 + 32 * nb + 8 * g, kk[nb]);
-#pragma unroll
-        for (int e = 0; e < 8; e++) qk[nb][e] = ((const float*)(key + Y::offQK))[(32 * nb + 8 * g + e) * 64 + own];
-      }
     if (down) {
       h8 o[KS][NPI], yh[KS], yl[KS];
 #pragma unroll
@@ -622,6 +613,16 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
         }
       }
     }
+    ahead();
+    float kk[2][8], qk[2][8];  // k_t.k_s and q_t.k_s of the down pairs
+    if (down)
+#pragma unroll
+      for (int nb = 0; nb < 2; nb++) {
+        if (nb > pb) continue;
+        load8<kF32>(key + Y::offKK, own * 64 + 32 * nb + 8 * g, kk[nb]);
+#pragma unroll
+        for (int e = 0; e < 8; e++) qk[nb][e] = ((const float*)(key + Y::offQK))[(32 * nb + 8 * g + e) * 64 + own];
+      }
     h8 fk[2][NPI], fq[2][NPI];  // this wave's rows of K^T and Q^T, for the products after the next barrier
 #pragma unroll
     for (int ks = 0; ks < 2; ks++)
