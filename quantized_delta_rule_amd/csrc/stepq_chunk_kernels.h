@@ -23,10 +23,16 @@ constexpr int kPitch = 68;  // floats of a row of the 64 x 64 matrices in LDS
 template <int D, int DT, bool QT>
 struct PrepSmem {
   static constexpr int NPI = kInPlanes<DT>;
-  _Float16 K[NPI][64][D + 8], Q[QT ? NPI : 1][QT ? 64 : 1][D + 8];
-  float X[64][kPitch];   // A, then T but for its lower left quarter
-  float Z[32][36];       // T's lower left quarter
-  float gate[4][5][64];  // a wave's copies: a, pre8, suf8, pre32, suf32
+  union {
+    struct {
+      _Float16 K[NPI][64][D + 8], Q[QT ? NPI : 1][QT ? 64 : 1][D + 8];
+    };
+    struct {
+      float X[64][kPitch];  // A, then T but for its lower left quarter
+      float Z[32][36];      // T's lower left quarter
+    };
+  };
+  float gate[5][64];  // a, pre8, suf8, pre32, suf32; every wave writes the same values for itself
   float isk[64], isq[64], be[64], most[4];
 };
 
@@ -134,7 +140,7 @@ __device__ __forceinline__ float invert_corner(const float (*X)[kPitch], float (
 
 // Y: the workspace's layout (LayF, or LayB: with the gradient's extra pieces).
 template <int D, int DT, class Y>
-__global__ __launch_bounds__(256, DT == kF32 ? 2 : 3) void k_chunk_prep(SeqArgs A) {
+__global__ __launch_bounds__(256, Y::grad ? 3 : 4) void k_chunk_prep(SeqArgs A) {
   constexpr int KS = D / 32, NPI = Y::NPI, NPO = Y::NPO;
   __shared__ PrepSmem<D, DT, Y::grad> sm;
   const long long j = blockIdx.x;
@@ -251,8 +257,9 @@ __global__ __launch_bounds__(256, DT == kF32 ? 2 : 3) void k_chunk_prep(SeqArgs 
     float* const tab = (float*)(head + Y::offTab);
     const float al = al_next, be = be_next;
     if (hh + 1 < A.grp) gates(hh + 1);
+    __syncthreads();  // the last head's gates and T have been read (the first head: K and Q)
     // running products, token = lane
-    float(*const gt)[64] = sm.gate[w];
+    float(*const gt)[64] = sm.gate;
     float p8 = al, s8 = 1.0f;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
@@ -332,7 +339,6 @@ __global__ __launch_bounds__(256, DT == kF32 ? 2 : 3) void k_chunk_prep(SeqArgs 
     };
     in_block(true);
     float pv[2][8];
-    __syncthreads();  // the last head's T has been read
     if (w == 0) sm.be[lane] = be;
 #pragma unroll
     for (int nb = 0; nb < 2; nb++) {
@@ -681,7 +687,8 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
         for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= f;
         unit = to;
       }
-      to_planes<2, 2>(R, w1 / unit, xh, xl);
+      // unit is a power of two: its inverse by the exponent
+      to_planes<2, 2>(R, w1 * __uint_as_float(0x7f000000u - __float_as_uint(unit)), xh, xl);
     }
     const float G = tab[kTabG + 63];
 #pragma unroll

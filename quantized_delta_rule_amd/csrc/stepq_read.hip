@@ -1,9 +1,8 @@
 // stepq_read.hip -- read packed states back (page: "STEPQuant" paper digest, Method 3:
 // X_hat[i,j] = r_i c_j z[i,j], FP16 pivot rows as stored), by slot, as binary32, bfloat16 or binary16.
 //
-// One workgroup per (request, head); wave w takes rows w, w + 4, ...  A row's codes sit at one bit
-// offset in all 64 lane streams, so its width, shift and factor are wave-uniform and a lane reads one
-// or two words.  r c z is formed as r (c z): c z is exact in binary32 (11 + 8 bits), so the value is
+// One workgroup per (request, head), a quarter of the rows a wave.  A row's codes sit at one bit offset in
+// all 64 lane streams, so its width, shift and factor are wave-uniform and a lane reads one or two words.  r c z is formed as r (c z): c z is exact in binary32 (11 + 8 bits), so the value is
 // the exact product rounded once, and once more where the output type is narrower.
 #include "stepq_delta.h"
 #include "stepq_internal.h"
@@ -44,35 +43,65 @@ __global__ __launch_bounds__(256) void k_read(DevPlan P, const uint8_t* pool, in
   const uint8_t* seg = pool + (long long)slot * P.bpr + P.head_off[h];
   const uint32_t* words = (const uint32_t*)seg + lane;
   const int nw = P.words[h];
+  const uint16_t* rb = (const uint16_t*)(seg + P.off_r[h]);
+  const uint16_t* pb = (const uint16_t*)(seg + P.off_piv[h]);
+  const long long out = ((long long)b * P.H + h) * D * D + G * lane;
+  constexpr int R = D / 4;  // rows of a wave, R w ..
+  // the wave's row words and factors, one a lane; a row's are broadcast from there
+  const int mine = R * w + (lane < R ? lane : R - 1);
+  const unsigned meta = (unsigned)P.rowmeta[h * D + mine];
+  auto values = [&](unsigned m, uint32_t lo, uint32_t hi, float r, const float* c, float* x) {
+    const int bits = (m >> 16) & 15;
+    const uint32_t y = __builtin_amdgcn_alignbit(hi, lo, m & 31);
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      x[g] = r * (c[g] * (float)(int)__builtin_amdgcn_sbfe((int)y, g * bits, bits));
+      // keeps the rounding to binary32: the product and a narrowing to binary16 would be fused
+      if constexpr (DT == kF16) asm("" : "+v"(x[g]));
+    }
+  };
   float c[G];
+  unsigned short fac = 0;
   if (nw) {
     const uint16_t* cb = (const uint16_t*)(seg + P.off_c[h]);
 #pragma unroll
     for (int g = 0; g < G; g++) c[g] = h_f(cb[G * lane + g]);
+    fac = rb[mine];
   }
-  const uint16_t* rb = (const uint16_t*)(seg + P.off_r[h]);
-  const uint16_t* pb = (const uint16_t*)(seg + P.off_piv[h]);
-  const long long out = ((long long)b * P.H + h) * D * D + G * lane;
-#pragma unroll 4
-  for (int i = w; i < D; i += 4) {
-    const unsigned m = (unsigned)P.rowmeta[h * D + i];
-    float x[G];
-    if (m & 0x80000000u) {
+  const bool piv = (meta & 0x80000000u) != 0;
+  if (__any(piv)) {  // FP16 pivot rows among them: a row at a time
+    for (int i = 0; i < R; i++) {
+      const unsigned m = __builtin_amdgcn_readlane(meta, i);
+      float x[G];
+      if (m & 0x80000000u) {
 #pragma unroll
-      for (int g = 0; g < G; g++) x[g] = h_f(pb[(m & 0x7fffffffu) * D + G * lane + g]);
-    } else {
-      const int sh = m & 31, wi = (m >> 8) & 255, bits = (m >> 16) & 15;
-      const uint32_t lo = words[wi * 64], hi = (m >> 20) & 1 ? words[(wi + 1) * 64] : 0u;
-      const uint32_t y = __builtin_amdgcn_alignbit(hi, lo, sh);
-      const float r = h_f(rb[i]);
-#pragma unroll
-      for (int g = 0; g < G; g++) {
-        x[g] = r * (c[g] * (float)(int)__builtin_amdgcn_sbfe((int)y, g * bits, bits));
-        // keeps the rounding to binary32: the product and a narrowing to binary16 would be fused
-        if constexpr (DT == kF16) asm("" : "+v"(x[g]));
+        for (int g = 0; g < G; g++) x[g] = h_f(pb[(m & 0x7fffffffu) * D + G * lane + g]);
+      } else {
+        const int wi = (m >> 8) & 255;
+        values(m, words[wi * 64], (m >> 20) & 1 ? words[(wi + 1) * 64] : 0u, h_f(__builtin_amdgcn_readlane(fac, i)), c, x);
       }
+      storen<DT, G>(S, out + (long long)(R * w + i) * D, x);
     }
-    storen<DT, G>(S, out + (long long)i * D, x);
+    return;
+  }
+  // all rows quantized: 8 rows' words in flight at once (a row whose codes end in one word reads it twice)
+#pragma unroll
+  for (int i0 = 0; i0 < R; i0 += 8) {
+    uint32_t lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const unsigned m = __builtin_amdgcn_readlane(meta, i0 + i);
+      const int wi = (m >> 8) & 255;
+      lo[i] = words[wi * 64];
+      hi[i] = words[(wi + ((m >> 20) & 1)) * 64];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const unsigned m = __builtin_amdgcn_readlane(meta, i0 + i);
+      float x[G];
+      values(m, lo[i], hi[i], h_f((unsigned short)__builtin_amdgcn_readlane(fac, i0 + i)), c, x);
+      storen<DT, G>(S, out + (long long)(R * w + i0 + i) * D, x);
+    }
   }
 }
 
