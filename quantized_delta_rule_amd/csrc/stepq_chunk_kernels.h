@@ -473,13 +473,26 @@ __global__ __launch_bounds__(256, Y::grad ? 3 : 4) void k_chunk_prep(SeqArgs A) 
 // accumulator order) and never needs another wave's: all waves of a workgroup read the same fragments,
 // staged in LDS one chunk ahead.  The state is held in units of a power of two per column (S = unit * St,
 // St within binary16's range, checked every chunk), so that it turns into an operand without a product and
-// the update accumulates on it directly.  For the gradient (LayB) nothing is read out: the states before
-// every chunk and W are kept.
-template <int D, int DT, int NW, class Y>
-__global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS, float* keepW) {
+// the update accumulates on it directly.
+//
+// kForward: the whole sequence, read out.  kKeep (gradient, LayB): no readout, the states before every chunk
+// and W are kept.  Where there are few (sequence, head) pairs and many chunks, the chunks of a sequence are
+// cut into segs.P segments (blockIdx.y): the state behind a segment is M S + N, so kSegment runs every
+// segment twice, from the unit matrix without V (M, blockIdx.z = 1) and from zero with V (N);
+// k_chunk_join then walks over the segments, and kReadout runs them all at once from their first states.
+struct Segs {
+  int P;            // segments of a sequence
+  float *MN, *S;    // [2][tiles][P][D][D] (N, then M), [tiles][P][D][D] first states
+};
+enum StateMode { kForward, kKeep, kSegment, kReadout };
+__device__ __forceinline__ int seg_chunks(int nc, int P) { return (nc + P - 1) / P; }
+
+template <int D, int DT, int NW, class Y, int MODE>
+__global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS, float* keepW, Segs segs) {
   constexpr int KS = D / 32, NPI = Y::NPI, NPO = Y::NPO, NB = D / 32;
   // staged: K, K^T (and Q), then T (and P), then the tables
-  constexpr int keyN = Y::grad ? Y::offQ : Y::key, triN = Y::grad ? Y::offTt : Y::offTab;
+  constexpr bool out_on = MODE == kForward || MODE == kReadout, cut = MODE == kSegment || MODE == kReadout;
+  constexpr int keyN = out_on ? Y::key : Y::offQ, triN = out_on ? Y::offTab : Y::grad ? Y::offTt : Y::offP;
   constexpr int offT = keyN, offP = keyN + Y::offP, offTab = keyN + triN;
   constexpr int part = offTab + 2048;
   constexpr int NBUF = 2 * part + NW * Slice<DT>::bytes <= 160 * 1024 ? 2 : 1;  // binary32 inputs: one
@@ -493,17 +506,33 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   const int c16 = lane & 15, g = lane >> 4;
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
-  const int slot = seq_slot(A, s, valid, h == 0 && blockIdx.y == 0 && tid == 0);
+  const int slot = seq_slot(A, s, valid, h == 0 && !cut && tid == 0);
   if (slot < 0) return;
-  if (t0 == t1 && (Y::grad || !A.S_out || A.S_out == A.S_in)) return;
-  const int col = 16 * ((int)blockIdx.y * NW + w) + c16;
+  if (t0 == t1 && MODE == kKeep) return;
+  if (t0 == t1 && MODE == kForward && (!A.S_out || A.S_out == A.S_in)) return;
+  const int col = 16 * w + c16;
   const long long so = ((long long)slot * A.H + h) * D * D + col;
+  const int nc = (t1 - t0 + kChunk - 1) / kChunk;
+  int c_first = 0, c_end = nc;
+  long long seg = 0;
+  if (cut) {
+    const int n = seg_chunks(nc, segs.P);
+    c_first = min((int)blockIdx.y * n, nc);
+    c_end = min(c_first + n, nc);
+    seg = (tile * segs.P + blockIdx.y) * D * D + col;
+  }
+  const bool unit_start = MODE == kSegment && blockIdx.z;
   auto state_row = [&](int rt, int i) { return 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i; };
   f4 St[2 * NB];
 #pragma unroll
   for (int rt = 0; rt < 2 * NB; rt++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) St[rt][i] = A.S_in ? A.S_in[so + (long long)state_row(rt, i) * D] : 0.0f;
+    for (int i = 0; i < 4; i++) {
+      const int r = state_row(rt, i);
+      if (MODE == kSegment) St[rt][i] = unit_start && r == col ? 1.0f : 0.0f;
+      else if (MODE == kReadout) St[rt][i] = segs.S[seg + (long long)r * D];
+      else St[rt][i] = A.S_in ? A.S_in[so + (long long)r * D] : 0.0f;
+    }
   float unit = 0x1p-10f;  // an empty state takes its unit from the first W
   auto rescale = [&](float m) {  // largest magnitude into [2^11, 2^12)
     float inv;
@@ -520,7 +549,6 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   const long long j0 = first_slot(A, s);
   const char* const heads = A.ws + key_bytes<Y>(A);
   const int hq = h / A.grp;
-  const int nc = (t1 - t0 + kChunk - 1) / kChunk;
   // chunk c's pieces on their way into LDS, 1 KiB a wave at a time: the key block's three parts and the head
   // block's, so that they can be issued between products
   const unsigned lds0 = lds_offset(buf), lane16 = 16 * lane;
@@ -530,7 +558,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     const unsigned at = lds0 + (NBUF == 2 ? (c & 1) * part : 0);
     if (n < 3) {
       copy_block<NW>(key, at, min(n * Y::offKT, keyN), min((n + 1) * Y::offKT, keyN), w, lane16);
-    } else if constexpr (Y::grad) {
+    } else if constexpr (!out_on) {
       copy_block<NW>(head, at + offT, 0, triN, w, lane16);
       copy_block<NW>(head + Y::offTab, at + offTab, 0, 2048, w, lane16);
     } else {
@@ -538,26 +566,27 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     }
   };
   char* const piece = buf + NBUF * part + w * trN;
-  const int col0 = 16 * ((int)blockIdx.y * NW + w);
+  const int col0 = 16 * w;
   const Tr vrows(piece, A.vs, col0, lane), orows(piece, A.os, col0, lane);
   const TrF krows(piece, D, col0, lane);
   typename Tr::u4 v[Tr::NL];  // V of the next chunk, as it lies in memory
   auto fetch_v = [&](int c) {
     const int tc = t0 + c * kChunk;
-    vrows.load(rows_at<DT>(A.v, tc, A.vs, h * D, D, t1 - tc < kChunk ? t1 - tc : kChunk), v);
+    // (M's segments: a descriptor without bytes, V = 0)
+    vrows.load(rows_at<DT>(A.v, tc, A.vs, h * D, unit_start ? 0 : D, unit_start ? 1 : min(t1 - tc, kChunk)), v);
   };
-  if (nc) {
+  if (c_first < c_end) {
 #pragma unroll
-    for (int n = 0; n < 4; n++) fetch(0, n);
-    fetch_v(0);
+    for (int n = 0; n < 4; n++) fetch(c_first, n);
+    fetch_v(c_first);
   }
   const f4 zero = {0, 0, 0, 0};
-  for (int c = 0; c < nc; c++) {
+  for (int c = c_first; c < c_end; c++) {
     const char* const lds = buf + (NBUF == 2 ? (c & 1) * part : 0);
     const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
     wait_copies();
     __syncthreads();  // chunk c is there, and every wave is done with chunk c - 1
-    const bool more = NBUF == 2 && c + 1 < nc;
+    const bool more = NBUF == 2 && c + 1 < c_end;
     const float* const tab = (const float*)(lds + offTab);
     auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane16); };
     auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
@@ -576,13 +605,13 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     f4 R[4];
     vrows.to_acc(v, R);
     if (more) fetch(c + 1, 0);
-    if (c + 1 < nc) fetch_v(c + 1);
+    if (c + 1 < c_end) fetch_v(c + 1);
     ahead();
     {
       const float m = tiles_max<2 * NB>(St);
       if (__any(m > 0x1p14f || (m < 1.0f && m > 0.0f))) rescale(m);
     }
-    if constexpr (Y::grad) krows.template store_all<2 * NB>(keepS + ((j0 + c) * A.H + h) * D * D, St, unit);
+    if constexpr (MODE == kKeep) krows.template store_all<2 * NB>(keepS + ((j0 + c) * A.H + h) * D * D, St, unit);
     to_planes<NB, 2, true>(St, 1.0f, Sh, Sl);
     auto times_state = [&](bool low) {
 #pragma unroll
@@ -632,15 +661,15 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     tri(ft, 0, xl, false);
     tri(ft, 1, xh, false);
     ahead();
-    if constexpr (!Y::grad) read(Y::offQ);
+    if constexpr (out_on) read(Y::offQ);
     else read(Y::offKT);
     if (more) fetch(c + 1, 2);
     ahead();
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) R[rt] = Y::grad ? z[rt] * rows(kTabT, rt) : z[rt];
-    if constexpr (Y::grad) {
+    if constexpr (MODE == kKeep) {
       krows.template store_all<4>(keepW + ((j0 + c) * A.H + h) * 64 * D, R, w1);
-    } else {
+    } else if constexpr (out_on) {
       // O = G Q S0 + P W
       const float iw = to_operand<2, NPO>(R, xh, xl) * w1;
       times_state(NPO == 2);
@@ -703,17 +732,77 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
 #pragma unroll
         for (int rt = 0; rt < 2 * NB; rt++) St[rt] = mfma(fl[2 * rt + ks], xh[ks], St[rt]);
     }
-    if (NBUF == 1 && c + 1 < nc) {
+    if (NBUF == 1 && c + 1 < c_end) {
       __syncthreads();
 #pragma unroll
       for (int n = 0; n < 4; n++) fetch(c + 1, n);
     }
   }
-  if (!Y::grad && A.S_out) {
+  float* dst = nullptr;
+  if (MODE == kForward || (MODE == kReadout && c_end == nc && (c_first < nc || (nc == 0 && blockIdx.y == 0))))
+    dst = A.S_out ? A.S_out + so : nullptr;
+  if (MODE == kSegment) dst = segs.MN + (unit_start ? (long long)gridDim.x * segs.P * D * D : 0LL) + seg;
+  if (dst) {
 #pragma unroll
     for (int rt = 0; rt < 2 * NB; rt++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) A.S_out[so + (long long)state_row(rt, i) * D] = St[rt][i] * unit;
+      for (int i = 0; i < 4; i++) dst[(long long)state_row(rt, i) * D] = St[rt][i] * unit;
+  }
+}
+
+// First states of the segments: S_0 = S_in, S_{p+1} = M_p S_p + N_p.  A wave owns 16 columns, as in the pass.
+template <int D>
+__global__ __launch_bounds__(4 * D) void k_chunk_join(SeqArgs A, Segs segs) {
+  constexpr int KS = D / 32, NB = D / 32;
+  __shared__ __attribute__((aligned(16))) char buf[(D / 16) * Slice<kF32>::bytes];
+  const long long tile = blockIdx.x;
+  const int s = (int)(tile / A.H), h = (int)(tile - (long long)s * A.H);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c16 = lane & 15, g = lane >> 4;
+  int t0, t1;
+  const bool valid = seq_range(A, s, t0, t1);
+  const int slot = seq_slot(A, s, valid, h == 0 && threadIdx.x == 0);
+  if (slot < 0) return;
+  const int col = 16 * w + c16;
+  const Slice<kF32> rows(buf + w * Slice<kF32>::bytes, D, 16 * w, lane);
+  auto at = [&](int rt, int i) { return (long long)(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i) * D + col; };
+  f4 S[2 * NB];
+#pragma unroll
+  for (int rt = 0; rt < 2 * NB; rt++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) S[rt][i] = A.S_in ? A.S_in[((long long)slot * A.H + h) * D * D + at(rt, i)] : 0.0f;
+  const int nc = (t1 - t0 + kChunk - 1) / kChunk, per = seg_chunks(nc, segs.P);
+  for (int p = 0;; p++) {
+    const long long seg = (tile * segs.P + p) * D * D;
+    rows.template store_all<2 * NB>(segs.S + seg, S, 1.0f);
+    if ((p + 1) * per >= nc) return;  // the last segment that has chunks
+    const float *N = segs.MN + seg, *M = N + (long long)gridDim.x * segs.P * D * D;
+    h8 Sh[NB], Sl[NB];
+    const float iS = to_operand<NB, 2>(S, Sh, Sl);
+#pragma unroll
+    for (int rt = 0; rt < 2 * NB; rt++) {
+      float x[KS][8], m = 0.0f, inv;
+      const int row = 32 * (rt >> 1) + perm_row(c16, rt & 1);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) load8<kF32>(M, row * D + 32 * ks + 8 * g, x[ks]);
+      f4 n;
+#pragma unroll
+      for (int i = 0; i < 4; i++) n[i] = N[at(rt, i)];
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[ks][e]));
+      const float sc = scale_of(col_max(m), inv);
+      f4 z = {0, 0, 0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) {
+        h8 hi, lo;
+        split8<2>(x[ks], sc, hi, lo);
+        z = mfma(lo, Sh[ks], mfma(hi, Sl[ks], mfma(hi, Sh[ks], z)));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; i++) S[rt][i] = fmaf(z[i], __shfl(inv, 4 * g + i) * iS, n[i]);
+    }
   }
 }
 

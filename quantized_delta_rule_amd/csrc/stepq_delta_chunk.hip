@@ -1,6 +1,7 @@
 // stepq_delta_chunk.hip -- the gated delta rule in chunks of 64 tokens, forward (see stepq_chunk.h for
 // the mathematics and the operands).  Two launches: the chunks' local matrices, all chunks at once
-// (k_chunk_prep), then one pass over the chunks of every sequence in order (k_chunk_state).
+// (k_chunk_prep), then one pass over the chunks of every sequence in order (k_chunk_state); four where a
+// few long sequences are cut into segments.
 #include "stepq_chunk_kernels.h"
 
 namespace stepq {
@@ -8,20 +9,50 @@ namespace {
 
 using namespace dlt;
 
+// Segments of a sequence: with at most 64 (sequence, head) pairs the chunks of a sequence are run in
+// 256 / pairs segments at once (at most 16), where there are at least four chunks a segment on average.
+// Every chunk is then run three times, so two segments gain nothing.
+int segments(const SeqArgs& a) {
+  const long long tiles = (long long)a.N * a.H;
+  if (tiles > 64) return 1;
+  long long P = 256 / tiles;
+  P = P > 16 ? 16 : P;
+  const long long chunks = (long long)a.T / ((long long)a.N * kChunk);
+  if (P > chunks / 4) P = chunks / 4;
+  return P < 4 ? 1 : (int)P;
+}
+
+template <int D, int DT>
+size_t fixed_bytes(const SeqArgs& a) {
+  return (size_t)(key_bytes<LayF<D, DT>>(a) + head_bytes<LayF<D, DT>>(a));
+}
 template <int D, int DT>
 size_t bytes(const SeqArgs& a) {
-  return (size_t)(key_bytes<LayF<D, DT>>(a) + head_bytes<LayF<D, DT>>(a));
+  const int P = segments(a);
+  return fixed_bytes<D, DT>(a) + (P > 1 ? (size_t)3 * a.N * a.H * P * D * D * sizeof(float) : 0);
 }
 
 template <int D, int DT>
 hipError_t launch(const SeqArgs& a, hipStream_t s) {
+  using Y = LayF<D, DT>;
   if (a.T > 0) {
-    hipLaunchKernelGGL((k_chunk_prep<D, DT, LayF<D, DT>>), dim3((unsigned)chunk_slots(a.T, a.N), a.Hq), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((k_chunk_prep<D, DT, Y>), dim3((unsigned)chunk_slots(a.T, a.N), a.Hq), dim3(256), 0, s, a);
     if (hipError_t e = hipGetLastError()) return e;
   }
   constexpr int NW = D / 16;
-  hipLaunchKernelGGL((k_chunk_state<D, DT, NW, LayF<D, DT>>), dim3((unsigned)((long long)a.N * a.H), 1), dim3(64 * NW), 0, s,
-                     a, nullptr, nullptr);
+  const unsigned tiles = (unsigned)((long long)a.N * a.H);
+  Segs g{segments(a), nullptr, nullptr};
+  if (g.P == 1) {
+    hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kForward>), dim3(tiles), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
+    return hipGetLastError();
+  }
+  g.MN = (float*)(a.ws + fixed_bytes<D, DT>(a));
+  g.S = g.MN + (size_t)2 * tiles * g.P * D * D;
+  hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kSegment>), dim3(tiles, g.P, 2), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
+  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL((k_chunk_join<D>), dim3(tiles), dim3(64 * NW), 0, s, a, g);
+  if (hipError_t e = hipGetLastError()) return e;
+  hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kReadout>), dim3(tiles, g.P), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
   return hipGetLastError();
 }
 

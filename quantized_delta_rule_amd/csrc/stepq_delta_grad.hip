@@ -881,7 +881,7 @@ hipError_t launch(GradArgs b, hipStream_t s) {
   a.status = nullptr;  // reported once, by the reverse pass
   if (a.T > 0) {
     hipLaunchKernelGGL((k_chunk_prep<D, DT, LayB<D, DT>>), slots, dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_chunk_state<D, DT, D / 16, LayB<D, DT>>), tiles, dim3(4 * D), 0, s, a, keep.S, keep.W);
+    hipLaunchKernelGGL((k_chunk_state<D, DT, D / 16, LayB<D, DT>, kKeep>), tiles, dim3(4 * D), 0, s, a, keep.S, keep.W, Segs{});
   }
   a.status = status;
   hipLaunchKernelGGL((k_chunk_reverse<D, DT, D / 16>), tiles, dim3(4 * D), 0, s, b, keep);

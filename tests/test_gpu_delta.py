@@ -101,3 +101,20 @@ def test_values_of_any_size(delta, scale):
     out, S = _forward(delta, x, cu, 1)
     want, wantS = R.run(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["S"], cu)
     assert R.rel(out, want) <= OUT[F32] and R.rel(S, wantS) <= STATE
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("lens", [[1100], [2000, 0, 65, 1500]], ids=str)
+def test_long_sequences_cut_into_segments(delta, d, dtype, lens):
+    """Few heads and many chunks: segments run at once and joined; sequences of a batch that have fewer
+    chunks than segments among them.  In place, as a state that a decode loop carries."""
+    cu = R.offsets(lens)
+    x = R.inputs(51 + d, cu[-1], 1, 2, d, len(lens), dtype)
+    g = _dev(x)
+    out = torch.empty_like(g["v"])
+    S = g["S"].clone()
+    delta.forward(g["q"], g["k"], g["v"], g["alpha"], g["beta"], out, state_in=S, state_out=S,
+                  cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    want, wantS = R.run(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["S"], cu)
+    assert R.rel(out, want) <= OUT[dtype] and R.rel(S, wantS) <= STATE
