@@ -750,21 +750,23 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   }
 }
 
-// First states of the segments: S_0 = S_in, S_{p+1} = M_p S_p + N_p.  A wave owns 16 columns, as in the pass.
+// First states of the segments: S_0 = S_in, S_{p+1} = M_p S_p + N_p.  A wave owns 16 columns, as in the pass,
+// and the waves of a state are spread over the card, two a workgroup: there is nothing they share but M,
+// whose rows are on their way one row tile ahead.
 template <int D>
-__global__ __launch_bounds__(4 * D) void k_chunk_join(SeqArgs A, Segs segs) {
+__global__ __launch_bounds__(128) void k_chunk_join(SeqArgs A, Segs segs) {
   constexpr int KS = D / 32, NB = D / 32;
-  __shared__ __attribute__((aligned(16))) char buf[(D / 16) * Slice<kF32>::bytes];
+  __shared__ __attribute__((aligned(16))) char buf[2 * Slice<kF32>::bytes];
   const long long tile = blockIdx.x;
   const int s = (int)(tile / A.H), h = (int)(tile - (long long)s * A.H);
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, v = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = 2 * blockIdx.y + v;
   const int c16 = lane & 15, g = lane >> 4;
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
-  const int slot = seq_slot(A, s, valid, h == 0 && threadIdx.x == 0);
+  const int slot = seq_slot(A, s, valid, h == 0 && blockIdx.y == 0 && threadIdx.x == 0);
   if (slot < 0) return;
   const int col = 16 * w + c16;
-  const Slice<kF32> rows(buf + w * Slice<kF32>::bytes, D, 16 * w, lane);
+  const Slice<kF32> rows(buf + v * Slice<kF32>::bytes, D, 16 * w, lane);
   auto at = [&](int rt, int i) { return (long long)(32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i) * D + col; };
   f4 S[2 * NB];
 #pragma unroll
@@ -774,34 +776,42 @@ __global__ __launch_bounds__(4 * D) void k_chunk_join(SeqArgs A, Segs segs) {
   const int nc = (t1 - t0 + kChunk - 1) / kChunk, per = seg_chunks(nc, segs.P);
   for (int p = 0;; p++) {
     const long long seg = (tile * segs.P + p) * D * D;
-    rows.template store_all<2 * NB>(segs.S + seg, S, 1.0f);
-    if ((p + 1) * per >= nc) return;  // the last segment that has chunks
+    const bool last = (p + 1) * per >= nc;  // of the segments that have chunks
     const float *N = segs.MN + seg, *M = N + (long long)gridDim.x * segs.P * D * D;
+    float x[2][KS][8];
+    f4 n[2];
+    auto fetch = [&](int rt) {
+      const int row = 32 * (rt >> 1) + perm_row(c16, rt & 1);
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) load8<kF32>(M, row * D + 32 * ks + 8 * g, x[rt & 1][ks]);
+#pragma unroll
+      for (int i = 0; i < 4; i++) n[rt & 1][i] = N[at(rt, i)];
+    };
+    if (!last) fetch(0);
+    rows.template store_all<2 * NB>(segs.S + seg, S, 1.0f);
+    if (last) return;
     h8 Sh[NB], Sl[NB];
     const float iS = to_operand<NB, 2>(S, Sh, Sl);
 #pragma unroll
     for (int rt = 0; rt < 2 * NB; rt++) {
-      float x[KS][8], m = 0.0f, inv;
-      const int row = 32 * (rt >> 1) + perm_row(c16, rt & 1);
-#pragma unroll
-      for (int ks = 0; ks < KS; ks++) load8<kF32>(M, row * D + 32 * ks + 8 * g, x[ks]);
-      f4 n;
-#pragma unroll
-      for (int i = 0; i < 4; i++) n[i] = N[at(rt, i)];
+      if (rt + 1 < 2 * NB) fetch(rt + 1);
+      ahead();
+      float m = 0.0f, inv;
 #pragma unroll
       for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-        for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[ks][e]));
+        for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[rt & 1][ks][e]));
       const float sc = scale_of(col_max(m), inv);
       f4 z = {0, 0, 0, 0};
 #pragma unroll
       for (int ks = 0; ks < KS; ks++) {
         h8 hi, lo;
-        split8<2>(x[ks], sc, hi, lo);
+        split8<2>(x[rt & 1][ks], sc, hi, lo);
         z = mfma(lo, Sh[ks], mfma(hi, Sl[ks], mfma(hi, Sh[ks], z)));
       }
 #pragma unroll
-      for (int i = 0; i < 4; i++) S[rt][i] = fmaf(z[i], __shfl(inv, 4 * g + i) * iS, n[i]);
+      for (int i = 0; i < 4; i++) S[rt][i] = fmaf(z[i], __shfl(inv, 4 * g + i) * iS, n[rt & 1][i]);
+      ahead();
     }
   }
 }

@@ -50,7 +50,7 @@ hipError_t launch(const SeqArgs& a, hipStream_t s) {
   g.S = g.MN + (size_t)2 * tiles * g.P * D * D;
   hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kSegment>), dim3(tiles, g.P, 2), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL((k_chunk_join<D>), dim3(tiles), dim3(64 * NW), 0, s, a, g);
+  hipLaunchKernelGGL((k_chunk_join<D>), dim3(tiles, D / 32), dim3(128), 0, s, a, g);
   if (hipError_t e = hipGetLastError()) return e;
   hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kReadout>), dim3(tiles, g.P), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
   return hipGetLastError();
