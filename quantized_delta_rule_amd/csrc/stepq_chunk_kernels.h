@@ -140,7 +140,7 @@ __device__ __forceinline__ float invert_corner(const float (*X)[kPitch], float (
 
 // Y: the workspace's layout (LayF, or LayB: with the gradient's extra pieces).
 template <int D, int DT, class Y>
-__global__ __launch_bounds__(256, Y::grad ? 3 : 4) void k_chunk_prep(SeqArgs A) {
+__global__ __launch_bounds__(256, Y::grad ? 2 : 3) void k_chunk_prep(SeqArgs A) {
   constexpr int KS = D / 32, NPI = Y::NPI, NPO = Y::NPO;
   __shared__ PrepSmem<D, DT, Y::grad> sm;
   const long long j = blockIdx.x;
@@ -312,12 +312,16 @@ __global__ __launch_bounds__(256, Y::grad ? 3 : 4) void k_chunk_prep(SeqArgs A) 
       }
     }
     const float be_own = __shfl(be, own);
-    const int og = c16 >> 2, oi = 4 * wp + (c16 & 3);  // own token: group of the block, place in the group
+    // own token: place in its block, group, place in that; opaque: the predicates made from them are not
+    // kept in scalar registers across heads
+    int po = own & 31, pg = g;
+    asm("" : "+v"(po), "+v"(pg));
+    const int og = po >> 3, oi = po & 7;
     // L between `own` and the 8 tokens 8 g + e of its own block: down: own is the later one
     float Lo[8];
     auto in_block = [&](bool down) {
       const float *a = &gt[0][32 * wb + 8 * g], *pre = &gt[1][32 * wb + 8 * g], *suf = &gt[2][32 * wb + 8 * g];
-      const int lo = down ? g : og, hi = down ? og : g;  // earlier and later group
+      const int lo = down ? pg : og, hi = down ? og : pg;  // earlier and later group
       const float b1 = wb ? B[5] : B[1], b2 = wb ? B[6] : B[2];
       float mid = gt[down ? 1 : 2][own];
       if (lo == 0 && hi > 1) mid *= b1;
@@ -326,14 +330,16 @@ __global__ __launch_bounds__(256, Y::grad ? 3 : 4) void k_chunk_prep(SeqArgs A) 
       if (down) {
 #pragma unroll
         for (int e = 7; e >= 0; e--) {
-          Lo[e] = g < og ? mid * suf[e] : g == og && e <= oi ? c : 0.0f;
+          const float l = pg < og ? mid * suf[e] : c;
+          Lo[e] = 8 * pg + e <= po ? l : 0.0f;
           if (e <= oi) c *= a[e];
         }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; e++) {
           if (e > oi) c *= a[e];
-          Lo[e] = g > og ? mid * pre[e] : g == og && e >= oi ? c : 0.0f;
+          const float l = pg > og ? mid * pre[e] : c;
+          Lo[e] = 8 * pg + e >= po ? l : 0.0f;
         }
       }
     };
@@ -348,7 +354,7 @@ __global__ __launch_bounds__(256, Y::grad ? 3 : 4) void k_chunk_prep(SeqArgs A) 
 #pragma unroll
       for (int e = 0; e < 8; e++) {
         const float l = nb == wb ? Lo[e] : pre * gt[4][8 * g + e];
-        const bool strict = nb < wb || g < og || e < oi;
+        const bool strict = nb < wb || 8 * pg + e < po;
         av[e] = strict ? be_own * (kk[nb][e] * l) : 0.0f;
         if constexpr (!Y::grad) pv[nb][e] = qk[nb][e] * l;
       }

@@ -74,6 +74,7 @@ class _Sequences:
             raise ValueError("q and v must be [tokens, heads, d]")
         if q.device.type != "cuda":
             raise ValueError(f"q must live on a GPU (got {q.device})")
+        self.torch_device = q.device
         self.device = dev = q.device.index
         T, Hq, d = q.shape
         H = v.shape[1]
@@ -105,6 +106,7 @@ class _Sequences:
         self.N = n
         st = None if status is None else _dev_tensor(status, "status", torch.int32, 1, dev)
         self.desc = _SeqDesc(int(kind), int(order), code, Hq, H, d, n, T, dev, qs, ks, vs, os_, cu, st)
+        self.current = stream is None
         if stream is None:
             stream = torch.cuda.current_stream(dev)
         elif stream.device.index != dev:
@@ -126,8 +128,12 @@ class _Sequences:
         if given is None:
             if need == 0:
                 return None, 0, None
-            with torch.cuda.stream(self.stream):
-                given = torch.empty(need, dtype=torch.uint8, device=f"cuda:{self.device}")
+            if self.current:  # the allocator's block belongs to the stream that the call runs on
+                given = torch.empty(need, dtype=torch.uint8, device=self.torch_device)
+            else:
+                with torch.cuda.stream(self.stream):
+                    given = torch.empty(need, dtype=torch.uint8, device=self.torch_device)
+            return given.data_ptr(), need, given
         p = _dev_tensor(given, "workspace", torch.uint8, given.numel(), self.device)
         return p, given.numel(), given
 
