@@ -220,8 +220,10 @@ const char* stepq_last_error(void);
  *   cu_seqlens   device int32 [n_seqs + 1]: sequence s is rows cu[s] .. cu[s+1] - 1 (0 <= cu[s] <=
  *                cu[s+1] <= n_tokens; lengths of zero are fine; the ranges must not meet).  Rows
  *                of no sequence are not read, and out is left as it was there.  A sequence whose
- *                offsets break the rule is skipped and raises STEPQ_FLAG_BAD_SEQ.  NULL: n_seqs
- *                sequences of n_tokens / n_seqs rows each (must divide).
+ *                two offsets break the rule is skipped and raises STEPQ_FLAG_BAD_SEQ; where that is
+ *                not the last sequence, what the call's other sequences write is unspecified (it
+ *                stays in their own rows and states).  NULL: n_seqs sequences of
+ *                n_tokens / n_seqs rows each (must divide).
  *   q_stride .. out_stride  elements from one token's row to the next (heads of a token are d
  *                elements apart); 0 = packed (heads * d).  A multiple of 16 bytes, below
  *                2^23 elements.
@@ -256,9 +258,11 @@ int stepq_delta_backward_workspace(const stepq_delta_desc* desc, size_t* bytes);
  *   alike), -1 = skip the sequence (its out rows and state are left as they were), any other
  *   index outside [0, n_slots) is skipped too and raises STEPQ_FLAG_BAD_SLOT.  Two sequences must
  *   not name one slot.  NULL: sequence s uses state s.
- * GDN sequences of 16 tokens and more on average run in chunks of 64 tokens on the matrix cores
- * (sums and states in binary32, operands in pairs of binary16 with power-of-two scales: 22 bits);
- * there a non-finite input makes its head's outputs from its chunk's first token on non-finite.
+ *   out must not overlap an input, nor the workspace anything.
+ * GDN sequences of 16 tokens and more on average run in chunks of 64 tokens on the matrix cores: sums
+ * and states in binary32; operands in pairs of binary16 with power-of-two scales, 22 bits of the largest
+ * element of a row, or of a column of a chunk; the last products of a BF16 out in single ones (11 bits).
+ * There a non-finite input may make its head's outputs non-finite from its chunk's first token on.
  * Otherwise tokens are taken one by one in binary32.  Only enqueues kernels: may be captured.
  */
 int stepq_delta_forward(const stepq_delta_desc* desc, const void* q, const void* k, const void* v,

@@ -37,10 +37,12 @@ int seq_args(const void* desc, SeqArgs* a) {
   if (!d->cu_seqlens && d->n_seqs > 0 && d->n_tokens % d->n_seqs)
     return fail(STEPQ_ERR_INVALID_ARG, "without cu_seqlens n_tokens (%d) must be a multiple of n_seqs (%d)",
                 d->n_tokens, d->n_seqs);
-  // one wave per (sequence, head, 32 columns), one workgroup per (chunk, head)
-  if ((long long)d->n_seqs * d->n_heads > INT_MAX / 4)
-    return fail(STEPQ_ERR_INVALID_ARG, "n_seqs * n_heads = %lld exceeds the launch grid",
-                (long long)d->n_seqs * d->n_heads);
+  // 4 d threads and fewer a (sequence, head) and a chunk: below 2^32 in a grid's first dimension
+  const long long pairs = (long long)d->n_seqs * d->n_heads;
+  const long long chunks = d->n_tokens / 64 + (long long)d->n_seqs + 1;
+  if ((pairs > chunks ? pairs : chunks) * 4 * d->d > UINT_MAX)
+    return fail(STEPQ_ERR_INVALID_ARG, "n_seqs * n_heads = %lld or n_tokens = %d exceeds the launch grid",
+                pairs, d->n_tokens);
   const long long unit = d->dtype == STEPQ_DTYPE_F32 ? 4 : 8;  // elements of 16 bytes
   const long long kd = (long long)d->n_qk_heads * d->d, vd = (long long)d->n_heads * d->d;
   const long long given[4] = {d->q_stride, d->k_stride, d->v_stride, d->out_stride};
@@ -52,9 +54,6 @@ int seq_args(const void* desc, SeqArgs* a) {
       return fail(STEPQ_ERR_INVALID_ARG, "%s_stride %lld must be %lld .. 2^23 - 1 and a multiple of 16 bytes",
                   i == 0 ? "q" : i == 1 ? "k" : i == 2 ? "v" : "out", st[i], packed[i]);
   }
-  int ndev = 0;
-  if (hipGetDeviceCount(&ndev) != hipSuccess || d->device < 0 || d->device >= ndev)
-    return fail(STEPQ_ERR_INVALID_ARG, "device %d not available (%d devices)", d->device, ndev);
   *a = SeqArgs{};
   a->kind = d->kind;
   a->order = d->order;
@@ -71,6 +70,13 @@ int seq_args(const void* desc, SeqArgs* a) {
   a->vs = st[2];
   a->os = st[3];
   a->status = d->status;
+  return STEPQ_OK;
+}
+
+static int seq_device(int device) {
+  int ndev = 0;
+  if (hipGetDeviceCount(&ndev) != hipSuccess || device < 0 || device >= ndev)
+    return fail(STEPQ_ERR_INVALID_ARG, "device %d not available (%d devices)", device, ndev);
   return STEPQ_OK;
 }
 
@@ -138,6 +144,7 @@ int stepq_delta_forward_workspace(const stepq_delta_desc* desc, size_t* bytes) {
   SeqArgs a;
   if (int rc = seq_args(desc, &a)) return rc;
   if (!bytes) return fail(STEPQ_ERR_INVALID_ARG, "bytes is NULL");
+  if (int rc = seq_device(desc->device)) return rc;
   *bytes = forward_bytes(a);
   return ok();
 }
@@ -146,6 +153,7 @@ int stepq_delta_backward_workspace(const stepq_delta_desc* desc, size_t* bytes) 
   SeqArgs a;
   if (int rc = backward_args(desc, &a)) return rc;
   if (!bytes) return fail(STEPQ_ERR_INVALID_ARG, "bytes is NULL");
+  if (int rc = seq_device(desc->device)) return rc;
   *bytes = chunk_backward_bytes(a);
   return ok();
 }
@@ -161,6 +169,7 @@ int stepq_delta_forward(const stepq_delta_desc* desc, const void* q, const void*
   if (int rc = aligned(S_out, 16, "S_out")) return rc;
   if (slots && n_slots < 1) return fail(STEPQ_ERR_INVALID_ARG, "n_slots must be >= 1");
   if (int rc = seq_workspace(workspace, workspace_bytes, forward_bytes(a))) return rc;
+  if (int rc = seq_device(desc->device)) return rc;
   a.S_in = S_in;
   a.S_out = S_out;
   a.n_slots = n_slots;
@@ -190,6 +199,7 @@ int stepq_delta_backward(const stepq_delta_desc* desc, const void* q, const void
   if (int rc = aligned(dalpha, 4, "dalpha")) return rc;
   if (int rc = aligned(dbeta, 4, "dbeta")) return rc;
   if (int rc = seq_workspace(workspace, workspace_bytes, chunk_backward_bytes(g.f))) return rc;
+  if (int rc = seq_device(desc->device)) return rc;
   g.f.S_in = S_in;
   g.f.ws = (char*)workspace;
   g.f.out = nullptr;

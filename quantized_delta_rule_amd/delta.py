@@ -103,6 +103,8 @@ class _Sequences:
             cu = _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32, n + 1, dev)
         else:
             n = 1 if n_seqs is None else int(n_seqs)
+        if max(T, n) > 0x7FFFFFFF:
+            raise ValueError(f"{T} tokens and {n} sequences: at most 2^31 - 1")
         self.N = n
         st = None if status is None else _dev_tensor(status, "status", torch.int32, 1, dev)
         self.desc = _SeqDesc(int(kind), int(order), code, Hq, H, d, n, T, dev, qs, ks, vs, os_, cu, st)
