@@ -46,7 +46,7 @@ template <int D, int DT> struct LayF {
   static constexpr int key = 3 * NPI * NF * kFrag, offKK = 0, offQK = 0;  // none
   static constexpr int offT = 0, offP = 2 * kTri * kFrag, offTab = offP + NPO * kTri * kFrag;
   static constexpr int offTt = offTab;  // none
-  static constexpr int head = offTab + 2048;
+  static constexpr int head = offTab + 2048, tab = 1280;  // bytes of the tables that the pass reads
 };
 // Workspace of the gradient.  Q^T in Q's place, K K^T [t][s] and Q K^T [s][t] (binary32, t >= s within 32-row
 // blocks) behind the fragments; T, T^T, P^T (two planes each).  Then, per chunk slot and value head in binary32: the
@@ -58,17 +58,17 @@ template <int D, int DT> struct LayB {
   static constexpr int offKK = 3 * NPI * NF * kFrag, offQK = offKK + 64 * 64 * 4;
   static constexpr int key = offQK + 64 * 64 * 4;
   static constexpr int offT = 0, offTt = 2 * kTri * kFrag, offP = 4 * kTri * kFrag, offTab = 6 * kTri * kFrag;
-  static constexpr int head = offTab + 4096;
+  static constexpr int head = offTab + 4096, tab = 2048;
 };
 // Row tables (64 floats each); inverse operand scales are folded in.
 constexpr int kTabU = 0;     // G / scale of K's row (gradient: times beta)
-constexpr int kTabB = 64;    // beta (0 behind the sequence's end)
-constexpr int kTabT = 128;   // [0] = 1 / scale of T (gradient: of T's rows)
-constexpr int kTabQ = 192;   // G / scale of Q's row
-constexpr int kTabP = 256;   // 1 / scale of P's (gradient: P^T's) row
-constexpr int kTabD = 320;   // L[C, s] / scale of K's row (K^T's column)
-constexpr int kTabG = 384;   // G; [63] = G_C
-constexpr int kTabTt = 448;  // 1 / scale of T^T's row            (gradient from here on)
+constexpr int kTabQ = 64;    // G / scale of Q's row
+constexpr int kTabP = 128;   // 1 / scale of P's (gradient: P^T's) row
+constexpr int kTabD = 192;   // L[C, s] / scale of K's row (K^T's column)
+constexpr int kTabG = 256;   // [62] = 1 / scale of T (forward), [63] = G_C
+constexpr int kTabT = 320;   // 1 / scale of T's row              (gradient from here on)
+constexpr int kTabB = 384;   // beta (0 behind the sequence's end)
+constexpr int kTabTt = 448;  // 1 / scale of T^T's row
 constexpr int kTabL = 512;   // L[C, s]
 constexpr int kTabIK = 576;  // 1 / scale of K's row
 constexpr int kTabIQ = 640;  // 1 / scale of Q's row

@@ -1,6 +1,8 @@
 // stepq_chunk_kernels.h -- kernels that the chunked forward pass and its gradient share: the chunks'
 // local matrices (k_chunk_prep) and the pass over the chunks (k_chunk_state).
 #pragma once
+#include <type_traits>
+
 #include "stepq_chunk.h"
 
 namespace stepq {
@@ -301,11 +303,11 @@ __global__ __launch_bounds__(256, Y::grad ? 2 : 3) void k_chunk_prep(SeqArgs A) 
       const float G = lane < 32 ? p32 : BL * p32, L63 = lane < 32 ? s32 * BU : s32;
       const float ik0 = sm.isk[lane], iq0 = sm.isq[lane];
       tab[kTabU + lane] = (Y::grad ? be * G : G) * ik0;
-      tab[kTabB + lane] = be;
       tab[kTabQ + lane] = G * iq0;
       tab[kTabD + lane] = L63 * ik0;
-      tab[kTabG + lane] = G;
+      if (lane == 63) tab[kTabG + 63] = G;
       if constexpr (Y::grad) {
+        tab[kTabB + lane] = be;
         tab[kTabL + lane] = L63;
         tab[kTabIK + lane] = ik0;
         tab[kTabIQ + lane] = iq0;
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(256, Y::grad ? 2 : 3) void k_chunk_prep(SeqArgs A) 
     if constexpr (!Y::grad) {
       float iT;
       const float sT = scale_of(fmaxf(fmaxf(sm.most[0], sm.most[1]), fmaxf(sm.most[2], sm.most[3])), iT);
-      if (tid == 0) tab[kTabT] = iT;
+      if (tid == 0) tab[kTabG + 62] = iT;
 #pragma unroll
       for (int ks = 0; ks < 2; ks++) {
         if (ks > wb) continue;
@@ -490,33 +492,72 @@ struct Segs {
   int P;            // segments of a sequence
   float *MN, *S;    // [2][tiles][P][D][D] (N, then M), [tiles][P][D][D] first states
 };
+// The sequence of a workgroup: where there are more states than CUs, the longest sequences first, so that
+// the last ones to finish are short (8 sequences of 0 .. 3,698 tokens x 48 states: 394 -> 346 us).  A wave ranks
+// up to 64 lengths for that; more sequences even out by themselves over many rounds of workgroups, and
+// with short ones the ranking costs more than it gives (16 x 48 states of two chunks: 60 -> 66 us).
+__device__ __forceinline__ int seq_in_order(const SeqArgs& A, int r) {
+  if (!A.cu || A.N > 64 || A.T < 256 * A.N || (long long)A.N * A.H <= 256) return r;
+  const int lane = threadIdx.x & 63;
+  int t0 = 0, t1 = -1;
+  if (lane < A.N) seq_range(A, lane, t0, t1);
+  const int len = t1 - t0;
+  int before = 0;
+  for (int j = 0; j < A.N; j++) {
+    const int l = __builtin_amdgcn_readlane(len, j);
+    before += l > len || (l == len && j < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < A.N && before == r));
+}
+
+// HV workgroups of NW waves share a state's columns.  They are 8 apart, on one XCD and its L2.
+template <int HV> __device__ __forceinline__ long long state_of(unsigned x) { return HV == 1 ? x : x / (8 * HV) * 8 + x % 8; }
+template <int HV> __device__ __forceinline__ int columns_of(unsigned x) { return HV == 1 ? 0 : x / 8 % HV; }
+template <int NW> unsigned workgroups(const SeqArgs& a, int D) {
+  const long long n = (long long)a.N * a.H, hv = D / (16 * NW);
+  return (unsigned)(hv == 1 ? n : (n + 7) / 8 * 8 * hv);
+}
+// Calls f with a workgroup's waves (an integral constant), for P passes over every state at once.
+// D = 128, 16-bit types: a state's columns go to two workgroups of four waves where the states leave CUs
+// idle (at most 128 passes; 128 states x 32 chunks: 225 -> 177 us kept, 308 -> 243 in reverse) and where
+// sequences are short (under 256 tokens: 70 x 48 states of two chunks 299 -> 285 us), because two such
+// workgroups share a CU and one's first and last states move while the other computes.  Elsewhere all
+// eight waves share one copy of the operands (384 states x 43 chunks: 394 us against 440).
+template <int D, int DT, class F>
+hipError_t with_state_waves(const SeqArgs& a, int P, F&& f) {
+  if constexpr (D == 64) return f(std::integral_constant<int, 4>{});
+  else if constexpr (DT == kF32) return f(std::integral_constant<int, 8>{});
+  else if ((long long)a.N * a.H * P > 128 && a.T >= 256LL * a.N) return f(std::integral_constant<int, 8>{});
+  else return f(std::integral_constant<int, 4>{});
+}
 enum StateMode { kForward, kKeep, kSegment, kReadout };
 __device__ __forceinline__ int seg_chunks(int nc, int P) { return (nc + P - 1) / P; }
 
 template <int D, int DT, int NW, class Y, int MODE>
-__global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS, float* keepW, Segs segs) {
+__global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chunk_state(SeqArgs A, float* keepS, float* keepW, Segs segs) {
   constexpr int KS = D / 32, NPI = Y::NPI, NPO = Y::NPO, NB = D / 32;
-  // staged: K, K^T (and Q), then T (and P), then the tables
   constexpr bool out_on = MODE == kForward || MODE == kReadout, cut = MODE == kSegment || MODE == kReadout;
-  constexpr int keyN = out_on ? Y::key : Y::offQ, triN = out_on ? Y::offTab : Y::grad ? Y::offTt : Y::offP;
-  constexpr int offT = keyN, offP = keyN + Y::offP, offTab = keyN + triN;
-  constexpr int part = offTab + 2048;
-  constexpr int NBUF = 2 * part + NW * Slice<DT>::bytes <= 160 * 1024 ? 2 : 1;  // binary32 inputs: one
+  // staged: K, K^T (and Q), then T (and P), then the tables of two chunks
+  constexpr int keyN = out_on ? Y::key : Y::offQ, HV = D / (16 * NW);
+  constexpr int offT = keyN, offP = keyN + Y::offP, offTab = offT + (out_on ? Y::offTab : 2 * kTri * kFrag);
+  constexpr int part = offTab + 2 * Y::tab;
   using Tr = Slice<DT>;
   using TrF = Slice<kF32>;
   constexpr int trN = Tr::bytes;
-  __shared__ __attribute__((aligned(16))) char buf[NBUF * part + NW * trN];
-  const long long tile = blockIdx.x;
-  const int s = (int)(tile / A.H), h = (int)(tile - (long long)s * A.H);
+  __shared__ __attribute__((aligned(16))) char buf[part + NW * trN];
+  const long long tile = state_of<HV>(blockIdx.x);
+  const int part0 = columns_of<HV>(blockIdx.x);
+  if (HV > 1 && tile >= (long long)A.N * A.H) return;
+  const int rank = (int)(tile / A.H), h = (int)(tile - (long long)rank * A.H), s = seq_in_order(A, rank);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, g = lane >> 4;
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
-  const int slot = seq_slot(A, s, valid, h == 0 && !cut && tid == 0);
+  const int slot = seq_slot(A, s, valid, h == 0 && !cut && part0 == 0 && tid == 0);
   if (slot < 0) return;
   if (t0 == t1 && MODE == kKeep) return;
   if (t0 == t1 && MODE == kForward && (!A.S_out || A.S_out == A.S_in)) return;
-  const int col = 16 * w + c16;
+  const int col0 = 16 * (part0 * NW + w), col = col0 + c16;
   const long long so = ((long long)slot * A.H + h) * D * D + col;
   const int nc = (t1 - t0 + kChunk - 1) / kChunk;
   int c_first = 0, c_end = nc;
@@ -555,24 +596,25 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
   const long long j0 = first_slot(A, s);
   const char* const heads = A.ws + key_bytes<Y>(A);
   const int hq = h / A.grp;
-  // chunk c's pieces on their way into LDS, 1 KiB a wave at a time: the key block's three parts and the head
-  // block's, so that they can be issued between products
+  // chunk c's pieces on their way into LDS, 1 KiB a wave at a time, each as soon as every wave holds the last
+  // chunk's in registers: K, Q and T (early), then P, K^T and the tables (late)
   const unsigned lds0 = lds_offset(buf), lane16 = 16 * lane;
-  auto fetch = [&](int c, int n) {
+  auto fetch = [&](int c, bool early) {
     const char* const key = A.ws + ((j0 + c) * A.Hq + hq) * Y::key;
     const char* const head = heads + ((j0 + c) * A.H + h) * Y::head;
-    const unsigned at = lds0 + (NBUF == 2 ? (c & 1) * part : 0);
-    if (n < 3) {
-      copy_block<NW>(key, at, min(n * Y::offKT, keyN), min((n + 1) * Y::offKT, keyN), w, lane16);
-    } else if constexpr (!out_on) {
-      copy_block<NW>(head, at + offT, 0, triN, w, lane16);
-      copy_block<NW>(head + Y::offTab, at + offTab, 0, 2048, w, lane16);
+    if (early) {
+      copy_block<NW>(key, lds0, 0, Y::offKT, w, lane16);
+      if constexpr (out_on) copy_block<NW>(key, lds0, Y::offQ, keyN, w, lane16);
+      copy_block<NW>(head, lds0 + offT, 0, 2 * kTri * kFrag, w, lane16);
     } else {
-      copy_block<NW>(head, at + offT, 0, Y::head, w, lane16);
+      copy_block<NW>(key, lds0, Y::offKT, 2 * Y::offKT, w, lane16);
+      if constexpr (out_on) copy_block<NW>(head, lds0 + offT, Y::offP, Y::offTab, w, lane16);
+      const unsigned at = lds0 + offTab + (c & 1) * Y::tab;
+      if (w == 0) copy_to_lds(head + Y::offTab, at, lane16);
+      if (w == 1 && lane < (Y::tab - 1024) / 16) copy_to_lds(head + Y::offTab + 1024, at + 1024, lane16);
     }
   };
-  char* const piece = buf + NBUF * part + w * trN;
-  const int col0 = 16 * w;
+  char* const piece = buf + part + w * trN;
   const Tr vrows(piece, A.vs, col0, lane), orows(piece, A.os, col0, lane);
   const TrF krows(piece, D, col0, lane);
   typename Tr::u4 v[Tr::NL];  // V of the next chunk, as it lies in memory
@@ -582,18 +624,18 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     vrows.load(rows_at<DT>(A.v, tc, A.vs, h * D, unit_start ? 0 : D, unit_start ? 1 : min(t1 - tc, kChunk)), v);
   };
   if (c_first < c_end) {
-#pragma unroll
-    for (int n = 0; n < 4; n++) fetch(c_first, n);
+    fetch(c_first, true);
+    fetch(c_first, false);
     fetch_v(c_first);
   }
   const f4 zero = {0, 0, 0, 0};
   for (int c = c_first; c < c_end; c++) {
-    const char* const lds = buf + (NBUF == 2 ? (c & 1) * part : 0);
+    const char* const lds = buf;
     const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
     wait_copies();
     __syncthreads();  // chunk c is there, and every wave is done with chunk c - 1
-    const bool more = NBUF == 2 && c + 1 < c_end;
-    const float* const tab = (const float*)(lds + offTab);
+    const bool more = c + 1 < c_end;
+    const float* const tab = (const float*)(lds + offTab + (c & 1) * Y::tab);
     auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane16); };
     auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
     // Every product's fragments are read while its other operand is formed.
@@ -610,8 +652,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     read(Y::offK);
     f4 R[4];
     vrows.to_acc(v, R);
-    if (more) fetch(c + 1, 0);
-    if (c + 1 < c_end) fetch_v(c + 1);
+    if (more) fetch_v(c + 1);
     ahead();
     {
       const float m = tiles_max<2 * NB>(St);
@@ -644,7 +685,6 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
       ft[1][n] = frag(offT, kTri, 1, n);
     }
     ahead();
-    if (more) fetch(c + 1, 1);
     // R = V - G K S0 (gradient: times beta)
     float ix, w1;
 #pragma unroll
@@ -655,7 +695,7 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     }
     ix = to_operand<2, 2>(R, xh, xl);
     // W = w1 z, z = T R (gradient: T's rows have scales of their own)
-    w1 = (Y::grad ? 1.0f : tab[kTabT]) * ix;
+    w1 = (Y::grad ? 1.0f : tab[kTabG + 62]) * ix;
     auto tri = [&](auto&& a, int p, const h8* b, bool first) {
 #pragma unroll
       for (int ks = 0; ks < 2; ks++)
@@ -669,7 +709,9 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
     ahead();
     if constexpr (out_on) read(Y::offQ);
     else read(Y::offKT);
-    if (more) fetch(c + 1, 2);
+    __syncthreads();
+    if (more) fetch(c + 1, true);
+    if (more && !out_on) fetch(c + 1, false);
     ahead();
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) R[rt] = Y::grad ? z[rt] * rows(kTabT, rt) : z[rt];
@@ -696,6 +738,8 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
       }
       ahead();
       read(Y::offKT);
+      __syncthreads();
+      if (more) fetch(c + 1, false);
       ahead();
 #pragma unroll
       for (int rt = 0; rt < 4; rt++) {
@@ -705,7 +749,6 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
       }
       orows.store(rows_at<DT>(A.out, tc, A.os, h * D, D, len), y);
     }
-    if (more) fetch(c + 1, 3);
     // S1 = G_C S0 + K^T diag(L[C, .]) W, in the state's units
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) R[rt] *= rows(kTabD, rt);
@@ -738,16 +781,11 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_state(SeqArgs A, float* keepS
 #pragma unroll
         for (int rt = 0; rt < 2 * NB; rt++) St[rt] = mfma(fl[2 * rt + ks], xh[ks], St[rt]);
     }
-    if (NBUF == 1 && c + 1 < c_end) {
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < 4; n++) fetch(c + 1, n);
-    }
   }
   float* dst = nullptr;
   if (MODE == kForward || (MODE == kReadout && c_end == nc && (c_first < nc || (nc == 0 && blockIdx.y == 0))))
     dst = A.S_out ? A.S_out + so : nullptr;
-  if (MODE == kSegment) dst = segs.MN + (unit_start ? (long long)gridDim.x * segs.P * D * D : 0LL) + seg;
+  if (MODE == kSegment) dst = segs.MN + (unit_start ? (long long)A.N * A.H * segs.P * D * D : 0LL) + seg;
   if (dst) {
 #pragma unroll
     for (int rt = 0; rt < 2 * NB; rt++)

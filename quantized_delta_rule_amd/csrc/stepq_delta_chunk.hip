@@ -39,21 +39,24 @@ hipError_t launch(const SeqArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((k_chunk_prep<D, DT, Y>), dim3((unsigned)chunk_slots(a.T, a.N), a.Hq), dim3(256), 0, s, a);
     if (hipError_t e = hipGetLastError()) return e;
   }
-  constexpr int NW = D / 16;
-  const unsigned tiles = (unsigned)((long long)a.N * a.H);
   Segs g{segments(a), nullptr, nullptr};
-  if (g.P == 1) {
-    hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kForward>), dim3(tiles), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
+  const long long states = (long long)a.N * a.H;
+  return with_state_waves<D, DT>(a, g.P, [&](auto nw) {
+    constexpr int NW = nw.value;
+    const unsigned tiles = workgroups<NW>(a, D);
+    if (g.P == 1) {
+      hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kForward>), dim3(tiles), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
+      return hipGetLastError();
+    }
+    g.MN = (float*)(a.ws + fixed_bytes<D, DT>(a));
+    g.S = g.MN + (size_t)2 * states * g.P * D * D;
+    hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kSegment>), dim3(tiles, g.P, 2), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
+    if (hipError_t e = hipGetLastError()) return e;
+    hipLaunchKernelGGL((k_chunk_join<D>), dim3((unsigned)states, D / 32), dim3(128), 0, s, a, g);
+    if (hipError_t e = hipGetLastError()) return e;
+    hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kReadout>), dim3(tiles, g.P), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
     return hipGetLastError();
-  }
-  g.MN = (float*)(a.ws + fixed_bytes<D, DT>(a));
-  g.S = g.MN + (size_t)2 * tiles * g.P * D * D;
-  hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kSegment>), dim3(tiles, g.P, 2), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
-  if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL((k_chunk_join<D>), dim3(tiles, D / 32), dim3(128), 0, s, a, g);
-  if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL((k_chunk_state<D, DT, NW, Y, kReadout>), dim3(tiles, g.P), dim3(64 * NW), 0, s, a, nullptr, nullptr, g);
-  return hipGetLastError();
+  });
 }
 
 }  // namespace

@@ -31,27 +31,28 @@ struct Keep {  // per chunk slot and value head, binary32
 // The reverse pass: like k_chunk_state a wave owns 16 columns of one state's gradient for the whole sequence
 // and holds it in units of a power of two per column.
 template <int D, int DT, int NW>
-__global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep) {
+__global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep keep) {
   using L = LayB<D, DT>;
   constexpr int KS = D / 32, NPI = L::NPI, NB = D / 32;
   constexpr int keyN = L::offKK, triN = 4 * kTri * kFrag;  // K, K^T, Q^T; T^T, P^T
   constexpr int offTt = keyN, offP = keyN + 2 * kTri * kFrag, offTab = keyN + triN;
-  constexpr int part = offTab + 2048;
-  constexpr int NBUF = 2 * part + NW * Slice<kF32>::bytes <= 160 * 1024 ? 2 : 1;
+  constexpr int part = offTab + 2 * L::tab, HV = D / (16 * NW);
   const SeqArgs& A = B.f;
   using Tr = Slice<DT>;
   using TrF = Slice<kF32>;
   constexpr int trN = TrF::bytes;
-  static_assert(NBUF * part + NW * trN <= 160 * 1024);
-  __shared__ __attribute__((aligned(16))) char buf[NBUF * part + NW * trN];
-  const long long tile = blockIdx.x;
-  const int s = (int)(tile / A.H), h = (int)(tile - (long long)s * A.H);
+  static_assert(part + NW * trN <= 160 * 1024);
+  __shared__ __attribute__((aligned(16))) char buf[part + NW * trN];
+  const long long tile = state_of<HV>(blockIdx.x);
+  const int part0 = columns_of<HV>(blockIdx.x);
+  if (HV > 1 && tile >= (long long)A.N * A.H) return;
+  const int rank = (int)(tile / A.H), h = (int)(tile - (long long)rank * A.H), s = seq_in_order(A, rank);
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c16 = lane & 15, g = lane >> 4;
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
-  if (seq_slot(A, s, valid, h == 0 && blockIdx.y == 0 && tid == 0) < 0) return;
-  const int col = 16 * ((int)blockIdx.y * NW + w) + c16;
+  if (seq_slot(A, s, valid, h == 0 && part0 == 0 && tid == 0) < 0) return;
+  const int col0 = 16 * (part0 * NW + w), col = col0 + c16;
   const long long so = ((long long)s * A.H + h) * D * D + col;
   auto state_row = [&](int rt, int i) { return 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i; };
   f4 Gt[2 * NB];
@@ -77,19 +78,19 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
   const int hq = h / A.grp;
   const int nc = (t1 - t0 + kChunk - 1) / kChunk;
   const unsigned lds0 = lds_offset(buf), lane16 = 16 * lane;
-  auto fetch = [&](int c, int n) {
+  auto fetch = [&](int c, bool early) {
     const char* const key = A.ws + ((j0 + c) * A.Hq + hq) * L::key;
     const char* const head = heads + ((j0 + c) * A.H + h) * L::head;
-    const unsigned at = lds0 + (NBUF == 2 ? (c & 1) * part : 0);
-    if (n < 3) {
-      copy_block<NW>(key, at, n * L::offKT, (n + 1) * L::offKT, w, lane16);
+    if (early) {
+      copy_block<NW>(key, lds0, 0, L::offKT, w, lane16);
+      copy_block<NW>(key, lds0, L::offQ, keyN, w, lane16);
+      copy_block<NW>(head + L::offTt, lds0 + offTt, 0, triN, w, lane16);
     } else {
-      copy_block<NW>(head + L::offTt, at + offTt, 0, triN, w, lane16);
-      copy_block<NW>(head + L::offTab, at + offTab, 0, 2048, w, lane16);
+      copy_block<NW>(key, lds0, L::offKT, L::offQ, w, lane16);
+      copy_block<NW>(head + L::offTab, lds0 + offTab + (c & 1) * L::tab, 0, L::tab, w, lane16);
     }
   };
-  char* const piece = buf + NBUF * part + w * trN;
-  const int col0 = 16 * ((int)blockIdx.y * NW + w);
+  char* const piece = buf + part + w * trN;
   const Tr orows(piece, A.os, col0, lane), vrows(piece, (long long)A.H * D, col0, lane);
   const TrF krows(piece, D, col0, lane);
   typename Tr::u4 o[Tr::NL];
@@ -98,18 +99,17 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     orows.load(rows_at<DT>(B.d_out, tc, A.os, h * D, D, t1 - tc < kChunk ? t1 - tc : kChunk), o);
   };
   if (nc) {
-#pragma unroll
-    for (int n = 0; n < 4; n++) fetch(nc - 1, n);
+    fetch(nc - 1, true);
+    fetch(nc - 1, false);
     fetch_o(nc - 1);
   }
   const f4 zero = {0, 0, 0, 0};
   for (int c = nc - 1; c >= 0; c--) {
-    const char* const lds = buf + (NBUF == 2 ? (c & 1) * part : 0);
+    const char* const lds = buf;
     const int tc = t0 + c * kChunk, len = t1 - tc < kChunk ? t1 - tc : kChunk;
     wait_copies();
     __syncthreads();
-    const bool more = NBUF == 2 && c;
-    const float* const tab = (const float*)(lds + offTab);
+    const float* const tab = (const float*)(lds + offTab + (c & 1) * L::tab);
     auto frag = [&](int off, int n, int p, int f) { return *(const h8*)(lds + off + (p * n + f) * kFrag + lane16); };
     auto rows = [&](int t, int rt) { return *(const f4*)(tab + t + 32 * (rt >> 1) + 8 * g + 4 * (rt & 1)); };
     h8 f[L::NF], fl[NPI == 2 ? L::NF : 1];
@@ -131,7 +131,6 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     read(L::offK);
     f4 dO[4];
     orows.to_acc(o, dO);
-    if (more) fetch(c - 1, 0);
     if (c) fetch_o(c - 1);
     ahead();
     {
@@ -160,7 +159,6 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     }
     ahead();
     read_tri(offP);
-    if (more) fetch(c - 1, 1);
     ahead();
     auto tri = [&](int p, const h8* b, bool first) {
 #pragma unroll
@@ -175,7 +173,6 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     if constexpr (NPI == 2) tri(0, xl, false);
     ahead();
     read_tri(offTt);
-    if (more) fetch(c - 1, 2);
     ahead();
     // dW = P^T dO + D K dS1, then Y = T^T dW
     f4 Y[4];
@@ -191,6 +188,8 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     tri(1, xh, false);
     ahead();
     read(L::offQ);
+    __syncthreads();
+    if (c) fetch(c - 1, true);
     ahead();
     {
       f4 dv[4];
@@ -202,7 +201,6 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
       krows.template store_all<4>(keep.Y + ((j0 + c) * A.H + h) * 64 * D, Y, 1.0f);
       vrows.store(rows_at<DT>(B.dv, tc, (long long)A.H * D, h * D, D, len), dv);
     }
-    if (more) fetch(c - 1, 3);
     // dS0 = G_C dS1 + Q^T G dO - K^T G diag(beta) Y, in the gradient's units
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) {
@@ -242,14 +240,11 @@ __global__ __launch_bounds__(64 * NW) void k_chunk_reverse(GradArgs B, Keep keep
     update();
     ahead();
     read(L::offKT);
+    __syncthreads();
+    if (c) fetch(c - 1, false);
     ahead();
     to_planes<2, 2>(Y, iu, xh, xl);
     update();
-    if (NBUF == 1 && c) {
-      __syncthreads();
-#pragma unroll
-      for (int n = 0; n < 4; n++) fetch(c - 1, n);
-    }
   }
   if (B.dS_in) krows.template store_all<2 * NB>(B.dS_in + ((long long)s * A.H + h) * D * D, Gt, unit);
 }
@@ -868,24 +863,33 @@ size_t bytes(const SeqArgs& a) {
 }
 
 template <int D, int DT>
-hipError_t launch(GradArgs b, hipStream_t s) {
-  SeqArgs& a = b.f;
+hipError_t launch(const GradArgs& b, hipStream_t s) {
+  const SeqArgs& a = b.f;
   const size_t n = (size_t)chunk_slots(a.T, a.N) * a.H;
   Keep keep;
   keep.S = (float*)(a.ws + fixed_bytes<D, DT>(a));
   keep.G = keep.S + n * D * D;
   keep.W = keep.G + n * D * D;
   keep.Y = keep.W + n * 64 * D;
-  const dim3 slots((unsigned)chunk_slots(a.T, a.N), a.Hq), tiles((unsigned)((long long)a.N * a.H));
-  unsigned* const status = a.status;
-  a.status = nullptr;  // reported once, by the reverse pass
+  const dim3 slots((unsigned)chunk_slots(a.T, a.N), a.Hq);
   if (a.T > 0) {
     hipLaunchKernelGGL((k_chunk_prep<D, DT, LayB<D, DT>>), slots, dim3(256), 0, s, a);
-    hipLaunchKernelGGL((k_chunk_state<D, DT, D / 16, LayB<D, DT>, kKeep>), tiles, dim3(4 * D), 0, s, a, keep.S, keep.W, Segs{});
+    if (hipError_t e = hipGetLastError()) return e;
   }
-  a.status = status;
-  hipLaunchKernelGGL((k_chunk_reverse<D, DT, D / 16>), tiles, dim3(4 * D), 0, s, b, keep);
-  if (a.T > 0) hipLaunchKernelGGL((k_chunk_grad<D, DT>), slots, dim3(4 * D), 0, s, b, keep);
+  const hipError_t rc = with_state_waves<D, DT>(a, 1, [&](auto nw) {
+    constexpr int NW = nw.value;
+    const dim3 tiles(workgroups<NW>(a, D));
+    if (a.T > 0) {
+      SeqArgs quiet = a;
+      quiet.status = nullptr;  // flags are raised once, by the reverse pass
+      hipLaunchKernelGGL((k_chunk_state<D, DT, NW, LayB<D, DT>, kKeep>), tiles, dim3(64 * NW), 0, s, quiet, keep.S, keep.W, Segs{});
+      if (hipError_t e = hipGetLastError()) return e;
+    }
+    hipLaunchKernelGGL((k_chunk_reverse<D, DT, NW>), tiles, dim3(64 * NW), 0, s, b, keep);
+    return hipGetLastError();
+  });
+  if (rc != hipSuccess || a.T == 0) return rc;
+  hipLaunchKernelGGL((k_chunk_grad<D, DT>), slots, dim3(4 * D), 0, s, b, keep);
   return hipGetLastError();
 }
 
