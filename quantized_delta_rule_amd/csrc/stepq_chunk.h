@@ -267,6 +267,16 @@ struct Slice {
 #pragma unroll
     for (int n = 0; n < NL; n++) __builtin_amdgcn_raw_buffer_store_b128(gather(y + TP * n), r, off(n), 0, 0);
   }
+  // NT row tiles of a packed binary32 matrix (this slice made with its stride), all rows
+  template <int NT>
+  __device__ void load_all(const float* src, f4* y) const {
+    static_assert(F);
+    u4 x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; n++) x[n] = *(const u4*)((const char*)src + off(n));
+#pragma unroll
+    for (int n = 0; n < NT; n += NL) to_acc(x + n, y + n);
+  }
   // NT row tiles times s to the rows of a packed binary32 matrix (this slice made with its stride), all rows
   template <int NT>
   __device__ void store_all(float* dst, const f4* y, float s) const {

@@ -558,7 +558,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
   if (t0 == t1 && MODE == kKeep) return;
   if (t0 == t1 && MODE == kForward && (!A.S_out || A.S_out == A.S_in)) return;
   const int col0 = 16 * (part0 * NW + w), col = col0 + c16;
-  const long long so = ((long long)slot * A.H + h) * D * D + col;
+  const long long so = ((long long)slot * A.H + h) * D * D;
   const int nc = (t1 - t0 + kChunk - 1) / kChunk;
   int c_first = 0, c_end = nc;
   long long seg = 0;
@@ -566,33 +566,12 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
     const int n = seg_chunks(nc, segs.P);
     c_first = min((int)blockIdx.y * n, nc);
     c_end = min(c_first + n, nc);
-    seg = (tile * segs.P + blockIdx.y) * D * D + col;
+    seg = (((long long)s * A.H + h) * segs.P + blockIdx.y) * D * D;
   }
   const bool unit_start = MODE == kSegment && blockIdx.z;
-  auto state_row = [&](int rt, int i) { return 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i; };
-  f4 St[2 * NB];
-#pragma unroll
-  for (int rt = 0; rt < 2 * NB; rt++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int r = state_row(rt, i);
-      if (MODE == kSegment) St[rt][i] = unit_start && r == col ? 1.0f : 0.0f;
-      else if (MODE == kReadout) St[rt][i] = segs.S[seg + (long long)r * D];
-      else St[rt][i] = A.S_in ? A.S_in[so + (long long)r * D] : 0.0f;
-    }
-  float unit = 0x1p-10f;  // an empty state takes its unit from the first W
-  auto rescale = [&](float m) {  // largest magnitude into [2^11, 2^12)
-    float inv;
-    const float f = m > 0.0f ? scale_of(m, inv) : (inv = 1.0f);
-    unit *= inv;
-#pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= f;
-  };
-  {
-    const float m = tiles_max<2 * NB>(St);
-    if (m > 0.0f) unit = 1.0f;
-    rescale(m);
-  }
+  char* const piece = buf + part + w * trN;
+  const Tr vrows(piece, A.vs, col0, lane), orows(piece, A.os, col0, lane);
+  const TrF krows(piece, D, col0, lane);
   const long long j0 = first_slot(A, s);
   const char* const heads = A.ws + key_bytes<Y>(A);
   const int hq = h / A.grp;
@@ -614,9 +593,6 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
       if (w == 1 && lane < (Y::tab - 1024) / 16) copy_to_lds(head + Y::offTab + 1024, at + 1024, lane16);
     }
   };
-  char* const piece = buf + part + w * trN;
-  const Tr vrows(piece, A.vs, col0, lane), orows(piece, A.os, col0, lane);
-  const TrF krows(piece, D, col0, lane);
   typename Tr::u4 v[Tr::NL];  // V of the next chunk, as it lies in memory
   auto fetch_v = [&](int c) {
     const int tc = t0 + c * kChunk;
@@ -626,7 +602,27 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
   if (c_first < c_end) {
     fetch(c_first, true);
     fetch(c_first, false);
-    fetch_v(c_first);
+  }
+  f4 St[2 * NB];
+#pragma unroll
+  for (int rt = 0; rt < 2 * NB; rt++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) St[rt][i] = unit_start && 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i == col ? 1.0f : 0.0f;
+  if (const float* const first = MODE == kSegment ? nullptr : MODE == kReadout ? segs.S + seg : A.S_in ? A.S_in + so : nullptr)
+    krows.template load_all<2 * NB>(first, St);
+  if (c_first < c_end) fetch_v(c_first);
+  float unit = 0x1p-10f;  // an empty state takes its unit from the first W
+  auto rescale = [&](float m) {  // largest magnitude into [2^11, 2^12)
+    float inv;
+    const float f = m > 0.0f ? scale_of(m, inv) : (inv = 1.0f);
+    unit *= inv;
+#pragma unroll
+    for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= f;
+  };
+  {
+    const float m = tiles_max<2 * NB>(St);
+    if (m > 0.0f) unit = 1.0f;
+    rescale(m);
   }
   const f4 zero = {0, 0, 0, 0};
   for (int c = c_first; c < c_end; c++) {
@@ -786,12 +782,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
   if (MODE == kForward || (MODE == kReadout && c_end == nc && (c_first < nc || (nc == 0 && blockIdx.y == 0))))
     dst = A.S_out ? A.S_out + so : nullptr;
   if (MODE == kSegment) dst = segs.MN + (unit_start ? (long long)A.N * A.H * segs.P * D * D : 0LL) + seg;
-  if (dst) {
-#pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) dst[(long long)state_row(rt, i) * D] = St[rt][i] * unit;
-  }
+  if (dst) krows.template store_all<2 * NB>(dst, St, unit);
 }
 
 // First states of the segments: S_0 = S_in, S_{p+1} = M_p S_p + N_p.  A wave owns 16 columns, as in the pass,

@@ -52,27 +52,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep k
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
   if (seq_slot(A, s, valid, h == 0 && part0 == 0 && tid == 0) < 0) return;
-  const int col0 = 16 * (part0 * NW + w), col = col0 + c16;
-  const long long so = ((long long)s * A.H + h) * D * D + col;
-  auto state_row = [&](int rt, int i) { return 32 * (rt >> 1) + 8 * g + 4 * (rt & 1) + i; };
-  f4 Gt[2 * NB];
-#pragma unroll
-  for (int rt = 0; rt < 2 * NB; rt++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) Gt[rt][i] = B.dS_out ? B.dS_out[so + (long long)state_row(rt, i) * D] : 0.0f;
-  float unit = 0x1p-10f;
-  auto rescale = [&](float m) {
-    float inv;
-    const float f = m > 0.0f ? scale_of(m, inv) : (inv = 1.0f);
-    unit *= inv;
-#pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] *= f;
-  };
-  {
-    const float m = tiles_max<2 * NB>(Gt);
-    if (m > 0.0f) unit = 1.0f;
-    rescale(m);
-  }
+  const int col0 = 16 * (part0 * NW + w);
+  char* const piece = buf + part + w * trN;
+  const Tr orows(piece, A.os, col0, lane), vrows(piece, (long long)A.H * D, col0, lane);
+  const TrF krows(piece, D, col0, lane);
+  const long long so = ((long long)s * A.H + h) * D * D;
   const long long j0 = first_slot(A, s);
   const char* const heads = A.ws + key_bytes<L>(A);
   const int hq = h / A.grp;
@@ -90,9 +74,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep k
       copy_block<NW>(head + L::offTab, lds0 + offTab + (c & 1) * L::tab, 0, L::tab, w, lane16);
     }
   };
-  char* const piece = buf + part + w * trN;
-  const Tr orows(piece, A.os, col0, lane), vrows(piece, (long long)A.H * D, col0, lane);
-  const TrF krows(piece, D, col0, lane);
   typename Tr::u4 o[Tr::NL];
   auto fetch_o = [&](int c) {
     const int tc = t0 + c * kChunk;
@@ -101,7 +82,24 @@ __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep k
   if (nc) {
     fetch(nc - 1, true);
     fetch(nc - 1, false);
-    fetch_o(nc - 1);
+  }
+  f4 Gt[2 * NB];
+#pragma unroll
+  for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] = f4{0, 0, 0, 0};
+  if (B.dS_out) krows.template load_all<2 * NB>(B.dS_out + so, Gt);
+  if (nc) fetch_o(nc - 1);
+  float unit = 0x1p-10f;
+  auto rescale = [&](float m) {
+    float inv;
+    const float f = m > 0.0f ? scale_of(m, inv) : (inv = 1.0f);
+    unit *= inv;
+#pragma unroll
+    for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] *= f;
+  };
+  {
+    const float m = tiles_max<2 * NB>(Gt);
+    if (m > 0.0f) unit = 1.0f;
+    rescale(m);
   }
   const f4 zero = {0, 0, 0, 0};
   for (int c = nc - 1; c >= 0; c--) {
@@ -246,7 +244,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep k
     to_planes<2, 2>(Y, iu, xh, xl);
     update();
   }
-  if (B.dS_in) krows.template store_all<2 * NB>(B.dS_in + ((long long)s * A.H + h) * D * D, Gt, unit);
+  if (B.dS_in) krows.template store_all<2 * NB>(B.dS_in + so, Gt, unit);
 }
 
 // ---------------------------------------------------------------------------------------------
