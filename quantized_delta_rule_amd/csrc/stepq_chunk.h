@@ -46,7 +46,7 @@ template <int D, int DT> struct LayF {
   static constexpr int key = 3 * NPI * NF * kFrag, offKK = 0, offQK = 0;  // none
   static constexpr int offT = 0, offP = 2 * kTri * kFrag, offTab = offP + NPO * kTri * kFrag;
   static constexpr int offTt = offTab;  // none
-  static constexpr int head = offTab + 2048, tab = 1280;  // bytes of the tables that the pass reads
+  static constexpr int tab = 1280, head = offTab + tab;  // bytes of the tables that the pass reads
 };
 // Workspace of the gradient.  Q^T in Q's place, K K^T [t][s] and Q K^T [s][t] (binary32, t >= s within 32-row
 // blocks) behind the fragments; T, T^T, P^T (two planes each).  Then, per chunk slot and value head in binary32: the

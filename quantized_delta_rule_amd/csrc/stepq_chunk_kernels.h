@@ -8,7 +8,15 @@
 namespace stepq {
 namespace dlt {
 
-constexpr int kPitch = 68;  // floats of a row of the 64 x 64 matrices in LDS
+// 64 rows of N elements in LDS, 16 bytes and, from row to row of 16, 64 bytes apart: the rows of an operand
+// (perm_row) and of K^T's columns are on different banks.
+template <class T, int N>
+struct LdsRows {
+  static constexpr int pad = 16 / (int)sizeof(T), pitch = N + pad;
+  T x[64 * pitch + 3 * 4 * pad];
+  __device__ T* operator[](int r) { return x + r * pitch + (r >> 4) * 4 * pad; }
+};
+using Square = LdsRows<float, 64>;
 
 // ---------------------------------------------------------------------------------------------
 // local matrices
@@ -27,15 +35,15 @@ struct PrepSmem {
   static constexpr int NPI = kInPlanes<DT>;
   union {
     struct {
-      _Float16 K[NPI][64][D + 8], Q[QT ? NPI : 1][QT ? 64 : 1][D + 8];
+      LdsRows<_Float16, D> K[NPI], Q[QT ? NPI : 1];
     };
-    struct {
-      float X[64][kPitch];  // A, then T but for its lower left quarter
-      float Z[32][36];      // T's lower left quarter
+    struct {               // of two heads
+      Square X[2];         // A, then T but for its lower left quarter
+      float Z[2][32][36];  // T's lower left quarter
     };
   };
-  float gate[5][64];  // a, pre8, suf8, pre32, suf32; every wave writes the same values for itself
-  float isk[64], isq[64], be[64], most[4];
+  float gate[2][5][64];  // a, pre8, suf8, pre32, suf32; every wave writes the same values for itself
+  float isk[64], isq[64], be[2][64], most[2][6];
 };
 
 // The wave's 16 rows of q or k as scaled planes (a lane: row `row`, elements 32 ks + 8 g ..); returns the
@@ -65,7 +73,7 @@ __device__ __forceinline__ float load_rows(const void* src, long long at, int g,
 // blocks by forward substitution (a column a lane, both blocks at once), then X10 = -X11 (A10 X00) on
 // binary32 matrix instructions.  Substitution, not a power series: keys that repeat make A's powers large.
 // Returns the largest magnitude written, columns times be.
-__device__ __forceinline__ float invert_block(float (*X)[kPitch], const float* be, int r0, int lane) {
+__device__ __forceinline__ float invert_block(Square& X, const float* be, int r0, int lane) {
   const int c = lane & 15, g = lane >> 4;
   float m = 0.0f;
   if (lane < 32) {
@@ -113,7 +121,7 @@ __device__ __forceinline__ float invert_block(float (*X)[kPitch], const float* b
 }
 
 // T's lower left 32 x 32 quarter, -X11 (A10 X00) with 32 x 32 blocks, one 16 x 16 tile a wave, into Z.
-__device__ __forceinline__ float invert_corner(const float (*X)[kPitch], float (*Z)[36], const float* be, int w, int lane) {
+__device__ __forceinline__ float invert_corner(Square& X, float (*Z)[36], const float* be, int w, int lane) {
   const int c = lane & 15, g = lane >> 4, cb = w & 1, r = 2 + (w >> 1);
   auto half = [&](int row) {
     f4 y = {0, 0, 0, 0};
@@ -196,7 +204,7 @@ __global__ __launch_bounds__(256, Y::grad ? 2 : 3) void k_chunk_prep(SeqArgs A) 
 #pragma unroll
         for (int n = 0; n < NPI; n++) {
           if (kk_on) fk[n] = *(const h8*)&sm.K[n][row][32 * ks + 8 * g];
-          if (Y::grad && qk_on) fq[n] = *(const h8*)&sm.Q[Y::grad ? n : 0][Y::grad ? row : 0][32 * ks + 8 * g];
+          if (Y::grad && qk_on) fq[n] = *(const h8*)&sm.Q[Y::grad ? n : 0][row][32 * ks + 8 * g];
         }
         if (kk_on) {
           a[p] = mfma(fk[0], kf[ks][0], a[p]);
@@ -253,220 +261,232 @@ __global__ __launch_bounds__(256, Y::grad ? 2 : 3) void k_chunk_prep(SeqArgs A) 
     }
   };
   gates(0);
-  for (int hh = 0; hh < A.grp; hh++) {
-    const int h = hq * A.grp + hh;
-    char* const head = A.ws + key_bytes<Y>(A) + (j * A.H + h) * Y::head;
-    float* const tab = (float*)(head + Y::offTab);
-    const float al = al_next, be = be_next;
-    if (hh + 1 < A.grp) gates(hh + 1);
-    __syncthreads();  // the last head's gates and T have been read (the first head: K and Q)
-    // running products, token = lane
-    float(*const gt)[64] = sm.gate;
-    float p8 = al, s8 = 1.0f;
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      const float x = __shfl_up(p8, o);
-      if ((lane & 7) >= o) p8 *= x;
-    }
-    {
-      float x = __shfl_down(al, 1);
-      s8 = (lane & 7) < 7 ? x : 1.0f;
+  char* const heads = A.ws + key_bytes<Y>(A) + (j * A.H + hq * A.grp) * Y::head;
+  // Two heads at a time: the four diagonal blocks of their A keep all waves busy
+  for (int h0 = 0; h0 < A.grp; h0 += 2) {
+    const int nh = min(2, A.grp - h0);
+    __syncthreads();  // the last heads' T has been read (the first heads: K and Q)
+    for (int u = 0; u < nh; u++) {
+      char* const head = heads + (h0 + u) * Y::head;
+      float* const tab = (float*)(head + Y::offTab);
+      const float al = al_next, be = be_next;
+      if (h0 + u + 1 < A.grp) gates(h0 + u + 1);
+      // running products, token = lane
+      float(*const gt)[64] = sm.gate[u];
+      float p8 = al, s8 = 1.0f;
 #pragma unroll
       for (int o = 1; o < 8; o <<= 1) {
-        x = __shfl_down(s8, o);
-        if ((lane & 7) + o < 8) s8 *= x;
+        const float x = __shfl_up(p8, o);
+        if ((lane & 7) >= o) p8 *= x;
       }
-    }
-    float B[8];  // whole groups of 8
+      {
+        float x = __shfl_down(al, 1);
+        s8 = (lane & 7) < 7 ? x : 1.0f;
 #pragma unroll
-    for (int n = 0; n < 8; n++) B[n] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p8), 8 * n + 7));
-    float p32 = p8, s32 = s8;
-    {
-      const int n = (lane >> 3) & 3;
-      const bool up = lane >= 32;
-      const float b0 = up ? B[4] : B[0], b1 = up ? B[5] : B[1], b2 = up ? B[6] : B[2], b3 = up ? B[7] : B[3];
-      if (n > 0) p32 *= b0;
-      if (n > 1) p32 *= b1;
-      if (n > 2) p32 *= b2;
-      if (n < 3) s32 *= b3;
-      if (n < 2) s32 *= b2;
-      if (n < 1) s32 *= b1;
-    }
-    gt[0][lane] = al;
-    gt[1][lane] = p8;
-    gt[2][lane] = s8;
-    gt[3][lane] = p32;
-    gt[4][lane] = s32;
-    __builtin_amdgcn_wave_barrier();
-    const float BL = B[0] * B[1] * B[2] * B[3], BU = B[4] * B[5] * B[6] * B[7];
-    if (w == 0) {
-      const float G = lane < 32 ? p32 : BL * p32, L63 = lane < 32 ? s32 * BU : s32;
-      const float ik0 = sm.isk[lane], iq0 = sm.isq[lane];
-      tab[kTabU + lane] = (Y::grad ? be * G : G) * ik0;
-      tab[kTabQ + lane] = G * iq0;
-      tab[kTabD + lane] = L63 * ik0;
-      if (lane == 63) tab[kTabG + 63] = G;
-      if constexpr (Y::grad) {
-        tab[kTabB + lane] = be;
-        tab[kTabL + lane] = L63;
-        tab[kTabIK + lane] = ik0;
-        tab[kTabIQ + lane] = iq0;
-      }
-    }
-    const float be_own = __shfl(be, own);
-    // own token: place in its block, group, place in that; opaque: the predicates made from them are not
-    // kept in scalar registers across heads
-    int po = own & 31, pg = g;
-    asm("" : "+v"(po), "+v"(pg));
-    const int og = po >> 3, oi = po & 7;
-    // L between `own` and the 8 tokens 8 g + e of its own block: down: own is the later one
-    float Lo[8];
-    auto in_block = [&](bool down) {
-      const float *a = &gt[0][32 * wb + 8 * g], *pre = &gt[1][32 * wb + 8 * g], *suf = &gt[2][32 * wb + 8 * g];
-      const int lo = down ? pg : og, hi = down ? og : pg;  // earlier and later group
-      const float b1 = wb ? B[5] : B[1], b2 = wb ? B[6] : B[2];
-      float mid = gt[down ? 1 : 2][own];
-      if (lo == 0 && hi > 1) mid *= b1;
-      if (lo <= 1 && hi == 3) mid *= b2;
-      float c = 1.0f;
-      if (down) {
-#pragma unroll
-        for (int e = 7; e >= 0; e--) {
-          const float l = pg < og ? mid * suf[e] : c;
-          Lo[e] = 8 * pg + e <= po ? l : 0.0f;
-          if (e <= oi) c *= a[e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-          if (e > oi) c *= a[e];
-          const float l = pg > og ? mid * pre[e] : c;
-          Lo[e] = 8 * pg + e >= po ? l : 0.0f;
+        for (int o = 1; o < 8; o <<= 1) {
+          x = __shfl_down(s8, o);
+          if ((lane & 7) + o < 8) s8 *= x;
         }
       }
-    };
-    in_block(true);
-    float pv[2][8];
-    if (w == 0) sm.be[lane] = be;
+      float B[8];  // whole groups of 8
 #pragma unroll
-    for (int nb = 0; nb < 2; nb++) {
-      if (nb > wb) continue;
-      float av[8];
-      const float pre = gt[3][own];
-#pragma unroll
-      for (int e = 0; e < 8; e++) {
-        const float l = nb == wb ? Lo[e] : pre * gt[4][8 * g + e];
-        const bool strict = nb < wb || 8 * pg + e < po;
-        av[e] = strict ? be_own * (kk[nb][e] * l) : 0.0f;
-        if constexpr (!Y::grad) pv[nb][e] = qk[nb][e] * l;
+      for (int n = 0; n < 8; n++) B[n] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(p8), 8 * n + 7));
+      float p32 = p8, s32 = s8;
+      {
+        const int n = (lane >> 3) & 3;
+        const bool up = lane >= 32;
+        const float b0 = up ? B[4] : B[0], b1 = up ? B[5] : B[1], b2 = up ? B[6] : B[2], b3 = up ? B[7] : B[3];
+        if (n > 0) p32 *= b0;
+        if (n > 1) p32 *= b1;
+        if (n > 2) p32 *= b2;
+        if (n < 3) s32 *= b3;
+        if (n < 2) s32 *= b2;
+        if (n < 1) s32 *= b1;
       }
-      store8<kF32>(&sm.X[own][0], 32 * nb + 8 * g, av);
-    }
-    if constexpr (Y::grad) {
-      in_block(false);
-#pragma unroll
-      for (int nb = 0; nb < 2; nb++) {
-        if (nb < wb) continue;
-        const float suf = gt[4][own];
-#pragma unroll
-        for (int e = 0; e < 8; e++) pv[nb][e] = qk[nb][e] * (nb == wb ? Lo[e] : suf * gt[3][32 + 8 * g + e]);
-      }
-    }
-    __syncthreads();
-    float m = 0.0f;
-    if (wp == 0) m = invert_block(sm.X, sm.be, 32 * wb, lane);
-    // P's (gradient: P^T's) fragments meanwhile
-    {
-      float mp = 0.0f;
-#pragma unroll
-      for (int nb = 0; nb < 2; nb++)
-        if (Y::grad ? nb >= wb : nb <= wb)
-#pragma unroll
-          for (int e = 0; e < 8; e++) mp = fmaxf(mp, fabsf(pv[nb][e]));
-      float ip;
-      const float sp = scale_of(col_max(mp), ip);
-      if (g == 0) tab[kTabP + own] = ip;
-#pragma unroll
-      for (int nb = 0; nb < 2; nb++)
-        if (Y::grad ? nb >= wb : nb <= wb) {
-          h8 hi, lo;
-          split8<2>(pv[nb], sp, hi, lo);
-          char* const dst = head + Y::offP + (Y::grad ? up_frag(w, nb) : tri_frag(w, nb)) * kFrag + lane * 16;
-          *(h8*)dst = hi;
-          if constexpr (NPO == 2) *(h8*)(dst + kTri * kFrag) = lo;
+      gt[0][lane] = al;
+      gt[1][lane] = p8;
+      gt[2][lane] = s8;
+      gt[3][lane] = p32;
+      gt[4][lane] = s32;
+      __builtin_amdgcn_wave_barrier();
+      const float BL = B[0] * B[1] * B[2] * B[3], BU = B[4] * B[5] * B[6] * B[7];
+      if (w == 0) {
+        const float G = lane < 32 ? p32 : BL * p32, L63 = lane < 32 ? s32 * BU : s32;
+        const float ik0 = sm.isk[lane], iq0 = sm.isq[lane];
+        tab[kTabU + lane] = (Y::grad ? be * G : G) * ik0;
+        tab[kTabQ + lane] = G * iq0;
+        tab[kTabD + lane] = L63 * ik0;
+        if (lane == 63) tab[kTabG + 63] = G;
+        if constexpr (Y::grad) {
+          tab[kTabB + lane] = be;
+          tab[kTabL + lane] = L63;
+          tab[kTabIK + lane] = ik0;
+          tab[kTabIQ + lane] = iq0;
         }
-    }
-    __syncthreads();
-    m = fmaxf(m, invert_corner(sm.X, sm.Z, sm.be, w, lane));
-    m = fmaxf(m, __shfl_xor(m, 1));
-    m = fmaxf(m, __shfl_xor(m, 2));
-    m = fmaxf(m, __shfl_xor(m, 4));
-    m = fmaxf(m, __shfl_xor(m, 8));
-    m = col_max(m);
-    if (lane == 0) sm.most[w] = m;
-    __syncthreads();
-    // T's fragments of row tile w
-    auto T_row = [&](int ks, float* x) {
-      const float* src = wb && !ks ? &sm.Z[own - 32][8 * g] : &sm.X[own][32 * ks + 8 * g];
-      const f4 x0 = *(const f4*)src, x1 = *(const f4*)(src + 4);
-#pragma unroll
-      for (int e = 0; e < 4; e++) x[e] = x0[e], x[4 + e] = x1[e];
-    };
-    if constexpr (!Y::grad) {
-      float iT;
-      const float sT = scale_of(fmaxf(fmaxf(sm.most[0], sm.most[1]), fmaxf(sm.most[2], sm.most[3])), iT);
-      if (tid == 0) tab[kTabG + 62] = iT;
-#pragma unroll
-      for (int ks = 0; ks < 2; ks++) {
-        if (ks > wb) continue;
-        float x[8];
-        T_row(ks, x);
-#pragma unroll
-        for (int e = 0; e < 8; e++) x[e] *= sm.be[32 * ks + 8 * g + e];
-        h8 hi, lo;
-        split8<2>(x, sT, hi, lo);
-        char* const dst = head + Y::offT + tri_frag(w, ks) * kFrag + lane * 16;
-        *(h8*)dst = hi;
-        *(h8*)(dst + kTri * kFrag) = lo;
       }
-    } else {
-      // T and T^T, rows scaled
-      float x[2][8], y[2][8], mt = 0.0f, mu = 0.0f;
+      const float be_own = __shfl(be, own);
+      // own token: place in its block, group, place in that; opaque: the predicates made from them are not
+      // kept in scalar registers across heads
+      int po = own & 31, pg = g;
+      asm("" : "+v"(po), "+v"(pg));
+      const int og = po >> 3, oi = po & 7;
+      // L between `own` and the 8 tokens 8 g + e of its own block: down: own is the later one
+      float Lo[8];
+      auto in_block = [&](bool down) {
+        const float *a = &gt[0][32 * wb + 8 * g], *pre = &gt[1][32 * wb + 8 * g], *suf = &gt[2][32 * wb + 8 * g];
+        const int lo = down ? pg : og, hi = down ? og : pg;  // earlier and later group
+        const float b1 = wb ? B[5] : B[1], b2 = wb ? B[6] : B[2];
+        float mid = gt[down ? 1 : 2][own];
+        if (lo == 0 && hi > 1) mid *= b1;
+        if (lo <= 1 && hi == 3) mid *= b2;
+        float c = 1.0f;
+        if (down) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ks++) {
-        if (ks <= wb) {
-          T_row(ks, x[ks]);
-#pragma unroll
-          for (int e = 0; e < 8; e++) mt = fmaxf(mt, fabsf(x[ks][e]));
-        }
-        if (ks >= wb) {
+          for (int e = 7; e >= 0; e--) {
+            const float l = pg < og ? mid * suf[e] : c;
+            Lo[e] = 8 * pg + e <= po ? l : 0.0f;
+            if (e <= oi) c *= a[e];
+          }
+        } else {
 #pragma unroll
           for (int e = 0; e < 8; e++) {
-            y[ks][e] = !wb && ks ? sm.Z[8 * g + e][own] : sm.X[32 * ks + 8 * g + e][own];
-            mu = fmaxf(mu, fabsf(y[ks][e]));
+            if (e > oi) c *= a[e];
+            const float l = pg > og ? mid * pre[e] : c;
+            Lo[e] = 8 * pg + e >= po ? l : 0.0f;
           }
         }
-      }
-      float it, iu;
-      const float st = scale_of(col_max(mt), it), su = scale_of(col_max(mu), iu);
-      if (g == 0) {
-        tab[kTabT + own] = it;
-        tab[kTabTt + own] = iu;
-      }
+      };
+      in_block(true);
+      float pv[2][8];
+      if (w == 0) sm.be[u][lane] = be;
 #pragma unroll
-      for (int ks = 0; ks < 2; ks++) {
-        h8 hi, lo;
-        if (ks <= wb) {
-          split8<2>(x[ks], st, hi, lo);
+      for (int nb = 0; nb < 2; nb++) {
+        if (nb > wb) continue;
+        float av[8];
+        const float pre = gt[3][own];
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const float l = nb == wb ? Lo[e] : pre * gt[4][8 * g + e];
+          const bool strict = nb < wb || 8 * pg + e < po;
+          av[e] = strict ? be_own * (kk[nb][e] * l) : 0.0f;
+          if constexpr (!Y::grad) pv[nb][e] = qk[nb][e] * l;
+        }
+        store8<kF32>(&sm.X[u][own][0], 32 * nb + 8 * g, av);
+      }
+      if constexpr (Y::grad) {
+        in_block(false);
+#pragma unroll
+        for (int nb = 0; nb < 2; nb++) {
+          if (nb < wb) continue;
+          const float suf = gt[4][own];
+#pragma unroll
+          for (int e = 0; e < 8; e++) pv[nb][e] = qk[nb][e] * (nb == wb ? Lo[e] : suf * gt[3][32 + 8 * g + e]);
+        }
+      }
+      // P's (gradient: P^T's) fragments
+      {
+        float mp = 0.0f;
+#pragma unroll
+        for (int nb = 0; nb < 2; nb++)
+          if (Y::grad ? nb >= wb : nb <= wb)
+#pragma unroll
+            for (int e = 0; e < 8; e++) mp = fmaxf(mp, fabsf(pv[nb][e]));
+        float ip;
+        const float sp = scale_of(col_max(mp), ip);
+        if (g == 0) tab[kTabP + own] = ip;
+#pragma unroll
+        for (int nb = 0; nb < 2; nb++)
+          if (Y::grad ? nb >= wb : nb <= wb) {
+            h8 hi, lo;
+            split8<2>(pv[nb], sp, hi, lo);
+            char* const dst = head + Y::offP + (Y::grad ? up_frag(w, nb) : tri_frag(w, nb)) * kFrag + lane * 16;
+            *(h8*)dst = hi;
+            if constexpr (NPO == 2) *(h8*)(dst + kTri * kFrag) = lo;
+          }
+      }
+    }
+    __syncthreads();
+    auto most = [&](float m, int u, int n) {
+      m = fmaxf(m, __shfl_xor(m, 1));
+      m = fmaxf(m, __shfl_xor(m, 2));
+      m = fmaxf(m, __shfl_xor(m, 4));
+      m = fmaxf(m, __shfl_xor(m, 8));
+      m = col_max(m);
+      if (lane == 0) sm.most[u][n] = m;
+    };
+    if (wb < nh) most(invert_block(sm.X[wb], sm.be[wb], 32 * wp, lane), wb, wp);
+    __syncthreads();
+    for (int u = 0; u < nh; u++) most(invert_corner(sm.X[u], sm.Z[u], sm.be[u], w, lane), u, 2 + w);
+    __syncthreads();
+    for (int u = 0; u < nh; u++) {
+      char* const head = heads + (h0 + u) * Y::head;
+      float* const tab = (float*)(head + Y::offTab);
+      // T's fragments of row tile w
+      auto T_row = [&](int ks, float* x) {
+        const float* src = wb && !ks ? &sm.Z[u][own - 32][8 * g] : &sm.X[u][own][32 * ks + 8 * g];
+        const f4 x0 = *(const f4*)src, x1 = *(const f4*)(src + 4);
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[e] = x0[e], x[4 + e] = x1[e];
+      };
+      if constexpr (!Y::grad) {
+        float iT;
+        float m = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 6; n++) m = fmaxf(m, sm.most[u][n]);
+        const float sT = scale_of(m, iT);
+        if (tid == 0) tab[kTabG + 62] = iT;
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) {
+          if (ks > wb) continue;
+          float x[8];
+          T_row(ks, x);
+#pragma unroll
+          for (int e = 0; e < 8; e++) x[e] *= sm.be[u][32 * ks + 8 * g + e];
+          h8 hi, lo;
+          split8<2>(x, sT, hi, lo);
           char* const dst = head + Y::offT + tri_frag(w, ks) * kFrag + lane * 16;
           *(h8*)dst = hi;
           *(h8*)(dst + kTri * kFrag) = lo;
         }
-        if (ks >= wb) {
-          split8<2>(y[ks], su, hi, lo);
-          char* const dst = head + Y::offTt + up_frag(w, ks) * kFrag + lane * 16;
-          *(h8*)dst = hi;
-          *(h8*)(dst + kTri * kFrag) = lo;
+      } else {
+        // T and T^T, rows scaled
+        float x[2][8], y[2][8], mt = 0.0f, mu = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) {
+          if (ks <= wb) {
+            T_row(ks, x[ks]);
+#pragma unroll
+            for (int e = 0; e < 8; e++) mt = fmaxf(mt, fabsf(x[ks][e]));
+          }
+          if (ks >= wb) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+              y[ks][e] = !wb && ks ? sm.Z[u][8 * g + e][own] : sm.X[u][32 * ks + 8 * g + e][own];
+              mu = fmaxf(mu, fabsf(y[ks][e]));
+            }
+          }
+        }
+        float it, iu;
+        const float st = scale_of(col_max(mt), it), su = scale_of(col_max(mu), iu);
+        if (g == 0) {
+          tab[kTabT + own] = it;
+          tab[kTabTt + own] = iu;
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ks++) {
+          h8 hi, lo;
+          if (ks <= wb) {
+            split8<2>(x[ks], st, hi, lo);
+            char* const dst = head + Y::offT + tri_frag(w, ks) * kFrag + lane * 16;
+            *(h8*)dst = hi;
+            *(h8*)(dst + kTri * kFrag) = lo;
+          }
+          if (ks >= wb) {
+            split8<2>(y[ks], su, hi, lo);
+            char* const dst = head + Y::offTt + up_frag(w, ks) * kFrag + lane * 16;
+            *(h8*)dst = hi;
+            *(h8*)(dst + kTri * kFrag) = lo;
+          }
         }
       }
     }
