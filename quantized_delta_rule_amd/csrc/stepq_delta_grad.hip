@@ -268,6 +268,10 @@ __device__ __forceinline__ float sum_rows(float x) {
 template <int D, int DT>
 struct GradSmem {
   static constexpr int NPI = kInPlanes<DT>, NW = D / 16;
+  // What the value heads share, every wave's as it reads it back: k_t.k_s and q_t.k_s of the down pairs, and
+  // (where there is room) its rows of K^T and Q^T.
+  static constexpr bool keep_kq = D == 64 || DT != kF32;
+  char pairs[4][8 * kFrag], kq[keep_kq ? NW : 1][keep_kq ? 4 * NPI * kFrag : 16];
   union {
     struct {  // fragments: row tiles in accumulator order, D / 32 steps each
       char O[NPI][4 * (D / 32) * kFrag], Y[2][4 * (D / 32) * kFrag], W[2][4 * (D / 32) * kFrag];
@@ -284,29 +288,31 @@ struct GradSmem {
   float be[64], yv[64], rowx[64], dot[3][NW][64], corner[NW], z[64], y[64], da[64];
 };
 
-// Row tile rt of a 64-row operand as fragments; zero where not `live` (the lane's row, at element `at`).
-// dot: also the row's product with a row of v (the strengths' gradient).
-template <int D, int DT, int ET, int NP>
-__device__ __forceinline__ void rows_in(const void* src, long long at, bool live, int rt, int lane, int row,
-                                        char (*dst)[4 * (D / 32) * kFrag], float* is, const void* vsrc, long long vat,
-                                        float* dot) {
-  constexpr int KS = D / 32;
-  const int g = lane >> 4;
-  float x[KS][8], m = 0.0f;
+// 8 elements as they lie in memory.
+template <int DT>
+struct Raw8 {
+  static constexpr int N = DT == kF32 ? 2 : 1;
+  typedef unsigned u4 __attribute__((ext_vector_type(4)));
+  u4 a[N];
+  __device__ void load(const void* p, long long at) {
 #pragma unroll
-  for (int ks = 0; ks < KS; ks++) load8<ET>(src, at + 32 * ks + 8 * g, x[ks]);
-  if (dot) {
-    float p = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++) {
-      float v[8];
-      load8<DT>(vsrc, vat + 32 * ks + 8 * g, v);
-#pragma unroll
-      for (int e = 0; e < 8; e++) p = fmaf(x[ks][e], v[e], p);
-    }
-    p = sum_rows(p);
-    if (g == 0) dot[row] = p;
+    for (int n = 0; n < N; n++) a[n] = ((const u4*)((const char*)p + at * (16 * N / 8)))[n];
   }
+  __device__ void get(float* x) const {
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      if constexpr (DT == kF32) x[e] = __uint_as_float(a[e >> 2][e & 3]);
+      else x[e] = e_f<DT>((unsigned short)(e & 1 ? a[0][e >> 1] >> 16 : a[0][e >> 1]));
+    }
+  }
+};
+
+// Row tile rt of a 64-row operand as fragments, from the lane's pieces of its row; zero where not `live`.
+template <int D, int NP>
+__device__ __forceinline__ void rows_put(float (*x)[8], bool live, int rt, int lane, int row,
+                                         char (*dst)[4 * (D / 32) * kFrag], float* is) {
+  constexpr int KS = D / 32;
+  float m = 0.0f;
 #pragma unroll
   for (int ks = 0; ks < KS; ks++)
 #pragma unroll
@@ -316,7 +322,7 @@ __device__ __forceinline__ void rows_in(const void* src, long long at, bool live
     }
   float inv;
   const float s = scale_of(col_max(m), inv);
-  if (g == 0) is[row] = inv;
+  if (lane < 16) is[row] = inv;
 #pragma unroll
   for (int ks = 0; ks < KS; ks++) {
     h8 hi, lo;
@@ -375,7 +381,46 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
     sm.isk[tid] = tab[kTabIK + tid];
     sm.isq[tid] = tab[kTabIQ + tid];
   }
-  int row = tid / TPR;
+  int row = tid / TPR, own = 32 * pb + perm_row(c16, pt & 1);
+  // what the value heads share
+  auto kq_at = [&](int n, int ks, int p) {  // fragments of this wave's rows of K^T (n = 0) and Q^T
+    return *(const h8*)(key + (n ? Y::offQ : Y::offKT) + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
+  };
+  if (down)
+#pragma unroll
+    for (int nb = 0; nb < 2; nb++) {
+      if (nb > pb) continue;
+      float x[8];
+      load8<kF32>(key + Y::offKK, own * 64 + 32 * nb + 8 * g, x);
+      store8<kF32>(sm.pairs[pt], (4 * nb * kFrag + lane * 32) / 4, x);
+#pragma unroll
+      for (int e = 0; e < 8; e++) x[e] = ((const float*)(key + Y::offQK))[(32 * nb + 8 * g + e) * 64 + own];
+      store8<kF32>(sm.pairs[pt], ((4 * nb + 2) * kFrag + lane * 32) / 4, x);
+    }
+  if constexpr (GradSmem<D, DT>::keep_kq)
+#pragma unroll
+    for (int n = 0; n < 4 * NPI; n++) *(h8*)(sm.kq[w] + n * kFrag + lane * 16) = kq_at(n / (2 * NPI), n / NPI % 2, n % NPI);
+  // What a wave brings in of a head: 16 rows of S0, row tile pt of Y and V or of W and dO (four waves: of
+  // both).  The next head's are on their way while the gates' sums run (binary32 inputs: no registers for that).
+  constexpr int NR = NW == 4 ? 2 : 1;
+  constexpr bool early = false;
+  float xs[KS][8], xr[NR][KS][8];
+  Raw8<DT> xe[NR][KS];
+  auto load_head = [&](int hh) {
+    const int h = hq * A.grp + hh;
+    const long long jh = j * A.H + h, tok = at.t0 + (long long)min(own, at.len - 1);
+#pragma unroll
+    for (int n = 0; n < NR; n++) {
+      const bool y = NR == 2 ? n == 0 : down;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) {
+        load8<kF32>(y ? keep.Y : keep.W, (jh * 64 + own) * D + 32 * ks + 8 * g, xr[n][ks]);
+        xe[n][ks].load(y ? A.v : B.d_out, tok * (y ? A.vs : A.os) + (long long)h * D + 32 * ks + 8 * g);
+      }
+    }
+#pragma unroll
+    for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.S, (jh * D + dk) * D + 32 * ks + 8 * g, xs[ks]);
+  };
   const f4 zero = {0, 0, 0, 0};
   f4 dQ[4] = {zero, zero, zero, zero}, dK[4] = {zero, zero, zero, zero};
   // the sums are taken where they stand: left to the end they would hold every term in registers
@@ -383,7 +428,6 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   for (int hh = 0; hh < A.grp; hh++) {
     const int h = hq * A.grp + hh;
     const long long jh = j * A.H + h;
-    int own;
     // opaque again at every phase: addresses and predicates made from the lane are not kept across phases
     // and heads, where they would spill
     auto rd = [&](const char* plane, int rt, int ks) { return *(const h8*)(plane + (rt * KS + ks) * kFrag + lane * 16); };
@@ -400,11 +444,8 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
     for (int rt = 0; rt < 4; rt++)
 #pragma unroll
       for (int i = 0; i < NV; i++) asm volatile("" : "+v"(qv[rt][i]), "+v"(kv[rt][i]));  // stay as they are packed
-    // S0 is on its way while the rows become operands, dS1 while S0's products run
-    float x[KS][8];
+    if (!early || !hh) load_head(hh);
     const long long sat = (jh * D + dk) * D + 8 * g;
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.S, sat + 32 * ks, x[ks]);
     float al = 1.0f, be = 0.0f;
     if (w == NW - 1 && lane < at.len) {
       const long long th = (at.t0 + (long long)lane) * A.H + h;
@@ -413,14 +454,26 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
     }
     ahead();
     __syncthreads();  // the last head's fragments have been read
-    {  // Y (with V) and then, or in the other four waves, W and dO: row tile pt
-      const bool live = own < at.len;
-      const long long tok = at.t0 + (long long)min(own, at.len - 1);
-      if (down) rows_in<D, DT, kF32, 2>(keep.Y, (jh * 64 + own) * D, live, pt, lane, own, sm.in.Y, sm.isY, A.v, tok * A.vs + (long long)h * D, sm.yv);
-      if (up) {
-        rows_in<D, DT, kF32, 2>(keep.W, (jh * 64 + own) * D, live, pt, lane, own, sm.in.W, sm.isW, nullptr, 0, nullptr);
-        rows_in<D, DT, DT, NPI>(B.d_out, tok * A.os + (long long)h * D, live, pt, lane, own, sm.in.O, sm.isO, nullptr, 0, nullptr);
+    const bool live = own < at.len;
+    if (down) {  // Y (with V)
+      float p = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) {
+        float v[8];
+        xe[0][ks].get(v);
+#pragma unroll
+        for (int e = 0; e < 8; e++) p = fmaf(xr[0][ks][e], v[e], p);
       }
+      p = sum_rows(p);
+      if (g == 0) sm.yv[own] = p;
+      rows_put<D, 2>(xr[0], live, pt, lane, own, sm.in.Y, sm.isY);
+    }
+    if (up) {  // W and dO
+      rows_put<D, 2>(xr[NR - 1], live, pt, lane, own, sm.in.W, sm.isW);
+      float x[KS][8];
+#pragma unroll
+      for (int ks = 0; ks < KS; ks++) xe[NR - 1][ks].get(x[ks]);
+      rows_put<D, NPI>(x, live, pt, lane, own, sm.in.O, sm.isO);
     }
     if (w == NW - 1) {
       float p8 = al, s8 = __shfl_down(al, 1);
@@ -458,12 +511,13 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
 #pragma unroll
       for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-        for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(x[ks][e]));
+        for (int e = 0; e < 8; e++) m = fmaxf(m, fabsf(xs[ks][e]));
       const float s = scale_of(col_max(m), iS);
 #pragma unroll
-      for (int ks = 0; ks < KS; ks++) split8<2>(x[ks], s, Sh[ks], Sl[ks]);
+      for (int ks = 0; ks < KS; ks++) split8<2>(xs[ks], s, Sh[ks], Sl[ks]);
     }
     ahead();
+    float x[KS][8];  // dS1's rows
 #pragma unroll
     for (int ks = 0; ks < KS; ks++) load8<kF32>(keep.G, sat + 32 * ks, x[ks]);
     ahead();
@@ -607,22 +661,12 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       }
     }
     ahead();
-    float kk[2][8], qk[2][8];  // k_t.k_s and q_t.k_s of the down pairs
-    if (down)
-#pragma unroll
-      for (int nb = 0; nb < 2; nb++) {
-        if (nb > pb) continue;
-        load8<kF32>(key + Y::offKK, own * 64 + 32 * nb + 8 * g, kk[nb]);
-#pragma unroll
-        for (int e = 0; e < 8; e++) qk[nb][e] = ((const float*)(key + Y::offQK))[(32 * nb + 8 * g + e) * 64 + own];
-      }
     h8 fk[2][NPI], fq[2][NPI];  // this wave's rows of K^T and Q^T, for the products after the next barrier
+    if constexpr (!GradSmem<D, DT>::keep_kq)
 #pragma unroll
-    for (int ks = 0; ks < 2; ks++)
-#pragma unroll
-      for (int p = 0; p < NPI; p++) {
-        fk[ks][p] = *(const h8*)(key + Y::offKT + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
-        fq[ks][p] = *(const h8*)(key + Y::offQ + (p * Y::NF + 2 * w + ks) * kFrag + lane * 16);
+      for (int n = 0; n < 2 * NPI; n++) {
+        fk[n / NPI][n % NPI] = kq_at(0, n / NPI, n % NPI);
+        fq[n / NPI][n % NPI] = kq_at(1, n / NPI, n % NPI);
       }
     ahead();
     __syncthreads();  // the planes are free: fragments and pairs in their place
@@ -663,6 +707,9 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
 #pragma unroll
         for (int nb = 0; nb < 2; nb++) {
           if (nb > pb) continue;
+          float kk[8], qk[8];  // k_t.k_s and q_t.k_s
+          load8<kF32>(sm.pairs[pt], (4 * nb * kFrag + lane * 32) / 4, kk);
+          load8<kF32>(sm.pairs[pt], ((4 * nb + 2) * kFrag + lane * 32) / 4, qk);
           float c = 1.0f;
 #pragma unroll
           for (int e = 7; e >= 0; e--) {
@@ -680,8 +727,8 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
             const float p = on ? pd[nb][e] : 0.0f, y = strict ? xd[nb][e] : 0.0f, ik = sm.isk[s];
             l = on ? l : 0.0f;
             const float by = be_own * y;
-            sm.m.xT[s][own] = fmaf(p, qk[nb][e], -by * kk[nb][e]);
-            rx = fmaf(y, l * kk[nb][e], rx);
+            sm.m.xT[s][own] = fmaf(p, qk[e], -by * kk[e]);
+            rx = fmaf(y, l * kk[e], rx);
             pd[nb][e] = p * l * ik;
             xd[nb][e] = -by * l * ik;
           }
@@ -732,6 +779,12 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
     fresh();
     // dQ += N K, dK += (Zd + Zu) K + N^T Q
     {
+      if constexpr (GradSmem<D, DT>::keep_kq)
+#pragma unroll
+        for (int i = 0; i < 2 * NPI; i++) {
+          fk[i / NPI][i % NPI] = *(const h8*)(sm.kq[w] + i * kFrag + lane * 16);
+          fq[i / NPI][i % NPI] = *(const h8*)(sm.kq[w] + (2 * NPI + i) * kFrag + lane * 16);
+        }
       f4 n[4], d[4], t[4], u[4];
 #pragma unroll
       for (int r = 0; r < 4; r++) n[r] = d[r] = t[r] = u[r] = zero;
@@ -778,6 +831,8 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       }
     }
     fresh();
+    if (early && hh + 1 < A.grp) load_head(hh + 1);
+    ahead();
     // gates: dalpha_r = sum over t >= r of L[t,r] F_r[t] with F_r[t] = sum over s < r of x[t,s] L[r-1,s]
     // (the state before the chunk as s = -1, the state behind it as one more t).  Lane t; a wave takes groups
     // of 8 gates: F at a group's first by a sum, then F_{r+1} = a_r F_r + x[t,r].
