@@ -400,10 +400,10 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   if constexpr (GradSmem<D, DT>::keep_kq)
 #pragma unroll
     for (int n = 0; n < 4 * NPI; n++) *(h8*)(sm.kq[w] + n * kFrag + lane * 16) = kq_at(n / (2 * NPI), n / NPI % 2, n % NPI);
-  // What a wave brings in of a head: 16 rows of S0, row tile pt of Y and V or of W and dO (four waves: of
-  // both).  The next head's are on their way while the gates' sums run (binary32 inputs: no registers for that).
+  // What a wave brings in of a head: row tile pt of Y and V or of W and dO (four waves: of both), 16 rows of S0.
+  // Not one head ahead: the registers that this takes cost more in spills than it hides (600 us -> 676 with
+  // S0 alone ahead; Y and W ahead in LDS 713 -> 742 before the fragments took their room).
   constexpr int NR = NW == 4 ? 2 : 1;
-  constexpr bool early = false;
   float xs[KS][8], xr[NR][KS][8];
   Raw8<DT> xe[NR][KS];
   auto load_head = [&](int hh) {
@@ -444,7 +444,7 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
     for (int rt = 0; rt < 4; rt++)
 #pragma unroll
       for (int i = 0; i < NV; i++) asm volatile("" : "+v"(qv[rt][i]), "+v"(kv[rt][i]));  // stay as they are packed
-    if (!early || !hh) load_head(hh);
+    load_head(hh);
     const long long sat = (jh * D + dk) * D + 8 * g;
     float al = 1.0f, be = 0.0f;
     if (w == NW - 1 && lane < at.len) {
@@ -831,8 +831,6 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
       }
     }
     fresh();
-    if (early && hh + 1 < A.grp) load_head(hh + 1);
-    ahead();
     // gates: dalpha_r = sum over t >= r of L[t,r] F_r[t] with F_r[t] = sum over s < r of x[t,s] L[r-1,s]
     // (the state before the chunk as s = -1, the state behind it as one more t).  Lane t; a wave takes groups
     // of 8 gates: F at a group's first by a sum, then F_{r+1} = a_r F_r + x[t,r].
