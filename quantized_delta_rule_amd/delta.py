@@ -44,21 +44,39 @@ def dtype_code(dtype):
     return code
 
 
-def _rows(t, name, dtype, shape, device):
-    """(pointer, token stride in elements) of a [tokens, heads, d] tensor whose heads are packed."""
-    if t.device.type != "cuda" or t.device.index != device:
+def _tensor(t, name, dtype, shape, device):
+    """Refuses what is no tensor of this type and shape on this device."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != device:  # -1: not on a GPU
         raise ValueError(f"{name} must live on cuda:{device} (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+
+
+def _dense(t, name, dtype, shape, device):
+    """Address of a contiguous tensor."""
+    _tensor(t, name, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape, device):
+    """(address, token stride in elements) of a [tokens, heads, d] tensor whose heads are packed."""
+    _tensor(t, name, dtype, shape, device)
     n, heads, d = shape
     st = t.stride()
     if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d):
         raise ValueError(f"{name}: the heads of a token must be packed (strides {list(st)})")
-    if n > 1 and st[0] < heads * d:
+    if n <= 1:
+        return t.data_ptr(), heads * d
+    if st[0] < heads * d:
         raise ValueError(f"{name}: tokens must not overlap (strides {list(st)})")
-    return t.data_ptr(), (st[0] if n > 1 else heads * d)
+    return t.data_ptr(), st[0]
 
 
 class _Sequences:
@@ -67,47 +85,43 @@ class _Sequences:
     def __init__(self, q, k, v, alpha, beta, out, out_name, cu_seqlens, n_seqs, kind, order, status,
                  stream):
         import torch
-        for t, name in ((q, "q"), (k, "k"), (v, "v"), (alpha, "alpha"), (beta, "beta"), (out, out_name)):
+        for t, name in ((q, "q"), (v, "v")):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name} must be a torch tensor")
-        if q.dim() != 3 or v.dim() != 3:
-            raise ValueError("q and v must be [tokens, heads, d]")
-        if q.device.type != "cuda":
+            if t.dim() != 3:
+                raise ValueError(f"{name} must be [tokens, heads, d]")
+        self.device = dev = q.get_device()
+        if dev < 0:
             raise ValueError(f"q must live on a GPU (got {q.device})")
-        self.torch_device = q.device
-        self.device = dev = q.device.index
         T, Hq, d = q.shape
         H = v.shape[1]
-        self.T, self.Hq, self.H, self.d, self.dtype = T, Hq, H, d, q.dtype
-        code = dtype_code(q.dtype)
-        self.q, qs = _rows(q, "q", q.dtype, (T, Hq, d), dev)
-        self.k, ks = _rows(k, "k", q.dtype, (T, Hq, d), dev)
-        self.v, vs = _rows(v, "v", q.dtype, (T, H, d), dev)
-        self.out, os_ = _rows(out, out_name, q.dtype, (T, H, d), dev)
-        kda = int(kind) == KDA
-        want = (T, H, d) if kda else (T, H)
-        if tuple(alpha.shape) != want:
-            raise ValueError(f"alpha must be {list(want)} (got {list(alpha.shape)})")
-        if tuple(beta.shape) != (T, H):
-            raise ValueError(f"beta must be {[T, H]} (got {list(beta.shape)})")
-        f = torch.float32
-        self.alpha = _dev_tensor(alpha, "alpha", f, T * H * (d if kda else 1), dev)
-        self.beta = _dev_tensor(beta, "beta", f, T * H, dev)
+        dt, f = q.dtype, torch.float32
+        self.T, self.Hq, self.H, self.d, self.dtype = T, Hq, H, d, dt
+        code = dtype_code(dt)
+        kind = int(kind)
+        self.q, qs = _rows(q, "q", dt, (T, Hq, d), dev)
+        self.k, ks = _rows(k, "k", dt, (T, Hq, d), dev)
+        self.v, vs = _rows(v, "v", dt, (T, H, d), dev)
+        self.out, os_ = _rows(out, out_name, dt, (T, H, d), dev)
+        self.alpha = _dense(alpha, "alpha", f, (T, H, d) if kind == KDA else (T, H), dev)
+        self.beta = _dense(beta, "beta", f, (T, H), dev)
         cu = None
         if cu_seqlens is not None:
-            if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-                raise ValueError("cu_seqlens must be [n_seqs + 1]")
+            if not isinstance(cu_seqlens, torch.Tensor):
+                raise TypeError("cu_seqlens must be a torch tensor")
             n = cu_seqlens.numel() - 1
+            if cu_seqlens.dim() != 1 or n < 0:
+                raise ValueError("cu_seqlens must be [n_seqs + 1]")
             if n_seqs is not None and n_seqs != n:
                 raise ValueError(f"cu_seqlens holds {n} sequences, n_seqs is {n_seqs}")
-            cu = _dev_tensor(cu_seqlens, "cu_seqlens", torch.int32, n + 1, dev)
+            cu = _dense(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev)
         else:
             n = 1 if n_seqs is None else int(n_seqs)
-        if max(T, n) > 0x7FFFFFFF:
+        if T > 0x7FFFFFFF or n > 0x7FFFFFFF:
             raise ValueError(f"{T} tokens and {n} sequences: at most 2^31 - 1")
         self.N = n
         st = None if status is None else _dev_tensor(status, "status", torch.int32, 1, dev)
-        self.desc = _SeqDesc(int(kind), int(order), code, Hq, H, d, n, T, dev, qs, ks, vs, os_, cu, st)
+        self.desc = _SeqDesc(kind, int(order), code, Hq, H, d, n, T, dev, qs, ks, vs, os_, cu, st)
         self.current = stream is None
         if stream is None:
             stream = torch.cuda.current_stream(dev)
@@ -119,10 +133,7 @@ class _Sequences:
         import torch
         if S is None:
             return None
-        n = self.N if n is None else n
-        if tuple(S.shape) != (n, self.H, self.d, self.d):
-            raise ValueError(f"{name} must be {[n, self.H, self.d, self.d]} (got {list(S.shape)})")
-        return _dev_tensor(S, name, torch.float32, n * self.H * self.d * self.d, self.device)
+        return _dense(S, name, torch.float32, (self.N if n is None else n, self.H, self.d, self.d), self.device)
 
     def workspace(self, given, need):
         """(pointer, bytes, keep-alive) of `need` bytes on the call's stream."""
@@ -131,16 +142,16 @@ class _Sequences:
             if need == 0:
                 return None, 0, None
             if self.current:  # the allocator's block belongs to the stream that the call runs on
-                given = torch.empty(need, dtype=torch.uint8, device=self.torch_device)
+                given = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", self.device))
             else:
                 with torch.cuda.stream(self.stream):
-                    given = torch.empty(need, dtype=torch.uint8, device=self.torch_device)
+                    given = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", self.device))
             return given.data_ptr(), need, given
         p = _dev_tensor(given, "workspace", torch.uint8, given.numel(), self.device)
         return p, given.numel(), given
 
     def ptr(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        return self.stream.cuda_stream
 
 
 def _need(fn, what, *args):
@@ -151,7 +162,7 @@ def _need(fn, what, *args):
 
 def _slots(slots, N, device):
     import torch
-    return None if slots is None else _dev_tensor(slots, "slots", torch.int32, N, device)
+    return None if slots is None else _dense(slots, "slots", torch.int32, (N,), device)
 
 
 def forward_workspace(q, k, v, alpha, beta, out, *, cu_seqlens=None, n_seqs=None, kind=GDN,
@@ -193,16 +204,10 @@ def backward(q, k, v, alpha, beta, d_out, dq, dk, dv, dalpha, dbeta, *, state_in
     import torch
     a = _Sequences(q, k, v, alpha, beta, d_out, "d_out", cu_seqlens, n_seqs, GDN, order, status, stream)
     dev, T, f = a.device, a.T, torch.float32
-    got = []
-    for t, name, shape, dt in ((dq, "dq", (T, a.Hq, a.d), a.dtype), (dk, "dk", (T, a.Hq, a.d), a.dtype),
-                               (dv, "dv", (T, a.H, a.d), a.dtype), (dalpha, "dalpha", (T, a.H), f),
-                               (dbeta, "dbeta", (T, a.H), f)):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-        n = 1
-        for x in shape:
-            n *= x
-        got.append(_dev_tensor(t, name, dt, n, dev))
+    got = [_dense(t, name, dt, shape, dev)
+           for t, name, shape, dt in ((dq, "dq", (T, a.Hq, a.d), a.dtype), (dk, "dk", (T, a.Hq, a.d), a.dtype),
+                                      (dv, "dv", (T, a.H, a.d), a.dtype), (dalpha, "dalpha", (T, a.H), f),
+                                      (dbeta, "dbeta", (T, a.H), f))]
     si = a.state(state_in, "state_in")
     ds1, ds0 = a.state(d_state_out, "d_state_out"), a.state(d_state_in, "d_state_in")
     L, d = lib(), ctypes.byref(a.desc)

@@ -139,8 +139,8 @@ def test_python_refusals():
     a = torch.zeros(4, 2)
     with pytest.raises(ValueError, match="GPU"):
         delta.forward(x, x, x, a, a, x)
-    with pytest.raises(TypeError, match="k must be a torch tensor"):
-        delta.forward(x, None, x, a, a, x)
+    with pytest.raises(TypeError, match="v must be a torch tensor"):
+        delta.forward(x, x, None, a, a, x)
     with pytest.raises(ValueError, match="tokens, heads, d"):
         delta.backward(x[0], x, x, a, a, x, x, x, x, a, a)
     with pytest.raises(TypeError, match="float32, bfloat16 or float16"):

@@ -407,3 +407,56 @@ def test_rows_past_four_gib(lib):
     delta.forward(e["q"], e["k"], e["v"], e["alpha"], e["beta"], o2, state_out=S2)
     assert R.rel(out[T - tail:], o2) <= 2 * OUT[BF16]
     assert R.rel(S, S2) <= 2 * STATE
+
+
+def test_python_refusals(lib):
+    """Wrong types, shapes, devices and strides are refused before anything is enqueued."""
+    stepq, delta = lib
+    g, cu = _case([70, 33], 2, 4, 64, BF16)
+    out = torch.full_like(g["v"], 55.0)
+    S = torch.full_like(g["S"], 55.0)
+
+    def call(error, match, **kw):
+        x = dict(g, out=out, state_in=g["S"], state_out=S, cu_seqlens=_ints(cu))
+        x.update(kw)
+        args = [x.pop(m) for m in ("q", "k", "v", "alpha", "beta", "out")]
+        with pytest.raises(error, match=match):
+            delta.forward(*args, **{m: x[m] for m in x if m not in ("S", "do", "dS")})
+
+    call(TypeError, "k must be a torch tensor", k=None)
+    call(TypeError, "k must be torch.bfloat16", k=g["k"].float())
+    call(ValueError, "k must live on cuda:0", k=g["k"].cpu())
+    call(ValueError, "k must be", k=g["k"][:-1])
+    call(ValueError, "alpha must be", alpha=g["beta"][:, :-1])
+    call(ValueError, "alpha must be contiguous", alpha=g["alpha"].t().contiguous().t())
+    call(ValueError, "alpha must be", kind=delta.KDA)
+    call(ValueError, "heads of a token must be packed", q=g["q"].transpose(0, 1).contiguous().transpose(0, 1))
+    call(ValueError, "tokens must not overlap", q=g["q"][:1].expand_as(g["q"]))
+    call(stepq.StepqError, "q_stride", q=torch.zeros(103, 2 * 64 + 4, dtype=BF16, device="cuda")[:, :128].view(103, 2, 64))
+    call(stepq.StepqError, "16-byte aligned", q=torch.zeros(103 * 128 + 1, dtype=BF16, device="cuda")[1:].view(103, 2, 64))
+    call(stepq.StepqError, "multiple of n_qk_heads", q=torch.zeros(103, 3, 64, dtype=BF16, device="cuda"),
+         k=torch.zeros(103, 3, 64, dtype=BF16, device="cuda"))
+    call(ValueError, "n_seqs is 3", n_seqs=3)
+    call(TypeError, "cu_seqlens must be torch.int32", cu_seqlens=_ints(cu).long())
+    call(stepq.StepqError, "multiple of n_seqs", cu_seqlens=None, n_seqs=2)
+    call(ValueError, "state_out must be", state_out=S[:1])
+    call(ValueError, "state_in must be", state_in=g["S"][:1])
+    call(ValueError, "slots must be", slots=_ints([0]))
+    call(ValueError, "slots need", slots=_ints([0, 1]), state_in=None, state_out=None)
+    call(stepq.StepqError, "workspace of 256 bytes", workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    call(stepq.StepqError, "256-byte aligned", workspace=torch.empty(1 << 24, dtype=torch.uint8, device="cuda")[16:])
+    with pytest.raises(ValueError, match="dbeta must be"):
+        delta.backward(g["q"], g["k"], g["v"], g["alpha"], g["beta"], g["do"], g["q"].clone(), g["k"].clone(),
+                       g["v"].clone(), g["alpha"].clone(), g["beta"][:-1].clone())
+    plan = _plan(stepq, "gdn", 64, 5)
+    pool = _filled(plan, 3)
+    was = pool.clone()
+    with pytest.raises(ValueError, match="plan's heads"):
+        plan.prefill_slots(pool, 3, _ints([0, 1]), g["q"], g["k"], g["v"], g["alpha"], g["beta"], out,
+                           cu_seqlens=_ints(cu))
+    with pytest.raises(TypeError, match="float32, bfloat16 or float16"):
+        plan.read_slots(pool, 3, _ints([0]), 1, torch.empty(1, 5, 64, 64, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ValueError, match="S has"):
+        plan.read_slots(pool, 3, _ints([0]), 1, torch.empty(1, 4, 64, 64, device="cuda"))
+    torch.cuda.synchronize()
+    assert (out == 55.0).all() and (S == 55.0).all() and torch.equal(pool, was)
