@@ -9,17 +9,17 @@ namespace {
 
 using namespace dlt;
 
-// Segments of a sequence: with at most 64 (sequence, head) pairs the chunks of a sequence are run in
-// 256 / pairs segments at once (at most 16), where there are at least four chunks a segment on average.
-// Every chunk is then run three times, so two segments gain nothing.
+// Segments of a sequence: with at most 32 (sequence, head) pairs and 40 chunks a sequence or more on
+// average, 256 / pairs segments (at most 16, of at least four chunks) run at once.  Every chunk is then run
+// three times, so it takes many idle CUs and long segments to gain (us, d = 128 bf16, cut against whole:
+// 1 x 32 heads of 1,024 / 2,048 / 4,096 / 16,384 tokens 80 / 137 / 204 / 676 against 73 / 131 / 254 / 984;
+// 1 x 4 heads of 1,024 / 4,096 tokens 61 / 140 against 65 / 219; 64 heads of 8,192 tokens 655 against 608).
 int segments(const SeqArgs& a) {
-  const long long tiles = (long long)a.N * a.H;
-  if (tiles > 64) return 1;
+  const long long tiles = (long long)a.N * a.H, chunks = (long long)a.T / ((long long)a.N * kChunk);
+  if (tiles > 32 || chunks < 40) return 1;
   long long P = 256 / tiles;
   P = P > 16 ? 16 : P;
-  const long long chunks = (long long)a.T / ((long long)a.N * kChunk);
-  if (P > chunks / 4) P = chunks / 4;
-  return P < 4 ? 1 : (int)P;
+  return (int)(P > chunks / 4 ? chunks / 4 : P);
 }
 
 template <int D, int DT>

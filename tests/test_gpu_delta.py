@@ -105,7 +105,7 @@ def test_values_of_any_size(delta, scale):
 
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
-@pytest.mark.parametrize("lens", [[1100], [2000, 0, 65, 1500]], ids=str)
+@pytest.mark.parametrize("lens", [[1100], [2700], [6000, 0, 65, 4500]], ids=str)
 def test_long_sequences_cut_into_segments(delta, d, dtype, lens):
     """Few heads and many chunks: segments run at once and joined; sequences of a batch that have fewer
     chunks than segments among them.  In place, as a state that a decode loop carries."""

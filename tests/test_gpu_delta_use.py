@@ -60,7 +60,7 @@ def _same(a, b):
 
 
 # chunks, segments (few long sequences), tokens one by one
-PATHS = {"chunks": [70, 130, 33], "segments": [2200], "tokens": [2, 0, 5]}
+PATHS = {"chunks": [70, 130, 33], "segments": [5200], "tokens": [2, 0, 5]}
 
 
 @pytest.mark.parametrize("path", PATHS)
@@ -123,7 +123,7 @@ def test_slots(lib, path, kda):
     stepq, delta = lib
     if kda and path == "segments":
         pytest.skip("KDA has one path")
-    lens = ([3300] if path == "segments" else PATHS[path]) + [40, 20]
+    lens = ([7800] if path == "segments" else PATHS[path]) + [40, 20]
     kind = delta.KDA if kda else delta.GDN
     g, cu = _case(lens, 2, 2, 64, BF16, kda=kda)
     n, N = 9, len(lens)
