@@ -27,6 +27,11 @@ using Square = LdsRows<float, 64>;
 // tiles as the A side the accumulators of a pair hold 8 consecutive tokens s of a lane's token t, which is
 // P's fragment as it is and two 16-byte stores of A.  (The gradient wants P^T: Q on the A side, s as columns.)
 //
+// 16,381 tokens x 48 heads on 16 key heads (d = 128 bf16): 165 us for 134 MB read and 446 MB written, 3.5 TB/s of the
+// 5.2 that a copy reaches; 8,192 tokens x 32 heads on 16 for the gradient 100 us.  Three workgroups a CU wait for
+// each other's memory most of the time (56% of wave cycles); the vector ALUs are busy 40%, LDS 35%.
+// A fourth workgroup would spill (188 us).
+//
 // Products of gates between two tokens come from running products inside groups of 8 and blocks of 32:
 //   L[t,s] = pre32[t] suf32[s] across blocks, pre8[t] mid suf8[s] across groups of a block,
 // pre = from the group's start to t, suf = behind s to the group's end; inside a group one by one.
@@ -503,6 +508,12 @@ __global__ __launch_bounds__(256, Y::grad ? 2 : 3) void k_chunk_prep(SeqArgs A) 
 // St within binary16's range, checked every chunk), so that it turns into an operand without a product and
 // the update accumulates on it directly.
 //
+// 8 sequences of 0 .. 3,698 tokens x 48 states (d = 128 bf16): 327 us, of it about 5.5 a chunk of the longest
+// sequence; 529 MB read, 221 written.  A chunk is one chain of products and roundings to operands (K S, T R, P W,
+// K^T W), and two waves a SIMD fill its gaps only in part: the vector ALUs are busy 48%, the matrix cores 29%,
+// 30% of the wave cycles wait.  Four waves a SIMD do not fit: a state column with its operands takes 190
+// registers.  The chain of a column does not shorten with more CUs, hence the segments below.
+//
 // kForward: the whole sequence, read out.  kKeep (gradient, LayB): no readout, the states before every chunk
 // and W are kept.  Where there are few (sequence, head) pairs and many chunks, the chunks of a sequence are
 // cut into segs.P segments (blockIdx.y): the state behind a segment is M S + N, so kSegment runs every
@@ -807,7 +818,8 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
 
 // First states of the segments: S_0 = S_in, S_{p+1} = M_p S_p + N_p.  A wave owns 16 columns, as in the pass,
 // and the waves of a state are spread over the card, two a workgroup: there is nothing they share but M,
-// whose rows are on their way one row tile ahead.
+// whose rows are on their way one row tile ahead.  32 states x 8 segments of 128 x 128: 50 us, the latency of 8
+// steps of a 128 x 128 by 128 x 16 product with M from HBM (eight waves a workgroup: 146 us).
 template <int D>
 __global__ __launch_bounds__(128) void k_chunk_join(SeqArgs A, Segs segs) {
   constexpr int KS = D / 32, NB = D / 32;

@@ -29,7 +29,9 @@ struct Keep {  // per chunk slot and value head, binary32
 };
 
 // The reverse pass: like k_chunk_state a wave owns 16 columns of one state's gradient for the whole sequence
-// and holds it in units of a power of two per column.
+// and holds it in units of a power of two per column.  4 sequences of 2,048 tokens x 32 states (d = 128
+// bf16): 241 us, 7.5 a chunk, 185 MB read and 459 written (the state's gradient behind every chunk among them): two
+// operands' roundings more a chunk than forward, and one wave a SIMD.
 template <int D, int DT, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep keep) {
   using L = LayB<D, DT>;
@@ -338,6 +340,11 @@ __device__ __forceinline__ void rows_put(float (*x)[8], bool live, int rt, int l
 // all products with the states and of dQ and dK.  The pairs of tokens are formed twice, with the later
 // token and with the earlier one as the lane's own (a wave each where there are eight): a lane then holds 8
 // consecutive partners (their row tiles permuted), which is the fragment of N, N^T and either half of Z + Z^T as it is.
+//
+// 8,192 tokens x 32 heads on 16 key heads (d = 128 bf16): 593 us, 36 a head and workgroup, 0.6 GB read.  One
+// workgroup a CU (operands of 64 x 128 in two planes fill LDS, 256 registers a lane), so a head's phases --
+// rows in, products with the states, pairs, gates -- follow each other with barriers between and half of
+// the wave cycles wait; the vector ALUs are busy 33%, the matrix cores 9%, LDS 33%.
 template <int D, int DT>
 __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   using Y = LayB<D, DT>;

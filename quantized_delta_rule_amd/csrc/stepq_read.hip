@@ -2,8 +2,13 @@
 // X_hat[i,j] = r_i c_j z[i,j], FP16 pivot rows as stored), by slot, as binary32, bfloat16 or binary16.
 //
 // One workgroup per (request, head), a quarter of the rows a wave.  A row's codes sit at one bit offset in
-// all 64 lane streams, so its width, shift and factor are wave-uniform and a lane reads one or two words.  r c z is formed as r (c z): c z is exact in binary32 (11 + 8 bits), so the value is
-// the exact product rounded once, and once more where the output type is narrower.
+// all 64 lane streams, so its width, shift and factor are wave-uniform and a lane reads one or two words.
+// r c z is formed as r (c z): c z is exact in binary32 (11 + 8 bits), so the value is the exact product
+// rounded once, and once more where the output type is narrower.
+//
+// Bound by HBM, written side: 16 x 48 states of 6 bits to binary32 (50 MB out, 10 in) take 12 us, 5.0 TB/s; to
+// bfloat16 10 us.  Eight rows' words are in flight at once: one row at a time waited for each (28 us
+// against 8 for 4 x 48 states of 8 bits).
 #include "stepq_delta.h"
 #include "stepq_internal.h"
 
