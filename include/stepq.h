@@ -259,7 +259,8 @@ int stepq_delta_backward_workspace(const stepq_delta_desc* desc, size_t* bytes);
  *   index outside [0, n_slots) is skipped too and raises STEPQ_FLAG_BAD_SLOT.  Two sequences must
  *   not name one slot.  NULL: sequence s uses state s.
  *   out must not overlap an input, nor the workspace anything.
- * GDN sequences of 16 tokens and more on average run in chunks of 64 tokens on the matrix cores: sums
+ * GDN sequences of 16 tokens and more (on average; each by itself where the average is below and
+ * n_tokens - n_seqs at least 128) run in chunks of 64 tokens on the matrix cores: sums
  * and states in binary32; operands in pairs of binary16 with power-of-two scales, 22 bits of the largest
  * element of a row, or of a column of a chunk; the last products of a BF16 out in single ones (11 bits).
  * There a non-finite input may make its head's outputs non-finite from its chunk's first token on.
@@ -275,7 +276,8 @@ int stepq_delta_forward(const stepq_delta_desc* desc, const void* q, const void*
  * stride) and dS_out [n_seqs, n_heads, d, d] fp32 (NULL = zero) to
  *   dq, dk [n_tokens, n_qk_heads, d] and dv [n_tokens, n_heads, d] of `dtype`, packed;
  *   dalpha, dbeta [n_tokens, n_heads] fp32;  dS_in [n_seqs, n_heads, d, d] fp32 (NULL = not wanted).
- * All are written, not added to; rows of no sequence are left as they were.  Value heads that share
+ * All are written, not added to; rows of no sequence are left as they were.  No output may overlap an
+ * input or another output, but dS_in may be dS_out (in place).  Value heads that share
  * a key head add up in index order in binary32, so results do not depend on scheduling.  No
  * division by a gate: gates of zero have their gradient.  KDA: STEPQ_ERR_UNSUPPORTED.
  */

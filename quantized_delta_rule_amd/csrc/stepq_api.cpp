@@ -560,7 +560,7 @@ int stepq_read_slots(stepq_plan_t p, const void* pool, int n_slots, const int32_
 static size_t prefill_bytes(const stepq_plan* p, const SeqArgs& a) {
   const size_t n = (size_t)a.N;
   return n * p->H * p->D * p->D * sizeof(float) + 2 * ((n * sizeof(int) + 255) / 256 * 256) +
-         (uses_chunks(a) ? chunk_forward_bytes(a) : 0);
+         forward_bytes(a);
 }
 
 // The plan fixes the kind, the gate order, the heads, d and the device of the description.
@@ -612,7 +612,7 @@ int stepq_prefill_slots(stepq_plan_t p, const stepq_delta_desc* d, void* pool, i
   a.n_slots = a.N;
   a.ws = w;
   a.status = nullptr;  // the read has reported bad slots and offsets
-  HIP_TRY(uses_chunks(a) ? launch_chunk_forward(a, s) : launch_recurrent(a, s));
+  HIP_TRY(launch_forward(a, s));
   return encode_impl(p, S, pool, n_slots, slot_of, a.N, stream);
 }
 

@@ -310,7 +310,7 @@ __device__ __forceinline__ bool chunk_at(const SeqArgs& A, long long j, ChunkAt&
   int t0, t1;
   seq_range(A, lo, t0, t1);
   const long long c = j - at.slot0;
-  if (c * kChunk >= t1 - t0) return false;
+  if (c * kChunk >= t1 - t0 || t1 - t0 < A.split) return false;
   at.c = (int)c;
   at.t0 = t0 + (int)c * kChunk;
   at.len = t1 - at.t0 < kChunk ? t1 - at.t0 : kChunk;

@@ -585,7 +585,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
   const int slot = seq_slot(A, s, valid, h == 0 && !cut && part0 == 0 && tid == 0);
-  if (slot < 0) return;
+  if (slot < 0 || t1 - t0 < A.split) return;
   if (t0 == t1 && MODE == kKeep) return;
   if (t0 == t1 && MODE == kForward && (!A.S_out || A.S_out == A.S_in)) return;
   const int col0 = 16 * (part0 * NW + w), col = col0 + c16;

@@ -34,6 +34,7 @@ struct SeqArgs {
   void* out;
   unsigned* status;         // may be nullptr
   char* ws;                 // chunked passes: workspace
+  int split;                // not 0: sequences of fewer tokens go token by token, the others in chunks
 };
 
 // Gradient of the chunked pass.
@@ -59,7 +60,8 @@ int seq_args(const void* desc, SeqArgs* a);
 int seq_inputs(SeqArgs* a, const void* q, const void* k, const void* v, const float* alpha,
                const float* beta, void* out);
 int seq_workspace(const void* ws, size_t have, size_t need);
-bool uses_chunks(const SeqArgs& a);
+size_t forward_bytes(const SeqArgs& a);                    // workspace of launch_forward
+hipError_t launch_forward(const SeqArgs& a, hipStream_t s);  // all sequences, by the paths that suit them
 
 size_t chunk_forward_bytes(const SeqArgs& a);
 size_t chunk_backward_bytes(const SeqArgs& a);

@@ -14,8 +14,27 @@ namespace stepq {
 // 64-row products whatever the length, a token by itself one step of the recurrence (us, d = 128 bf16,
 // chunks against token by token at 8 / 16 / 32 tokens: 1 x 32 heads 16 / 16 / 16 against 12 / 21 / 39,
 // 8 x 48 heads 42 / 42 / 43 against 20 / 29 / 51, 70 x 48 heads 179 / 182 / 190 against 103 / 165 / 304).
-bool uses_chunks(const SeqArgs& a) {
-  return a.kind == STEPQ_KIND_GDN && a.N > 0 && (long long)a.T >= 16LL * a.N;
+// Lengths are on the device.  Where they are shorter on average, but one may be long -- decoding requests
+// and a prompt in one call --, both paths are launched and each takes its sequences (48 heads: 64 single tokens
+// and 512 693 -> 122 us, 16 and 129 170 -> 51; where none is long the second path's empty launches cost
+// 6 us: 64 of 4 tokens 76 -> 83).
+constexpr int kShort = 16, kMaybeLong = 128;
+enum Path { kTokens, kChunks, kBoth };
+static Path forward_path(const SeqArgs& a) {
+  if (a.kind != STEPQ_KIND_GDN || a.N <= 0) return kTokens;
+  if ((long long)a.T >= (long long)kShort * a.N) return kChunks;
+  return a.cu && a.T - a.N >= kMaybeLong ? kBoth : kTokens;
+}
+
+size_t forward_bytes(const SeqArgs& a) { return forward_path(a) == kTokens ? 0 : chunk_forward_bytes(a); }
+
+hipError_t launch_forward(const SeqArgs& a, hipStream_t s) {
+  const Path path = forward_path(a);
+  if (path != kBoth) return path == kChunks ? launch_chunk_forward(a, s) : launch_recurrent(a, s);
+  SeqArgs b = a;
+  b.split = kShort;
+  if (hipError_t e = launch_recurrent(b, s)) return e;
+  return launch_chunk_forward(b, s);
 }
 
 int seq_args(const void* desc, SeqArgs* a) {
@@ -129,8 +148,6 @@ int launched(hipError_t e, const char* what) {
   return ok();
 }
 
-size_t forward_bytes(const SeqArgs& a) { return uses_chunks(a) ? chunk_forward_bytes(a) : 0; }
-
 int backward_args(const stepq_delta_desc* desc, SeqArgs* a) {
   if (int rc = seq_args(desc, a)) return rc;
   if (a->kind != STEPQ_KIND_GDN)
@@ -181,7 +198,7 @@ int stepq_delta_forward(const stepq_delta_desc* desc, const void* q, const void*
   DeviceGuard dg(desc->device);
   if (!dg.ok_) return fail(STEPQ_ERR_HIP, "hipSetDevice(%d) failed", desc->device);
   hipStream_t s = (hipStream_t)stream;
-  return launched(uses_chunks(a) ? launch_chunk_forward(a, s) : launch_recurrent(a, s), "delta_forward");
+  return launched(launch_forward(a, s), "delta_forward");
 }
 
 int stepq_delta_backward(const stepq_delta_desc* desc, const void* q, const void* k, const void* v,

@@ -39,7 +39,7 @@ __global__ __launch_bounds__(256) void k_recurrent(SeqArgs A) {
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
   const int slot = seq_slot(A, s, valid, h == 0 && sl == 0 && lane == 0);
-  if (slot < 0) return;
+  if (slot < 0 || (A.split && t1 - t0 >= A.split)) return;
   if (t0 == t1 && (!A.S_out || A.S_out == A.S_in)) return;
   const int col = 32 * sl + 4 * (lane & 7), row = R * (lane >> 3);
   const long long so = (((long long)slot * A.H + h) * D + row) * D + col;

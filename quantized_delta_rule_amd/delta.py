@@ -12,7 +12,8 @@ token dimension may be strided, in multiples of 16 bytes), alpha [tokens, value 
 value heads, d] (KDA), beta [tokens, value heads], states [n, value heads, d, d], all float32.  Calls
 enqueue kernels on `stream` (default: the current stream of the tensors' device) and return; every tensor
 must stay alive until then as for any stream work.  A workspace is taken from torch's allocator on that
-stream unless one is passed.
+stream unless one is passed (uint8, 256-byte aligned, of forward_workspace(), backward_workspace() or
+Plan.prefill_workspace() bytes; calls that may run at once need one each).
 """
 from __future__ import annotations
 
@@ -170,6 +171,12 @@ def forward_workspace(q, k, v, alpha, beta, out, *, cu_seqlens=None, n_seqs=None
     """Bytes of workspace that forward() with these arguments takes."""
     a = _Sequences(q, k, v, alpha, beta, out, "out", cu_seqlens, n_seqs, kind, order, None, None)
     return _need(lib().stepq_delta_forward_workspace, "delta_forward_workspace", ctypes.byref(a.desc))
+
+
+def backward_workspace(q, k, v, alpha, beta, d_out, *, cu_seqlens=None, n_seqs=None, order=DELTA_FIRST):
+    """Bytes of workspace that backward() with these arguments takes."""
+    a = _Sequences(q, k, v, alpha, beta, d_out, "d_out", cu_seqlens, n_seqs, GDN, order, None, None)
+    return _need(lib().stepq_delta_backward_workspace, "delta_backward_workspace", ctypes.byref(a.desc))
 
 
 def forward(q, k, v, alpha, beta, out, *, state_in=None, state_out=None, cu_seqlens=None, n_seqs=None,

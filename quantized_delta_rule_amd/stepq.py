@@ -231,10 +231,8 @@ class Plan:
                                              _stream_ptr(stream)), "decode_step_slots")
 
     # -- prompts into the pool, and its values -------------------------------------------------
-    def prefill_slots(self, pool, n_slots, slots, q, k, v, alpha, beta, out, *, cu_seqlens=None,
-                      n_seqs=None, workspace=None, stream=None):
-        """Runs each sequence's tokens from the packed state in its slot and packs the last state
-        back (tensors and offsets as for delta.forward)."""
+    def _prefill(self, q, k, v, alpha, beta, out, cu_seqlens, n_seqs, stream):
+        """The checked description of a prompt pass and the bytes of its workspace."""
         from . import delta
         a = delta._Sequences(q, k, v, alpha, beta, out, "out", cu_seqlens, n_seqs, self.kind,
                              self.order, None, stream)
@@ -242,9 +240,20 @@ class Plan:
             raise ValueError(f"q must live on cuda:{self.device} (got cuda:{a.device})")
         if (a.H, a.d) != (self.H, self.d):
             raise ValueError(f"v must have the plan's heads [{self.H}, {self.d}] (got [{a.H}, {a.d}])")
+        return a, delta._need(lib().stepq_prefill_workspace, "prefill_workspace", self._h,
+                              ctypes.byref(a.desc))
+
+    def prefill_workspace(self, q, k, v, alpha, beta, out, *, cu_seqlens=None, n_seqs=None):
+        """Bytes of workspace that prefill_slots() with these arguments takes."""
+        return self._prefill(q, k, v, alpha, beta, out, cu_seqlens, n_seqs, None)[1]
+
+    def prefill_slots(self, pool, n_slots, slots, q, k, v, alpha, beta, out, *, cu_seqlens=None,
+                      n_seqs=None, workspace=None, stream=None):
+        """Runs each sequence's tokens from the packed state in its slot and packs the last state
+        back (tensors and offsets as for delta.forward)."""
+        a, need = self._prefill(q, k, v, alpha, beta, out, cu_seqlens, n_seqs, stream)
         L, d = lib(), ctypes.byref(a.desc)
-        ws, size, keep = a.workspace(workspace, delta._need(L.stepq_prefill_workspace,
-                                                            "prefill_workspace", self._h, d))
+        ws, size, keep = a.workspace(workspace, need)
         _check(L.stepq_prefill_slots(self._h, d, self._pool(pool, n_slots), int(n_slots),
                                      self._slots(slots, a.N), a.q, a.k, a.v, a.alpha, a.beta, a.out,
                                      ws, size, a.ptr()), "prefill_slots")

@@ -59,8 +59,9 @@ def _same(a, b):
     return all(torch.equal(x, y) for x, y in zip(a, b))
 
 
-# chunks, segments (few long sequences), tokens one by one
-PATHS = {"chunks": [70, 130, 33], "segments": [5200], "tokens": [2, 0, 5]}
+# chunks, segments (few long sequences), tokens one by one, both (a long one among short ones)
+PATHS = {"chunks": [70, 130, 33], "segments": [5200], "tokens": [2, 0, 5],
+         "both": [150, 1, 16, 0, 15] + 11 * [1]}
 
 
 @pytest.mark.parametrize("path", PATHS)
@@ -90,6 +91,35 @@ def test_strided_rows(lib, path, dtype):
     s["do"].copy_(g["do"])
     ref = _backward(delta, g, cu)
     assert _same(ref, _backward(delta, s, cu, into={m: torch.empty_like(ref[m]) for m in ref}))
+
+
+@pytest.mark.parametrize("kind", ["state", "no state"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("lens", [PATHS["both"], [3] * 30 + [257] + [7] * 20, [1] * 200 + [16, 129, 15]], ids=len)
+def test_decoding_and_prompts_in_one_call(lib, lens, dtype, d, kind):
+    """Short sequences go token by token and long ones in chunks, each against binary64."""
+    _, delta = lib
+    cu = R.offsets(lens)
+    assert cu[-1] < 16 * len(lens) and cu[-1] - len(lens) >= 128  # both paths
+    x = R.inputs(21 + d, cu[-1], 1, 2, d, len(lens), dtype)
+    if kind != "state":
+        x["S"].zero_()
+    g = {m: t.cuda() for m, t in x.items()}
+    out, S = torch.empty_like(g["v"]), torch.empty_like(g["S"])
+    delta.forward(g["q"], g["k"], g["v"], g["alpha"], g["beta"], out, state_in=g["S"] if kind == "state" else None,
+                  state_out=S, cu_seqlens=_ints(cu))
+    want, wantS = R.run(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["S"], cu)
+    # Every sequence by itself: a long one must not hide a short one.  Relative to the outputs alone there is
+    # no bound: one token from the zero state has o = beta (k.q) v, and a binary32 sum errs by up to d 2^-24
+    # sum |k_i q_i| <= d 2^-24 (unit k, q) however small k.q is -- 7.6e-6 beta |v| at d = 128, with |S| = beta |v|.
+    # So the states' share counts from the states: STATE |S| for each of the len tokens (|q| = 1).
+    for n in range(len(lens)):
+        if lens[n]:
+            o, w = out[cu[n]:cu[n + 1]].double().cpu(), want[cu[n]:cu[n + 1]]
+            bound = 2 * OUT[dtype] * float(w.norm()) + STATE * lens[n] ** 0.5 * float(wantS[n].norm())
+            assert float((o - w).norm()) <= bound, n
+    assert R.rel(out, want) <= OUT[dtype] and R.rel(S, wantS) <= STATE
 
 
 @pytest.mark.parametrize("N,L", [(3, 70), (5, 1), (1, 1024), (4, 0)])
@@ -123,12 +153,12 @@ def test_slots(lib, path, kda):
     stepq, delta = lib
     if kda and path == "segments":
         pytest.skip("KDA has one path")
-    lens = ([7800] if path == "segments" else PATHS[path]) + [40, 20]
+    lens = {"segments": [7800], "both": [1, 150, 3, 16] + 12 * [1]}.get(path, PATHS[path]) + [40, 20]
     kind = delta.KDA if kda else delta.GDN
     g, cu = _case(lens, 2, 2, 64, BF16, kda=kda)
-    n, N = 9, len(lens)
+    n, N = 20, len(lens)
     pool = torch.randn(n, 2, 64, 64, device="cuda")
-    pick = list(range(8, 8 - N, -1))
+    pick = list(range(n - 1, n - 1 - N, -1))
     pick[-2], pick[-1] = -1, n  # skip, out of range
     g["S"] = torch.stack([pool[s] if 0 <= s < n else torch.zeros_like(pool[0]) for s in pick])
     out, S = _forward(delta, g, cu, kind=kind)
@@ -147,7 +177,7 @@ def test_slots(lib, path, kda):
 @pytest.mark.parametrize("path", PATHS)
 def test_broken_offsets_skip_their_sequence(lib, path):
     stepq, delta = lib
-    g, cu = _case(PATHS[path] + [20 if path == "tokens" else 64], 1, 2, 64, BF16)
+    g, cu = _case(PATHS[path] + [{"tokens": 20, "both": 30}.get(path, 64)], 1, 2, 64, BF16)
     N, T = len(cu) - 1, cu[-1]
     want = _forward(delta, g, cu)
     grads = _backward(delta, g, cu)
@@ -172,7 +202,7 @@ def test_offsets_out_of_order_raise_the_flag(lib, path):
     """An offset in the middle that breaks the order: the flag is raised, rows of no sequence and other
     states stay, the call ends (what the other sequences hold is not specified)."""
     stepq, delta = lib
-    n = 20 if path == "tokens" else 64
+    n = 20 if path in ("tokens", "both") else 64
     g, cu = _case([n] + PATHS[path] + [n], 1, 2, 64, BF16, first=2, last=3)
     for bad in (cu[-1] + 9, -1, 2 ** 31 - 1, -2 ** 31, 0):
         status, off = _ints([0]), list(cu)
@@ -243,6 +273,15 @@ def test_a_non_finite_input_shows(lib, where, what, path):
         assert not torch.isfinite(S[0, 1]).all()
 
 
+def test_state_gradient_in_place(lib):
+    _, delta = lib
+    g, cu = _case(PATHS["chunks"], 2, 4, 64, BF16)
+    want = _backward(delta, g, cu)
+    o = {m: torch.empty_like(t) for m, t in want.items()}
+    o["dS"] = g["dS"]
+    assert _same(want, _backward(delta, g, cu, into=o))
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_results_do_not_depend_on_the_run(lib, path):
     _, delta = lib
@@ -297,8 +336,10 @@ def test_captured_graphs(lib, path):
                       cu_seqlens=c, workspace=ws)
     o = {m: torch.empty_like(t) for m, t in dict(dq=g["q"], dk=g["k"], dv=g["v"], dalpha=g["alpha"],
                                                  dbeta=g["beta"], dS=g["S"]).items()}
+    need = delta.backward_workspace(g["q"], g["k"], g["v"], g["alpha"], g["beta"], g["do"], cu_seqlens=c)
+    wb = torch.empty(need, dtype=torch.uint8, device="cuda") if path == "chunks" else None
     with torch.cuda.graph(gb):
-        _backward(delta, g, c, into=o)  # its workspace from the graph's own pool
+        _backward(delta, g, c, into=o, workspace=wb)  # None: from the graph's own pool
     for i in range(4):
         for m in ("q", "k", "v", "do", "S"):
             g[m].copy_(torch.roll(g[m], 1, 0))
@@ -318,8 +359,12 @@ def test_prefill_and_read_captured(lib):
     out, S = torch.empty_like(g["v"]), torch.empty(2, 4, 64, 64, dtype=BF16, device="cuda")
     o2, S2 = torch.empty_like(out), torch.empty_like(S)
 
+    need = plan.prefill_workspace(g["q"], g["k"], g["v"], g["alpha"], g["beta"], out, cu_seqlens=c)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
     def run(pool, out, S):
-        plan.prefill_slots(pool, 4, pick, g["q"], g["k"], g["v"], g["alpha"], g["beta"], out, cu_seqlens=c)
+        plan.prefill_slots(pool, 4, pick, g["q"], g["k"], g["v"], g["alpha"], g["beta"], out, cu_seqlens=c,
+                           workspace=ws)
         plan.read_slots(pool, 4, pick, 2, S)
     run(pool.clone(), out, S)
     torch.cuda.synchronize()
