@@ -642,19 +642,7 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
   if (const float* const first = MODE == kSegment ? nullptr : MODE == kReadout ? segs.S + seg : A.S_in ? A.S_in + so : nullptr)
     krows.template load_all<2 * NB>(first, St);
   if (c_first < c_end) fetch_v(c_first);
-  float unit = 0x1p-10f;  // an empty state takes its unit from the first W
-  auto rescale = [&](float m) {  // largest magnitude into [2^11, 2^12)
-    float inv;
-    const float f = m > 0.0f ? scale_of(m, inv) : (inv = 1.0f);
-    unit *= inv;
-#pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= f;
-  };
-  {
-    const float m = tiles_max<2 * NB>(St);
-    if (m > 0.0f) unit = 1.0f;
-    rescale(m);
-  }
+  float unit = 1.0f;
   const f4 zero = {0, 0, 0, 0};
   for (int c = c_first; c < c_end; c++) {
     const char* const lds = buf;
@@ -681,10 +669,8 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
     vrows.to_acc(v, R);
     if (more) fetch_v(c + 1);
     ahead();
-    {
-      const float m = tiles_max<2 * NB>(St);
-      if (__any(m > 0x1p14f || (m < 1.0f && m > 0.0f))) rescale(m);
-    }
+    float most = tiles_max<2 * NB>(St);
+    fit<2 * NB>(St, unit, most);
     if constexpr (MODE == kKeep) krows.template store_all<2 * NB>(keepS + ((j0 + c) * A.H + h) * D * D, St, unit);
     to_planes<NB, 2, true>(St, 1.0f, Sh, Sl);
     auto times_state = [&](bool low) {
@@ -779,25 +765,9 @@ __global__ __launch_bounds__(64 * NW, D == 64 && DT != kF32 ? 3 : 2) void k_chun
     // S1 = G_C S0 + K^T diag(L[C, .]) W, in the state's units
 #pragma unroll
     for (int rt = 0; rt < 4; rt++) R[rt] *= rows(kTabD, rt);
-    {
-      const float m = tiles_max<4>(R) * w1;
-      if (__any(m > unit * 0x1p14f)) {  // W outgrows the units: they become W's
-        float inv, to = unit;
-        if (m > unit * 0x1p14f) {
-          (void)scale_of(m, inv);
-          to = inv;
-        }
-        const float f = unit / to;  // both powers of two
-#pragma unroll
-        for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= f;
-        unit = to;
-      }
-      // unit is a power of two: its inverse by the exponent
-      to_planes<2, 2>(R, w1 * __uint_as_float(0x7f000000u - __float_as_uint(unit)), xh, xl);
-    }
-    const float G = tab[kTabG + 63];
-#pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++) St[rt] *= G;
+    fit_sum<2 * NB>(St, unit, most, tab[kTabG + 63], tiles_max<4>(R) * w1);
+    // unit is a power of two: its inverse by the exponent
+    to_planes<2, 2>(R, w1 * __uint_as_float(0x7f000000u - __float_as_uint(unit)), xh, xl);
 #pragma unroll
     for (int ks = 0; ks < 2; ks++) {
 #pragma unroll

@@ -90,19 +90,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep k
   for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] = f4{0, 0, 0, 0};
   if (B.dS_out) krows.template load_all<2 * NB>(B.dS_out + so, Gt);
   if (nc) fetch_o(nc - 1);
-  float unit = 0x1p-10f;
-  auto rescale = [&](float m) {
-    float inv;
-    const float f = m > 0.0f ? scale_of(m, inv) : (inv = 1.0f);
-    unit *= inv;
-#pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] *= f;
-  };
-  {
-    const float m = tiles_max<2 * NB>(Gt);
-    if (m > 0.0f) unit = 1.0f;
-    rescale(m);
-  }
+  float unit = 1.0f;
   const f4 zero = {0, 0, 0, 0};
   for (int c = nc - 1; c >= 0; c--) {
     const char* const lds = buf;
@@ -133,10 +121,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep k
     orows.to_acc(o, dO);
     if (c) fetch_o(c - 1);
     ahead();
-    {
-      const float m = tiles_max<2 * NB>(Gt);
-      if (__any(m > 0x1p14f || (m < 1.0f && m > 0.0f))) rescale(m);
-    }
+    float most = tiles_max<2 * NB>(Gt);
+    fit<2 * NB>(Gt, unit, most);
     krows.template store_all<2 * NB>(keep.G + ((j0 + c) * A.H + h) * D * D, Gt, unit);
     h8 xh[2], xl[2];
     f4 z[4], y[4];
@@ -207,23 +193,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep k
       dO[rt] *= rows(kTabQ, rt);
       Y[rt] *= -rows(kTabU, rt);
     }
-    {
-      const float m = fmaxf(tiles_max<4>(dO), tiles_max<4>(Y));
-      if (__any(m > unit * 0x1p14f)) {
-        float inv, to = unit;
-        if (m > unit * 0x1p14f) {
-          (void)scale_of(m, inv);
-          to = inv;
-        }
-        const float r = unit / to;
-#pragma unroll
-        for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] *= r;
-        unit = to;
-      }
-    }
-    const float GC = tab[kTabG + 63], iu = 1.0f / unit;
-#pragma unroll
-    for (int rt = 0; rt < 2 * NB; rt++) Gt[rt] *= GC;
+    fit_sum<2 * NB>(Gt, unit, most, tab[kTabG + 63], fmaxf(tiles_max<4>(dO), tiles_max<4>(Y)));
+    const float iu = 1.0f / unit;
     auto update = [&]() {
 #pragma unroll
       for (int ks = 0; ks < 2; ks++) {

@@ -118,3 +118,31 @@ def test_long_sequences_cut_into_segments(delta, d, dtype, lens):
                   cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
     want, wantS = R.run(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["S"], cu)
     assert R.rel(out, want) <= OUT[dtype] and R.rel(S, wantS) <= STATE
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [1e-30, 1e-20, 1e-8, 1e15])
+def test_values_of_any_size_from_the_zero_state(delta, d, scale):
+    cu = [0, 200]
+    x = R.inputs(15, 200, 2, 2, d, 1, F32)
+    x["v"], x["S"] = x["v"] * scale, torch.zeros_like(x["S"])
+    out, S = _forward(delta, x, cu, 1)
+    want, wantS = R.run(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["S"], cu)
+    assert R.rel(out, want) <= OUT[F32] and R.rel(S, wantS) <= STATE
+
+
+@pytest.mark.parametrize("t", [64, 128])
+@pytest.mark.parametrize("gate", [0.0, 1e-30])
+@pytest.mark.parametrize("scale", [1e-12, 1e-6, 1e6])
+def test_values_of_another_size_behind_a_closed_gate(delta, t, gate, scale):
+    """Chunks behind a closed gate owe nothing to the size of what was before it (inside a chunk a column
+    has one scale); one column is zero throughout."""
+    cu = [0, 250]
+    x = R.inputs(19, 250, 2, 2, 128, 1, F32)
+    x["alpha"][t] = gate
+    x["v"][t:] *= scale
+    x["v"][..., 5], x["S"][..., 5] = 0.0, 0.0
+    out, S = _forward(delta, x, cu, 1)
+    want, wantS = R.run(x["q"], x["k"], x["v"], x["alpha"], x["beta"], x["S"], cu)
+    assert R.rel(out[:t], want[:t]) <= OUT[F32] and R.rel(out[t:], want[t:]) <= OUT[F32]
+    assert R.rel(S, wantS) <= STATE

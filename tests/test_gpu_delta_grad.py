@@ -95,3 +95,20 @@ def test_gradient_of_gates_of_any_value(delta):
     cu = [0, 100, 130]
     x = R.inputs(41, 130, 1, 2, 128, 2, F32, gates="any")
     _check(_backward(delta, x, cu), _want(x, cu), cu, F32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [1e-20, 1e-8, 1e8])
+def test_gradients_of_any_size(delta, scale):
+    """Small and large output gradients with none behind the last token; and in a chunk before a closed
+    gate, with others of another size behind it."""
+    cu = [0, 200]
+    x = R.inputs(23, 200, 2, 2, 128, 1, F32)
+    x["do"], x["dS"] = x["do"] * scale, torch.zeros_like(x["dS"])
+    _check(_backward(delta, x, cu), _want(x, cu), cu, F32)
+    x["do"][64:] /= scale
+    x["alpha"][64] = 0.0
+    got, want = _backward(delta, x, cu), _want(x, cu)
+    for m in ("dq", "dk", "dv"):
+        assert R.rel(got[m][:64], want[m][:64]) <= TOL and R.rel(got[m][64:], want[m][64:]) <= TOL, m
+    assert R.rel(got["dS"], want["dS"]) <= TOL
