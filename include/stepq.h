@@ -277,10 +277,10 @@ int stepq_delta_forward(const stepq_delta_desc* desc, const void* q, const void*
  *   dq, dk [n_tokens, n_qk_heads, d] and dv [n_tokens, n_heads, d] of `dtype`, packed;
  *   dalpha, dbeta [n_tokens, n_heads] fp32;  dS_in [n_seqs, n_heads, d, d] fp32 (NULL = not wanted).
  * All are written, not added to; rows of no sequence are left as they were.  No output may overlap an
- * input or another output, but dS_in may be dS_out (in place).  Sums and operands as for
- * stepq_delta_forward's chunks.  Value heads that share
- * a key head add up in index order in binary32, so results do not depend on scheduling.  No
- * division by a gate: gates of zero have their gradient.  KDA: STEPQ_ERR_UNSUPPORTED.
+ * input or another output, but dS_in may be dS_out (in place).  Sums and operands
+ * as for stepq_delta_forward's chunks.  Value heads that share a key head add up in index order in
+ * binary32, so results do not depend on scheduling.  No division by a gate: gates of zero have their
+ * gradient.  KDA: STEPQ_ERR_UNSUPPORTED.
  */
 int stepq_delta_backward(const stepq_delta_desc* desc, const void* q, const void* k, const void* v,
                          const float* alpha, const float* beta, const float* S_in,
