@@ -36,7 +36,7 @@ using Square = LdsRows<float, 64>;
 //   L[t,s] = pre32[t] suf32[s] across blocks, pre8[t] mid suf8[s] across groups of a block,
 // pre = from the group's start to t, suf = behind s to the group's end; inside a group one by one.
 template <int D, int DT, bool QT>
-struct PrepSmem {
+struct alignas(16) PrepSmem {
   static constexpr int NPI = kInPlanes<DT>;
   union {
     struct {
