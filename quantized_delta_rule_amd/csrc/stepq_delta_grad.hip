@@ -314,10 +314,10 @@ __device__ __forceinline__ void rows_put(float (*x)[8], bool live, int rt, int l
 // token and with the earlier one as the lane's own (a wave each where there are eight): a lane then holds 8
 // consecutive partners (their row tiles permuted), which is the fragment of N, N^T and either half of Z + Z^T as it is.
 //
-// 8,192 tokens x 32 heads on 16 key heads (d = 128 bf16): 593 us, 36 a head and workgroup, 0.6 GB read.  One
+// 8,192 tokens x 32 heads on 16 key heads (d = 128 bf16): 480 .. 550 us, 32 a head and workgroup, 0.6 GB read.  One
 // workgroup a CU (operands of 64 x 128 in two planes fill LDS, 256 registers a lane), so a head's phases --
 // rows in, products with the states, pairs, gates -- follow each other with barriers between and half of
-// the wave cycles wait; the vector ALUs are busy 33%, the matrix cores 9%, LDS 33%.
+// the wave cycles wait; the vector ALUs are busy 38%, the matrix cores 11%, LDS 18%.
 template <int D, int DT>
 __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
   using Y = LayB<D, DT>;
@@ -381,8 +381,8 @@ __global__ __launch_bounds__(4 * D) void k_chunk_grad(GradArgs B, Keep keep) {
 #pragma unroll
     for (int n = 0; n < 4 * NPI; n++) *(h8*)(sm.kq[w] + n * kFrag + lane * 16) = kq_at(n / (2 * NPI), n / NPI % 2, n % NPI);
   // What a wave brings in of a head: row tile pt of Y and V or of W and dO (four waves: of both), 16 rows of S0.
-  // Not one head ahead: the registers that this takes cost more in spills than it hides (600 us -> 676 with
-  // S0 alone ahead; Y and W ahead in LDS 713 -> 742 before the fragments took their room).
+  // Not one head ahead: the registers that this takes cost more in spills than it hides (a kernel of 600 us
+  // took 676 with S0 alone ahead; with Y and W ahead in LDS 742 instead of 713).
   constexpr int NR = NW == 4 ? 2 : 1;
   float xs[KS][8], xr[NR][KS][8];
   Raw8<DT> xe[NR][KS];
