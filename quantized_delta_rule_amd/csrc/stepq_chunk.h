@@ -171,17 +171,20 @@ __device__ __forceinline__ void copy_block(const char* src, unsigned at, int fro
     if (i + NW * kFrag <= to - from || i + w * kFrag < to - from) copy_to_lds(src + i, at + i, lane16);
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-// The units of a column's tiles x (the column is unit * x): its largest magnitude m (in units) in [2^11, 2^12)
-// after `fit`, in [1, 2^14] while it is left alone.  A column of zeros has the least unit, so that whatever
-// is added first sets it.
+// The units of a column's tiles x (the column is unit * x): its largest magnitude m (in units) in [2^13, 2^14)
+// after `fit`, in [2^12, 2^15] while it is left alone.  Above 2^16 it would not be a binary16; below 2^12 the
+// update would be coarse: y of the update K^T y is written in these units as two binary16 planes, off by
+// max(2^-22 |y|, 2^-25), and K's planes (below 2^12) raise that to 2^-13 units a token -- 2^-25 of a column's
+// largest, 2^-22 where 64 tokens err the same way.  (Left alone down to 1, states of size one kept 12 bits.)
+// A column of zeros has the least unit, so that whatever is added first sets it.
 constexpr float kLeastUnit = 0x1p-110f;
 template <int NT>
 __device__ __forceinline__ void fit(f4* x, float& unit, float& m) {
-  if (!__any(m > 0x1p14f || (m < 1.0f && unit > kLeastUnit))) return;
+  if (!__any(m > 0x1p15f || (m < 0x1p12f && unit > kLeastUnit))) return;
   float inv, f = 1.0f, to = kLeastUnit;
   if (m > 0.0f) {
     (void)scale_of(m, inv);
-    to = fmaxf(unit * inv, kLeastUnit);
+    to = fmaxf(unit * (0.25f * inv), kLeastUnit);
     f = unit / to;  // both powers of two
   }
 #pragma unroll
@@ -189,19 +192,19 @@ __device__ __forceinline__ void fit(f4* x, float& unit, float& m) {
   m *= f;
   unit = to;
 }
-// The column becomes G x + y, with y's largest magnitude my (not in units): x times G, and in units that suit
-// the sum's larger part.  y may be far below what x was before G.
+// The column becomes G x + K^T y, with y's largest magnitude my (not in units): x times G, and in units that suit
+// the larger of the two, where K's planes make K^T y about 2^11 my.  It may be far below what x was before G.
 template <int NT>
 __device__ __forceinline__ void fit_sum(f4* x, float& unit, float m, float G, float my) {
 #pragma unroll
   for (int t = 0; t < NT; t++) x[t] *= G;
-  const float top = fmaxf(my, fabsf(G) * m * unit);
-  const bool off = my > unit * 0x1p14f || (top < unit && top > 0.0f && unit > kLeastUnit);
+  const float top = fmaxf(0x1p11f * my, fabsf(G) * m * unit);
+  const bool off = my > unit * 0x1p14f || (top < unit * 0x1p12f && top > 0.0f && unit > kLeastUnit);
   if (!__any(off)) return;
   float inv, to = unit;
   if (off) {
     (void)scale_of(top, inv);
-    to = fmaxf(fmaxf(inv, kLeastUnit), unit * 0x1p-100f);
+    to = fmaxf(fmaxf(0.25f * inv, kLeastUnit), unit * 0x1p-100f);
   }
   const float f = unit / to;
 #pragma unroll
