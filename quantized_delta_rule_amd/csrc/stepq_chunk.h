@@ -172,10 +172,10 @@ __device__ __forceinline__ void copy_block(const char* src, unsigned at, int fro
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // The units of a column's tiles x (the column is unit * x): its largest magnitude m (in units) in [2^13, 2^14)
-// after `fit`, in [2^12, 2^15] while it is left alone.  Above 2^16 it would not be a binary16; below 2^12 the
+// after `fit`, in [2^12, 2^15] while it is left alone.  Above 2^16 it would not be a binary16; far below, the
 // update would be coarse: y of the update K^T y is written in these units as two binary16 planes, off by
 // max(2^-22 |y|, 2^-25), and K's planes (below 2^12) raise that to 2^-13 units a token -- 2^-25 of a column's
-// largest, 2^-22 where 64 tokens err the same way.  (Left alone down to 1, states of size one kept 12 bits.)
+// largest.  (Left alone down to 1, states of size one kept 12 bits.)
 // A column of zeros has the least unit, so that whatever is added first sets it.
 constexpr float kLeastUnit = 0x1p-110f;
 template <int NT>
@@ -194,12 +194,15 @@ __device__ __forceinline__ void fit(f4* x, float& unit, float& m) {
 }
 // The column becomes G x + K^T y, with y's largest magnitude my (not in units): x times G, and in units that suit
 // the larger of the two, where K's planes make K^T y about 2^11 my.  It may be far below what x was before G.
+// Left alone down to 2^10 units (2^-23 a token; 64 that err independently, on K's mean instead of its largest
+// elements, 2^-22.4): at 2^12 an ordinary chunk's gates moved the units every time, for no measurable bit
+// (8 ragged prompts of 16,381 tokens x 48 heads: 460 us a call against 450).
 template <int NT>
 __device__ __forceinline__ void fit_sum(f4* x, float& unit, float m, float G, float my) {
 #pragma unroll
   for (int t = 0; t < NT; t++) x[t] *= G;
   const float top = fmaxf(0x1p11f * my, fabsf(G) * m * unit);
-  const bool off = my > unit * 0x1p14f || (top < unit * 0x1p12f && top > 0.0f && unit > kLeastUnit);
+  const bool off = my > unit * 0x1p14f || (top < unit * 0x1p10f && top > 0.0f && unit > kLeastUnit);
   if (!__any(off)) return;
   float inv, to = unit;
   if (off) {

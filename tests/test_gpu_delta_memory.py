@@ -5,10 +5,11 @@ recurrence in binary64.
 Tolerances as in test_gpu_delta.py and test_gpu_delta_grad.py (relative 2-norms).  The update K^T diag(L) W of a
 state column is the one operand without a scale of its own: it is written in the state's units.  A term
 y K has y as two binary16 planes, off by at most max(2^-22 |y|, 2^-25) units, times K's planes below 2^12: 2^-13
-units a token, with a column whose largest magnitude is at least 2^12 units: 2^-25 of it a token, 2^-22 for 64
-tokens that all err the same way.  This is one of the 12 * 2^-22 that the tolerances count for a chain.  Errors of
-chunks before add up as independent ones while gates of one keep them and the delta rule shrinks them: ten chunks
-are sqrt(10) * 2^-22 = 7.5e-7 here, well inside.  16-bit outputs add half a step of their type."""
+units a token, where the column (or what its gates leave of it) is at least 2^10 units: 2^-23 of its largest.  64
+tokens that err independently, on K's elements of a third of its largest, uniformly (3^-0.5): 8 / 3 / 3^0.5 * 2^-23 =
+2^-22.4, one of the 12 * 2^-22 that the tolerances count for a chain.  Errors of chunks before add up as
+independent ones while gates of one keep them and the delta rule shrinks them: ten chunks are sqrt(10) * 2^-22.4 =
+5.7e-7 here, well inside.  16-bit outputs add half a step of their type."""
 import pytest
 
 pytestmark = pytest.mark.gpu
