@@ -15,6 +15,7 @@
 
 #include "stepq.h"
 #include "stepq_delta.h"
+#include "stepq_host.h"
 #include "stepq_internal.h"
 
 using namespace stepq;

@@ -69,6 +69,12 @@ hipError_t launch_recurrent(const SeqArgs& a, hipStream_t s);
 hipError_t launch_chunk_forward(const SeqArgs& a, hipStream_t s);
 hipError_t launch_chunk_backward(const GradArgs& a, hipStream_t s);
 
+// Values of packed states by slot (stepq_read.hip); seq, slot_out and row_out: for a prompt pass.
+struct DevPlan;
+hipError_t launch_read(const DevPlan& P, const uint8_t* pool, int n_slots, const int* slots, int B,
+                       void* S, int dtype, const SeqArgs* seq, int* slot_out, int* row_out,
+                       hipStream_t s);
+
 #ifdef __HIPCC__
 namespace dlt {
 

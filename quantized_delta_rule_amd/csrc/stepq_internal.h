@@ -78,11 +78,6 @@ struct StepArgs {
 hipError_t launch_step(int kind, Mode mode, const StepArgs& a, hipStream_t s);
 hipError_t launch_unpack(const DevPlan& P, const uint8_t* pool, int B, float* S, uint16_t* r,
                          uint16_t* c, int8_t* z, hipStream_t s);
-// Values of packed states by slot (stepq_read.hip); seq, slot_out and row_out: for a prompt pass.
-struct SeqArgs;
-hipError_t launch_read(const DevPlan& P, const uint8_t* pool, int n_slots, const int* slots, int B,
-                       void* S, int dtype, const SeqArgs* seq, int* slot_out, int* row_out,
-                       hipStream_t s);
 hipError_t launch_row_impact(int kind, int order, int H, int D, int B, const float* q,
                              const float* k, const float* alpha, const float* beta, double* acc,
                              hipStream_t s);
@@ -97,28 +92,5 @@ int scratch_resolve(int device, void** out);
 // message and returns code; clear_error() empties it.  Shared by every host entry point.
 int fail(int code, const char* fmt, ...);
 void clear_error();
-
-
-// Makes a device current and restores the caller's on scope exit; when it is already
-// current (the usual case) no device switch is made either way.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok_ = false;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) {
-      prev = -1;
-      return;
-    }
-    if (prev == dev) {
-      prev = -1;
-      ok_ = true;
-      return;
-    }
-    if (hipSetDevice(dev) == hipSuccess) ok_ = true;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) (void)hipSetDevice(prev);
-  }
-};
 
 }  // namespace stepq

@@ -21,3 +21,13 @@ def test_committed_profiles_name_one_kernel_source_hash():
     shas = {json.load(open(os.path.join(prof, f)))["kernel_sha"]
             for f in os.listdir(prof) if f.endswith(".json")}
     assert len(shas) == 1
+
+
+def test_counter_traffic_is_reported():
+    """The decode kernels' sources are those that the committed counters were taken on."""
+    sys.path.insert(0, ROOT)
+    import bench
+    from quantized_delta_rule_amd import synth
+    found = [bench.committed(f, w) for w in synth.WORKLOADS.values() for f in (bench.COUNTERS, bench.SQ_COUNTERS)
+             if os.path.exists(f.format(name=w.name))]
+    assert found and all(found)
