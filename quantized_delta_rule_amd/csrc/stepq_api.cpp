@@ -595,7 +595,7 @@ int stepq_prefill_slots(stepq_plan_t p, const stepq_delta_desc* d, void* pool, i
   if (int rc = check_slots(pool, n_slots, slots, a.N)) return rc;
   if (int rc = seq_inputs(&a, q, k, v, alpha, beta, out)) return rc;
   if (int rc = seq_workspace(workspace, workspace_bytes, prefill_bytes(p, a))) return rc;
-  if (a.N == 0 || a.T == 0) return ok();
+  if (a.N == 0) return ok();
   DeviceGuard dg(p->device);
   hipStream_t s = (hipStream_t)stream;
   if (int rc = refuse_capture(p, s, "prefill_slots")) return rc;
@@ -613,6 +613,7 @@ int stepq_prefill_slots(stepq_plan_t p, const stepq_delta_desc* d, void* pool, i
   a.n_slots = a.N;
   a.ws = w;
   a.status = nullptr;  // the read has reported bad slots and offsets
+  if (a.T == 0) return ok();
   HIP_TRY(launch_forward(a, s));
   return encode_impl(p, S, pool, n_slots, slot_of, a.N, stream);
 }

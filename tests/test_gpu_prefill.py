@@ -99,3 +99,21 @@ def test_prefill_slots(lib, kind, order, d, dtype):
     plan.encode_slots(S1, ref, n_slots, _slots([7, -1, 5, 0, -1]), 5)
     assert torch.equal(ref, pool)
     assert plan.status() == 0
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+def test_prompts_without_tokens_report_their_slots_and_offsets(lib, mode):
+    """No token at all: every slot keeps its bytes, and a bad slot or bad offsets raise their flags as they do
+    beside sequences with tokens."""
+    stepq, _ = lib
+    plan = _plan(stepq, "gdn", 64, 4, mode=mode)
+    pool = _filled(plan, 3)
+    was = pool.clone()
+    x = {m: t.cuda() for m, t in R.inputs(1, 0, 4, 4, 64, 2, BF16).items()}
+    out = torch.empty_like(x["v"])
+    for cu, pick, flag in (([0, 0, 0], [1, -1], 0), ([0, 0, 0], [1, 3], stepq.FLAG_BAD_SLOT),
+                           ([0, 5, 0], [1, 2], stepq.FLAG_BAD_SEQ)):
+        plan.prefill_slots(pool, 3, _slots(pick), x["q"], x["k"], x["v"], x["alpha"], x["beta"], out,
+                           cu_seqlens=_slots(cu))
+        assert plan.status(reset=True) == flag, (cu, pick)
+        assert torch.equal(pool, was)
