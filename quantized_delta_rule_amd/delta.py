@@ -14,10 +14,14 @@ enqueue kernels on `stream` (default: the current stream of the tensors' device)
 must stay alive until then as for any stream work.  A workspace is taken from torch's allocator on that
 stream unless one is passed (uint8, 256-byte aligned, of forward_workspace(), backward_workspace() or
 Plan.prefill_workspace() bytes; calls that may run at once need one each).
+
+No call records an autograd graph: a program that trains calls forward() and backward() from the forward and
+backward of a torch.autograd.Function.  forward() warns where a graph is wanted and none is recorded.
 """
 from __future__ import annotations
 
 import ctypes
+import warnings
 
 from .stepq import (DECAY_FIRST, DELTA_FIRST, GDN, KDA, StepqError, _check, _dev_tensor, lib)  # noqa: F401
 
@@ -179,6 +183,14 @@ def backward_workspace(q, k, v, alpha, beta, d_out, *, cu_seqlens=None, n_seqs=N
     return _need(lib().stepq_delta_backward_workspace, "delta_backward_workspace", ctypes.byref(a.desc))
 
 
+def _no_graph():
+    import torch
+    if torch.is_grad_enabled():
+        warnings.warn("delta.forward records no graph: out and state_out get no gradient (call it from a "
+                      "torch.autograd.Function, with delta.backward as its backward, or under torch.no_grad)",
+                      stacklevel=3)
+
+
 def forward(q, k, v, alpha, beta, out, *, state_in=None, state_out=None, cu_seqlens=None, n_seqs=None,
             slots=None, kind=GDN, order=DELTA_FIRST, status=None, workspace=None, stream=None):
     """Runs every sequence from its state: S_t = A_t S_{t-1} + beta_t k_t v_t^T, out_t = S_t^T q_t.
@@ -195,6 +207,9 @@ def forward(q, k, v, alpha, beta, out, *, state_in=None, state_out=None, cu_seql
             raise ValueError("slots need state_in or state_out")
         n_slots = S.shape[0]
     si, so = a.state(state_in, "state_in", n_slots), a.state(state_out, "state_out", n_slots)
+    if (q.requires_grad or k.requires_grad or v.requires_grad or alpha.requires_grad or beta.requires_grad
+            or (state_in is not None and state_in.requires_grad)):
+        _no_graph()
     sl = _slots(slots, a.N, a.device)
     L, d = lib(), ctypes.byref(a.desc)
     ws, size, keep = a.workspace(workspace, _need(L.stepq_delta_forward_workspace,
