@@ -262,7 +262,12 @@ int stepq_delta_backward_workspace(const stepq_delta_desc* desc, size_t* bytes);
  * GDN sequences of 16 tokens and more (on average; each by itself where the average is below and
  * n_tokens - n_seqs at least 128) run in chunks of 64 tokens on the matrix cores: sums
  * and states in binary32; operands in pairs of binary16 with power-of-two scales, 22 bits of the largest
- * element of a row, or of a column of a chunk; the last products of a BF16 out in single ones (11 bits).
+ * element of a row, or of a column of a chunk (of a state: of its largest in that chunk); the last products
+ * of a BF16 out in single ones: 11 bits of every term, so that an output that is a small difference of large
+ * terms has 11 bits of those (F32 and F16 outputs: 22).
+ * Paths, and where few sequences are long also the segments they are cut into, follow n_tokens, n_seqs and
+ * n_heads: a sequence alone may differ in its last bits, within these bounds, from the same one beside others.
+ * The same call on the same inputs gives the same bits.
  * There a non-finite input may make its head's outputs non-finite from its chunk's first token on.
  * Otherwise tokens are taken one by one in binary32.  Only enqueues kernels: may be captured.
  */

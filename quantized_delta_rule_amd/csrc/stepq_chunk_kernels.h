@@ -27,7 +27,7 @@ using Square = LdsRows<float, 64>;
 // tiles as the A side the accumulators of a pair hold 8 consecutive tokens s of a lane's token t, which is
 // P's fragment as it is and two 16-byte stores of A.  (The gradient wants P^T: Q on the A side, s as columns.)
 //
-// 16,381 tokens x 48 heads on 16 key heads (d = 128 bf16): 165 us for 134 MB read and 446 MB written, 3.5 TB/s of the
+// 16,381 tokens x 48 heads on 16 key heads (d = 128 bf16): 163 us for 105 MB read and 446 MB written, 3.4 TB/s of the
 // 5.2 that a copy reaches; 8,192 tokens x 32 heads on 16 for the gradient 100 us.  Three workgroups a CU wait for
 // each other's memory most of the time (56% of wave cycles); the vector ALUs are busy 40%, LDS 35%.
 // A fourth workgroup would spill (188 us).
@@ -508,8 +508,8 @@ __global__ __launch_bounds__(256, Y::grad ? 2 : 3) void k_chunk_prep(SeqArgs A) 
 // St within binary16's range, checked every chunk), so that it turns into an operand without a product and
 // the update accumulates on it directly.
 //
-// 8 sequences of 0 .. 3,698 tokens x 48 states (d = 128 bf16): 327 us, of it about 5.5 a chunk of the longest
-// sequence; 529 MB read, 221 written.  A chunk is one chain of products and roundings to operands (K S, T R, P W,
+// 8 sequences of 0 .. 3,698 tokens x 48 states (d = 128 bf16): 331 us (median of calls; 319 .. 350), of it about 5.5 a
+// chunk of the longest sequence; 541 MB read, 226 written.  A chunk is one chain of products and roundings to operands (K S, T R, P W,
 // K^T W), and two waves a SIMD fill its gaps only in part: the vector ALUs are busy 48%, the matrix cores 29%,
 // 30% of the wave cycles wait.  Four waves a SIMD do not fit: a state column with its operands takes 190
 // registers.  The chain of a column does not shorten with more CUs, hence the segments below.

@@ -30,7 +30,7 @@ struct Keep {  // per chunk slot and value head, binary32
 
 // The reverse pass: like k_chunk_state a wave owns 16 columns of one state's gradient for the whole sequence
 // and holds it in units of a power of two per column.  4 sequences of 2,048 tokens x 32 states (d = 128
-// bf16): 241 us, 7.5 a chunk, 185 MB read and 459 written (the state's gradient behind every chunk among them): two
+// bf16): 245 us (median of calls; 237 .. 255), 7.6 a chunk, 189 MB read and 470 written (the state's gradient behind every chunk among them): two
 // operands' roundings more a chunk than forward, and one wave a SIMD.
 template <int D, int DT, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_chunk_reverse(GradArgs B, Keep keep) {

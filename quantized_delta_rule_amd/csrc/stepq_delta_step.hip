@@ -9,9 +9,9 @@
 // over a lane's rows and then over the 8 row groups.
 //
 // Bound by HBM: a single token reads and writes every state once and computes 6 operations an entry.  70 x 48
-// states of 128 x 128 (440 MB) take 62 us with a part of them in the memory-side cache and 80 us without
-// (5.5 TB/s; a copy reaches 5.2); 64 x 32 states and four tokens with row gates 58 us; one request's
-// 48 states 5.3 us.  32 columns a wave, not 64: one request then still has 192 waves on as many SIMDs.
+// states of 128 x 128 (440 MB) take 62 us where a part of them is in the memory-side cache (the same states call
+// after call) and 87 us where six pools take turns (5.0 TB/s; a copy reaches 5.2); 64 x 32 states and four tokens
+// with row gates 58 and 71 us; one request's 48 states 5.3 us.  32 columns a wave, not 64: one request then still has 192 waves on as many SIMDs.
 #include "stepq_delta.h"
 
 namespace stepq {
