@@ -181,7 +181,8 @@ __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)
 // update would be coarse: y of the update K^T y is written in these units as two binary16 planes, off by
 // max(2^-22 |y|, 2^-25), and K's planes (below 2^12) raise that to 2^-13 units a token -- 2^-25 of a column's
 // largest.  (Left alone down to 1, states of size one kept 12 bits.)
-// A column of zeros has the least unit, so that whatever is added first sets it.
+// A column of zeros has the least unit, so that whatever is added first sets it.  Columns below 2^-98 (3e-30) stay at
+// the least unit and lose bits as they shrink.
 constexpr float kLeastUnit = 0x1p-110f;
 template <int NT>
 __device__ __forceinline__ void fit(f4* x, float& unit, float& m) {
