@@ -99,7 +99,7 @@ def draw(rng):
     ragged, state = rng.random() < 0.75, rng.random() < 0.7
     if op.endswith("step"):
         ch, n = 8 * _log_int(rng, 8, 1280), rng.choice([8, 16, 16, 32, 64])
-        seqs = _log_int(rng, 1, min(256, 70_000_000 // (ch * n)))
+        seqs = _log_int(rng, 1, min(256, 60_000_000 // (ch * n)))
         each = rng.choice([1, 1, 1, 2, 4, 7])
         if op == "conv-step":
             return _conv(None, op, dtype, seqs, seqs * each, ch, rng.choice([2, 3, 4, 4]), rng.random() < 0.8,
