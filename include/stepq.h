@@ -59,8 +59,12 @@ enum { STEPQ_ORDER_DELTA_FIRST = 0, STEPQ_ORDER_DECAY_FIRST = 1 };
 #define STEPQ_FLAG_BAD_SLOT 8u  /* a slot index outside [0, n_slots) other than -1          */
 #define STEPQ_FLAG_BAD_SEQ 16u  /* token offsets that are not 0 <= cu[s] <= cu[s+1] <= n_tokens */
 
-/* element types of the sequence calls' q, k, v and out, and of stepq_read_slots' values */
-enum { STEPQ_DTYPE_F32 = 0, STEPQ_DTYPE_BF16 = 1, STEPQ_DTYPE_F16 = 2 };
+/* element types of the sequence calls' q, k, v and out, of stepq_read_slots' values and of the layer
+   calls' rows; the last two for the norm's output only */
+enum { STEPQ_DTYPE_F32 = 0, STEPQ_DTYPE_BF16 = 1, STEPQ_DTYPE_F16 = 2, STEPQ_DTYPE_E4M3 = 3, STEPQ_DTYPE_I8 = 4 };
+
+/* activation of the convolution's output, and of the norm's gate */
+enum { STEPQ_ACT_NONE = 0, STEPQ_ACT_SILU = 1, STEPQ_ACT_SIGMOID = 2 };
 
 /*
  * Plan description (Method 1: the offline precision map, pivots and impact scores).
@@ -312,6 +316,150 @@ int stepq_prefill_slots(stepq_plan_t plan, const stepq_delta_desc* desc, void* p
    row b as it was; other indices outside [0, n_slots) do too and raise STEPQ_FLAG_BAD_SLOT. */
 int stepq_read_slots(stepq_plan_t plan, const void* pool, int n_slots, const int32_t* slots, int B,
                      void* S, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------------- */
+/* Around the recurrence: the short causal convolution in front of it, the selective state    */
+/* space scan (the recurrence whose states decay by themselves), the norm behind it.          */
+/* ---------------------------------------------------------------------------------------- */
+
+/*
+ * Common to the convolution and the scan: n_seqs, n_tokens, cu_seqlens, slots, status and device mean what
+ * they mean for the delta rule's sequence calls (rows of no sequence are not read, and outputs are left as
+ * they were there; bad offsets and slots raise flags and skip their sequence).  Row strides are in elements from
+ * one token's row to the next, 0 = packed; rows and strides are multiples of 16 bytes, pointers to rows and
+ * states 16-byte aligned.  Calls only enqueue kernels and may be captured.  Sums are binary32 in an order
+ * that the sizes alone fix: the same call on the same inputs gives the same bits.
+ */
+
+/*
+ * Short causal convolution over the tokens of each channel by itself:
+ *   u_t[c] = bias[c] + sum_{j < width} weight[c, j] x_{t - (width - 1) + j}[c],  out = u (STEPQ_ACT_NONE)
+ *   or u sigmoid(u) (STEPQ_ACT_SILU).  Inputs before a sequence's first token are its state's rows.
+ *   dtype        type of x, out, states and their gradients (F32, BF16, F16).
+ *   param_dtype  type of weight and bias (the same three).
+ *   channels     a multiple of 8;  width 2, 3 or 4.
+ */
+typedef struct {
+  int dtype, param_dtype;
+  int channels, width, activation;
+  int n_seqs, n_tokens;
+  int device;
+  long long x_stride, out_stride;
+  const int32_t* cu_seqlens;
+  uint32_t* status;
+} stepq_conv_desc;
+
+/*
+ *   x, out [n_tokens, channels];  weight [channels, width], bias [channels] or NULL;
+ *   S_in [.., width - 1, channels] the inputs before the first token, oldest first (NULL = zeros);
+ *   S_out the same after the last token (NULL = not kept); may be S_in (in place), but must not overlap it
+ *   otherwise.  A sequence without tokens copies its state.  slots as for stepq_delta_forward.
+ *   out must not overlap an input.
+ */
+int stepq_conv_forward(const stepq_conv_desc* desc, const void* x, const void* weight, const void* bias,
+                       const void* S_in, void* S_out, int n_slots, const int32_t* slots, void* out,
+                       void* stream);
+
+/*
+ * Gradient of stepq_conv_forward (no slots): from d_out [n_tokens, channels] (dtype, out_stride) and dS_out
+ * [n_seqs, width - 1, channels] (NULL = zero) to dx [n_tokens, channels] (packed), dweight [channels, width]
+ * and dbias [channels] (binary32; dbias NULL = not wanted), dS_in [n_seqs, width - 1, channels] (NULL = not
+ * wanted).  All are written, not added to; no output may overlap an input or another output.  The workspace
+ * (256-byte aligned) belongs to the call until its work is done.
+ */
+int stepq_conv_backward_workspace(const stepq_conv_desc* desc, size_t* bytes);
+int stepq_conv_backward(const stepq_conv_desc* desc, const void* x, const void* weight, const void* bias,
+                        const void* S_in, const void* d_out, const void* dS_out, void* dx, float* dweight,
+                        float* dbias, void* dS_in, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Selective state space scan.  Per channel c and state n, with step D_t[c] > 0:
+ *   D_t = softplus(dt_t + dt_bias) (softplus = 1) or dt_t + dt_bias (softplus = 0);
+ *   h_t[c, n] = exp(D_t[c] A[c, n]) h_{t-1}[c, n] + D_t[c] B_t[g, n] x_t[c];
+ *   out_t[c] = (sum_n C_t[g, n] h_t[c, n] + D[c] x_t[c]) z_t[c] sigmoid(z_t[c]);
+ * channel c reads group g = c / (channels / n_groups) of B and C; without z its factor is one, without D its
+ * term is missing.
+ *   dtype      type of x, dt, B, C, z, out and their gradients; A, D, dt_bias and states are binary32.
+ *   channels   a multiple of 8 n_groups;  d_state 8, 16, 32 or 64.
+ */
+typedef struct {
+  int dtype;
+  int channels, n_groups, d_state, softplus;
+  int n_seqs, n_tokens;
+  int device;
+  long long x_stride, dt_stride, z_stride, out_stride, b_stride, c_stride;
+  const int32_t* cu_seqlens;
+  uint32_t* status;
+} stepq_scan_desc;
+
+/*
+ *   x, dt, z, out [n_tokens, channels];  B, C [n_tokens, n_groups, d_state];  A [channels, d_state];
+ *   D, dt_bias [channels] or NULL;  z NULL = no gate;
+ *   S_in [.., channels, d_state] first states (NULL = zero), S_out last states (NULL = not kept); may be S_in
+ *   (in place).  slots as for stepq_delta_forward.  out must not overlap an input, nor the workspace anything.
+ * Non-finite inputs reach their channel's outputs from their token on (B and C: their group's).
+ */
+int stepq_scan_forward_workspace(const stepq_scan_desc* desc, size_t* bytes);
+int stepq_scan_forward(const stepq_scan_desc* desc, const void* x, const void* dt, const float* A, const void* B,
+                       const void* C, const float* D, const float* dt_bias, const void* z, const float* S_in,
+                       float* S_out, int n_slots, const int32_t* slots, void* out, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of stepq_scan_forward (no slots): from d_out [n_tokens, channels] (dtype, out_stride) and dS_out
+ * [n_seqs, channels, d_state] (NULL = zero) to dx, ddt, dz [n_tokens, channels], dB, dC [n_tokens, n_groups,
+ * d_state] (dtype, packed), dA [channels, d_state], dD, ddt_bias [channels] and dS_in [n_seqs, channels,
+ * d_state] (binary32).  dD, ddt_bias and dS_in may be NULL (not wanted); dz goes with z.  All are written, not
+ * added to; rows of no sequence are left as they were.  No output may overlap an input or another output.
+ */
+int stepq_scan_backward_workspace(const stepq_scan_desc* desc, size_t* bytes);
+int stepq_scan_backward(const stepq_scan_desc* desc, const void* x, const void* dt, const float* A, const void* B,
+                        const void* C, const float* D, const float* dt_bias, const void* z, const float* S_in,
+                        const void* d_out, const float* dS_out, void* dx, void* ddt, float* dA, void* dB, void* dC,
+                        float* dD, float* ddt_bias, void* dz, float* dS_in, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/*
+ * Root-mean-square norm over the d columns of every head's row:
+ *   h = x + residual;  y = h / sqrt(mean(h^2) + eps) * weight * act(z);
+ * residual_out = h rounded once (y is computed from h before that rounding); act(z) = z sigmoid(z)
+ * (STEPQ_ACT_SILU) or sigmoid(z) (STEPQ_ACT_SIGMOID).
+ *   dtype        type of x, residual, residual_out, z (F32, BF16, F16);  param_dtype that of weight.
+ *   out_dtype    dtype, or E4M3 or I8: eight bits with scales: scale = max |y| / 448 (E4M3) or / 127 (I8) over
+ *                a head's row (group = 0) or every `group` (64 or 128; d a multiple) of its columns, out = y / scale to
+ *                the nearest (ties to even); a group of zeros has scale 1.  The scale is at least the smallest
+ *                normal binary32.  A y that is NaN takes no part in the maximum: its code is NaN (E4M3) or 0 (I8).
+ *   n_rows       rows of n_heads * d elements, n_heads x n_rows below 2^31;  d a multiple of 8, at most 32768.
+ *   strides      elements between rows, 0 = packed; multiples of 16 bytes (out's of 8 bytes with 8 bits).
+ */
+typedef struct {
+  int dtype, param_dtype, out_dtype;
+  int n_rows, n_heads, d;
+  int gate, group;
+  float eps;
+  int device;
+  long long x_stride, residual_stride, z_stride, out_stride;
+} stepq_norm_desc;
+
+/*
+ *   x, residual, residual_out, z, out [n_rows, n_heads, d] (residual, residual_out and z may be NULL;
+ *   residual_out has residual's stride), weight [d] or NULL (ones), scale [n_rows, n_heads] or [n_rows, n_heads,
+ *   d / group] binary32 (8-bit outputs only).  out may be x, and residual_out may be residual or x, each with the
+ *   other's type and stride (in place); no output may overlap anything else.
+ */
+int stepq_norm_forward(const stepq_norm_desc* desc, const void* x, const void* weight, const void* residual,
+                       const void* z, void* out, float* scale, void* residual_out, void* stream);
+
+/*
+ * Gradient of the norm at h [n_rows, n_heads, d] (x's stride; the sum that the norm was taken of, that is x or
+ * residual_out): from d_out (dtype, out_stride) and d_residual (NULL = zero; residual_stride: the gradient that
+ * reaches h by the residual's own way) to dx [n_rows, n_heads, d] (packed; the gradient of x and of the residual alike),
+ * dz (packed; goes with z) and dweight [d] (binary32, NULL = not wanted).  out_dtype is dtype, group 0.
+ */
+int stepq_norm_backward_workspace(const stepq_norm_desc* desc, size_t* bytes);
+int stepq_norm_backward(const stepq_norm_desc* desc, const void* h, const void* weight, const void* z,
+                        const void* d_out, const void* d_residual, void* dx, float* dweight, void* dz,
+                        void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------- */
 /* Offline planning on the host (Method 1, Method 2).  binary64, host pointers.            */

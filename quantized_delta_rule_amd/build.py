@@ -27,7 +27,9 @@ HIPCC_FLAGS = [
 
 SOURCES = ("stepq_k128_gdn.hip", "stepq_k128_kda.hip", "stepq_k64.hip", "stepq_calib.hip",
            "stepq_noalloc.hip", "stepq_delta_step.hip", "stepq_delta_chunk.hip",
-           "stepq_delta_grad.hip", "stepq_read.hip", "stepq_api.cpp", "stepq_delta_api.cpp",
+           "stepq_delta_grad.hip", "stepq_read.hip", "stepq_conv.hip", "stepq_scan.hip",
+           "stepq_scan_grad.hip", "stepq_norm.hip", "stepq_layer_sum.hip", "stepq_api.cpp",
+           "stepq_delta_api.cpp", "stepq_layer_api.cpp",
            "stepq_offline.cpp")
 OBJDIR = os.path.join(HERE, "_build")
 

@@ -1,0 +1,285 @@
+// stepq_conv.hip -- short causal convolution of each channel over its own tokens, and its gradient:
+//   u_t = b + sum_{j < W} w_j x_{t - (W - 1) + j},  y = u or u sigmoid(u)
+//   du = dy act'(u);  dx_t = sum_j w_j du_{t + (W - 1) - j};  dw_j = sum_t du_t x_{t - (W - 1) + j};  db = sum_t du_t
+// A lane owns a few neighbouring channels of one piece of a sequence and goes down its tokens with the last W - 1
+// inputs (and, backwards, derivatives) in registers, so every row is read once but for W - 1 rows at a piece's ends.
+// Bound by HBM: 2 W + 5 operations an element against 4 bytes of a 16-bit type.
+#include "stepq_layer.h"
+
+namespace stepq {
+namespace {
+
+using namespace lay;
+
+constexpr int kSh = 5, kPiece = 1 << kSh;  // tokens of a piece
+
+// The part of a sequence that a wave works on.
+struct Part {
+  int s, slot;
+  long long t0, len, p, end;  // first row and length of the sequence, the piece's positions p .. end - 1 in it
+  bool first;
+};
+
+// False where the wave has nothing to do.  One lane a sequence raises the flags.
+__device__ __forceinline__ bool part_of(const ConvArgs& A, long long j, bool report, int lane, Part& P) {
+  int a, b;
+  if (report && j < A.N) {
+    const bool ok = seq_range(A, (int)j, a, b);
+    seq_slot(A, (int)j, ok, lane == 0);
+  }
+  long long idx;
+  if (!piece(A, kSh, j, lane, P.s, idx)) return false;
+  const bool ok = seq_range(A, P.s, a, b);
+  P.slot = seq_slot(A, P.s, ok, false);
+  P.t0 = a;
+  P.len = b - a;
+  P.p = idx << kSh;
+  P.end = P.p + kPiece < P.len ? P.p + kPiece : P.len;
+  P.first = idx == 0;
+  return P.slot >= 0 && (P.p < P.len || P.first);
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void row(const void* p, long long i, float* x) {
+  if constexpr (V == 8) load8<DT>(p, i, x);
+  else loadn<DT, V>(p, i, x);
+}
+template <int DT, int V>
+__device__ __forceinline__ void put(void* p, long long i, const float* x) {
+  if constexpr (V == 8) store8<DT>(p, i, x);
+  else storen<DT, V>(p, i, x);
+}
+
+// Weights of V channels, [j][channel], and their bias.
+template <int W, int V>
+__device__ __forceinline__ void weights(const ConvArgs& A, int c, float (&w)[W][V], float (&b)[V]) {
+  float raw[W * V];
+#pragma unroll
+  for (int i = 0; i < W * V; i += 4) load4_any(A.pdtype, A.w, (long long)c * W + i, raw + i);
+#pragma unroll
+  for (int v = 0; v < V; v++) {
+    b[v] = 0;
+#pragma unroll
+    for (int j = 0; j < W; j++) w[j][v] = raw[v * W + j];
+  }
+  if (A.b) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4) load4_any(A.pdtype, A.b, c + v, b + v);
+  }
+}
+
+template <int DT, int W, int V>
+__global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
+  const int lane = threadIdx.x & 63;
+  const int cb = blockIdx.x % blocks;
+  const long long j = (long long)(blockIdx.x / blocks) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Part P;
+  if (!part_of(A, j, cb == 0, lane, P)) return;
+  const int c = (cb * 64 + lane) * V;
+  if (c >= A.C) return;
+  float w[W][V], b[V], x[W][V];  // x: the last W inputs
+  weights<W, V>(A, c, w, b);
+  const long long so = (long long)P.slot * (W - 1) * A.C + c;
+#pragma unroll
+  for (int i = 0; i < W - 1; i++) {
+    const long long at = P.p - (W - 1) + i;
+    if (at >= 0) row<DT, V>(A.x, (P.t0 + at) * A.xs + c, x[i]);
+    else if (A.S_in) row<DT, V>(A.S_in, so + (at + W - 1) * A.C, x[i]);
+    else {
+#pragma unroll
+      for (int v = 0; v < V; v++) x[i][v] = 0;
+    }
+  }
+  if (P.first && A.S_out) {  // the piece that read the old state is the one that writes the new one
+    float last[W - 1][V];
+#pragma unroll
+    for (int i = 0; i < W - 1; i++) {
+      const long long at = P.len - (W - 1) + i;
+      if (at >= 0) row<DT, V>(A.x, (P.t0 + at) * A.xs + c, last[i]);
+      else {  // row at + W - 1 of the old one
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+          float o = 0;
+#pragma unroll
+          for (int k = 0; k < W - 1; k++) o = at + W - 1 == k ? x[k][v] : o;
+          last[i][v] = o;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < W - 1; i++) put<DT, V>(A.S_out, so + (long long)i * A.C, last[i]);
+  }
+  for (long long t = P.t0 + P.p; t < P.t0 + P.end; t++) {
+    row<DT, V>(A.x, t * A.xs + c, x[W - 1]);
+    float y[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      float u = b[v];
+#pragma unroll
+      for (int i = 0; i < W; i++) u = fmaf(w[i][v], x[i][v], u);
+      y[v] = act_of(A.act, u);
+    }
+    put<DT, V>(A.out, t * A.os + c, y);
+#pragma unroll
+    for (int i = 0; i < W - 1; i++) {
+#pragma unroll
+      for (int v = 0; v < V; v++) x[i][v] = x[i + 1][v];
+    }
+  }
+}
+
+// A piece's wave goes from its first token to W - 1 tokens behind its last: with du of the last W tokens it
+// settles dx of the token W - 1 back.  Positions before the sequence are the state's rows, so the first piece
+// begins W - 1 tokens earlier, where du is zero.  Sums of dw and db are over the piece's own tokens.
+template <int DT, int W, int V>
+__global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
+  __shared__ float sum[4][(W + 1) * V][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cb = blockIdx.x % blocks;
+  const long long j = (long long)(blockIdx.x / blocks) * 4 + wave;
+  const int c = (cb * 64 + lane) * V;
+  float dw[W][V], db[V];
+#pragma unroll
+  for (int v = 0; v < V; v++) {
+    db[v] = 0;
+#pragma unroll
+    for (int i = 0; i < W; i++) dw[i][v] = 0;
+  }
+  Part P;
+  if (part_of(A, j, cb == 0, lane, P) && c < A.C) {
+    float w[W][V], b[V], x[W][V], du[W][V];
+    weights<W, V>(A, c, w, b);
+    const long long so = (long long)P.s * (W - 1) * A.C + c;
+#pragma unroll
+    for (int i = 0; i < W - 1; i++) {
+      const long long at = P.p - (W - 1) + i;
+      if (at >= 0) row<DT, V>(A.x, (P.t0 + at) * A.xs + c, x[i]);
+      else if (A.S_in) row<DT, V>(A.S_in, so + (at + W - 1) * A.C, x[i]);
+      else {
+#pragma unroll
+        for (int v = 0; v < V; v++) x[i][v] = 0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < W; i++) {
+#pragma unroll
+      for (int v = 0; v < V; v++) du[i][v] = 0;
+    }
+    // positions settled: p .. end - 1, from -(W - 1) in the first piece
+    const long long from = P.first ? -(long long)(W - 1) : P.p;
+    for (long long q = P.p; q < P.end + W - 1; q++) {
+      const bool in = q < P.len;
+#pragma unroll
+      for (int v = 0; v < V; v++) du[W - 1][v] = 0;
+      if (in) {
+        float dy[V];
+        row<DT, V>(A.x, (P.t0 + q) * A.xs + c, x[W - 1]);
+        row<DT, V>(A.d_out, (P.t0 + q) * A.os + c, dy);
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+          float u = b[v];
+#pragma unroll
+          for (int i = 0; i < W; i++) u = fmaf(w[i][v], x[i][v], u);
+          float d = dy[v];
+          if (A.act == kSilu) {
+            const float s = sigmoid(u);
+            d *= fmaf(u * s, 1.0f - s, s);
+          }
+          du[W - 1][v] = d;
+          if (q < P.end) {
+            db[v] += d;
+#pragma unroll
+            for (int i = 0; i < W; i++) dw[i][v] = fmaf(d, x[i][v], dw[i][v]);
+          }
+        }
+      }
+      const long long o = q - (W - 1);
+      if (o >= from && o < P.end) {
+        float g[V];
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+          g[v] = 0;
+#pragma unroll
+          for (int i = 0; i < W; i++) g[v] = fmaf(w[W - 1 - i][v], du[i][v], g[v]);
+        }
+        const long long r = o - P.len + W - 1;  // the last rows are the state that the sequence leaves
+        if (r >= 0 && A.dS_out) {
+          float more[V];
+          row<DT, V>(A.dS_out, so + r * A.C, more);
+#pragma unroll
+          for (int v = 0; v < V; v++) g[v] += more[v];
+        }
+        if (o >= 0) put<DT, V>(A.dx, (P.t0 + o) * A.C + c, g);
+        else if (A.dS_in) put<DT, V>(A.dS_in, so + (o + W - 1) * A.C, g);
+      }
+#pragma unroll
+      for (int i = 0; i < W - 1; i++) {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+          x[i][v] = x[i + 1][v];
+          du[i][v] = du[i + 1][v];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; v++) {
+#pragma unroll
+    for (int i = 0; i < W; i++) sum[wave][v * W + i][lane] = dw[i][v];
+    sum[wave][W * V + v][lane] = db[v];
+  }
+  __syncthreads();
+  // row of the partial sums: dw as [C, W], then db
+  float* part = A.ws + (long long)(blockIdx.x / blocks) * A.C * (W + 1);
+  for (int i = threadIdx.x; i < W * V * 64; i += 256) {
+    const int l = i / (W * V), e = i % (W * V);
+    const long long m = (long long)cb * 64 * V * W + i;
+    if (m < (long long)A.C * W) part[m] = sum[0][e][l] + sum[1][e][l] + sum[2][e][l] + sum[3][e][l];
+  }
+  for (int i = threadIdx.x; i < V * 64; i += 256) {
+    const int l = i / V, e = W * V + i % V;
+    const long long m = (long long)cb * 64 * V + i;
+    if (m < A.C) part[(long long)A.C * W + m] = sum[0][e][l] + sum[1][e][l] + sum[2][e][l] + sum[3][e][l];
+  }
+}
+
+constexpr int kFwdV = 8, kBwdV = 4;
+
+template <int DT, int W>
+hipError_t launch(const ConvArgs& a, bool back, hipStream_t s) {
+  const int V = back ? kBwdV : kFwdV, blocks = (a.C + 64 * V - 1) / (64 * V);
+  const long long groups = (pieces(a, kSh) + 3) / 4;
+  const dim3 grid((unsigned)(groups * blocks)), block(256);
+  if (back) hipLaunchKernelGGL((k_conv_grad<DT, W, kBwdV>), grid, block, 0, s, a, blocks);
+  else hipLaunchKernelGGL((k_conv<DT, W, kFwdV>), grid, block, 0, s, a, blocks);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t by_width(const ConvArgs& a, bool back, hipStream_t s) {
+  return a.W == 2 ? launch<DT, 2>(a, back, s) : a.W == 3 ? launch<DT, 3>(a, back, s) : launch<DT, 4>(a, back, s);
+}
+
+hipError_t by_type(const ConvArgs& a, bool back, hipStream_t s) {
+  return a.dtype == kF32 ? by_width<kF32>(a, back, s)
+                         : a.dtype == kBF16 ? by_width<kBF16>(a, back, s) : by_width<kF16>(a, back, s);
+}
+
+}  // namespace
+
+hipError_t launch_conv(const ConvArgs& a, hipStream_t s) { return a.N <= 0 ? hipSuccess : by_type(a, false, s); }
+
+size_t conv_backward_bytes(const ConvArgs& a) {
+  return (size_t)((pieces(a, kSh) + 3) / 4) * a.C * (a.W + 1) * sizeof(float);
+}
+
+hipError_t launch_conv_backward(const ConvArgs& a, hipStream_t s) {
+  SumArgs m{a.ws, (int)((pieces(a, kSh) + 3) / 4), (long long)a.C * (a.W + 1), (long long)a.C * a.W, a.C, a.dw, a.db,
+            nullptr};
+  if (a.N > 0) {
+    if (hipError_t e = by_type(a, true, s)) return e;
+  }
+  return launch_sum(m, s);  // without a sequence: sums of nothing
+}
+
+}  // namespace stepq

@@ -60,6 +60,8 @@ int seq_args(const void* desc, SeqArgs* a);
 int seq_inputs(SeqArgs* a, const void* q, const void* k, const void* v, const float* alpha,
                const float* beta, void* out);
 int seq_workspace(const void* ws, size_t have, size_t need);
+int seq_device(int device);
+int aligned(const void* p, unsigned to, const char* what);
 size_t forward_bytes(const SeqArgs& a);                    // workspace of launch_forward
 hipError_t launch_forward(const SeqArgs& a, hipStream_t s);  // all sequences, by the paths that suit them
 
@@ -182,7 +184,8 @@ __device__ __forceinline__ void storen(void* p, long long i, const float* x) {
 
 // Token range [t0, t1) of sequence s; false (and an empty range) where the offsets are not
 // 0 <= cu[s] <= cu[s + 1] <= T, so that no caller reads or writes outside the T rows.
-__device__ __forceinline__ bool seq_range(const SeqArgs& A, int s, int& t0, int& t1) {
+template <class Args>
+__device__ __forceinline__ bool seq_range(const Args& A, int s, int& t0, int& t1) {
   if (!A.cu) {
     const int L = A.T / A.N;
     t0 = s * L;
@@ -198,7 +201,8 @@ __device__ __forceinline__ bool seq_range(const SeqArgs& A, int s, int& t0, int&
 
 // State index of sequence s (itself, or its slot); -1: skip the sequence.  `report`: one thread of the
 // launch per sequence, which raises the flags.
-__device__ __forceinline__ int seq_slot(const SeqArgs& A, int s, bool valid, bool report) {
+template <class Args>
+__device__ __forceinline__ int seq_slot(const Args& A, int s, bool valid, bool report) {
   int slot = s;
   unsigned flag = valid ? 0u : kFlagBadSeq;
   if (A.slots) {

@@ -95,14 +95,14 @@ int seq_args(const void* desc, SeqArgs* a) {
   return STEPQ_OK;
 }
 
-static int seq_device(int device) {
+int seq_device(int device) {
   int ndev = 0;
   if (hipGetDeviceCount(&ndev) != hipSuccess || device < 0 || device >= ndev)
     return fail(STEPQ_ERR_INVALID_ARG, "device %d not available (%d devices)", device, ndev);
   return STEPQ_OK;
 }
 
-static int aligned(const void* p, unsigned to, const char* what) {
+int aligned(const void* p, unsigned to, const char* what) {
   if (((uintptr_t)p & (to - 1)) != 0)
     return fail(STEPQ_ERR_INVALID_ARG, "%s must be %u-byte aligned", what, to);
   return STEPQ_OK;

@@ -1,0 +1,297 @@
+// stepq_norm.hip -- root-mean-square norm of a head's row, with the residual's addition before it, a gate and eight
+// bits behind it, and its gradient:
+//   h = x + residual, r = 1 / sqrt(mean h^2 + eps), y = h r w act(z);  scale = max |y| / top, code = y / scale
+//   p = dy w act(z):  dh = r (p - h r mean(p h r)) + d_residual;  dw = sum dy act(z) h r;  dz = dy h r w act'(z)
+// A row stays in registers from its load to its store, eight neighbouring columns a lane: 8 to 64 lanes a row (to 512
+// columns), or a workgroup of 256 (to 8,192) or 1,024 (to 32,768).  Bound by HBM: some ten operations an element.
+#include "stepq_layer.h"
+
+namespace stepq {
+namespace {
+
+using namespace lay;
+
+// Sum over the TPR threads of a row; `mem` holds one value a wave where a row has several.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* mem) {
+#pragma unroll
+  for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2) v += __shfl_xor(v, m);
+  if constexpr (TPR > 64) {
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) mem[wave] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; i++) v += mem[i];
+  }
+  return v;
+}
+template <int TPR>
+__device__ __forceinline__ float row_max(float v, float* mem) {
+#pragma unroll
+  for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2) v = fmaxf(v, __shfl_xor(v, m));
+  if constexpr (TPR > 64) {
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) mem[wave] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < TPR / 64; i++) v = fmaxf(v, mem[i]);
+  }
+  return v;
+}
+
+// Address of head row i where rows of H heads are `stride` elements apart.
+__device__ __forceinline__ long long at_row(const NormArgs& A, long long i, long long stride) {
+  if (A.H == 1) return i * stride;
+  const long long t = i / A.H;
+  return t * stride + (i - t * A.H) * A.D;
+}
+
+// Codes of eight values times 1 / scale.
+__device__ __forceinline__ void store_codes(int odt, void* out, long long i, const float* y, float inv) {
+  int w[2];
+  if (odt == kE4M3) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const float u = y[j] * inv;
+      v[j] = u == u ? fminf(fmaxf(u, -448.0f), 448.0f) : u;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      w[k] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k], v[4 * k + 1], 0, false);
+      w[k] = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k + 2], v[4 * k + 3], w[k], true);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+      w[k] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const float u = y[4 * k + j] * inv, q = rintf(fminf(fmaxf(u, -127.0f), 127.0f));
+        w[k] |= ((u == u ? (int)q : 0) & 255) << (8 * j);
+      }
+    }
+  }
+  *(int2*)((char*)out + i) = int2{w[0], w[1]};
+}
+
+template <int DT, int TPR, int K>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormArgs A) {
+  constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
+  __shared__ float mem[THREADS / 64];
+  const int r = threadIdx.x % TPR;
+  const long long i = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
+  const bool live = i < A.R;  // one row a workgroup where waves meet: there every row is live
+  const long long row = live ? i : A.R - 1;
+  const long long xo = at_row(A, row, A.xs), ro = at_row(A, row, A.rs), zo = at_row(A, row, A.zs);
+  const long long oo = at_row(A, row, A.os);
+  float h[K][8], z[K][8], sq = 0;
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+    const int c = (k * TPR + r) * 8;
+    if (c < A.D) {
+      load8<DT>(A.x, xo + c, h[k]);
+      if (A.z) load8<DT>(A.z, zo + c, z[k]);
+      if (A.res) {
+        float more[8];
+        load8<DT>(A.res, ro + c, more);
+#pragma unroll
+        for (int j = 0; j < 8; j++) h[k][j] += more[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j++) h[k][j] = 0, z[k][j] = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) sq = fmaf(h[k][j], h[k][j], sq);
+  }
+  const float rms = 1.0f / sqrtf(row_sum<TPR>(sq, mem) / (float)A.D + A.eps);
+  float top = 0;
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+    const int c = (k * TPR + r) * 8;
+    if (c >= A.D) continue;
+    if (A.res_out && live) store8<DT>(A.res_out, ro + c, h[k]);
+    float w[8];
+    if (A.w) load8_any(A.pdtype, A.w, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      h[k][j] *= rms;
+      if (A.w) h[k][j] *= w[j];
+      if (A.z) h[k][j] *= act_of(A.gate, z[k][j]);
+      top = fmaxf(top, fabsf(h[k][j]));
+    }
+    if (A.odtype == DT && live) store8<DT>(A.out, oo + c, h[k]);
+  }
+  if (A.odtype == DT) return;
+  const float most = A.odtype == kE4M3 ? 448.0f : 127.0f;
+  if (A.group == 0) top = row_max<TPR>(top, mem);
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+    const int c = (k * TPR + r) * 8;
+    if (A.group) {  // 8 or 16 neighbouring lanes
+      top = 0;
+#pragma unroll
+      for (int j = 0; j < 8; j++) top = fmaxf(top, fabsf(h[k][j]));
+      for (int m = 1; m < A.group / 8; m *= 2) top = fmaxf(top, __shfl_xor(top, m));
+    }
+    const float scale = top > 0 ? fmaxf(top / most, 1.17549435e-38f) : 1.0f;
+    if (c >= A.D || !live) continue;
+    if (A.group == 0 ? c == 0 : c % A.group == 0) A.scale[A.group ? row * (A.D / A.group) + c / A.group : row] = scale;
+    store_codes(A.odtype, A.out, oo + c, h[k], 1.0f / scale);
+  }
+}
+
+// Each workgroup takes every gridDim.x'th set of rows and adds up its part of dw on the way.
+template <int DT, int TPR, int K>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A) {
+  constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
+  __shared__ float mem[THREADS / 64];
+  __shared__ float part[TPR < 256 ? 4 : 1][TPR < 256 ? 512 : 1];
+  const int r = threadIdx.x % TPR;
+  float dw[K][8], w[K][8];
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+    const int c = (k * TPR + r) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; j++) dw[k][j] = 0, w[k][j] = 1;
+    if (A.w && c < A.D) load8_any(A.pdtype, A.w, c, w[k]);
+  }
+  for (long long i0 = (long long)blockIdx.x * ROWS; i0 < A.R; i0 += (long long)gridDim.x * ROWS) {
+    const long long i = i0 + threadIdx.x / TPR;
+    const bool live = i < A.R;
+    const long long row = live ? i : A.R - 1;
+    const long long xo = at_row(A, row, A.xs), ro = at_row(A, row, A.rs), zo = at_row(A, row, A.zs);
+    const long long oo = at_row(A, row, A.os);
+    float h[K][8], p[K][8], z[K][8], sq = 0;
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      const int c = (k * TPR + r) * 8;
+      if (c < A.D) {
+        load8<DT>(A.x, xo + c, h[k]);
+        load8<DT>(A.d_out, oo + c, p[k]);
+        if (A.z) load8<DT>(A.z, zo + c, z[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++) h[k][j] = 0, p[k][j] = 0, z[k][j] = 0;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) sq = fmaf(h[k][j], h[k][j], sq);
+    }
+    const float rms = 1.0f / sqrtf(row_sum<TPR>(sq, mem) / (float)A.D + A.eps);
+    float dot = 0;
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      const int c = (k * TPR + r) * 8;
+      float dz[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        h[k][j] *= rms;
+        if (A.z) {
+          const float s = sigmoid(z[k][j]);
+          const float slope = A.gate == kSilu ? fmaf(z[k][j] * s, 1.0f - s, s) : s * (1.0f - s);
+          dz[j] = p[k][j] * h[k][j] * w[k][j] * slope;
+          p[k][j] *= A.gate == kSilu ? z[k][j] * s : s;
+        }
+        if (live) dw[k][j] = fmaf(p[k][j], h[k][j], dw[k][j]);
+        p[k][j] *= w[k][j];
+        dot = fmaf(p[k][j], h[k][j], dot);
+      }
+      if (A.z && c < A.D && live) store8<DT>(A.dz, row * A.D + c, dz);
+    }
+    const float mean = row_sum<TPR>(dot, mem) / (float)A.D;
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      const int c = (k * TPR + r) * 8;
+      if (c >= A.D || !live) continue;
+      float g[8], more[8];
+      if (A.res) load8<DT>(A.res, ro + c, more);
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        g[j] = rms * fmaf(-h[k][j], mean, p[k][j]);
+        if (A.res) g[j] += more[j];
+      }
+      store8<DT>(A.dx, row * A.D + c, g);
+    }
+  }
+  if (!A.dw) return;
+  float* out = A.ws + (long long)blockIdx.x * A.D;
+  if constexpr (TPR < 256) {  // rows of a wave, then its four waves
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+    for (int m = TPR; m < 64; m *= 2) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) dw[0][j] += __shfl_xor(dw[0][j], m);
+    }
+    if (lane < TPR) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) part[wave][lane * 8 + j] = dw[0][j];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < A.D; c += 256) out[c] = part[0][c] + part[1][c] + part[2][c] + part[3][c];
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      const int c = (k * TPR + r) * 8;
+      if (c < A.D) store8<kF32>(out, c, dw[k]);
+    }
+  }
+}
+
+// Workgroups of the gradient: enough to fill 256 CUs twice.
+long long grad_groups(const NormArgs& a, int rows) {
+  const long long sets = (a.R + rows - 1) / rows;
+  return sets < 512 ? sets : 512;
+}
+
+template <int DT, int TPR, int K>
+hipError_t launch(const NormArgs& a, bool back, hipStream_t s) {
+  constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
+  if (back) {
+    const long long groups = grad_groups(a, ROWS);
+    hipLaunchKernelGGL((k_norm_grad<DT, TPR, K>), dim3((unsigned)groups), dim3(THREADS), 0, s, a);
+    if (hipError_t e = hipGetLastError()) return e;
+    if (!a.dw) return hipSuccess;
+    SumArgs m{a.ws, (int)groups, a.D, a.D, 0, a.dw, nullptr, nullptr};
+    return launch_sum(m, s);
+  }
+  hipLaunchKernelGGL((k_norm<DT, TPR, K>), dim3((unsigned)((a.R + ROWS - 1) / ROWS)), dim3(THREADS), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t by_size(const NormArgs& a, bool back, hipStream_t s) {
+  const int D = a.D;
+  if (D <= 64) return launch<DT, 8, 1>(a, back, s);
+  if (D <= 128) return launch<DT, 16, 1>(a, back, s);
+  if (D <= 256) return launch<DT, 32, 1>(a, back, s);
+  if (D <= 512) return launch<DT, 64, 1>(a, back, s);
+  if (D <= 2048) return launch<DT, 256, 1>(a, back, s);
+  if (D <= 4096) return launch<DT, 256, 2>(a, back, s);
+  if (D <= 8192) return launch<DT, 256, 4>(a, back, s);
+  if (D <= 16384) return launch<DT, 1024, 2>(a, back, s);
+  return launch<DT, 1024, 4>(a, back, s);
+}
+
+hipError_t by_type(const NormArgs& a, bool back, hipStream_t s) {
+  return a.dtype == kF32 ? by_size<kF32>(a, back, s)
+                         : a.dtype == kBF16 ? by_size<kBF16>(a, back, s) : by_size<kF16>(a, back, s);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) { return a.R <= 0 ? hipSuccess : by_type(a, false, s); }
+
+size_t norm_backward_bytes(const NormArgs& a) { return a.R > 0 ? (size_t)512 * a.D * sizeof(float) : 0; }
+
+hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
+  if (a.R > 0) return by_type(a, true, s);
+  SumArgs m{nullptr, 0, a.D, a.D, 0, a.dw, nullptr, nullptr};
+  return a.dw ? launch_sum(m, s) : hipSuccess;
+}
+
+}  // namespace stepq

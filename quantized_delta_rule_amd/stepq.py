@@ -64,6 +64,16 @@ def lib() -> ctypes.CDLL:
         "stepq_prefill_workspace": (i, [P, P, ctypes.POINTER(sz)]),
         "stepq_prefill_slots": (i, [P, P, P, i] + [P] * 8 + [sz, P]),
         "stepq_read_slots": (i, [P, P, i, P, i, P, i, P]),
+        "stepq_conv_forward": (i, [P] * 6 + [i, P, P, P]),
+        "stepq_conv_backward_workspace": (i, [P, ctypes.POINTER(sz)]),
+        "stepq_conv_backward": (i, [P] * 12 + [sz, P]),
+        "stepq_scan_forward_workspace": (i, [P, ctypes.POINTER(sz)]),
+        "stepq_scan_forward": (i, [P] * 11 + [i, P, P, P, sz, P]),
+        "stepq_scan_backward_workspace": (i, [P, ctypes.POINTER(sz)]),
+        "stepq_scan_backward": (i, [P] * 22 + [sz, P]),
+        "stepq_norm_forward": (i, [P] * 9),
+        "stepq_norm_backward_workspace": (i, [P, ctypes.POINTER(sz)]),
+        "stepq_norm_backward": (i, [P] * 10 + [sz, P]),
         "stepq_get_status": (i, [P, ctypes.POINTER(ctypes.c_uint32), i]),
         "stepq_sync": (i, [P]),
         "stepq_debug_side_delay": (i, [P, ctypes.c_longlong]),
