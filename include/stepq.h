@@ -326,7 +326,7 @@ int stepq_read_slots(stepq_plan_t plan, const void* pool, int n_slots, const int
  * Common to the convolution and the scan: n_seqs, n_tokens, cu_seqlens, slots, status and device mean what
  * they mean for the delta rule's sequence calls (rows of no sequence are not read, and outputs are left as
  * they were there; bad offsets and slots raise flags and skip their sequence).  Row strides are in elements from
- * one token's row to the next, 0 = packed; rows and strides are multiples of 16 bytes, pointers to rows and
+ * one token's row to the next, 0 = packed, below 2^24; rows and strides are multiples of 16 bytes, pointers to rows and
  * states 16-byte aligned.  Calls only enqueue kernels and may be captured.  Sums are binary32 in an order
  * that the sizes alone fix: the same call on the same inputs gives the same bits.
  */
@@ -430,7 +430,8 @@ int stepq_scan_backward(const stepq_scan_desc* desc, const void* x, const void* 
  *                the nearest (ties to even); a group of zeros has scale 1.  The scale is at least the smallest
  *                normal binary32.  A y that is NaN takes no part in the maximum: its code is NaN (E4M3) or 0 (I8).
  *   n_rows       rows of n_heads * d elements, n_heads x n_rows below 2^31;  d a multiple of 8, at most 32768.
- *   strides      elements between rows, 0 = packed; multiples of 16 bytes (out's of 8 bytes with 8 bits).
+ *   strides      elements between rows, 0 = packed; multiples of 16 bytes (out's of 8 bytes with 8 bits), below
+ *                2^24.
  */
 typedef struct {
   int dtype, param_dtype, out_dtype;

@@ -39,17 +39,6 @@ __device__ __forceinline__ bool part_of(const ConvArgs& A, long long j, bool rep
   return P.slot >= 0 && (P.p < P.len || P.first);
 }
 
-template <int DT, int V>
-__device__ __forceinline__ void row(const void* p, long long i, float* x) {
-  if constexpr (V == 8) load8<DT>(p, i, x);
-  else loadn<DT, V>(p, i, x);
-}
-template <int DT, int V>
-__device__ __forceinline__ void put(void* p, long long i, const float* x) {
-  if constexpr (V == 8) store8<DT>(p, i, x);
-  else storen<DT, V>(p, i, x);
-}
-
 // Weights of V channels, [j][channel], and their bias.
 template <int W, int V>
 __device__ __forceinline__ void weights(const ConvArgs& A, int c, float (&w)[W][V], float (&b)[V]) {
@@ -83,8 +72,8 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
 #pragma unroll
   for (int i = 0; i < W - 1; i++) {
     const long long at = P.p - (W - 1) + i;
-    if (at >= 0) row<DT, V>(A.x, (P.t0 + at) * A.xs + c, x[i]);
-    else if (A.S_in) row<DT, V>(A.S_in, so + (at + W - 1) * A.C, x[i]);
+    if (at >= 0) loadv<DT, V>(A.x, (P.t0 + at) * A.xs + c, x[i]);
+    else if (A.S_in) loadv<DT, V>(A.S_in, so + (at + W - 1) * A.C, x[i]);
     else {
 #pragma unroll
       for (int v = 0; v < V; v++) x[i][v] = 0;
@@ -95,7 +84,7 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
 #pragma unroll
     for (int i = 0; i < W - 1; i++) {
       const long long at = P.len - (W - 1) + i;
-      if (at >= 0) row<DT, V>(A.x, (P.t0 + at) * A.xs + c, last[i]);
+      if (at >= 0) loadv<DT, V>(A.x, (P.t0 + at) * A.xs + c, last[i]);
       else {  // row at + W - 1 of the old one
 #pragma unroll
         for (int v = 0; v < V; v++) {
@@ -107,10 +96,10 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < W - 1; i++) put<DT, V>(A.S_out, so + (long long)i * A.C, last[i]);
+    for (int i = 0; i < W - 1; i++) storev<DT, V>(A.S_out, so + (long long)i * A.C, last[i]);
   }
   for (long long t = P.t0 + P.p; t < P.t0 + P.end; t++) {
-    row<DT, V>(A.x, t * A.xs + c, x[W - 1]);
+    loadv<DT, V>(A.x, t * A.xs + c, x[W - 1]);
     float y[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
@@ -119,7 +108,7 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
       for (int i = 0; i < W; i++) u = fmaf(w[i][v], x[i][v], u);
       y[v] = act_of(A.act, u);
     }
-    put<DT, V>(A.out, t * A.os + c, y);
+    storev<DT, V>(A.out, t * A.os + c, y);
 #pragma unroll
     for (int i = 0; i < W - 1; i++) {
 #pragma unroll
@@ -153,8 +142,8 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
 #pragma unroll
     for (int i = 0; i < W - 1; i++) {
       const long long at = P.p - (W - 1) + i;
-      if (at >= 0) row<DT, V>(A.x, (P.t0 + at) * A.xs + c, x[i]);
-      else if (A.S_in) row<DT, V>(A.S_in, so + (at + W - 1) * A.C, x[i]);
+      if (at >= 0) loadv<DT, V>(A.x, (P.t0 + at) * A.xs + c, x[i]);
+      else if (A.S_in) loadv<DT, V>(A.S_in, so + (at + W - 1) * A.C, x[i]);
       else {
 #pragma unroll
         for (int v = 0; v < V; v++) x[i][v] = 0;
@@ -173,8 +162,8 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
       for (int v = 0; v < V; v++) du[W - 1][v] = 0;
       if (in) {
         float dy[V];
-        row<DT, V>(A.x, (P.t0 + q) * A.xs + c, x[W - 1]);
-        row<DT, V>(A.d_out, (P.t0 + q) * A.os + c, dy);
+        loadv<DT, V>(A.x, (P.t0 + q) * A.xs + c, x[W - 1]);
+        loadv<DT, V>(A.d_out, (P.t0 + q) * A.os + c, dy);
 #pragma unroll
         for (int v = 0; v < V; v++) {
           float u = b[v];
@@ -205,12 +194,12 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
         const long long r = o - P.len + W - 1;  // the last rows are the state that the sequence leaves
         if (r >= 0 && A.dS_out) {
           float more[V];
-          row<DT, V>(A.dS_out, so + r * A.C, more);
+          loadv<DT, V>(A.dS_out, so + r * A.C, more);
 #pragma unroll
           for (int v = 0; v < V; v++) g[v] += more[v];
         }
-        if (o >= 0) put<DT, V>(A.dx, (P.t0 + o) * A.C + c, g);
-        else if (A.dS_in) put<DT, V>(A.dS_in, so + (o + W - 1) * A.C, g);
+        if (o >= 0) storev<DT, V>(A.dx, (P.t0 + o) * A.C + c, g);
+        else if (A.dS_in) storev<DT, V>(A.dS_in, so + (o + W - 1) * A.C, g);
       }
 #pragma unroll
       for (int i = 0; i < W - 1; i++) {

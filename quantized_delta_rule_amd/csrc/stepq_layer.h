@@ -124,6 +124,18 @@ __device__ __forceinline__ float act_of(int act, float v) {
   return act == kSilu ? v * s : s;
 }
 
+// V (1, 2, 4 or 8) consecutive elements.
+template <int DT, int V>
+__device__ __forceinline__ void loadv(const void* p, long long i, float* x) {
+  if constexpr (V == 8) load8<DT>(p, i, x);
+  else loadn<DT, V>(p, i, x);
+}
+template <int DT, int V>
+__device__ __forceinline__ void storev(void* p, long long i, const float* x) {
+  if constexpr (V == 8) store8<DT>(p, i, x);
+  else storen<DT, V>(p, i, x);
+}
+
 // 8 consecutive parameters whose type is known at run time.
 __device__ __forceinline__ void load8_any(int dt, const void* p, long long i, float* x) {
   if (dt == kF32) load8<kF32>(p, i, x);

@@ -38,8 +38,8 @@ int sequences(int n_seqs, int n_tokens, const void* cu) {
 // A row stride: `given` or packed, in whole units of `unit` elements (16 bytes; 8 of 8-bit rows).
 int stride(long long given, long long packed, long long unit, const char* what, long long* st) {
   *st = given ? given : packed;
-  if (*st < packed || *st % unit || *st >= (1LL << 31))
-    return fail(STEPQ_ERR_INVALID_ARG, "%s_stride %lld must be %lld .. 2^31 - 1 and a multiple of %lld elements", what,
+  if (*st < packed || *st % unit || *st >= (1LL << 24))
+    return fail(STEPQ_ERR_INVALID_ARG, "%s_stride %lld must be %lld .. 2^24 - 1 and a multiple of %lld elements", what,
                 *st, packed, unit);
   return STEPQ_OK;
 }
@@ -64,8 +64,8 @@ int conv_args(const stepq_conv_desc* d, ConvArgs* a) {
   if (!row_type(d->dtype)) return fail(STEPQ_ERR_INVALID_ARG, "dtype must be STEPQ_DTYPE_F32, _BF16 or _F16");
   if (!row_type(d->param_dtype))
     return fail(STEPQ_ERR_INVALID_ARG, "param_dtype must be STEPQ_DTYPE_F32, _BF16 or _F16");
-  if (d->channels < 8 || d->channels % 8 || d->channels > (1 << 24))
-    return fail(STEPQ_ERR_INVALID_ARG, "channels (%d) must be a multiple of 8, 8 .. 2^24", d->channels);
+  if (d->channels < 8 || d->channels % 8 || d->channels >= (1 << 24))
+    return fail(STEPQ_ERR_INVALID_ARG, "channels (%d) must be a multiple of 8, 8 .. 2^24 - 8", d->channels);
   if (d->width < 2 || d->width > 4) return fail(STEPQ_ERR_UNSUPPORTED, "width must be 2, 3 or 4 (got %d)", d->width);
   if (d->activation != STEPQ_ACT_NONE && d->activation != STEPQ_ACT_SILU)
     return fail(STEPQ_ERR_INVALID_ARG, "activation must be STEPQ_ACT_NONE or STEPQ_ACT_SILU");
@@ -94,8 +94,8 @@ int conv_args(const stepq_conv_desc* d, ConvArgs* a) {
 int scan_args(const stepq_scan_desc* d, ScanArgs* a) {
   if (!d) return fail(STEPQ_ERR_INVALID_ARG, "desc is NULL");
   if (!row_type(d->dtype)) return fail(STEPQ_ERR_INVALID_ARG, "dtype must be STEPQ_DTYPE_F32, _BF16 or _F16");
-  if (d->n_groups < 1 || d->channels < 8 || d->channels > (1 << 24) || d->channels % (8LL * d->n_groups))
-    return fail(STEPQ_ERR_INVALID_ARG, "channels (%d) must be a multiple of 8 n_groups (%d), 8 .. 2^24", d->channels,
+  if (d->n_groups < 1 || d->channels < 8 || d->channels >= (1 << 24) || d->channels % (8LL * d->n_groups))
+    return fail(STEPQ_ERR_INVALID_ARG, "channels (%d) must be a multiple of 8 n_groups (%d), 8 .. 2^24 - 8", d->channels,
                 d->n_groups);
   if (d->d_state != 8 && d->d_state != 16 && d->d_state != 32 && d->d_state != 64)
     return fail(STEPQ_ERR_UNSUPPORTED, "d_state must be 8, 16, 32 or 64 (got %d)", d->d_state);
@@ -103,7 +103,8 @@ int scan_args(const stepq_scan_desc* d, ScanArgs* a) {
   STEPQ_TRY(sequences(d->n_seqs, d->n_tokens, d->cu_seqlens));
   // threads of a launch, below 2^32: four states each of every sequence, an element each of dB and dC
   const long long tiles = (d->channels / d->n_groups * (long long)d->d_state + 255) / 256 * d->n_groups;
-  if (tiles * d->n_seqs * 64 + 256 > UINT_MAX || 2LL * d->n_groups * d->d_state * d->n_tokens + 256 > UINT_MAX)
+  const long long wide = ((d->channels / d->n_groups + 63LL) / 64) * d->n_groups;  // 64 channels by 8 waves
+  if (tiles * d->n_seqs * 64 + 256 > UINT_MAX || wide * d->n_seqs * 512 > UINT_MAX || 2LL * d->n_groups * d->d_state * d->n_tokens + 256 > UINT_MAX)
     return fail(STEPQ_ERR_INVALID_ARG, "n_tokens (%d), n_seqs (%d) and channels (%d) exceed the launch grid", d->n_tokens,
                 d->n_seqs, d->channels);
   const long long unit = d->dtype == STEPQ_DTYPE_F32 ? 4 : 8, gn = (long long)d->n_groups * d->d_state;

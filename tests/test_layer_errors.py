@@ -85,7 +85,7 @@ SEQS = [
     (dict(n_seqs=1, n_tokens=2 ** 31 - 1, channels=8192), INVALID, "launch grid"),
     (dict(x_stride=56), INVALID, "x_stride"), (dict(x_stride=68), INVALID, "x_stride"),
     (dict(dtype=0, x_stride=66), INVALID, "x_stride"), (dict(out_stride=-64), INVALID, "out_stride"),
-    (dict(out_stride=2 ** 31), INVALID, "out_stride"),
+    (dict(out_stride=2 ** 24), INVALID, "out_stride"),
 ], ids=str)
 def test_conv_descriptions(L, kw, code, text):
     for rc in conv_calls(L, conv_desc(**kw)):
@@ -114,7 +114,7 @@ def test_scan_descriptions(L, kw, code, text):
     (dict(gate=0), INVALID, "gate"), (dict(group=128), INVALID, "group"), (dict(eps=-1e-6), INVALID, "eps"),
     (dict(eps=float("nan")), INVALID, "eps"), (dict(eps=float("inf")), INVALID, "eps"), (dict(x_stride=8), INVALID, "x_stride"),
     (dict(residual_stride=260), INVALID, "residual_stride"), (dict(z_stride=-256), INVALID, "z_stride"),
-    (dict(out_stride=2 ** 31), INVALID, "out_stride"),
+    (dict(out_stride=2 ** 24), INVALID, "out_stride"),
 ], ids=str)
 def test_norm_descriptions(L, kw, code, text):
     for rc in norm_calls(L, norm_desc(**kw)):
