@@ -7,9 +7,6 @@
 
 #include "stepq_scan.h"
 
-#ifndef NS16
-#define NS16 4
-#endif
 namespace stepq {
 namespace {
 
@@ -62,10 +59,10 @@ __global__ __launch_bounds__(256) void k_scan_tokens(ScanArgs A, int tiles) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Blocks of tokens: a workgroup takes 64 channels of a sequence, or of one of its segments, a lane a channel.  Its NW
-// waves share the states out, NS each, so that B and C of a token are the same for a whole wave: every 16 lanes hold
-// the values of a token or two, and an instruction takes one of them for all lanes by itself (row broadcast of its
-// operand).  For each block of 16 tokens the waves first turn raw steps into (D, D x) in LDS, a token of 64 channels
+// Blocks of tokens: a workgroup takes CH channels of a sequence, or of one of its segments.  64 / CH
+// parts of a wave and the NW waves share a channel's states out, NS each, so that 16 neighbouring lanes have the same B
+// and C of a token: they hold the values of a token or two, and an instruction takes one of them for all lanes by itself (row broadcast of its
+// operand).  For each block of 16 tokens the waves first turn raw steps into (D, D x) in LDS, a few channels
 // each, then run all of them on their states, and add their parts of C . h up through LDS.
 // ---------------------------------------------------------------------------------------------
 
@@ -151,17 +148,21 @@ __device__ __forceinline__ void put_states(float* p, const float* h) {
 }
 
 // PASS 0: a whole sequence.  1: a segment's last state and steps.  2: a segment.
-template <int DT, int NS, int NW, int PASS>
+template <int DT, int NS, int CH, int NW, int PASS>
 __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
-  constexpr int n = NS * NW, E = kBlock / NW;  // neighbouring channels of a token that a thread prepares and finishes
+  constexpr int P = 64 / CH, n = NS * P * NW;  // parts of a channel's states in a wave
+  constexpr int E = kBlock * CH / (64 * NW);  // neighbouring channels of a token that a thread prepares and finishes
   constexpr int V = 2 * NS, PT = 16 / V;       // values of a token, NS of B and of C; tokens in 16 lanes
   constexpr int R = kBlock / PT;
-  __shared__ float2 steps[2][kBlock][64];
-  __shared__ float parts[PASS == 1 ? 1 : 2][NW][kBlock][64];
+  __shared__ float2 steps[2][kBlock][CH];
+  __shared__ float parts[PASS == 1 ? 1 : 2][PASS == 1 ? 1 : NW * P][kBlock][CH];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = Q.tiles * A.G;
-  const long long j = blockIdx.x / per;
-  const int tg = blockIdx.x % per, g = tg / Q.tiles, tile = tg - g * Q.tiles;
+  // Neighbouring channels share cache lines: workgroups that share an L2, every eighth one, take neighbouring tiles.
+  unsigned unit = blockIdx.x;
+  if (unit < gridDim.x / (8 * P) * (8 * P)) unit = unit / (8 * P) * (8 * P) + unit % 8 * P + unit / 8 % P;
+  const long long j = unit / per;
+  const int tg = unit % per, g = tg / Q.tiles, tile = tg - g * Q.tiles;
   int s, a, b;
   long long idx = 0;
   if (PASS != 2 && tg == 0 && j < A.N) {  // one workgroup a sequence raises its flags
@@ -173,23 +174,24 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   const bool valid = seq_range(A, s, a, b);
   const int slot = seq_slot(A, s, valid, false);
   if (slot < 0) return;
+  const int part = wave * P + lane / CH;  // which NS of a channel's states
   const long long len = b - a, p = PASS == 0 ? 0 : idx << Q.sh;
   if (PASS != 0 && p >= len && idx > 0) return;
   const bool ends = PASS == 0 || p + (1LL << Q.sh) >= len;
   const int count = (int)(ends ? len - p : 1LL << Q.sh);
-  const int cg = tile * 64 + lane;
+  const int cl = lane % CH, cg = tile * CH + cl;
   const bool live = cg < A.Cg;
   const int c = g * A.Cg + (live ? cg : A.Cg - 1);  // lanes past the group's end repeat its last channel
-  const long long so = ((long long)slot * A.C + c) * n + wave * NS;
+  const long long so = ((long long)slot * A.C + c) * n + part * NS;
   float h[NS], a2[NS];
-  get_states<NS>(A.A + (long long)c * n + wave * NS, a2);
+  get_states<NS>(A.A + (long long)c * n + part * NS, a2);
 #pragma unroll
   for (int i = 0; i < NS; i++) a2[i] *= kLog2e, h[i] = 0;
-  if (PASS == 2 && idx > 0) get_states<NS>(Q.last + ((j - idx) * A.C + c) * n + wave * NS, h);
-  else if (PASS == 2) get_states<NS>(Q.first + ((long long)s * A.C + c) * n + wave * NS, h);
+  if (PASS == 2 && idx > 0) get_states<NS>(Q.last + ((j - idx) * A.C + c) * n + part * NS, h);
+  else if (PASS == 2) get_states<NS>(Q.first + ((long long)s * A.C + c) * n + part * NS, h);
   else if (A.S_in && idx == 0) get_states<NS>(A.S_in + so, h);
   if constexpr (PASS == 1) {
-    if (idx == 0 && live) put_states<NS>(Q.first + ((long long)s * A.C + c) * n + wave * NS, h);
+    if (idx == 0 && live) put_states<NS>(Q.first + ((long long)s * A.C + c) * n + part * NS, h);
     if (ends) return;
   }
   if constexpr (PASS == 2) {
@@ -197,13 +199,13 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
       const long long o = (j - idx + k) * A.C + c;
       const float D = Q.steps[o];
       float e[NS];
-      get_states<NS>(Q.last + o * n + wave * NS, e);
+      get_states<NS>(Q.last + o * n + part * NS, e);
 #pragma unroll
       for (int i = 0; i < NS; i++) h[i] = fmaf(decay(D, a2[i]), h[i], e[i]);
     }
   }
   // this thread's token of a block and its channels there
-  const int tok = threadIdx.x / (64 / E), ch = threadIdx.x % (64 / E) * E, cgo = tile * 64 + ch;
+  const int tok = threadIdx.x / (CH / E), ch = threadIdx.x % (CH / E) * E, cgo = tile * CH + ch;
   const bool mine = cgo < A.Cg;  // a group is whole in eights: all E channels or none
   const int co = g * A.Cg + (mine ? cgo : A.Cg - 8);
   float skip[E], bias[E];
@@ -230,7 +232,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   for (int i = 0; i < E; i++) all[i] = 0;
   const int sub = (lane & 15) / V, val = lane % V;  // this lane's token of PT, its value
   const unsigned vs = (unsigned)(val < NS ? A.bs : A.cs) * size;
-  const char* vp = (const char*)(val < NS ? A.B : A.Cm) + row0 * vs + (long long)(g * n + wave * NS + val % NS) * size;
+  const char* vp = (const char*)(val < NS ? A.B : A.Cm) + row0 * vs + (long long)(g * n + part * NS + val % NS) * size;
   auto fetch = [&](int k) {  // blocks in order: the addresses move on
     const int most = count - k * kBlock - 1;  // the last token of the block, at most
     const unsigned t = tok < most ? tok : most;
@@ -267,7 +269,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
     float y[E];
     loadv<kF32, E>(&parts[k & 1][0][tok][ch], 0, y);
 #pragma unroll
-    for (int w = 1; w < NW; w++) {
+    for (int w = 1; w < NW * P; w++) {
       float m[E];
       loadv<kF32, E>(&parts[k & 1][w][tok][ch], 0, m);
 #pragma unroll
@@ -283,7 +285,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
     op += (long long)ao * kBlock;
   };
   auto one = [&]<int T>(int k, float bc) {  // token T of a block, whose values lie in lanes of `bc`
-    const float2 d = steps[k & 1][T][lane];
+    const float2 d = steps[k & 1][T][cl];
     float y = 0;
     [&]<int... I>(std::integer_sequence<int, I...>) {
       ((h[I] = fmaf(decay(d.x, a2[I]), h[I], row_lane<T % PT * V + I>(bc) * d.y)), ...);
@@ -292,7 +294,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
       if constexpr (NS == 2) y = row_dot2<T % PT * V + NS>(bc, h);
       else y = row_dot<T % PT * V + NS, false>(y, bc, h);
       if constexpr (NS == 8) y = row_dot<T % PT * V + NS + 4, true>(y, bc, h + 4);
-      parts[k & 1][wave][T][lane] = y;
+      parts[k & 1][part][T][cl] = y;
     }
   };
   const int blocks = (count + kBlock - 1) / kBlock;
@@ -322,17 +324,17 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   }
   if constexpr (PASS == 1) {
     const long long o = j * A.C + c;
-    float* sum = &parts[0][0][0][0];  // [16][64]
+    float* sum = &parts[0][0][0][0];  // [kBlock][CH]
 #pragma unroll
-    for (int i = 0; i < E; i++) sum[tok * 64 + ch + i] = all[i];
+    for (int i = 0; i < E; i++) sum[tok * CH + ch + i] = all[i];
     __syncthreads();
-    if (wave == 0 && live) {
+    if (wave == 0 && live && lane < CH) {
       float D = sum[lane];
 #pragma unroll
-      for (int t = 1; t < kBlock; t++) D += sum[t * 64 + lane];
+      for (int t = 1; t < kBlock; t++) D += sum[t * CH + lane];
       Q.steps[o] = D;
     }
-    if (live) put_states<NS>(Q.last + o * n + wave * NS, h);
+    if (live) put_states<NS>(Q.last + o * n + part * NS, h);
   } else if (ends && A.S_out && live) {
     put_states<NS>(A.S_out + so, h);
   }
@@ -345,10 +347,10 @@ struct Path {
 };
 Path path_of(const ScanArgs& a) {
   Path p{a.N > 0 && (long long)a.T >= 16LL * a.N, 0};
-  const long long tiles = (a.Cg + 63) / 64 * a.G;
+  const long long tiles = (a.Cg + 31) / 32 * a.G;
   if (p.blocks && tiles * a.N < 512) {
     int sh = 6;
-    while (sh < 30 && ((long long)a.T >> sh) * tiles > 768) sh++;
+    while (sh < 30 && ((long long)a.T >> sh) * tiles > 1024) sh++;
     if (a.T / a.N >= 2 << sh) p.sh = sh;
   }
   return p;
@@ -363,21 +365,21 @@ hipError_t tokens(const ScanArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int DT, int NS, int NW>
+template <int DT, int NS, int CH, int NW>
 hipError_t blocks(const ScanArgs& a, int sh, hipStream_t s) {
-  Segments q{(a.Cg + 63) / 64, sh, nullptr, nullptr, nullptr};
+  Segments q{(a.Cg + CH - 1) / CH, sh, nullptr, nullptr, nullptr};
   const long long per = (long long)q.tiles * a.G;
   if (!sh) {
-    hipLaunchKernelGGL((k_scan_run<DT, NS, NW, 0>), dim3((unsigned)(per * a.N)), dim3(64 * NW), 0, s, a, q);
+    hipLaunchKernelGGL((k_scan_run<DT, NS, CH, NW, 0>), dim3((unsigned)(per * a.N)), dim3(64 * NW), 0, s, a, q);
     return hipGetLastError();
   }
   const long long m = pieces(a, sh);
   q.last = (float*)a.ws;
   q.steps = (float*)(a.ws + up((size_t)m * a.C * a.n * 4));
   q.first = (float*)((char*)q.steps + up((size_t)m * a.C * 4));
-  hipLaunchKernelGGL((k_scan_run<DT, NS, NW, 1>), dim3((unsigned)(per * m)), dim3(64 * NW), 0, s, a, q);
+  hipLaunchKernelGGL((k_scan_run<DT, NS, CH, NW, 1>), dim3((unsigned)(per * m)), dim3(64 * NW), 0, s, a, q);
   if (hipError_t e = hipGetLastError()) return e;
-  hipLaunchKernelGGL((k_scan_run<DT, NS, NW, 2>), dim3((unsigned)(per * m)), dim3(64 * NW), 0, s, a, q);
+  hipLaunchKernelGGL((k_scan_run<DT, NS, CH, NW, 2>), dim3((unsigned)(per * m)), dim3(64 * NW), 0, s, a, q);
   return hipGetLastError();
 }
 
@@ -388,10 +390,10 @@ hipError_t by_states(const ScanArgs& a, hipStream_t s) {
     return a.n == 8 ? tokens<DT, 2>(a, s)
                     : a.n == 16 ? tokens<DT, 4>(a, s) : a.n == 32 ? tokens<DT, 8>(a, s) : tokens<DT, 16>(a, s);
   }
-  return a.n == 8    ? blocks<DT, 4, 2>(a, p.sh, s)
-         : a.n == 16 ? blocks<DT, NS16, 16 / NS16>(a, p.sh, s)
-         : a.n == 32 ? blocks<DT, 8, 4>(a, p.sh, s)
-                     : blocks<DT, 8, 8>(a, p.sh, s);
+  return a.n == 8    ? blocks<DT, 2, 32, 2>(a, p.sh, s)
+         : a.n == 16 ? blocks<DT, 2, 32, 4>(a, p.sh, s)
+         : a.n == 32 ? blocks<DT, 4, 32, 4>(a, p.sh, s)
+                     : blocks<DT, 8, 32, 4>(a, p.sh, s);
 }
 
 }  // namespace
