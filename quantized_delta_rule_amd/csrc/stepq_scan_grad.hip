@@ -4,133 +4,328 @@
 //   dC_t = sum_c e_t h_t;  dB_t = sum_c g_t D_t x_t;  dx_t = D_t sum_n g_t B_t + D e_t
 //   dD_t = sum_n g_t (A a_t h_{t-1} + B_t x_t), ddt_t = dD_t sigmoid(dt + bias);  dA = sum_t D_t g_t a_t h_{t-1}
 //   dz_t = dout_t (C_t . h_t + D x_t) (z sigmoid(z))';  dD = sum_t e_t x_t;  dS_in = a_1 g_1
-#include "stepq_scan.h"
+// The forward pass keeps the states before every block of 16 tokens (k_scan_run, PASS 3); the reverse pass runs a
+// block's tokens again from them, with the states and decays in registers, and then back.
+#include "stepq_scan_block.h"
 
 namespace stepq {
 namespace {
 
-using namespace lay;
-
-constexpr size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
-
-// Workspace: every token's state, partial dB and dC of every tile, partial dA, dD and dbias of every sequence.
+// Workspace behind the segments': the kept states; partial dB and dC of every tile of channels; partial dA, dD and
+// dbias of every segment; for segments, the gradients before them from zero behind them.
 struct Space {
-  int tiles;
-  long long row;  // dA | dD | dbias
-  size_t h, bc, par, all;
+  Segments q;
+  long long segs, row;  // segments, or sequences where there are none; floats of a row of dA | dD | dbias
+  float* bc;
+  float* par;
+  float* back;
 };
-Space space(const ScanArgs& a) {
-  Space w;
-  const int gw = 256 / a.n;
-  w.tiles = (a.Cg + gw - 1) / gw;
-  w.row = (long long)a.C * a.n + 2 * a.C;
-  w.h = 0;
-  w.bc = w.h + up((size_t)a.T * a.C * a.n * 4);
-  w.par = w.bc + up((size_t)w.tiles * a.T * a.G * a.n * 8);
-  w.all = w.par + up((size_t)a.N * w.row * 4);
-  return w;
+size_t space(const ScanArgs& a, char* ws, Space* w) {
+  const int sh = segments_of(a);
+  char* p;
+  w->q = lay_segments(a, sh, ws, &p);
+  w->segs = sh ? pieces(a, sh) : a.N;
+  w->row = (long long)a.C * a.n + 2 * a.C;
+  w->q.kept = (float*)p;
+  p += up((size_t)pieces(a, 4) * w->q.tiles * a.G * 32 * a.n * 4);
+  w->bc = (float*)p;
+  p += up((size_t)w->q.tiles * a.T * a.G * a.n * 8);
+  w->par = (float*)p;
+  p += up((size_t)w->segs * w->row * 4);
+  w->back = (float*)p;
+  if (sh) p += up((size_t)w->segs * a.C * a.n * 4);
+  return (size_t)(p - ws);
 }
 
-template <int DT, int LN>
-__global__ __launch_bounds__(256) void k_scan_grad(ScanArgs A, Space W) {
-  constexpr int GW = 64 / LN, n = 4 * LN;
-  const int lane = threadIdx.x & 63;
-  const long long unit = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const long long per = (long long)W.tiles * A.G;
-  if (unit >= per * A.N) return;
-  const int s = (int)(unit / per), tg = (int)(unit - s * per), g = tg / W.tiles, tile = tg - g * W.tiles;
-  int t0, t1;
-  const bool valid = seq_range(A, s, t0, t1);
-  seq_slot(A, s, valid, tg == 0 && lane == 0);
-  const int cg = tile * GW + lane / LN, part = lane % LN;
+// v += (lane I of each 16 lanes' b) * e
+template <int I>
+__device__ __forceinline__ void row_fmac(float& v, float b, float e) {
+  asm("s_nop 1\n\tv_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 row_mask:0xf bank_mask:0xf" : "+v"(v) : "v"(b), "v"(e), "n"(I));
+}
+
+// Four values' sums over every fourth of 16 lanes: the first four lanes get u0's (of lanes 0, 4, 8, 12; 1, 5, ..), the next
+// four u1's, then u2's and u3's.  Each step adds a lane's value to that of the lane eight, then four, away, and
+// writes only the lanes that go on with this value.
+__device__ __forceinline__ float quarter_sums(float u0, float u1, float u2, float u3) {
+  float r0, r1, q;
+  asm("s_nop 1\n\t"
+      "v_add_f32_dpp %0, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %0, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %1, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %1, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %2, %0, %0 row_ror:12 row_mask:0xf bank_mask:0x5\n\t"
+      "s_nop 0\n\t"
+      "v_add_f32_dpp %2, %1, %1 row_ror:4 row_mask:0xf bank_mask:0xa"
+      : "=&v"(r0), "=&v"(r1), "=&v"(q)
+      : "v"(u0), "v"(u1), "v"(u2), "v"(u3));
+  return q;
+}
+
+// Of two values the sums of a wave's halves: u's in the first 32 lanes, v's in the others.
+__device__ __forceinline__ float half_sums(float u, float v) {
+  float r;
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %1, %2\n\tv_add_f32 %0, %1, %2" : "=&v"(r), "+v"(u), "+v"(v));
+  return r;
+}
+
+// PASS 0: whole sequences.  1: the gradient before a segment from zero behind it.  2: segments.
+template <int DT, int NS, int NW, int PASS>
+__global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
+  constexpr int CH = 32, P = 2, n = NS * P * NW;
+  constexpr int E = kBlock * CH / (64 * NW);
+  constexpr int V = 2 * NS, PT = 16 / V, R = kBlock / PT;
+  constexpr bool OUT = PASS != 1;
+  __shared__ float2 steps[kBlock][CH];                     // D, D x
+  __shared__ float ups[kBlock][CH];                        // e
+  __shared__ float parts[OUT ? 3 : 1][NW][kBlock][CH];     // C . h, B . g, A . (g a h)
+  __shared__ float quarters[OUT ? NS / 2 : 1][kBlock][NW][64];  // of g D x and e h, by state
+  const Segments& Q = S.q;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int per = Q.tiles * A.G;
+  const unsigned unit = neighbours(blockIdx.x, P);
+  const long long j = unit / per;
+  const int tg = unit % per, g = tg / Q.tiles, tile = tg - g * Q.tiles;
+  const int sh = PASS == 0 ? 0 : Q.sh;
+  Place W;
+  const bool here = place(A, sh, j, false, lane, W);
+  const int part = wave * P + lane / CH;
+  const int cl = lane % CH, cg = tile * CH + cl;
   const bool live = cg < A.Cg;
   const int c = g * A.Cg + (live ? cg : A.Cg - 1);
-  const long long so = ((long long)s * A.C + c) * n + 4 * part;
-  float* H = (float*)(A.ws + W.h);
-  float* bc = (float*)(A.ws + W.bc);
-  float* par = (float*)(A.ws + W.par) + s * W.row;
-  f4 h = valid && A.S_in ? *(const f4*)(A.S_in + so) : f4{0, 0, 0, 0};
-  const f4 a = *(const f4*)(A.A + (long long)c * n + 4 * part);
-  const float skip = A.D ? A.D[c] : 0.0f, bias = A.bias ? A.bias[c] : 0.0f;
-  for (int t = t0; t < t1; t++) {
-    float x, raw, slope;
-    loadn<DT, 1>(A.x, t * A.xs + c, &x);
-    loadn<DT, 1>(A.dt, t * A.dts + c, &raw);
-    const f4 B = load4<DT>(A.B, t * A.bs + g * n + 4 * part);
-    const float D = step_of(A.softplus, raw + bias, slope);
-    if (live) *(f4*)(H + ((long long)t * A.C + c) * n + 4 * part) = h;  // h_{t-1}
+  float* par = S.par + j * S.row;
+  if (!here) {  // nothing to add
+    if (OUT && live) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) h[i] = fmaf(decay(D, a[i] * kLog2e), h[i], D * x * B[i]);
+      for (int i = 0; i < NS; i++) par[(long long)c * n + part * NS + i] = 0;
+      if (part < 2) par[(long long)A.C * n + (long long)part * A.C + c] = 0;
+    }
+    return;
   }
-  f4 G = valid && A.dS_out ? *(const f4*)(A.dS_out + so) : f4{0, 0, 0, 0}, dA = {0, 0, 0, 0};
-  float dD = 0, dbias = 0;
-  for (int t = t1 - 1; t >= t0; t--) {
-    float x, raw, slope, up, z = 0;
-    loadn<DT, 1>(A.x, t * A.xs + c, &x);
-    loadn<DT, 1>(A.dt, t * A.dts + c, &raw);
-    loadn<DT, 1>(A.d_out, t * A.os + c, &up);
-    const f4 B = load4<DT>(A.B, t * A.bs + g * n + 4 * part), Cm = load4<DT>(A.Cm, t * A.cs + g * n + 4 * part);
-    const f4 was = *(const f4*)(H + ((long long)t * A.C + c) * n + 4 * part);
-    const float D = step_of(A.softplus, raw + bias, slope);
-    float e = up;
+  if (PASS == 1 && W.idx == 0) return;
+  const int count = W.count;
+  const long long so = ((long long)W.s * A.C + c) * n + part * NS;
+  float a1[NS], a2[NS], G[NS], dA[NS];
+  get_states<NS>(A.A + (long long)c * n + part * NS, a1);
+#pragma unroll
+  for (int i = 0; i < NS; i++) a2[i] = a1[i] * kLog2e, G[i] = 0, dA[i] = 0;
+  if (A.dS_out && (OUT || W.ends)) get_states<NS>(A.dS_out + so, G);
+  if (PASS == 2 && !W.ends) {  // what the segments behind this one make of it, from the last one on
+    const long long last = (W.len - 1) >> sh;
+    const float* back = S.back + (long long)part * NS;
+    // the last segment's already holds the last state's gradient
+    get_states<NS>(back + ((j - W.idx + last) * A.C + c) * n, G);
+#pragma unroll 4
+    for (long long k = last - 1; k > W.idx; k--) {
+      const long long o = (j - W.idx + k) * A.C + c;
+      const float D = Q.steps[o];
+      float e[NS];
+      get_states<NS>(back + o * n, e);
+#pragma unroll
+      for (int i = 0; i < NS; i++) G[i] = fmaf(decay(D, a2[i]), G[i], e[i]);
+    }
+  }
+  // this thread's token of a block and its channels there
+  const int tok = threadIdx.x / (CH / E), ch = threadIdx.x % (CH / E) * E, cgo = tile * CH + ch;
+  const bool mine = cgo < A.Cg;  // a group is whole in eights: all E channels or none
+  const int co = g * A.Cg + (mine ? cgo : A.Cg - 8);
+  float skip[E], bias[E], dD[E], dbias[E];
+#pragma unroll
+  for (int i = 0; i < E; i++) {
+    skip[i] = A.D ? A.D[co + i] : 0.0f;
+    bias[i] = A.bias ? A.bias[co + i] : 0.0f;
+    dD[i] = dbias[i] = 0;
+  }
+  constexpr int size = DT == kF32 ? 4 : 2;
+  const void* zp = A.z ? A.z : A.x;
+  const unsigned ax = (unsigned)A.xs * size, ad = (unsigned)A.dts * size, az = (unsigned)(A.z ? A.zs : A.xs) * size;
+  const unsigned au = (unsigned)A.os * size;
+  const int blocks = (count + kBlock - 1) / kBlock;
+  const long long kept0 = OUT ? first_block(A, W) : 0;
+  Raw<DT, E> rx, rd, rz, ru;
+  Raw<DT, 1> rv[R];
+  float hk[NS];
+  const int sub = (lane & 15) / V, val = lane % V;  // this lane's token of PT, its value
+  const unsigned vs = (unsigned)(val < NS ? A.bs : A.cs) * size;
+  const char* vp = (const char*)(val < NS ? A.B : A.Cm) + (long long)(g * n + part * NS + val % NS) * size;
+  auto fetch = [&](int k) {
+    const int most = count - k * kBlock - 1;
+    const unsigned t = tok < most ? tok : most;
+    const long long row = W.row0 + (long long)k * kBlock;
+    rx.load((const char*)A.x + row * ax, t * ax + co * size);
+    rd.load((const char*)A.dt + row * ad, t * ad + co * size);
+    rz.load((const char*)zp + row * az, t * az + co * size);
+    ru.load((const char*)A.d_out + row * au, t * au + co * size);
+    const char* v = vp + row * vs;
+#pragma unroll
+    for (int i = 0; i < R; i++) {
+      const unsigned t = i * PT + sub < most ? i * PT + sub : most;
+      rv[i].load(v + (unsigned long long)t * vs, 0);
+    }
+    if (OUT) get_states<NS>(Q.kept + ((kept0 + k) * per + tg) * (64 * NW * NS) + threadIdx.x * NS, hk);
+  };
+  // of the block that runs: raw values, slopes of the steps, and z's part of the output
+  Raw<DT, E> x0, z0, u0;
+  float D0[E], slope0[E], e0[E];
+  auto prepare = [&](int k) {
+    x0 = rx;
+    z0 = rz;
+    u0 = ru;
+#pragma unroll
+    for (int i = 0; i < E; i++) D0[i] = rd[i] + bias[i], slope0[i] = 1, e0[i] = ru[i];
+    if (A.softplus) {
+#pragma unroll
+      for (int i = 0; i < E; i++) D0[i] = step_of(1, D0[i], slope0[i]);
+    }
     if (A.z) {
-      loadn<DT, 1>(A.z, t * A.zs + c, &z);
-      e *= z * sigmoid(z);
+#pragma unroll
+      for (int i = 0; i < E; i++) e0[i] *= z0[i] * sigmoid(z0[i]);
     }
-    float y = 0, gB = 0, gA = 0;
-    f4 pB, pC;
+    const bool in = k * kBlock + tok < count && mine;  // a token behind the last, a channel behind the group's: no step
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const float al = decay(D, a[i] * kLog2e);
-      const float now = fmaf(al, was[i], D * x * B[i]);
-      y = fmaf(Cm[i], now, y);
-      G[i] = fmaf(Cm[i], e, G[i]);
-      pC[i] = live ? e * now : 0.0f;
-      pB[i] = live ? G[i] * (D * x) : 0.0f;
-      gB = fmaf(G[i], B[i], gB);
-      G[i] *= al;
-      const float w = G[i] * was[i];
-      gA = fmaf(a[i], w, gA);
-      dA[i] = fmaf(D, w, dA[i]);
+    for (int i = 0; i < E; i++) {
+      steps[tok][ch + i] = in ? float2{D0[i], D0[i] * x0[i]} : float2{0, 0};
+      ups[tok][ch + i] = in ? e0[i] : 0.0f;
     }
+  };
+  auto finish = [&](int k) {
+    const int t = k * kBlock + tok;
+    float y[E], gB[E], gA[E], dx[E], ddt[E], dz[E];
 #pragma unroll
-    for (int m = 1; m < LN; m *= 2) {
-      y += __shfl_xor(y, m);
-      gB += __shfl_xor(gB, m);
-      gA += __shfl_xor(gA, m);
+    for (int i = 0; i < E; i++) y[i] = gB[i] = gA[i] = 0;
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+      float m[E];
+      loadv<kF32, E>(&parts[0][w][tok][ch], 0, m);
+#pragma unroll
+      for (int i = 0; i < E; i++) y[i] += m[i];
+      loadv<kF32, E>(&parts[1][w][tok][ch], 0, m);
+#pragma unroll
+      for (int i = 0; i < E; i++) gB[i] += m[i];
+      loadv<kF32, E>(&parts[2][w][tok][ch], 0, m);
+#pragma unroll
+      for (int i = 0; i < E; i++) gA[i] += m[i];
     }
+    if (t < count && mine) {
+      const long long o = (W.row0 + t) * A.C + co;
 #pragma unroll
-    for (int m = LN; m < 64; m *= 2) {
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        pB[i] += __shfl_xor(pB[i], m);
-        pC[i] += __shfl_xor(pC[i], m);
+      for (int i = 0; i < E; i++) {
+        dx[i] = fmaf(D0[i], gB[i], skip[i] * e0[i]);
+        ddt[i] = fmaf(x0[i], gB[i], gA[i]) * slope0[i];
+        dD[i] = fmaf(e0[i], x0[i], dD[i]);
+        dbias[i] += ddt[i];
       }
-    }
-    if (lane < LN) {
-      float* o = bc + (((long long)tile * A.T + t) * A.G + g) * 2 * n + 4 * part;
-      *(f4*)o = pB;
-      *(f4*)(o + n) = pC;
-    }
-    const float step = fmaf(x, gB, gA) * slope, dx = fmaf(D, gB, skip * e);
-    dD = fmaf(e, x, dD);
-    dbias += step;
-    if (live && part == 0) {
-      const long long o = (long long)t * A.C + c;
-      storen<DT, 1>(A.dx, o, &dx);
-      storen<DT, 1>(A.ddt, o, &step);
+      storev<DT, E>(A.dx, o, dx);
+      storev<DT, E>(A.ddt, o, ddt);
       if (A.z) {
-        const float sg = sigmoid(z), dz = up * fmaf(skip, x, y) * fmaf(z * sg, 1.0f - sg, sg);
-        storen<DT, 1>(A.dz, o, &dz);
+#pragma unroll
+        for (int i = 0; i < E; i++) {
+          const float z = z0[i], sg = sigmoid(z);
+          dz[i] = u0[i] * fmaf(skip[i], x0[i], y[i]) * fmaf(z * sg, 1.0f - sg, sg);
+        }
+        storev<DT, E>(A.dz, o, dz);
       }
     }
+    // dB and dC of this tile: a thread adds up one part's four values (two states of each) of a token
+    for (int i = threadIdx.x; i < NS / 2 * kBlock * NW * P * 4; i += 64 * NW) {
+      const int b = i % 4, pt = i / 4 % (NW * P), tk = i / (4 * NW * P) % kBlock, v = i / (4 * NW * P * kBlock);
+      const float* q = &quarters[v][tk][pt / P][pt % P * 32 + 4 * b];
+      float m[4], sum = 0;
+#pragma unroll
+      for (int r = 0; r < 2; r++) {
+        loadn<kF32, 4>(q, 16 * r, m);
+        sum += (m[0] + m[1]) + (m[2] + m[3]);
+      }
+      if (k * kBlock + tk < count)
+        S.bc[(((long long)tile * A.T + W.row0 + k * kBlock + tk) * A.G + g) * 2 * n + (b < 2 ? 0 : n) + pt * NS + 2 * v + b % 2] = sum;
+    }
+  };
+  if (blocks > 0) {
+    fetch(blocks - 1);
+    prepare(blocks - 1);
   }
-  if (!live) return;
-  if (valid && A.dS_in) *(f4*)(A.dS_in + so) = G;
-  *(f4*)(par + (long long)c * n + 4 * part) = dA;
-  if (part == 0) {
-    par[(long long)A.C * n + c] = dD;
-    par[(long long)A.C * n + A.C + c] = dbias;
+  for (int k = blocks - 1; k >= 0; k--) {
+    float bc[R], h[NS], al[OUT ? kBlock : 1][NS], was[OUT ? kBlock : 1][NS], cA[NS];
+    const int most = count - k * kBlock - 1;
+#pragma unroll
+    for (int i = 0; i < R; i++) bc[i] = i * PT + sub <= most ? rv[i][0] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NS; i++) h[i] = hk[i], cA[i] = 0;
+    if (k > 0) fetch(k - 1);
+    __syncthreads();
+    if constexpr (OUT) {
+      unrolled<kBlock>([&](auto t) {
+        constexpr int T = t;
+        const float2 d = steps[T][cl];
+        unrolled<NS>([&](auto i) {
+          al[T][i] = decay(d.x, a2[i]);
+          was[T][i] = h[i];
+          h[i] = fmaf(al[T][i], h[i], row_lane<T % PT * V + i>(bc[T / PT]) * d.y);
+        });
+      });
+    }
+    float gA_odd = 0;
+    unrolled<kBlock>([&](auto t) {
+      constexpr int T = kBlock - 1 - t, base = T % PT * V;
+      const float b = bc[T / PT], e = ups[T][cl];
+      const float2 d = steps[T][cl];
+      unrolled<NS>([&](auto i) { row_fmac<base + NS + i>(G[i], b, e); });
+      if constexpr (OUT) {
+          float vB[NS], vC[NS], y = 0, gB = 0, gA = 0;
+#pragma unroll
+          for (int i = 0; i < NS; i++) vC[i] = e * h[i], vB[i] = G[i] * d.y;
+          if constexpr (NS == 2) {
+            y = row_dot2<base + NS>(b, h);
+            gB = row_dot2<base>(b, G);
+          } else {
+            y = row_dot<base + NS, false>(y, b, h);
+            gB = row_dot<base, false>(gB, b, G);
+          }
+#pragma unroll
+          for (int i = 0; i < NS; i++) {
+            G[i] *= al[T][i];
+            const float w = G[i] * was[T][i];
+            gA = fmaf(a1[i], w, gA);
+            cA[i] = fmaf(d.x, w, cA[i]);
+            h[i] = was[T][i];
+          }
+#pragma unroll
+          for (int v = 0; v < NS / 2; v++)
+            quarters[v][T][wave][lane] = quarter_sums(vB[2 * v], vB[2 * v + 1], vC[2 * v], vC[2 * v + 1]);
+          parts[lane / CH][wave][T][cl] = half_sums(y, gB);
+          if constexpr (T % 2) gA_odd = gA;
+          else parts[2][wave][T + lane / CH][cl] = half_sums(gA, gA_odd);
+        } else {
+#pragma unroll
+          for (int i = 0; i < NS; i++) G[i] *= decay(d.x, a2[i]);
+        }
+    });
+#pragma unroll
+    for (int i = 0; i < NS; i++) dA[i] += cA[i];
+    __syncthreads();
+    if (OUT) finish(k);
+    if (k > 0) prepare(k - 1);
+  }
+  if constexpr (PASS == 1) {
+    if (live) put_states<NS>(S.back + (j * A.C + c) * n + part * NS, G);
+  } else {
+    if (live) {
+      if (W.idx == 0 && A.dS_in) put_states<NS>(A.dS_in + so, G);
+      put_states<NS>(par + (long long)c * n + part * NS, dA);
+    }
+    float* sum = &parts[0][0][0][0];  // [2][kBlock][CH]; parts is large enough, its last reads are behind the next barrier
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < E; i++) {
+      sum[tok * CH + ch + i] = dD[i];
+      sum[(kBlock + tok) * CH + ch + i] = dbias[i];
+    }
+    __syncthreads();
+    if (wave == 0 && live) {  // one half of the wave adds dD up, the other dbias
+      float m = 0;
+#pragma unroll
+      for (int t = 0; t < kBlock; t++) m += sum[(lane / CH * kBlock + t) * CH + cl];
+      par[(long long)A.C * n + (long long)(lane / CH) * A.C + c] = m;
+    }
   }
 }
 
@@ -150,17 +345,27 @@ __global__ __launch_bounds__(256) void k_scan_bc(ScanArgs A, Space W) {
     int t0, t1;
     if (!seq_range(A, lo, t0, t1) || t < t0 || t >= t1) return;
   }
-  const float* p = (const float*)(A.ws + W.bc) + i;
+  const float* p = W.bc + i;
   float acc = 0;
-  for (int q = 0; q < W.tiles; q++) acc += p[q * row * A.T];
+#pragma unroll 8
+  for (int q = 0; q < W.q.tiles; q++) acc += p[q * row * A.T];
   const long long o = ((long long)t * A.G + g) * A.n + (m < A.n ? m : m - A.n);
   storen<DT, 1>(m < A.n ? A.dB : A.dC, o, &acc);
 }
 
-template <int DT, int LN>
+template <int DT, int NS, int NW>
 hipError_t launch(const ScanArgs& a, const Space& w, hipStream_t s) {
-  const long long units = (long long)w.tiles * a.G * a.N;
-  hipLaunchKernelGGL((k_scan_grad<DT, LN>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s, a, w);
+  const dim3 grid((unsigned)(w.segs * w.q.tiles * a.G)), block(64 * NW);
+  if (w.q.sh) {
+    hipLaunchKernelGGL((k_scan_run<DT, NS, 32, NW, 1>), grid, block, 0, s, a, w.q);
+    if (hipError_t e = hipGetLastError()) return e;
+    hipLaunchKernelGGL((k_scan_back<DT, NS, NW, 1>), grid, block, 0, s, a, w);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  hipLaunchKernelGGL((k_scan_run<DT, NS, 32, NW, 3>), grid, block, 0, s, a, w.q);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (w.q.sh) hipLaunchKernelGGL((k_scan_back<DT, NS, NW, 2>), grid, block, 0, s, a, w);
+  else hipLaunchKernelGGL((k_scan_back<DT, NS, NW, 0>), grid, block, 0, s, a, w);
   if (hipError_t e = hipGetLastError()) return e;
   const long long all = 2LL * a.G * a.n * a.T;
   if (all) hipLaunchKernelGGL((k_scan_bc<DT>), dim3((unsigned)((all + 255) / 256)), dim3(256), 0, s, a, w);
@@ -169,23 +374,29 @@ hipError_t launch(const ScanArgs& a, const Space& w, hipStream_t s) {
 
 template <int DT>
 hipError_t by_states(const ScanArgs& a, const Space& w, hipStream_t s) {
-  return a.n == 8 ? launch<DT, 2>(a, w, s)
-                  : a.n == 16 ? launch<DT, 4>(a, w, s) : a.n == 32 ? launch<DT, 8>(a, w, s) : launch<DT, 16>(a, w, s);
+  return a.n == 8    ? launch<DT, 2, 2>(a, w, s)
+         : a.n == 16 ? launch<DT, 2, 4>(a, w, s)
+         : a.n == 32 ? launch<DT, 4, 4>(a, w, s)
+                     : launch<DT, 4, 8>(a, w, s);
 }
 
 }  // namespace
 
-size_t scan_backward_bytes(const ScanArgs& a) { return space(a).all; }
+size_t scan_backward_bytes(const ScanArgs& a) {
+  Space w;
+  return space(a, nullptr, &w);
+}
 
 hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
-  const Space w = space(a);
+  Space w;
+  space(a, a.ws, &w);
   if (a.N > 0) {
     const hipError_t e = a.dtype == kF32    ? by_states<kF32>(a, w, s)
                          : a.dtype == kBF16 ? by_states<kBF16>(a, w, s)
                                             : by_states<kF16>(a, w, s);
     if (e) return e;
   }
-  SumArgs m{(const float*)(a.ws + w.par), a.N, w.row, (long long)a.C * a.n, a.C, a.dA, a.dD, a.dbias};
+  SumArgs m{w.par, (int)w.segs, w.row, (long long)a.C * a.n, a.C, a.dA, a.dD, a.dbias};
   return launch_sum(m, s);
 }
 
