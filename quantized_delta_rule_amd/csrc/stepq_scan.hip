@@ -69,7 +69,7 @@ hipError_t tokens(const ScanArgs& a, hipStream_t s) {
 template <int DT, int NS, int NW>
 hipError_t blocks(const ScanArgs& a, hipStream_t s) {
   char* end;
-  const int sh = segments_of(a);
+  const int sh = segments_of(a, kLeastForward);
   const Segments q = lay_segments(a, sh, a.ws, &end);
   const long long per = (long long)q.tiles * a.G;
   if (!sh) {
@@ -100,7 +100,7 @@ hipError_t by_states(const ScanArgs& a, hipStream_t s) {
 size_t scan_forward_bytes(const ScanArgs& a) {
   if (!in_blocks(a)) return 0;
   char* end;
-  lay_segments(a, segments_of(a), nullptr, &end);
+  lay_segments(a, segments_of(a, kLeastForward), nullptr, &end);
   return (size_t)end;
 }
 

@@ -339,16 +339,16 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   }
 }
 
-// Segments (0: none) where workgroups of 32 channels of whole sequences would leave CUs idle: enough of them for four
-// workgroups a CU, but no more than 64 of a sequence of mean length (each looks at all before it), of at least 64
-// tokens.
-inline int segments_of(const ScanArgs& a) {
+// Segments (0: none) where workgroups of 32 channels of whole sequences would be fewer than `least`: about ten
+// workgroups a CU, but no more than 64 of a sequence of mean length (each looks at all before it), of at least 64 tokens.
+inline int segments_of(const ScanArgs& a, int least) {
   const long long tiles = (a.Cg + 31) / 32 * a.G, mean = a.N > 0 ? a.T / a.N : 0;
-  if (a.N <= 0 || tiles * a.N >= 512) return 0;
+  if (a.N <= 0 || tiles * a.N >= least) return 0;
   int sh = 6;
-  while (sh < 30 && (((long long)a.T >> sh) * tiles > 1024 || mean >> sh > 64)) sh++;
-  return mean >= 2LL << sh ? sh : 0;
+  while (sh < 30 && (((long long)a.T >> sh) * tiles > 2560 || mean >> sh > 64)) sh++;
+  return mean > 1LL << sh ? sh : 0;
 }
+constexpr int kLeastForward = 256, kLeastBackward = 512;
 
 constexpr size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 

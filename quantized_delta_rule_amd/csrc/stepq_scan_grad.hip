@@ -21,7 +21,7 @@ struct Space {
   float* back;
 };
 size_t space(const ScanArgs& a, char* ws, Space* w) {
-  const int sh = segments_of(a);
+  const int sh = segments_of(a, kLeastBackward);
   char* p;
   w->q = lay_segments(a, sh, ws, &p);
   w->segs = sh ? pieces(a, sh) : a.N;
