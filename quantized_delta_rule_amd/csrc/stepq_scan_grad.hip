@@ -37,28 +37,88 @@ size_t space(const ScanArgs& a, char* ws, Space* w) {
   return (size_t)(p - ws);
 }
 
+// What a token adds to NS states' gradients and takes from them across lanes.  With B and C in lanes I .. and I + NS ..
+// of each 16 lanes' b:
+//   g_i += C_i e;  y = sum_i C_i h_i, gB = sum_i B_i g_i, of which `both` is the sums of the wave's halves: y's in the
+//   first 32 lanes, gB's in the others;
+//   q: four values (g D x of two states, e h of the same) summed over every fourth of 16 lanes: the first four lanes
+//   get the first value's sums (of lanes 0, 4, 8, 12; 1, 5, ..), the next four the second's, and so on.  Each step
+//   adds a lane's value to that of the lane eight, then four, away, and writes only the lanes that go on with this value.
+// One block of instructions, ordered so that none reads across lanes what one of the two before it wrote (two wait states; the
+// s_nop is for b).
+template <int I>
+__device__ __forceinline__ void across2(float b, float e, float dx, const float* h, float* g, float& both, float* q) {
+  float y, gB, u0, u1, u2, u3, r0, r1;
+  asm("s_nop 1\n\t"
+      "v_fmac_f32_dpp %0, %11, %12 row_newbcast:%18 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %11, %12 row_newbcast:%19 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %2, %11, %14 row_newbcast:%18 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %3, %11, %0 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32 %4, %0, %13\n\t"
+      "v_fmac_f32_dpp %2, %11, %15 row_newbcast:%19 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32 %5, %1, %13\n\t"
+      "v_fmac_f32_dpp %3, %11, %1 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32 %6, %12, %14\n\t"
+      "v_mul_f32 %7, %12, %15\n\t"
+      "v_add_f32_dpp %8, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %9, %5, %5 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_permlane32_swap_b32 %2, %3\n\t"
+      "v_add_f32_dpp %8, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %9, %7, %7 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32 %2, %2, %3\n\t"
+      "s_nop 0\n\t"
+      "v_add_f32_dpp %10, %8, %8 row_ror:12 row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %10, %9, %9 row_ror:4 row_mask:0xf bank_mask:0xa"
+      : "+&v"(g[0]), "+&v"(g[1]), "=&v"(y), "=&v"(gB), "=&v"(u0), "=&v"(u1), "=&v"(u2), "=&v"(u3), "=&v"(r0), "=&v"(r1),
+        "=&v"(q[0])
+      : "v"(b), "v"(e), "v"(dx), "v"(h[0]), "v"(h[1]), "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3));
+  both = y;
+}
+
+template <int I>
+__device__ __forceinline__ void across4(float b, float e, float dx, const float* h, float* g, float& both, float* q) {
+  float y, gB, u0, u1, u2, u3, r0, r1;
+  asm("s_nop 1\n\t"
+      "v_fmac_f32_dpp %0, %6, %7 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %1, %6, %7 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %2, %6, %7 row_newbcast:%18 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %3, %6, %7 row_newbcast:%19 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %4, %6, %8 row_newbcast:%16 row_mask:0xf bank_mask:0xf\n\t"
+      "v_mul_f32_dpp %5, %6, %0 row_newbcast:%12 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %4, %6, %9 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %5, %6, %1 row_newbcast:%13 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %4, %6, %10 row_newbcast:%18 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %5, %6, %2 row_newbcast:%14 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %4, %6, %11 row_newbcast:%19 row_mask:0xf bank_mask:0xf\n\t"
+      "v_fmac_f32_dpp %5, %6, %3 row_newbcast:%15 row_mask:0xf bank_mask:0xf\n\t"
+      "s_nop 1\n\t"
+      "v_permlane32_swap_b32 %4, %5\n\t"
+      "v_add_f32 %4, %4, %5"
+      : "+&v"(g[0]), "+&v"(g[1]), "+&v"(g[2]), "+&v"(g[3]), "=&v"(y), "=&v"(gB)
+      : "v"(b), "v"(e), "v"(h[0]), "v"(h[1]), "v"(h[2]), "v"(h[3]), "n"(I), "n"(I + 1), "n"(I + 2), "n"(I + 3), "n"(I + 4),
+        "n"(I + 5), "n"(I + 6), "n"(I + 7));
+  both = y;
+#pragma unroll
+  for (int k = 0; k < 2; k++)
+    asm("v_mul_f32 %0, %7, %9\n\t"
+        "v_mul_f32 %1, %8, %9\n\t"
+        "v_mul_f32 %2, %10, %11\n\t"
+        "v_mul_f32 %3, %10, %12\n\t"
+        "v_add_f32_dpp %4, %0, %0 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %4, %2, %2 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %5, %1, %1 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %5, %3, %3 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+        "v_add_f32_dpp %6, %4, %4 row_ror:12 row_mask:0xf bank_mask:0x5\n\t"
+        "s_nop 0\n\t"
+        "v_add_f32_dpp %6, %5, %5 row_ror:4 row_mask:0xf bank_mask:0xa"
+        : "=&v"(u0), "=&v"(u1), "=&v"(u2), "=&v"(u3), "=&v"(r0), "=&v"(r1), "=&v"(q[k])
+        : "v"(g[2 * k]), "v"(g[2 * k + 1]), "v"(dx), "v"(e), "v"(h[2 * k]), "v"(h[2 * k + 1]));
+}
+
 // v += (lane I of each 16 lanes' b) * e
 template <int I>
 __device__ __forceinline__ void row_fmac(float& v, float b, float e) {
   asm("s_nop 1\n\tv_fmac_f32_dpp %0, %1, %2 row_newbcast:%3 row_mask:0xf bank_mask:0xf" : "+v"(v) : "v"(b), "v"(e), "n"(I));
-}
-
-// Four values' sums over every fourth of 16 lanes: the first four lanes get u0's (of lanes 0, 4, 8, 12; 1, 5, ..), the next
-// four u1's, then u2's and u3's.  Each step adds a lane's value to that of the lane eight, then four, away, and
-// writes only the lanes that go on with this value.
-__device__ __forceinline__ float quarter_sums(float u0, float u1, float u2, float u3) {
-  float r0, r1, q;
-  asm("s_nop 1\n\t"
-      "v_add_f32_dpp %0, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
-      "v_add_f32_dpp %0, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
-      "v_add_f32_dpp %1, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
-      "v_add_f32_dpp %1, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
-      "v_add_f32_dpp %2, %0, %0 row_ror:12 row_mask:0xf bank_mask:0x5\n\t"
-      "s_nop 0\n\t"
-      "v_add_f32_dpp %2, %1, %1 row_ror:4 row_mask:0xf bank_mask:0xa"
-      : "=&v"(r0), "=&v"(r1), "=&v"(q)
-      : "v"(u0), "v"(u1), "v"(u2), "v"(u3));
-  return q;
 }
 
 // Of two values the sums of a wave's halves: u's in the first 32 lanes, v's in the others.
@@ -75,8 +135,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
   constexpr int E = kBlock * CH / (64 * NW);
   constexpr int V = 2 * NS, PT = 16 / V, R = kBlock / PT;
   constexpr bool OUT = PASS != 1;
-  __shared__ float2 steps[kBlock][CH];                     // D, D x
-  __shared__ float ups[kBlock][CH];                        // e
+  __shared__ f4 steps[kBlock][CH];                         // D, D x, e
   __shared__ float parts[OUT ? 3 : 1][NW][kBlock][CH];     // C . h, B . g, A . (g a h)
   __shared__ float quarters[OUT ? NS / 2 : 1][kBlock][NW][64];  // of g D x and e h, by state
   const Segments& Q = S.q;
@@ -183,8 +242,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
     const bool in = k * kBlock + tok < count && mine;  // a token behind the last, a channel behind the group's: no step
 #pragma unroll
     for (int i = 0; i < E; i++) {
-      steps[tok][ch + i] = in ? float2{D0[i], D0[i] * x0[i]} : float2{0, 0};
-      ups[tok][ch + i] = in ? e0[i] : 0.0f;
+      steps[tok][ch + i] = in ? f4{D0[i], D0[i] * x0[i], e0[i], 0} : f4{0, 0, 0, 0};
     }
   };
   auto finish = [&](int k) {
@@ -255,7 +313,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
     if constexpr (OUT) {
       unrolled<kBlock>([&](auto t) {
         constexpr int T = t;
-        const float2 d = steps[T][cl];
+        const float2 d = *(const float2*)&steps[T][cl];
         unrolled<NS>([&](auto i) {
           al[T][i] = decay(d.x, a2[i]);
           was[T][i] = h[i];
@@ -266,38 +324,31 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
     float gA_odd = 0;
     unrolled<kBlock>([&](auto t) {
       constexpr int T = kBlock - 1 - t, base = T % PT * V;
-      const float b = bc[T / PT], e = ups[T][cl];
-      const float2 d = steps[T][cl];
-      unrolled<NS>([&](auto i) { row_fmac<base + NS + i>(G[i], b, e); });
+      const float b = bc[T / PT];
+      const f4 d = steps[T][cl];
       if constexpr (OUT) {
-          float vB[NS], vC[NS], y = 0, gB = 0, gA = 0;
+        float both, q[NS / 2], gA = 0;
+        if constexpr (NS == 2) across2<base>(b, d[2], d[1], h, G, both, q);
+        else across4<base>(b, d[2], d[1], h, G, both, q);
+        parts[lane / CH][wave][T][cl] = both;
 #pragma unroll
-          for (int i = 0; i < NS; i++) vC[i] = e * h[i], vB[i] = G[i] * d.y;
-          if constexpr (NS == 2) {
-            y = row_dot2<base + NS>(b, h);
-            gB = row_dot2<base>(b, G);
-          } else {
-            y = row_dot<base + NS, false>(y, b, h);
-            gB = row_dot<base, false>(gB, b, G);
-          }
+        for (int v = 0; v < NS / 2; v++) quarters[v][T][wave][lane] = q[v];
 #pragma unroll
-          for (int i = 0; i < NS; i++) {
-            G[i] *= al[T][i];
-            const float w = G[i] * was[T][i];
-            gA = fmaf(a1[i], w, gA);
-            cA[i] = fmaf(d.x, w, cA[i]);
-            h[i] = was[T][i];
-          }
-#pragma unroll
-          for (int v = 0; v < NS / 2; v++)
-            quarters[v][T][wave][lane] = quarter_sums(vB[2 * v], vB[2 * v + 1], vC[2 * v], vC[2 * v + 1]);
-          parts[lane / CH][wave][T][cl] = half_sums(y, gB);
-          if constexpr (T % 2) gA_odd = gA;
-          else parts[2][wave][T + lane / CH][cl] = half_sums(gA, gA_odd);
-        } else {
-#pragma unroll
-          for (int i = 0; i < NS; i++) G[i] *= decay(d.x, a2[i]);
+        for (int i = 0; i < NS; i++) {
+          G[i] *= al[T][i];
+          const float w = G[i] * was[T][i];
+          gA = fmaf(a1[i], w, gA);
+          cA[i] = fmaf(d[0], w, cA[i]);
+          h[i] = was[T][i];
         }
+        if constexpr (T % 2) gA_odd = gA;
+        else parts[2][wave][T + lane / CH][cl] = half_sums(gA, gA_odd);
+      } else {
+        unrolled<NS>([&](auto i) {
+          row_fmac<base + NS + i>(G[i], b, d[2]);
+          G[i] *= decay(d[0], a2[i]);
+        });
+      }
     });
 #pragma unroll
     for (int i = 0; i < NS; i++) dA[i] += cA[i];
