@@ -224,7 +224,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
   };
   // of the block that runs: raw values, slopes of the steps, and z's part of the output
   Raw<DT, E> x0, z0, u0;
-  float D0[E], slope0[E], e0[E];
+  float D0[E], slope0[E], e0[E], s0[E];
   auto prepare = [&](int k) {
     x0 = rx;
     z0 = rz;
@@ -237,7 +237,10 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
     }
     if (A.z) {
 #pragma unroll
-      for (int i = 0; i < E; i++) e0[i] *= z0[i] * sigmoid(z0[i]);
+      for (int i = 0; i < E; i++) {
+        s0[i] = sigmoid(z0[i]);
+        e0[i] *= z0[i] * s0[i];
+      }
     }
     const bool in = k * kBlock + tok < count && mine;  // a token behind the last, a channel behind the group's: no step
 #pragma unroll
@@ -245,6 +248,8 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
       steps[tok][ch + i] = in ? f4{D0[i], D0[i] * x0[i], e0[i], 0} : f4{0, 0, 0, 0};
     }
   };
+  const int b4 = threadIdx.x % 4, pt = threadIdx.x / 4 % (NW * P), tk = threadIdx.x / (4 * NW * P);
+  float* bcp = S.bc + (((long long)tile * A.T + W.row0 + tk) * A.G + g) * (2 * n) + (b4 < 2 ? 0 : n) + pt * NS + b4 % 2;
   auto finish = [&](int k) {
     const int t = k * kBlock + tok;
     float y[E], gB[E], gA[E], dx[E], ddt[E], dz[E];
@@ -277,24 +282,25 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
       if (A.z) {
 #pragma unroll
         for (int i = 0; i < E; i++) {
-          const float z = z0[i], sg = sigmoid(z);
-          dz[i] = u0[i] * fmaf(skip[i], x0[i], y[i]) * fmaf(z * sg, 1.0f - sg, sg);
+          dz[i] = u0[i] * fmaf(skip[i], x0[i], y[i]) * fmaf(z0[i] * s0[i], 1.0f - s0[i], s0[i]);
         }
         storev<DT, E>(A.dz, o, dz);
       }
     }
-    // dB and dC of this tile: a thread adds up one part's four values (two states of each) of a token
-    for (int i = threadIdx.x; i < NS / 2 * kBlock * NW * P * 4; i += 64 * NW) {
-      const int b = i % 4, pt = i / 4 % (NW * P), tk = i / (4 * NW * P) % kBlock, v = i / (4 * NW * P * kBlock);
-      const float* q = &quarters[v][tk][pt / P][pt % P * 32 + 4 * b];
-      float m[4], sum = 0;
+    // dB and dC of this tile: a thread adds up one value of one part for every eighth token
+    const int most = count - k * kBlock;
+    float* to = bcp + (long long)k * kBlock * (2 * n * A.G);
 #pragma unroll
-      for (int r = 0; r < 2; r++) {
-        loadn<kF32, 4>(q, 16 * r, m);
-        sum += (m[0] + m[1]) + (m[2] + m[3]);
+    for (int r = 0; r < 2; r++) {
+#pragma unroll
+      for (int v = 0; v < NS / 2; v++) {
+        const float* q = &quarters[v][tk + 8 * r][pt / P][pt % P * 32 + 4 * b4];
+        float m0[4], m1[4];
+        loadn<kF32, 4>(q, 0, m0);
+        loadn<kF32, 4>(q, 16, m1);
+        const float sum = ((m0[0] + m0[1]) + (m0[2] + m0[3])) + ((m1[0] + m1[1]) + (m1[2] + m1[3]));
+        if (tk + 8 * r < most) to[8 * r * (2 * n * A.G) + 2 * v] = sum;
       }
-      if (k * kBlock + tk < count)
-        S.bc[(((long long)tile * A.T + W.row0 + k * kBlock + tk) * A.G + g) * 2 * n + (b < 2 ? 0 : n) + pt * NS + 2 * v + b % 2] = sum;
     }
   };
   if (blocks > 0) {
