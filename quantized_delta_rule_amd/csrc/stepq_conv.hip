@@ -11,7 +11,10 @@ namespace {
 
 using namespace lay;
 
-constexpr int kSh = 5, kPiece = 1 << kSh;  // tokens of a piece
+constexpr int kShF = 5, kShB = 6;          // tokens of a piece: 2^kShF forward, 2^kShB backward
+constexpr int kAhead = 4;                  // rows read at once
+template <int DT>
+constexpr int kSize = DT == kF32 ? 4 : 2;
 
 // The part of a sequence that a wave works on.
 struct Part {
@@ -21,6 +24,7 @@ struct Part {
 };
 
 // False where the wave has nothing to do.  One lane a sequence raises the flags.
+template <int SH>
 __device__ __forceinline__ bool part_of(const ConvArgs& A, long long j, bool report, int lane, Part& P) {
   int a, b;
   if (report && j < A.N) {
@@ -28,13 +32,13 @@ __device__ __forceinline__ bool part_of(const ConvArgs& A, long long j, bool rep
     seq_slot(A, (int)j, ok, lane == 0);
   }
   long long idx;
-  if (!piece(A, kSh, j, lane, P.s, idx)) return false;
+  if (!piece(A, SH, j, lane, P.s, idx)) return false;
   const bool ok = seq_range(A, P.s, a, b);
   P.slot = seq_slot(A, P.s, ok, false);
   P.t0 = a;
   P.len = b - a;
-  P.p = idx << kSh;
-  P.end = P.p + kPiece < P.len ? P.p + kPiece : P.len;
+  P.p = idx << SH;
+  P.end = P.p + (1 << SH) < P.len ? P.p + (1 << SH) : P.len;
   P.first = idx == 0;
   return P.slot >= 0 && (P.p < P.len || P.first);
 }
@@ -63,7 +67,7 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
   const int cb = blockIdx.x % blocks;
   const long long j = (long long)(blockIdx.x / blocks) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Part P;
-  if (!part_of(A, j, cb == 0, lane, P)) return;
+  if (!part_of<kShF>(A, j, cb == 0, lane, P)) return;
   const int c = (cb * 64 + lane) * V;
   if (c >= A.C) return;
   float w[W][V], b[V], x[W][V];  // x: the last W inputs
@@ -98,21 +102,40 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
 #pragma unroll
     for (int i = 0; i < W - 1; i++) storev<DT, V>(A.S_out, so + (long long)i * A.C, last[i]);
   }
-  for (long long t = P.t0 + P.p; t < P.t0 + P.end; t++) {
-    loadv<DT, V>(A.x, t * A.xs + c, x[W - 1]);
-    float y[V];
+  // rows are read kAhead at a time, the next ones while these are worked on
+  const int n = (int)(P.end - P.p);
+  const char* px = (const char*)A.x + ((P.t0 + P.p) * A.xs + c) * kSize<DT>;
+  char* po = (char*)A.out + ((P.t0 + P.p) * A.os + c) * kSize<DT>;
+  const long long ax = A.xs * kSize<DT>, ao = A.os * kSize<DT>;
+  Raw<DT, V> next[kAhead];
+  auto fetch = [&](int t0) {
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-      float u = b[v];
+    for (int i = 0; i < kAhead; i++) next[i].load(px + (t0 + i < n ? t0 + i : n - 1) * ax);
+  };
+  if (n > 0) fetch(0);
+  for (int t0 = 0; t0 < n; t0 += kAhead) {
+    Raw<DT, V> now[kAhead];
 #pragma unroll
-      for (int i = 0; i < W; i++) u = fmaf(w[i][v], x[i][v], u);
-      y[v] = act_of(A.act, u);
-    }
-    storev<DT, V>(A.out, t * A.os + c, y);
+    for (int i = 0; i < kAhead; i++) now[i] = next[i];
+    if (t0 + kAhead < n) fetch(t0 + kAhead);
 #pragma unroll
-    for (int i = 0; i < W - 1; i++) {
+    for (int r = 0; r < kAhead; r++) {
+      if (t0 + r >= n) break;
+      float y[V];
 #pragma unroll
-      for (int v = 0; v < V; v++) x[i][v] = x[i + 1][v];
+      for (int v = 0; v < V; v++) {
+        x[W - 1][v] = now[r][v];
+        float u = b[v];
+#pragma unroll
+        for (int i = 0; i < W; i++) u = fmaf(w[i][v], x[i][v], u);
+        y[v] = act_of(A.act, u);
+      }
+      storev<DT, V>(po + (t0 + r) * ao, 0, y);
+#pragma unroll
+      for (int i = 0; i < W - 1; i++) {
+#pragma unroll
+        for (int v = 0; v < V; v++) x[i][v] = x[i + 1][v];
+      }
     }
   }
 }
@@ -135,7 +158,7 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
     for (int i = 0; i < W; i++) dw[i][v] = 0;
   }
   Part P;
-  if (part_of(A, j, cb == 0, lane, P) && c < A.C) {
+  if (part_of<kShB>(A, j, cb == 0, lane, P) && c < A.C) {
     float w[W][V], b[V], x[W][V], du[W][V];
     weights<W, V>(A, c, w, b);
     const long long so = (long long)P.s * (W - 1) * A.C + c;
@@ -156,14 +179,34 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
     }
     // positions settled: p .. end - 1, from -(W - 1) in the first piece
     const long long from = P.first ? -(long long)(W - 1) : P.p;
-    for (long long q = P.p; q < P.end + W - 1; q++) {
+    const char* px = (const char*)A.x + (P.t0 * A.xs + c) * kSize<DT>;
+    const char* pu = (const char*)A.d_out + (P.t0 * A.os + c) * kSize<DT>;
+    const long long ax = A.xs * kSize<DT>, au = A.os * kSize<DT>, most = P.len - 1;
+    Raw<DT, V> nx[kAhead], nu[kAhead], rx[kAhead], ru[kAhead];
+    auto fetch = [&](long long q) {
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) {
+        const long long t = q + i < P.len ? q + i : most;
+        nx[i].load(px + t * ax);
+        nu[i].load(pu + t * au);
+      }
+    };
+    if (P.p < P.len) fetch(P.p);
+    for (long long q0 = P.p; q0 < P.end + W - 1; q0 += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; i++) rx[i] = nx[i], ru[i] = nu[i];
+      if (q0 + kAhead < P.end + W - 1 && q0 + kAhead < P.len) fetch(q0 + kAhead);
+#pragma unroll
+      for (int r = 0; r < kAhead; r++) {
+      const long long q = q0 + r;
+      if (q >= P.end + W - 1) break;
       const bool in = q < P.len;
 #pragma unroll
       for (int v = 0; v < V; v++) du[W - 1][v] = 0;
       if (in) {
         float dy[V];
-        loadv<DT, V>(A.x, (P.t0 + q) * A.xs + c, x[W - 1]);
-        loadv<DT, V>(A.d_out, (P.t0 + q) * A.os + c, dy);
+#pragma unroll
+        for (int v = 0; v < V; v++) x[W - 1][v] = rx[r][v], dy[v] = ru[r][v];
 #pragma unroll
         for (int v = 0; v < V; v++) {
           float u = b[v];
@@ -209,6 +252,7 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
           du[i][v] = du[i + 1][v];
         }
       }
+      }
     }
   }
 #pragma unroll
@@ -237,7 +281,7 @@ constexpr int kFwdV = 8, kBwdV = 4;
 template <int DT, int W>
 hipError_t launch(const ConvArgs& a, bool back, hipStream_t s) {
   const int V = back ? kBwdV : kFwdV, blocks = (a.C + 64 * V - 1) / (64 * V);
-  const long long groups = (pieces(a, kSh) + 3) / 4;
+  const long long groups = (pieces(a, back ? kShB : kShF) + 3) / 4;
   const dim3 grid((unsigned)(groups * blocks)), block(256);
   if (back) hipLaunchKernelGGL((k_conv_grad<DT, W, kBwdV>), grid, block, 0, s, a, blocks);
   else hipLaunchKernelGGL((k_conv<DT, W, kFwdV>), grid, block, 0, s, a, blocks);
@@ -259,11 +303,11 @@ hipError_t by_type(const ConvArgs& a, bool back, hipStream_t s) {
 hipError_t launch_conv(const ConvArgs& a, hipStream_t s) { return a.N <= 0 ? hipSuccess : by_type(a, false, s); }
 
 size_t conv_backward_bytes(const ConvArgs& a) {
-  return (size_t)((pieces(a, kSh) + 3) / 4) * a.C * (a.W + 1) * sizeof(float);
+  return (size_t)((pieces(a, kShB) + 3) / 4) * a.C * (a.W + 1) * sizeof(float);
 }
 
 hipError_t launch_conv_backward(const ConvArgs& a, hipStream_t s) {
-  SumArgs m{a.ws, (int)((pieces(a, kSh) + 3) / 4), (long long)a.C * (a.W + 1), (long long)a.C * a.W, a.C, a.dw, a.db,
+  SumArgs m{a.ws, (int)((pieces(a, kShB) + 3) / 4), (long long)a.C * (a.W + 1), (long long)a.C * a.W, a.C, a.dw, a.db,
             nullptr};
   if (a.N > 0) {
     if (hipError_t e = by_type(a, true, s)) return e;

@@ -2,6 +2,8 @@
 // state space scan (stepq_scan.hip, stepq_scan_grad.hip), root-mean-square norm (stepq_norm.hip); arguments and
 // what their kernels share.  Not part of the public ABI.
 #pragma once
+#include <type_traits>
+
 #include "stepq_delta.h"
 
 namespace stepq {
@@ -135,6 +137,22 @@ __device__ __forceinline__ void storev(void* p, long long i, const float* x) {
   if constexpr (V == 8) store8<DT>(p, i, x);
   else storen<DT, V>(p, i, x);
 }
+
+// E neighbouring elements as they lie in memory: kept until they are used, so that their load is not waited for before.
+template <int DT, int E>
+struct Raw {
+  typedef typename std::conditional<DT == kF32, float, unsigned short>::type T;
+  typedef T V __attribute__((ext_vector_type(E)));
+  typename std::conditional<E == 1, T, V>::type v;
+  __device__ __forceinline__ void load(const void* p, long long at = 0) { v = *(const decltype(v)*)((const char*)p + at); }
+  __device__ __forceinline__ float operator[](int i) const {
+    T x;
+    if constexpr (E == 1) x = v;
+    else x = v[i];
+    if constexpr (DT == kF32) return x;
+    else return e_f<DT>(x);
+  }
+};
 
 // 8 consecutive parameters whose type is known at run time.
 __device__ __forceinline__ void load8_any(int dt, const void* p, long long i, float* x) {

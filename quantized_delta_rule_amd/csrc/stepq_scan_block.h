@@ -1,7 +1,6 @@
 // stepq_scan_block.h -- the scan in blocks of 16 tokens: the kernel of its forward pass, which the gradient runs for the
 // states that it needs, and the pieces that the gradient's own kernel shares with it.
 #pragma once
-#include <type_traits>
 #include <utility>
 
 #include "stepq_scan.h"
@@ -37,22 +36,6 @@ struct Segments {
   float* steps; // [segments, C]
   float* first; // [N, C, n]: the sequences' first states (S_out may be S_in)
   float* kept;  // states before every block of 16 tokens, as the kernel's lanes hold them (PASS 3)
-};
-
-// E neighbouring elements as they lie in memory: kept until they are used, so that their load is not waited for before.
-template <int DT, int E>
-struct Raw {
-  typedef typename std::conditional<DT == kF32, float, unsigned short>::type T;
-  typedef T V __attribute__((ext_vector_type(E)));
-  typename std::conditional<E == 1, T, V>::type v;
-  __device__ __forceinline__ void load(const char* p, unsigned at) { v = *(const decltype(v)*)(p + at); }
-  __device__ __forceinline__ float operator[](int i) const {
-    T x;
-    if constexpr (E == 1) x = v;
-    else x = v[i];
-    if constexpr (DT == kF32) return x;
-    else return e_f<DT>(x);
-  }
 };
 
 // Lane I of each 16 lanes' value, for all of them.
