@@ -15,8 +15,10 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from .layer import (any_dense, dense, device_of, dtype_code, need, no_graph, rows, sequences, slots_of, status_of,
-                    stream_of, torch_, workspace_of)
+                    stream_of, workspace_of)
 from .stepq import StepqError, _check, lib  # noqa: F401
 
 NONE, SILU = 0, 1
@@ -35,7 +37,7 @@ def _describe(x, weight, bias, out, out_name, activation, cu_seqlens, n_seqs, st
     T, C = x.shape
     dt = x.dtype
     code = dtype_code(dt)
-    if not isinstance(weight, torch_().Tensor) or weight.dim() != 2:
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a tensor [channels, width]")
     W = weight.shape[1]
     px, xs = rows(x, "x", dt, (T, C), dev)
@@ -55,10 +57,10 @@ def forward(x, weight, out, *, bias=None, activation=SILU, state_in=None, state_
     d, dev, px, po, pw, pb, n, _, C, W = _describe(x, weight, bias, out, "out", activation, cu_seqlens, n_seqs, status)
     sl, many = slots_of(slots, state_in, state_out, n, dev)
     shape = (many, W - 1, C)
-    si, so = dense(state_in, "state_in", x.dtype, shape, dev), dense(state_out, "state_out", x.dtype, shape, dev)
+    si = dense(state_in, "state_in", x.dtype, shape, dev)
+    so = si if state_out is state_in else dense(state_out, "state_out", x.dtype, shape, dev)
     no_graph("conv", x, weight, bias, state_in)
-    s = stream_of(stream, dev)
-    _check(lib().stepq_conv_forward(ctypes.byref(d), px, pw, pb, si, so, many if sl else 0, sl, po, s.cuda_stream),
+    _check(lib().stepq_conv_forward(ctypes.byref(d), px, pw, pb, si, so, many if sl else 0, sl, po, stream_of(stream, dev)),
            "conv_forward")
 
 
@@ -73,15 +75,14 @@ def backward(x, weight, d_out, dx, dweight, *, bias=None, dbias=None, activation
     """Gradient of forward(): from d_out and d_state_out (None = zero) into dx (packed), dweight, dbias and d_state_in
     (None = not wanted), all overwritten."""
     d, dev, px, po, pw, pb, n, T, C, W = _describe(x, weight, bias, d_out, "d_out", activation, cu_seqlens, n_seqs, status)
-    dt, f = x.dtype, torch_().float32
+    dt, f = x.dtype, torch.float32
     shape = (n, W - 1, C)
     si, ds1 = dense(state_in, "state_in", dt, shape, dev), dense(d_state_out, "d_state_out", dt, shape, dev)
     ds0 = dense(d_state_in, "d_state_in", dt, shape, dev)
     gx, gw = dense(dx, "dx", dt, (T, C), dev), dense(dweight, "dweight", f, (C, W), dev)
     gb = dense(dbias, "dbias", f, (C,), dev)
-    s = stream_of(stream, dev)
     p = ctypes.byref(d)
     ws, size, keep = workspace_of(workspace, need(lib().stepq_conv_backward_workspace, "conv_backward_workspace", p),
-                                  dev, s, stream is None)
-    _check(lib().stepq_conv_backward(p, px, pw, pb, si, po, ds1, gx, gw, gb, ds0, ws, size, s.cuda_stream),
+                                  dev, stream)
+    _check(lib().stepq_conv_backward(p, px, pw, pb, si, po, ds1, gx, gw, gb, ds0, ws, size, stream_of(stream, dev)),
            "conv_backward")

@@ -11,34 +11,21 @@ namespace {
 
 using namespace lay;
 
-// Sum over the TPR threads of a row; `mem` holds one value a wave where a row has several.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* mem) {
+// Sum (or maximum of values that are not negative) over the TPR threads of a row.  Where a row has several waves,
+// `mem` holds one value of each; the next use of the same `mem` has to lie behind another barrier.
+template <int TPR, bool MAX>
+__device__ __forceinline__ float over_row(float v, float* mem) {
 #pragma unroll
-  for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2) v += __shfl_xor(v, m);
-  if constexpr (TPR > 64) {
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) mem[wave] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int i = 0; i < TPR / 64; i++) v += mem[i];
+  for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2) {
+    const float o = __shfl_xor(v, m);
+    v = MAX ? fmaxf(v, o) : v + o;
   }
-  return v;
-}
-template <int TPR>
-__device__ __forceinline__ float row_max(float v, float* mem) {
-#pragma unroll
-  for (int m = 1; m < (TPR < 64 ? TPR : 64); m *= 2) v = fmaxf(v, __shfl_xor(v, m));
   if constexpr (TPR > 64) {
-    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) mem[threadIdx.x >> 6] = v;
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) mem[wave] = v;
-    __syncthreads();
-    v = 0;
+    v = mem[0];
 #pragma unroll
-    for (int i = 0; i < TPR / 64; i++) v = fmaxf(v, mem[i]);
+    for (int i = 1; i < TPR / 64; i++) v = MAX ? fmaxf(v, mem[i]) : v + mem[i];
   }
   return v;
 }
@@ -82,7 +69,7 @@ __device__ __forceinline__ void store_codes(int odt, void* out, long long i, con
 template <int DT, int TPR, int K>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormArgs A) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
-  __shared__ float mem[THREADS / 64];
+  __shared__ float mem[2][THREADS / 64];
   const int r = threadIdx.x % TPR;
   const long long i = (long long)blockIdx.x * ROWS + threadIdx.x / TPR;
   const bool live = i < A.R;  // one row a workgroup where waves meet: there every row is live
@@ -109,7 +96,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormArgs A) {
 #pragma unroll
     for (int j = 0; j < 8; j++) sq = fmaf(h[k][j], h[k][j], sq);
   }
-  const float rms = 1.0f / sqrtf(row_sum<TPR>(sq, mem) / (float)A.D + A.eps);
+  const float rms = 1.0f / sqrtf(over_row<TPR, false>(sq, mem[0]) / (float)A.D + A.eps);
   float top = 0;
 #pragma unroll
   for (int k = 0; k < K; k++) {
@@ -129,7 +116,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormArgs A) {
   }
   if (A.odtype == DT) return;
   const float most = A.odtype == kE4M3 ? 448.0f : 127.0f;
-  if (A.group == 0) top = row_max<TPR>(top, mem);
+  if (A.group == 0) top = over_row<TPR, true>(top, mem[1]);
 #pragma unroll
   for (int k = 0; k < K; k++) {
     const int c = (k * TPR + r) * 8;
@@ -146,11 +133,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormArgs A) {
   }
 }
 
-// Each workgroup takes every gridDim.x'th set of rows and adds up its part of dw on the way.
+// Each workgroup takes every gridDim.x'th set of rows and adds up its part of dw on the way; a set's rows are read while
+// the set before it is worked on.
 template <int DT, int TPR, int K>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
-  __shared__ float mem[THREADS / 64];
+  constexpr int size = DT == kF32 ? 4 : 2;
+  __shared__ float mem[2][THREADS / 64];
   __shared__ float part[TPR < 256 ? 4 : 1][TPR < 256 ? 512 : 1];
   const int r = threadIdx.x % TPR;
   float dw[K][8], w[K][8];
@@ -161,28 +150,42 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A)
     for (int j = 0; j < 8; j++) dw[k][j] = 0, w[k][j] = 1;
     if (A.w && c < A.D) load8_any(A.pdtype, A.w, c, w[k]);
   }
-  for (long long i0 = (long long)blockIdx.x * ROWS; i0 < A.R; i0 += (long long)gridDim.x * ROWS) {
-    const long long i = i0 + threadIdx.x / TPR;
-    const bool live = i < A.R;
-    const long long row = live ? i : A.R - 1;
-    const long long xo = at_row(A, row, A.xs), ro = at_row(A, row, A.rs), zo = at_row(A, row, A.zs);
-    const long long oo = at_row(A, row, A.os);
-    float h[K][8], p[K][8], z[K][8], sq = 0;
+  Raw<DT, 8> nx[K], nu[K], nz[K], nr[K];  // without gate or residual their loads repeat x's
+  const void *zp = A.z ? A.z : A.x, *rp = A.res ? A.res : A.x;
+  const long long zs = A.z ? A.zs : A.xs, rs = A.res ? A.rs : A.xs, last = A.D - 8;
+  auto fetch = [&](long long i) {
+    const long long row = i < A.R ? i : A.R - 1;
+    const long long xo = at_row(A, row, A.xs), uo = at_row(A, row, A.os), zo = at_row(A, row, zs), ro = at_row(A, row, rs);
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      const int c = (k * TPR + r) * 8;
-      if (c < A.D) {
-        load8<DT>(A.x, xo + c, h[k]);
-        load8<DT>(A.d_out, oo + c, p[k]);
-        if (A.z) load8<DT>(A.z, zo + c, z[k]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) h[k][j] = 0, p[k][j] = 0, z[k][j] = 0;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; j++) sq = fmaf(h[k][j], h[k][j], sq);
+      const long long c = (k * TPR + r) * 8, at = c < last ? c : last;
+      nx[k].load(A.x, (xo + at) * size);
+      nu[k].load(A.d_out, (uo + at) * size);
+      nz[k].load(zp, (zo + at) * size);
+      nr[k].load(rp, (ro + at) * size);
     }
-    const float rms = 1.0f / sqrtf(row_sum<TPR>(sq, mem) / (float)A.D + A.eps);
+  };
+  const long long step = (long long)gridDim.x * ROWS;
+  fetch((long long)blockIdx.x * ROWS + threadIdx.x / TPR);
+  for (long long i0 = (long long)blockIdx.x * ROWS; i0 < A.R; i0 += step) {
+    const long long row = i0 + threadIdx.x / TPR;
+    const bool live = row < A.R;
+    float h[K][8], p[K][8], sq = 0;
+    Raw<DT, 8> z[K], more[K];
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      const bool in = (k * TPR + r) * 8 < A.D;
+      z[k] = nz[k];
+      more[k] = nr[k];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        h[k][j] = in ? nx[k][j] : 0;
+        p[k][j] = in ? nu[k][j] : 0;
+        sq = fmaf(h[k][j], h[k][j], sq);
+      }
+    }
+    if (i0 + step < A.R) fetch(row + step);
+    const float rms = 1.0f / sqrtf(over_row<TPR, false>(sq, mem[0]) / (float)A.D + A.eps);
     float dot = 0;
 #pragma unroll
     for (int k = 0; k < K; k++) {
@@ -192,10 +195,10 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A)
       for (int j = 0; j < 8; j++) {
         h[k][j] *= rms;
         if (A.z) {
-          const float s = sigmoid(z[k][j]);
-          const float slope = A.gate == kSilu ? fmaf(z[k][j] * s, 1.0f - s, s) : s * (1.0f - s);
+          const float v = z[k][j], s = sigmoid(v);
+          const float slope = A.gate == kSilu ? fmaf(v * s, 1.0f - s, s) : s * (1.0f - s);
           dz[j] = p[k][j] * h[k][j] * w[k][j] * slope;
-          p[k][j] *= A.gate == kSilu ? z[k][j] * s : s;
+          p[k][j] *= A.gate == kSilu ? v * s : s;
         }
         if (live) dw[k][j] = fmaf(p[k][j], h[k][j], dw[k][j]);
         p[k][j] *= w[k][j];
@@ -203,17 +206,16 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A)
       }
       if (A.z && c < A.D && live) store8<DT>(A.dz, row * A.D + c, dz);
     }
-    const float mean = row_sum<TPR>(dot, mem) / (float)A.D;
+    const float mean = over_row<TPR, false>(dot, mem[1]) / (float)A.D;
 #pragma unroll
     for (int k = 0; k < K; k++) {
       const int c = (k * TPR + r) * 8;
       if (c >= A.D || !live) continue;
-      float g[8], more[8];
-      if (A.res) load8<DT>(A.res, ro + c, more);
+      float g[8];
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         g[j] = rms * fmaf(-h[k][j], mean, p[k][j]);
-        if (A.res) g[j] += more[j];
+        if (A.res) g[j] += more[k][j];
       }
       store8<DT>(A.dx, row * A.D + c, g);
     }

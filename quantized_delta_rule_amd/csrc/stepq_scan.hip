@@ -9,9 +9,11 @@ namespace {
 
 using namespace lay;
 
+constexpr int kTiles = 2;  // of 64 / LN channels, in a wave
+
 template <int DT, int LN>
 __global__ __launch_bounds__(256) void k_scan_tokens(ScanArgs A, int tiles) {
-  constexpr int GW = 64 / LN, n = 4 * LN;
+  constexpr int GW = 64 / LN, n = 4 * LN, K = kTiles;
   const int lane = threadIdx.x & 63;
   const long long unit = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const long long per = (long long)tiles * A.G;
@@ -22,37 +24,61 @@ __global__ __launch_bounds__(256) void k_scan_tokens(ScanArgs A, int tiles) {
   const int slot = seq_slot(A, s, valid, tg == 0 && lane == 0);
   if (slot < 0) return;
   if (t0 == t1 && (!A.S_out || A.S_out == A.S_in)) return;
-  const int cg = tile * GW + lane / LN, part = lane % LN;
-  const bool live = cg < A.Cg;
-  const int c = g * A.Cg + (live ? cg : A.Cg - 1);  // lanes past the group's end repeat its last channel
-  const long long so = ((long long)slot * A.C + c) * n + 4 * part;
-  f4 h = A.S_in ? *(const f4*)(A.S_in + so) : f4{0, 0, 0, 0};
-  f4 a2 = *(const f4*)(A.A + (long long)c * n + 4 * part);
+  const int part = lane % LN;
+  int c[K];
+  bool live[K];
+  f4 h[K], a2[K];
+  float skip[K], bias[K];
 #pragma unroll
-  for (int i = 0; i < 4; i++) a2[i] *= kLog2e;
-  const float skip = A.D ? A.D[c] : 0.0f, bias = A.bias ? A.bias[c] : 0.0f;
-  for (int t = t0; t < t1; t++) {
-    float x, raw, z, slope;
-    loadn<DT, 1>(A.x, t * A.xs + c, &x);
-    loadn<DT, 1>(A.dt, t * A.dts + c, &raw);
-    const f4 B = load4<DT>(A.B, t * A.bs + g * n + 4 * part), Cm = load4<DT>(A.Cm, t * A.cs + g * n + 4 * part);
-    const float D = step_of(A.softplus, raw + bias, slope), dx = D * x;
-    float y = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      h[i] = fmaf(decay(D, a2[i]), h[i], dx * B[i]);
-      y = fmaf(Cm[i], h[i], y);
-    }
-#pragma unroll
-    for (int m = 1; m < LN; m *= 2) y += __shfl_xor(y, m);
-    if (A.D) y = fmaf(skip, x, y);
-    if (A.z) {
-      loadn<DT, 1>(A.z, t * A.zs + c, &z);
-      y *= z * sigmoid(z);
-    }
-    if (live && part == 0) storen<DT, 1>(A.out, t * A.os + c, &y);
+  for (int k = 0; k < K; k++) {
+    const int cg = (tile * K + k) * GW + lane / LN;
+    live[k] = cg < A.Cg;
+    c[k] = g * A.Cg + (live[k] ? cg : A.Cg - 1);  // lanes past the group's end repeat its last channel
+    const long long so = ((long long)slot * A.C + c[k]) * n + 4 * part;
+    h[k] = A.S_in ? *(const f4*)(A.S_in + so) : f4{0, 0, 0, 0};
+    a2[k] = *(const f4*)(A.A + (long long)c[k] * n + 4 * part);
+    skip[k] = A.D ? A.D[c[k]] : 0.0f;
+    bias[k] = A.bias ? A.bias[c[k]] : 0.0f;
   }
-  if (A.S_out && live) *(f4*)(A.S_out + so) = h;
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) a2[k][i] *= kLog2e;
+  }
+  const void* zp = A.z ? A.z : A.x;  // without a gate its loads repeat x's
+  const long long zs = A.z ? A.zs : A.xs;
+  for (int t = t0; t < t1; t++) {
+    Raw<DT, 1> rx[K], rd[K], rz[K];
+    constexpr int size = DT == kF32 ? 4 : 2;
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      rx[k].load(A.x, (t * A.xs + c[k]) * size);
+      rd[k].load(A.dt, (t * A.dts + c[k]) * size);
+      rz[k].load(zp, (t * zs + c[k]) * size);
+    }
+    const f4 B = load4<DT>(A.B, t * A.bs + g * n + 4 * part), Cm = load4<DT>(A.Cm, t * A.cs + g * n + 4 * part);
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+      float slope, x = rx[k][0], z = rz[k][0];
+      const float D = step_of(A.softplus, rd[k][0] + bias[k], slope), dx = D * x;
+      float y = 0;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        h[k][i] = fmaf(decay(D, a2[k][i]), h[k][i], dx * B[i]);
+        y = fmaf(Cm[i], h[k][i], y);
+      }
+#pragma unroll
+      for (int m = 1; m < LN; m *= 2) y += __shfl_xor(y, m);
+      if (A.D) y = fmaf(skip[k], x, y);
+      if (A.z) y *= z * sigmoid(z);
+      if (live[k] && part == 0) storen<DT, 1>(A.out, t * A.os + c[k], &y);
+    }
+  }
+  if (!A.S_out) return;
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+    if (live[k]) *(f4*)(A.S_out + ((long long)slot * A.C + c[k]) * n + 4 * part) = h[k];
+  }
 }
 
 // Blocks pay from 16 tokens a sequence on.
@@ -60,7 +86,7 @@ bool in_blocks(const ScanArgs& a) { return a.N > 0 && (long long)a.T >= 16LL * a
 
 template <int DT, int LN>
 hipError_t tokens(const ScanArgs& a, hipStream_t s) {
-  const int tiles = (a.Cg + 64 / LN - 1) / (64 / LN);
+  const int wide = kTiles * 64 / LN, tiles = (a.Cg + wide - 1) / wide;
   const long long units = (long long)tiles * a.G * a.N;
   hipLaunchKernelGGL((k_scan_tokens<DT, LN>), dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s, a, tiles);
   return hipGetLastError();

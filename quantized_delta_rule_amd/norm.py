@@ -16,7 +16,9 @@ from __future__ import annotations
 
 import ctypes
 
-from .layer import (any_dense, dense, device_of, dtype_code, need, no_graph, rows, stream_of, torch_, workspace_of)
+import torch
+
+from .layer import (any_dense, dense, device_of, dtype_code, need, no_graph, rows, stream_of, workspace_of)
 from .stepq import StepqError, _check, lib  # noqa: F401
 
 SILU, SIGMOID = 1, 2
@@ -46,7 +48,6 @@ def forward(x, weight, out, *, eps=1e-6, residual=None, residual_out=None, z=Non
     weight None: ones.  gate: what z goes through, SILU or SIGMOID.  8-bit out: scale = max |y| / 448 (e4m3) or
     / 127 (int8) of a row or of every `group` columns, out = y / scale to the nearest.  out may be x, residual_out may
     be residual or x (in place)."""
-    torch = torch_()
     dev, shape, R, H, d = _shape(x)
     t = x.dtype
     code = dtype_code(t)
@@ -77,7 +78,7 @@ def forward(x, weight, out, *, eps=1e-6, residual=None, residual_out=None, z=Non
     ps = dense(scale, "scale", torch.float32, shape[:-1] + ((d // group,) if group else ()), dev)
     no_graph("norm", x, weight, residual, z)
     desc = _NormDesc(code, pcode, ocode, R, H, d, int(gate), group, eps, dev, xs, rs, zs, os_)
-    _check(lib().stepq_norm_forward(ctypes.byref(desc), px, pw, pr, pz, po, ps, ph, stream_of(stream, dev).cuda_stream),
+    _check(lib().stepq_norm_forward(ctypes.byref(desc), px, pw, pr, pz, po, ps, ph, stream_of(stream, dev)),
            "norm_forward")
 
 
@@ -111,8 +112,8 @@ def backward(h, weight, d_out, dx, dweight=None, *, eps=1e-6, z=None, dz=None, g
     if (z is None) != (dz is None):
         raise ValueError("dz goes with z")
     gx, gz = dense(dx, "dx", h.dtype, shape, dev), dense(dz, "dz", h.dtype, shape, dev)
-    gw = dense(dweight, "dweight", torch_().float32, (shape[-1],), dev)
-    s, d = stream_of(stream, dev), ctypes.byref(desc)
+    gw = dense(dweight, "dweight", torch.float32, (shape[-1],), dev)
+    d = ctypes.byref(desc)
     ws, size, keep = workspace_of(workspace, need(lib().stepq_norm_backward_workspace, "norm_backward_workspace", d), dev,
-                                  s, stream is None)
-    _check(lib().stepq_norm_backward(d, *p, gx, gw, gz, ws, size, s.cuda_stream), "norm_backward")
+                                  stream)
+    _check(lib().stepq_norm_backward(d, *p, gx, gw, gz, ws, size, stream_of(stream, dev)), "norm_backward")

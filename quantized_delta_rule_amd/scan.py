@@ -15,8 +15,10 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from .layer import (dense, device_of, dtype_code, need, no_graph, rows, sequences, slots_of, status_of, stream_of,
-                    torch_, workspace_of)
+                    workspace_of)
 from .stepq import StepqError, _check, lib  # noqa: F401
 
 
@@ -35,10 +37,10 @@ class _Call:
     def __init__(self, x, dt, A, B, C, out, out_name, D, dt_bias, softplus, z, cu_seqlens, n_seqs, status):
         self.dev = dev = device_of(x, "x", (2,))
         T, ch = x.shape
-        if not isinstance(B, torch_().Tensor) or B.dim() != 3:
+        if not isinstance(B, torch.Tensor) or B.dim() != 3:
             raise ValueError("B must be a tensor [tokens, groups, states]")
         G, n = B.shape[1], B.shape[2]
-        t, f = x.dtype, torch_().float32
+        t, f = x.dtype, torch.float32
         code = dtype_code(t)
         self.T, self.ch, self.G, self.n, self.dtype = T, ch, G, n, t
         px, xs = rows(x, "x", t, (T, ch), dev)
@@ -57,7 +59,7 @@ class _Call:
         self.ptr = ctypes.byref(self.desc)
 
     def state(self, S, name, many=None):
-        return dense(S, name, torch_().float32, (self.N if many is None else many, self.ch, self.n), self.dev)
+        return dense(S, name, torch.float32, (self.N if many is None else many, self.ch, self.n), self.dev)
 
 
 def forward_workspace(x, dt, A, B, C, out, *, D=None, dt_bias=None, softplus=True, z=None, cu_seqlens=None, n_seqs=None):
@@ -82,12 +84,12 @@ def forward(x, dt, A, B, C, out, *, D=None, dt_bias=None, softplus=True, z=None,
     status as for delta.forward."""
     a = _Call(x, dt, A, B, C, out, "out", D, dt_bias, softplus, z, cu_seqlens, n_seqs, status)
     sl, many = slots_of(slots, state_in, state_out, a.N, a.dev)
-    si, so = a.state(state_in, "state_in", many), a.state(state_out, "state_out", many)
+    si = a.state(state_in, "state_in", many)
+    so = si if state_out is state_in else a.state(state_out, "state_out", many)
     no_graph("scan", x, dt, A, B, C, D, dt_bias, z, state_in)
-    s = stream_of(stream, a.dev)
     ws, size, keep = workspace_of(workspace, need(lib().stepq_scan_forward_workspace, "scan_forward_workspace", a.ptr),
-                                  a.dev, s, stream is None)
-    _check(lib().stepq_scan_forward(a.ptr, *a.inputs, si, so, many if sl else 0, sl, a.out, ws, size, s.cuda_stream),
+                                  a.dev, stream)
+    _check(lib().stepq_scan_forward(a.ptr, *a.inputs, si, so, many if sl else 0, sl, a.out, ws, size, stream_of(stream, a.dev)),
            "scan_forward")
 
 
@@ -97,7 +99,7 @@ def backward(x, dt, A, B, C, d_out, dx, ddt, dA, dB, dC, *, D=None, dD=None, dt_
     """Gradient of forward(): from d_out and d_state_out (None = zero) into dx, ddt, dz [tokens, channels], dB, dC
     (packed), dA, dD, ddt_bias and d_state_in (None = not wanted), all overwritten."""
     a = _Call(x, dt, A, B, C, d_out, "d_out", D, dt_bias, softplus, z, cu_seqlens, n_seqs, status)
-    f, dev, t = torch_().float32, a.dev, a.dtype
+    f, dev, t = torch.float32, a.dev, a.dtype
     for v, name in ((dx, "dx"), (ddt, "ddt"), (dA, "dA"), (dB, "dB"), (dC, "dC")):
         if v is None:
             raise TypeError(f"{name} must be a torch tensor")
@@ -109,7 +111,6 @@ def backward(x, dt, A, B, C, d_out, dx, ddt, dA, dB, dC, *, D=None, dD=None, dt_
            dense(ddt_bias, "ddt_bias", f, (a.ch,), dev), dense(dz, "dz", t, wide, dev),
            a.state(d_state_in, "d_state_in"))
     si, ds1 = a.state(state_in, "state_in"), a.state(d_state_out, "d_state_out")
-    s = stream_of(stream, dev)
     ws, size, keep = workspace_of(workspace, need(lib().stepq_scan_backward_workspace, "scan_backward_workspace", a.ptr),
-                                  dev, s, stream is None)
-    _check(lib().stepq_scan_backward(a.ptr, *a.inputs, si, a.out, ds1, *got, ws, size, s.cuda_stream), "scan_backward")
+                                  dev, stream)
+    _check(lib().stepq_scan_backward(a.ptr, *a.inputs, si, a.out, ds1, *got, ws, size, stream_of(stream, a.dev)), "scan_backward")
