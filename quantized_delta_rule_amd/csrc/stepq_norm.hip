@@ -139,16 +139,23 @@ template <int DT, int TPR, int K>
 __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
   constexpr int size = DT == kF32 ? 4 : 2;
+  // long rows: neither the next row nor the weights fit into registers beside a row
+  constexpr bool AHEAD = K <= 2 && TPR <= 256;
   __shared__ float mem[2][THREADS / 64];
   __shared__ float part[TPR < 256 ? 4 : 1][TPR < 256 ? 512 : 1];
   const int r = threadIdx.x % TPR;
-  float dw[K][8], w[K][8];
-#pragma unroll
-  for (int k = 0; k < K; k++) {
+  float dw[K][8], kept[AHEAD ? K : 1][8];
+  auto weight = [&](int k, float* w) {
     const int c = (k * TPR + r) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; j++) dw[k][j] = 0, w[k][j] = 1;
-    if (A.w && c < A.D) load8_any(A.pdtype, A.w, c, w[k]);
+    for (int j = 0; j < 8; j++) w[j] = 1;
+    if (A.w && c < A.D) load8_any(A.pdtype, A.w, c, w);
+  };
+#pragma unroll
+  for (int k = 0; k < K; k++) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) dw[k][j] = 0;
+    if (AHEAD) weight(k, kept[k]);
   }
   Raw<DT, 8> nx[K], nu[K], nz[K], nr[K];  // without gate or residual their loads repeat x's
   const void *zp = A.z ? A.z : A.x, *rp = A.res ? A.res : A.x;
@@ -166,10 +173,11 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A)
     }
   };
   const long long step = (long long)gridDim.x * ROWS;
-  fetch((long long)blockIdx.x * ROWS + threadIdx.x / TPR);
+  if (AHEAD) fetch((long long)blockIdx.x * ROWS + threadIdx.x / TPR);
   for (long long i0 = (long long)blockIdx.x * ROWS; i0 < A.R; i0 += step) {
     const long long row = i0 + threadIdx.x / TPR;
     const bool live = row < A.R;
+    if (!AHEAD) fetch(row);
     float h[K][8], p[K][8], sq = 0;
     Raw<DT, 8> z[K], more[K];
 #pragma unroll
@@ -184,24 +192,30 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A)
         sq = fmaf(h[k][j], h[k][j], sq);
       }
     }
-    if (i0 + step < A.R) fetch(row + step);
+    if (AHEAD && i0 + step < A.R) fetch(row + step);
     const float rms = 1.0f / sqrtf(over_row<TPR, false>(sq, mem[0]) / (float)A.D + A.eps);
     float dot = 0;
 #pragma unroll
     for (int k = 0; k < K; k++) {
       const int c = (k * TPR + r) * 8;
-      float dz[8];
+      float dz[8], w[8];
+      if (AHEAD) {
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[j] = kept[k][j];
+      } else {
+        weight(k, w);
+      }
 #pragma unroll
       for (int j = 0; j < 8; j++) {
         h[k][j] *= rms;
         if (A.z) {
           const float v = z[k][j], s = sigmoid(v);
           const float slope = A.gate == kSilu ? fmaf(v * s, 1.0f - s, s) : s * (1.0f - s);
-          dz[j] = p[k][j] * h[k][j] * w[k][j] * slope;
+          dz[j] = p[k][j] * h[k][j] * w[j] * slope;
           p[k][j] *= A.gate == kSilu ? v * s : s;
         }
         if (live) dw[k][j] = fmaf(p[k][j], h[k][j], dw[k][j]);
-        p[k][j] *= w[k][j];
+        p[k][j] *= w[j];
         dot = fmaf(p[k][j], h[k][j], dot);
       }
       if (A.z && c < A.D && live) store8<DT>(A.dz, row * A.D + c, dz);
@@ -244,10 +258,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A)
   }
 }
 
-// Workgroups of the gradient: enough to fill 256 CUs twice.
+// Workgroups of the gradient: four a CU where a workgroup's rows are short, two where they fill its registers and
+// each adds a longer row of partial sums (us of 512 and 1,024 workgroups: 8,192 rows of 2,048 35 and 29, 262,144
+// of 128 50 and 41; 8,192 of 4,096 45 and 49, 4,096 of 8,192 47 and 54).
+constexpr long long kGroups = 1024;
 long long grad_groups(const NormArgs& a, int rows) {
-  const long long sets = (a.R + rows - 1) / rows;
-  return sets < 512 ? sets : 512;
+  const long long sets = (a.R + rows - 1) / rows, most = a.D <= 2048 ? kGroups : kGroups / 2;
+  return sets < most ? sets : most;
 }
 
 template <int DT, int TPR, int K>
@@ -275,7 +292,7 @@ hipError_t by_size(const NormArgs& a, bool back, hipStream_t s) {
   if (D <= 2048) return launch<DT, 256, 1>(a, back, s);
   if (D <= 4096) return launch<DT, 256, 2>(a, back, s);
   if (D <= 8192) return launch<DT, 256, 4>(a, back, s);
-  if (D <= 16384) return launch<DT, 1024, 2>(a, back, s);
+  if (D <= 16384) return back ? launch<DT, 512, 4>(a, true, s) : launch<DT, 1024, 2>(a, false, s);
   return launch<DT, 1024, 4>(a, back, s);
 }
 
@@ -288,7 +305,7 @@ hipError_t by_type(const NormArgs& a, bool back, hipStream_t s) {
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) { return a.R <= 0 ? hipSuccess : by_type(a, false, s); }
 
-size_t norm_backward_bytes(const NormArgs& a) { return a.R > 0 ? (size_t)512 * a.D * sizeof(float) : 0; }
+size_t norm_backward_bytes(const NormArgs& a) { return a.R > 0 ? (size_t)kGroups * a.D * sizeof(float) : 0; }
 
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
   if (a.R > 0) return by_type(a, true, s);
