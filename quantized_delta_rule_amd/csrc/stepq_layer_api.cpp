@@ -56,6 +56,13 @@ int all_aligned(const void* const* p, const char* const* names, int n, unsigned 
   return STEPQ_OK;
 }
 
+// Outputs that other workgroups would overwrite while an input at the same place is still read.
+int apart(const void* out, const char* what, const void* const* in, const char* const* names, int n) {
+  for (int i = 0; i < n; i++)
+    if (out && out == in[i]) return fail(STEPQ_ERR_INVALID_ARG, "%s must not overlap %s", what, names[i]);
+  return STEPQ_OK;
+}
+
 #define STEPQ_TRY(call) \
   if (int rc_ = (call)) return rc_
 
@@ -220,6 +227,7 @@ int stepq_conv_forward(const stepq_conv_desc* desc, const void* x, const void* w
   STEPQ_TRY(pointers(a.T > 0 && a.N > 0, p, names, 2));
   STEPQ_TRY(pointers(a.N > 0, p + 2, names + 2, 1));
   STEPQ_TRY(all_aligned(p, names, 6, 16));
+  STEPQ_TRY(apart(a.T > 0 ? out : nullptr, "out", p, names, 1));
   if (slots && n_slots < 1) return fail(STEPQ_ERR_INVALID_ARG, "n_slots must be >= 1");
   STEPQ_ON_DEVICE(desc->device);
   a.x = x;
@@ -248,6 +256,8 @@ int stepq_conv_backward(const stepq_conv_desc* desc, const void* x, const void* 
   STEPQ_TRY(pointers(a.N > 0, p + 3, names + 3, 1));
   STEPQ_TRY(pointers(true, p + 4, names + 4, 1));
   STEPQ_TRY(all_aligned(p, names, 9, 16));
+  STEPQ_TRY(apart(a.T > 0 ? dx : nullptr, "dx", p, names, 2));
+  STEPQ_TRY(apart(dS_in, "dS_in", p + 6, names + 6, 2));
   STEPQ_TRY(aligned(dbias, 4, "dbias"));
   STEPQ_TRY(seq_workspace(workspace, workspace_bytes, conv_backward_bytes(a)));
   STEPQ_ON_DEVICE(desc->device);
@@ -281,6 +291,9 @@ int stepq_scan_forward(const stepq_scan_desc* desc, const void* x, const void* d
   STEPQ_TRY(scan_args(desc, &a));
   STEPQ_TRY(scan_inputs(&a, x, dt, A, B, C, D, dt_bias, z, S_in, out));
   STEPQ_TRY(aligned(S_out, 16, "S_out"));
+  const void* in[] = {x, dt, z};
+  const char* in_names[] = {"x", "dt", "z"};
+  STEPQ_TRY(apart(a.T > 0 ? out : nullptr, "out", in, in_names, 3));
   if (slots && n_slots < 1) return fail(STEPQ_ERR_INVALID_ARG, "n_slots must be >= 1");
   STEPQ_TRY(seq_workspace(workspace, workspace_bytes, scan_forward_bytes(a)));
   STEPQ_ON_DEVICE(desc->device);
@@ -306,6 +319,17 @@ int stepq_scan_backward(const stepq_scan_desc* desc, const void* x, const void* 
   STEPQ_TRY(pointers(true, p + 4, names + 4, 1));
   STEPQ_TRY(pointers(z && a.T > 0 && a.N > 0, p + 5, names + 5, 1));
   STEPQ_TRY(all_aligned(p, names, 8, 16));
+  const void* in[] = {x, dt, z, d_out};
+  const char* in_names[] = {"x", "dt", "z", "d_out"};
+  const void* out[] = {dx, ddt, dz};
+  const char* out_names[] = {"dx", "ddt", "dz"};
+  for (int i = 0; i < 3 && a.T > 0; i++) {
+    STEPQ_TRY(apart(out[i], out_names[i], in, in_names, 4));
+    STEPQ_TRY(apart(out[i], out_names[i], out, out_names, i));
+  }
+  const void* st[] = {dS_out, S_in};
+  const char* st_names[] = {"dS_out", "S_in"};
+  STEPQ_TRY(apart(dS_in, "dS_in", st, st_names, 2));
   STEPQ_TRY(aligned(dD, 4, "dD"));
   STEPQ_TRY(aligned(ddt_bias, 4, "ddt_bias"));
   STEPQ_TRY(seq_workspace(workspace, workspace_bytes, scan_backward_bytes(a)));

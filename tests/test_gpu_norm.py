@@ -182,6 +182,17 @@ def test_strided_rows(norm):
     assert torch.equal(da, db) and torch.equal(wa, wb)
 
 
+def test_strided_eight_bits(norm):
+    """Codes into a part of wider rows (strides of eight)."""
+    x = torch.randn(21, 264).to(BF16).cuda()
+    a, b = torch.zeros(21, 600, dtype=torch.int8).cuda(), torch.empty(21, 264, dtype=torch.int8).cuda()
+    sa, sb = torch.empty(21).cuda(), torch.empty(21).cuda()
+    norm.forward(x, None, a[:, 8:272], scale=sa)
+    norm.forward(x, None, b, scale=sb)
+    assert torch.equal(a[:, 8:272], b) and torch.equal(sa, sb)
+    assert int(a[:, :8].abs().max()) == 0 and int(a[:, 272:].abs().max()) == 0
+
+
 def test_non_finite_rows_keep_to_themselves(norm):
     x = inputs(51, (6, 640), F32)
     x["x"][1, 3], x["x"][3, 7] = float("nan"), float("inf")

@@ -10,6 +10,7 @@ torch = pytest.importorskip("torch")
 INVALID, UNSUPPORTED = -1, -2
 V = ctypes.c_void_p
 AT = 4096  # an aligned address that nothing may read
+MANY = [ctypes.c_void_p(AT * (i + 1)) for i in range(32)]  # .. and others, no two the same
 
 
 @pytest.fixture(scope="module")
@@ -50,17 +51,17 @@ def refused(L, rc, code, text):
 def conv_calls(L, d):
     """Every call of the convolution with this description, all pointers good."""
     n = ctypes.c_size_t()
-    p, q = ctypes.byref(d), V(AT)
-    return [L.stepq_conv_forward(p, q, q, q, q, q, 0, None, q, None), L.stepq_conv_backward_workspace(p, ctypes.byref(n)),
-            L.stepq_conv_backward(p, *[q] * 11, 1 << 40, None)]
+    p, q = ctypes.byref(d), MANY
+    return [L.stepq_conv_forward(p, *q[:5], 0, None, q[5], None), L.stepq_conv_backward_workspace(p, ctypes.byref(n)),
+            L.stepq_conv_backward(p, *q[:11], 1 << 40, None)]
 
 
 def scan_calls(L, d):
     n = ctypes.c_size_t()
-    p, q = ctypes.byref(d), V(AT)
+    p, q = ctypes.byref(d), MANY
     return [L.stepq_scan_forward_workspace(p, ctypes.byref(n)), L.stepq_scan_backward_workspace(p, ctypes.byref(n)),
-            L.stepq_scan_forward(p, *[q] * 10, 0, None, q, q, 1 << 40, None),
-            L.stepq_scan_backward(p, *[q] * 21, 1 << 40, None)]
+            L.stepq_scan_forward(p, *q[:10], 0, None, q[10], q[11], 1 << 40, None),
+            L.stepq_scan_backward(p, *q[:21], 1 << 40, None)]
 
 
 def norm_calls(L, d):
@@ -134,11 +135,11 @@ def test_norm_eight_bits(L):
 def _pointers(L, call, names, needed, loose=()):
     """NULL (where it is needed) and misaligned pointers, one at a time."""
     for i, name in enumerate(names):
-        args = [V(AT)] * len(names)
+        args = MANY[:len(names)]
         if name in needed:
             args[i] = None
             refused(L, call(args), INVALID, f"{name} must be non-NULL")
-        args[i] = V(AT + 2)
+        args[i] = V(AT * 40 + 2)
         refused(L, call(args), INVALID, f"{name} must be {4 if name in loose else 16}-byte aligned")
 
 
@@ -173,13 +174,37 @@ def test_workspaces_slots_and_missing_pieces(L):
                   (L.stepq_scan_backward_workspace, s), (L.stepq_norm_backward_workspace, m)):
         refused(L, fn(d, None), INVALID, "bytes is NULL")
         assert fn(d, ctypes.byref(n)) == 0
-    refused(L, L.stepq_conv_forward(c, q, q, q, q, q, 0, q, q, None), INVALID, "n_slots must be >= 1")
-    refused(L, L.stepq_scan_forward(s, *[q] * 10, 0, q, q, q, 1 << 40, None), INVALID, "n_slots must be >= 1")
-    for call in (lambda w, b: L.stepq_conv_backward(c, *[q] * 10, w, b, None), lambda w, b: L.stepq_scan_backward(s, *[q] * 20, w, b, None),
-                 lambda w, b: L.stepq_norm_backward(m, *[q] * 8, w, b, None)):
+    refused(L, L.stepq_conv_forward(c, *MANY[:5], 0, q, MANY[6], None), INVALID, "n_slots must be >= 1")
+    refused(L, L.stepq_scan_forward(s, *MANY[:10], 0, q, *MANY[11:13], 1 << 40, None), INVALID, "n_slots must be >= 1")
+    for call in (lambda w, b: L.stepq_conv_backward(c, *MANY[:10], w, b, None),
+                 lambda w, b: L.stepq_scan_backward(s, *MANY[:20], w, b, None),
+                 lambda w, b: L.stepq_norm_backward(m, *MANY[:8], w, b, None)):
         refused(L, call(q, 16), INVALID, "workspace of 16 bytes")
         refused(L, call(None, 1 << 40), INVALID, "workspace is NULL")
         refused(L, call(V(AT + 128), 1 << 40), INVALID, "workspace must be 256-byte aligned")
+
+
+def test_outputs_in_the_place_of_inputs(L):
+    c, s = ctypes.byref(conv_desc()), ctypes.byref(scan_desc())
+
+    def same(a, b, n):
+        p = list(MANY[:n])
+        p[b] = p[a]
+        return p
+    p = same(0, 5, 6)
+    refused(L, L.stepq_conv_forward(c, *p[:5], 0, None, p[5], None), INVALID, "out must not overlap x")
+    names = ["x", "weight", "bias", "S_in", "d_out", "dS_out", "dx", "dweight", "dbias", "dS_in"]
+    for a, b in (("x", "dx"), ("d_out", "dx"), ("S_in", "dS_in"), ("dS_out", "dS_in")):
+        p = same(names.index(a), names.index(b), 11)
+        refused(L, L.stepq_conv_backward(c, *p, 1 << 40, None), INVALID, f"{b} must not overlap {a}")
+    for a, name in ((0, "x"), (1, "dt"), (7, "z")):
+        p = same(a, 10, 12)
+        refused(L, L.stepq_scan_forward(s, *p[:10], 0, None, *p[10:], 1 << 40, None), INVALID, f"out must not overlap {name}")
+    names = ["x", "dt", "A", "B", "C", "D", "dt_bias", "z", "S_in", "d_out", "dS_out", "dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias",
+             "dz", "dS_in"]
+    for a, b in (("x", "dx"), ("d_out", "ddt"), ("z", "dz"), ("dx", "dz"), ("dt", "ddt"), ("S_in", "dS_in"), ("dS_out", "dS_in")):
+        p = same(names.index(a), names.index(b), 21)
+        refused(L, L.stepq_scan_backward(s, *p, 1 << 40, None), INVALID, f"{b} must not overlap {a}")
 
 
 def test_good_calls_fail_only_at_the_device(L):
