@@ -59,8 +59,8 @@ __global__ __launch_bounds__(256) void k_scan_tokens(ScanArgs A, int tiles) {
     const f4 B = load4<DT>(A.B, t * A.bs + g * n + 4 * part), Cm = load4<DT>(A.Cm, t * A.cs + g * n + 4 * part);
 #pragma unroll
     for (int k = 0; k < K; k++) {
-      float slope, x = rx[k][0], z = rz[k][0];
-      const float D = step_of(A.softplus, rd[k][0] + bias[k], slope), dx = D * x;
+      const float x = rx[k][0], z = rz[k][0];
+      const float D = step_of(A.softplus, rd[k][0] + bias[k]), dx = D * x;
       float y = 0;
 #pragma unroll
       for (int i = 0; i < 4; i++) {

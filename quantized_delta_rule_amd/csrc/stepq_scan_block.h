@@ -211,16 +211,29 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   const int sub = (lane & 15) / V, val = lane % V;  // this lane's token of PT, its value
   const unsigned vs = (unsigned)(val < NS ? A.bs : A.cs) * size;
   const char* vp = (const char*)(val < NS ? A.B : A.Cm) + row0 * vs + (long long)(g * n + part * NS + val % NS) * size;
+  // offsets from a block's first row, as they are where the block is whole
+  const unsigned ox = tok * ax + co * size, od = tok * ad + co * size, oz = tok * az + co * size;
+  unsigned ov[R];
+#pragma unroll
+  for (int i = 0; i < R; i++) ov[i] = (i * PT + sub) * vs;
   auto fetch = [&](int k) {  // blocks in order: the addresses move on
     const int most = count - k * kBlock - 1;  // the last token of the block, at most
-    const unsigned t = tok < most ? tok : most;
-    rx.load(xp, t * ax + co * size);
-    rd.load(dp, t * ad + co * size);
-    if (OUT) rz.load(zq, t * az + co * size);
+    if (most >= kBlock - 1) {
+      rx.load(xp + ox);
+      rd.load(dp + od);
+      if (OUT) rz.load(zq + oz);
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-      const unsigned t = i * PT + sub < most ? i * PT + sub : most;
-      rv[i].load(vp + (unsigned long long)t * vs, 0);
+      for (int i = 0; i < R; i++) rv[i].load(vp + ov[i]);
+    } else {
+      const unsigned t = tok < most ? tok : most;
+      rx.load(xp + (t * ax + co * size));
+      rd.load(dp + (t * ad + co * size));
+      if (OUT) rz.load(zq + (t * az + co * size));
+#pragma unroll
+      for (int i = 0; i < R; i++) {
+        const unsigned t = i * PT + sub < most ? i * PT + sub : most;
+        rv[i].load(vp + t * vs);
+      }
     }
     xp += (long long)ax * kBlock;
     dp += (long long)ad * kBlock;
@@ -228,12 +241,12 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
     vp += (long long)vs * kBlock;
   };
   auto prepare = [&](int k) {
-    float D[E], slope;
+    float D[E];
 #pragma unroll
     for (int i = 0; i < E; i++) D[i] = rd[i] + bias[i];
     if (A.softplus) {
 #pragma unroll
-      for (int i = 0; i < E; i++) D[i] = step_of(1, D[i], slope);
+      for (int i = 0; i < E; i++) D[i] = step_of(1, D[i]);
     }
 #pragma unroll
     for (int i = 0; i < E; i++) {

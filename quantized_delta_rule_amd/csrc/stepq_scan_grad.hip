@@ -206,19 +206,34 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
   const int sub = (lane & 15) / V, val = lane % V;  // this lane's token of PT, its value
   const unsigned vs = (unsigned)(val < NS ? A.bs : A.cs) * size;
   const char* vp = (const char*)(val < NS ? A.B : A.Cm) + (long long)(g * n + part * NS + val % NS) * size;
+  // offsets from a block's first row, as they are where the block is whole
+  const unsigned ox = tok * ax + co * size, od = tok * ad + co * size, oz = tok * az + co * size, ou = tok * au + co * size;
+  unsigned ov[R];
+#pragma unroll
+  for (int i = 0; i < R; i++) ov[i] = (i * PT + sub) * vs;
   auto fetch = [&](int k) {
     const int most = count - k * kBlock - 1;
-    const unsigned t = tok < most ? tok : most;
     const long long row = W.row0 + (long long)k * kBlock;
-    rx.load((const char*)A.x + row * ax, t * ax + co * size);
-    rd.load((const char*)A.dt + row * ad, t * ad + co * size);
-    rz.load((const char*)zp + row * az, t * az + co * size);
-    ru.load((const char*)A.d_out + row * au, t * au + co * size);
-    const char* v = vp + row * vs;
+    const char *xp = (const char*)A.x + row * ax, *dp = (const char*)A.dt + row * ad, *zq = (const char*)zp + row * az;
+    const char *up = (const char*)A.d_out + row * au, *v = vp + row * vs;
+    if (most >= kBlock - 1) {
+      rx.load(xp + ox);
+      rd.load(dp + od);
+      rz.load(zq + oz);
+      ru.load(up + ou);
 #pragma unroll
-    for (int i = 0; i < R; i++) {
-      const unsigned t = i * PT + sub < most ? i * PT + sub : most;
-      rv[i].load(v + (unsigned long long)t * vs, 0);
+      for (int i = 0; i < R; i++) rv[i].load(v + ov[i]);
+    } else {
+      const unsigned t = tok < most ? tok : most;
+      rx.load(xp + (t * ax + co * size));
+      rd.load(dp + (t * ad + co * size));
+      rz.load(zq + (t * az + co * size));
+      ru.load(up + (t * au + co * size));
+#pragma unroll
+      for (int i = 0; i < R; i++) {
+        const unsigned t = i * PT + sub < most ? i * PT + sub : most;
+        rv[i].load(v + t * vs);
+      }
     }
     if (OUT) get_states<NS>(Q.kept + ((kept0 + k) * per + tg) * (64 * NW * NS) + threadIdx.x * NS, hk);
   };
@@ -269,7 +284,8 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
       for (int i = 0; i < E; i++) gA[i] += m[i];
     }
     if (t < count && mine) {
-      const long long o = (W.row0 + t) * A.C + co;
+      const long long base = (W.row0 + (long long)k * kBlock) * A.C * size;
+      const unsigned o = (unsigned)(tok * A.C + co) * size;
 #pragma unroll
       for (int i = 0; i < E; i++) {
         dx[i] = fmaf(D0[i], gB[i], skip[i] * e0[i]);
@@ -277,14 +293,14 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
         dD[i] = fmaf(e0[i], x0[i], dD[i]);
         dbias[i] += ddt[i];
       }
-      storev<DT, E>(A.dx, o, dx);
-      storev<DT, E>(A.ddt, o, ddt);
+      storev<DT, E>((char*)A.dx + base + o, 0, dx);
+      storev<DT, E>((char*)A.ddt + base + o, 0, ddt);
       if (A.z) {
 #pragma unroll
         for (int i = 0; i < E; i++) {
           dz[i] = u0[i] * fmaf(skip[i], x0[i], y[i]) * fmaf(z0[i] * s0[i], 1.0f - s0[i], s0[i]);
         }
-        storev<DT, E>(A.dz, o, dz);
+        storev<DT, E>((char*)A.dz + base + o, 0, dz);
       }
     }
     // dB and dC of this tile: a thread adds up one value of one part for every eighth token
