@@ -58,6 +58,7 @@ struct ScanArgs {
   float* S_out;
   void* out;
   char* ws;
+  int split;                // not 0: sequences of fewer tokens go token by token, the others in blocks
   // gradient
   const void* d_out;
   const float* dS_out;

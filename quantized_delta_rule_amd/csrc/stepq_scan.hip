@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256) void k_scan_tokens(ScanArgs A, int tiles) {
   int t0, t1;
   const bool valid = seq_range(A, s, t0, t1);
   const int slot = seq_slot(A, s, valid, tg == 0 && lane == 0);
-  if (slot < 0) return;
+  if (slot < 0 || (A.split && t1 - t0 >= A.split)) return;
   if (t0 == t1 && (!A.S_out || A.S_out == A.S_in)) return;
   const int part = lane % LN;
   int c[K];
@@ -81,8 +81,15 @@ __global__ __launch_bounds__(256) void k_scan_tokens(ScanArgs A, int tiles) {
   }
 }
 
-// Blocks pay from 16 tokens a sequence on.
-bool in_blocks(const ScanArgs& a) { return a.N > 0 && (long long)a.T >= 16LL * a.N; }
+// Blocks pay from about 16 tokens a sequence on in large batches, earlier in small ones (us, token by token against
+// blocks at 4 / 8 / 16 / 32 tokens of 4,096 channels, 16 states, bf16: 70 sequences 15 / 24 / 42 / 84 against 28 / 32 / 35 /
+// 52, one 5.4 / 7.5 / 12 / 20 against 3.9 / 4.2 / 4.2 / 5.3).  Lengths are on the device: where they are shorter on
+// average but one may be long, both kernels are launched and each takes its sequences (MIXED).
+constexpr int kShort = 16, kMaybeLong = 128;
+bool in_blocks(const ScanArgs& a) {
+  return a.N > 0 && ((long long)a.T >= (long long)kShort * a.N || (a.cu && a.T - a.N >= kMaybeLong));
+}
+bool in_tokens(const ScanArgs& a) { return (long long)a.T < (long long)kShort * a.N; }
 
 template <int DT, int LN>
 hipError_t tokens(const ScanArgs& a, hipStream_t s) {
@@ -110,10 +117,15 @@ hipError_t blocks(const ScanArgs& a, hipStream_t s) {
 }
 
 template <int DT>
-hipError_t by_states(const ScanArgs& a, hipStream_t s) {
-  if (!in_blocks(a)) {
-    return a.n == 8 ? tokens<DT, 2>(a, s)
-                    : a.n == 16 ? tokens<DT, 4>(a, s) : a.n == 32 ? tokens<DT, 8>(a, s) : tokens<DT, 16>(a, s);
+hipError_t by_states(const ScanArgs& given, hipStream_t s) {
+  ScanArgs a = given;
+  if (in_tokens(a)) {
+    if (in_blocks(a)) a.split = kShort;
+    const hipError_t e = a.n == 8    ? tokens<DT, 2>(a, s)
+                         : a.n == 16 ? tokens<DT, 4>(a, s)
+                         : a.n == 32 ? tokens<DT, 8>(a, s)
+                                     : tokens<DT, 16>(a, s);
+    if (e || !in_blocks(a)) return e;
   }
   return a.n == 8    ? blocks<DT, 2, 2>(a, s)
          : a.n == 16 ? blocks<DT, 2, 4>(a, s)

@@ -34,7 +34,7 @@ struct Segments {
   int sh;
   float* last;  // [segments, C, n]: the first of a sequence from its state, the others from zero
   float* steps; // [segments, C]
-  float* first; // [N, C, n]: the sequences' first states (S_out may be S_in)
+  float* first; // [N, C, n]: the first states of sequences of several segments (S_out may be S_in)
   float* kept;  // states before every block of 16 tokens, as the kernel's lanes hold them (PASS 3)
 };
 
@@ -114,7 +114,7 @@ __device__ __forceinline__ bool place(const ScanArgs& A, int sh, long long j, bo
   Q.ends = !sh || Q.p + (1LL << sh) >= Q.len;
   Q.count = (int)(Q.ends ? Q.len - Q.p : 1LL << sh);
   Q.row0 = a + Q.p;
-  return Q.slot >= 0 && (Q.p < Q.len || Q.idx == 0);
+  return Q.slot >= 0 && (Q.p < Q.len || Q.idx == 0) && Q.len >= A.split;
 }
 
 // Number of a segment's first block of 16 tokens among all sequences' (pieces of 2^4 tokens).
@@ -151,6 +151,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   const int count = W.count, s = W.s;
   const long long idx = W.idx;
   const bool ends = W.ends;
+  if (PASS == 1 && ends) return;  // nothing comes behind
   const int part = wave * P + lane / CH;  // which NS of a channel's states
   const int cl = lane % CH, cg = tile * CH + cl;
   const bool live = cg < A.Cg;
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   get_states<NS>(A.A + (long long)c * n + part * NS, a2);
 #pragma unroll
   for (int i = 0; i < NS; i++) a2[i] *= kLog2e, h[i] = 0;
-  if (PASS == 0 || PASS == 1 || !sh) {
+  if (PASS < 2 || !sh || (idx == 0 && ends)) {  // a sequence of one segment is its own workgroup's alone
     if (A.S_in && idx == 0) get_states<NS>(A.S_in + so, h);
   } else if (idx > 0) {
     get_states<NS>(Q.last + ((j - idx) * A.C + c) * n + part * NS, h);
@@ -169,7 +170,6 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   }
   if constexpr (PASS == 1) {
     if (idx == 0 && live) put_states<NS>(Q.first + ((long long)s * A.C + c) * n + part * NS, h);
-    if (ends) return;
   }
   if (PASS >= 2) {
 #pragma unroll 4
@@ -335,11 +335,18 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   }
 }
 
-// Segments (0: none) where workgroups of 32 channels of whole sequences would be fewer than `least`: about ten
+// Segments (0: none).  Where workgroups of 32 channels of whole sequences would be fewer than `least`: about ten
 // workgroups a CU, but no more than 64 of a sequence of mean length (each looks at all before it), of at least 64 tokens.
+// Where they are enough, but lengths differ and one may be eight times the mean, or 512 tokens, and more: segments of
+// that length, so that one long prompt beside single tokens or short ones does not run as one chain.
 inline int segments_of(const ScanArgs& a, int least) {
   const long long tiles = (a.Cg + 31) / 32 * a.G, mean = a.N > 0 ? a.T / a.N : 0;
-  if (a.N <= 0 || tiles * a.N >= least) return 0;
+  if (a.N <= 0) return 0;
+  if (tiles * a.N >= least) {
+    int sh = 9;
+    while (1LL << sh < 8 * mean) sh++;
+    return a.cu && (long long)a.T - a.N > 1LL << sh ? sh : 0;
+  }
   int sh = 6;
   while (sh < 30 && (((long long)a.T >> sh) * tiles > 2560 || mean >> sh > 64)) sh++;
   return mean > 1LL << sh ? sh : 0;

@@ -72,6 +72,32 @@ def test_long_sequences(scan, T, ch, N):
         assert R.rel(out[a:a + 500], o[a:a + 500]) <= TOL
 
 
+MIXED = [  # single tokens beside a prompt: lengths, channels
+    ([1] * 40 + [300] + [1] * 20, 64), ([2, 0, 1, 15, 16, 17, 1, 1, 1, 1, 1, 1, 1, 1, 160], 40), ([1] * 64 + [1500], 1024),
+    ([3] * 30 + [1100] + [20] * 9 + [900], 512), ([1] * 9 + [700, 650], 4096),
+]
+
+
+@pytest.mark.parametrize("lens,ch", MIXED, ids=lambda x: str(x)[:24])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_short_and_long_in_one_call(scan, lens, ch, dtype):
+    """Each sequence takes its path, long ones in segments; states by slot and in place."""
+    cu = R.offsets(lens)
+    x = R.scan_inputs(21, cu[-1], ch, 1, 16, len(lens), dtype)
+    g = {m: dev(v) for m, v in x.items()}
+    slots = torch.randperm(len(lens), generator=torch.Generator().manual_seed(1)).to(torch.int32)
+    pool = torch.empty_like(g["S"])
+    pool[slots.long().cuda()] = g["S"]
+    out = torch.empty_like(g["x"])
+    scan.forward(g["x"], g["dt"], g["A"], g["B"], g["C"], out, D=g["D"], dt_bias=g["bias"], z=g["z"], state_in=pool, state_out=pool,
+                 slots=slots.cuda(), cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+    o, s = want(x, cu)
+    last = pool[slots.long().cuda()]
+    for i in range(len(lens)):
+        assert R.rel(out[cu[i]:cu[i + 1]], o[cu[i]:cu[i + 1]]) <= TOL + HALF[dtype], i
+        assert R.rel(last[i], s[i]) <= TOL, i
+
+
 @pytest.mark.parametrize("slow", [1e-3, 1e-4])
 def test_states_that_last(scan, slow):
     """Steps so small that a state remembers all of 3,000 tokens: roundings of the decays add up.  They err

@@ -57,6 +57,13 @@ def test_long_sequences(scan, T, ch, N):  # noqa: F811
     check(backward(scan, x, cu, equal=True), want(x, cu), F32)
 
 
+@pytest.mark.parametrize("lens,ch", [([1] * 20 + [900], 1024), ([5] * 9 + [700, 0, 640], 2048)], ids=lambda x: str(x)[:16])
+def test_one_long_beside_short(scan, lens, ch):  # noqa: F811
+    """Enough workgroups, but one sequence many times the mean: it runs in segments."""
+    x = R.scan_inputs(42, sum(lens), ch, 1, 16, len(lens), F32)
+    check(backward(scan, x, R.offsets(lens)), want(x, R.offsets(lens)), F32)
+
+
 def test_states_that_last(scan):  # noqa: F811
     x = R.scan_inputs(34, 1500, 32, 1, 16, 1, F32, slow=1e-3)
     check(backward(scan, x, [0, 1500]), want(x, [0, 1500]), F32)
