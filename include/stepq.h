@@ -328,7 +328,9 @@ int stepq_read_slots(stepq_plan_t plan, const void* pool, int n_slots, const int
  * they were there; bad offsets and slots raise flags and skip their sequence).  Row strides are in elements from
  * one token's row to the next, 0 = packed, below 2^24; rows and strides are multiples of 16 bytes, pointers to rows and
  * states 16-byte aligned.  Calls only enqueue kernels and may be captured.  Sums are binary32 in an order
- * that the sizes alone fix: the same call on the same inputs gives the same bits.
+ * that the sizes alone fix: the same call on the same inputs gives the same bits.  Which kernels run, and where a
+ * sequence is cut into segments that run at once, follow n_tokens, n_seqs and the channels: the scan's results for a
+ * sequence alone may differ in their last bits from those for the same one beside others (the convolution's outputs do not).
  */
 
 /*
@@ -381,6 +383,8 @@ int stepq_conv_backward(const stepq_conv_desc* desc, const void* x, const void* 
  * term is missing.
  *   dtype      type of x, dt, B, C, z, out and their gradients; A, D, dt_bias and states are binary32.
  *   channels   a multiple of 8 n_groups;  d_state 8, 16, 32 or 64.
+ * Workspaces: forward none, or some states for each segment of long sequences; backward about n_tokens * channels *
+ * d_state / 4 bytes (the states before every 16 tokens) and as much again for the tiles' parts of dB and dC.
  */
 typedef struct {
   int dtype;

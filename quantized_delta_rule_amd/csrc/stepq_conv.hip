@@ -3,7 +3,11 @@
 //   du = dy act'(u);  dx_t = sum_j w_j du_{t + (W - 1) - j};  dw_j = sum_t du_t x_{t - (W - 1) + j};  db = sum_t du_t
 // A lane owns a few neighbouring channels of one piece of a sequence and goes down its tokens with the last W - 1
 // inputs (and, backwards, derivatives) in registers, so every row is read once but for W - 1 rows at a piece's ends.
-// Bound by HBM: 2 W + 5 operations an element against 4 bytes of a 16-bit type.
+// Bound by HBM: 2 W + 5 operations an element against 4 bytes of a 16-bit type.  16,381 tokens x 10,240 channels, bf16: 138 us,
+// 4.9 TB/s (a copy reaches 5.05); the gradient of 8,192 x 8,192 89 us for its 403 MB, 4.5 TB/s, and 5 for the last sums; 70
+// single tokens x 10,240 7.5 us.  Eight channels a lane forward (16 bytes), four backward, where five sums and two windows
+// a channel are held.  Four rows in flight, not one: 158 -> 138 us and 112 -> 107.  Pieces of 32 tokens forward and 64
+// backward (64 / 128: 152 and 99 us; backward 32: 107): shorter ones read more rows twice, longer ones fill fewer CUs.
 #include "stepq_layer.h"
 
 namespace stepq {

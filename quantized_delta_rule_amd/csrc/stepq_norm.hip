@@ -3,7 +3,11 @@
 //   h = x + residual, r = 1 / sqrt(mean h^2 + eps), y = h r w act(z);  scale = max |y| / top, code = y / scale
 //   p = dy w act(z):  dh = r (p - h r mean(p h r)) + d_residual;  dw = sum dy act(z) h r;  dz = dy h r w act'(z)
 // A row stays in registers from its load to its store, eight neighbouring columns a lane: 8 to 64 lanes a row (to 512
-// columns), or a workgroup of 256 (to 8,192) or 1,024 (to 32,768).  Bound by HBM: some ten operations an element.
+// columns), or a workgroup of 256 (to 8,192) or 1,024 (to 32,768; 512 for the gradient to 16,384).  Bound by HBM, some ten
+// operations an element: 16,381 x 48 rows of 128 with a gate, bf16, 120 us, 5.0 TB/s (a copy reaches 5.05); the gradient of
+// 8,192 rows of 4,096 with the residual's 44 us for its 268 MB and 5 for the last sums (without reading the next row
+// ahead 69); 70 rows of 4,096 with the residual and e4m3 out 5.3 us.  The gradient of rows above 16,384 spills registers
+// (1,024 of 32,768: 219 us, 0.9 TB/s).
 #include "stepq_layer.h"
 
 namespace stepq {

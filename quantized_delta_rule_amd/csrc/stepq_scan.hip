@@ -1,7 +1,9 @@
-// stepq_scan.hip -- selective state space scan, token by token:
+// stepq_scan.hip -- selective state space scan, token by token, and the choice between that and blocks of tokens
+// (stepq_scan_block.h):
 //   h_t = exp(D_t A) h_{t-1} + D_t B_t x_t,  out_t = (C_t . h_t + D x_t) z sigmoid(z)
-// A wave owns 256 / n channels of one group of a sequence: n / 4 neighbouring lanes a channel, four states a lane,
-// so that states are read and written 16 bytes a lane side by side.
+// A wave owns two tiles of 256 / n channels of one group of a sequence: n / 4 neighbouring lanes a channel, four states a
+// lane, so that states are read and written 16 bytes a lane side by side.  Bound by HBM: 70 single tokens x 6,144 channels of
+// 16 states, bf16, 12.4 us for 59 MB, 4.8 TB/s (one tile a wave 15.8 us, four 14.6).
 #include "stepq_scan_block.h"
 
 namespace stepq {

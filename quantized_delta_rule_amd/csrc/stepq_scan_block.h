@@ -16,6 +16,15 @@ using namespace lay;
 // token: they hold the values of a token or more, and an instruction takes one of them for all 16 lanes by itself
 // (row broadcast of its operand).  For each block of 16 tokens the waves first turn raw steps into (D, D x) in LDS,
 // a few channels each, then run all of them on their states, and add their parts of C . h up through LDS.
+//
+// Bound by vector issue: a state and token take an exponential (two slots), the argument's product, two multiply-adds and a
+// product, six slots; steps, gates and the parts' sums make it 9.7 (counted: 163 M slots of 64 lanes for 16,381 tokens x
+// 4,096 channels x 16 states).  One sequence of 16,384 x 2,048 runs both its passes, 118 and 168 us, at 98% of the issue of
+// CUs that this load holds at 2.0 GHz; eight ragged prompts of 16,381 x 4,096 take 327 us, 87% of the issue while
+// a CU is busy, the rest is that prompts of 1 to 3,698 tokens are unequal.  What the layout is worth there (us, 16,381 x
+// 4,096 / 16,384 x 2,048): B and C through scalar loads 876 / 443 (their wait stops every LDS read too), row broadcasts 581 /
+// 310; a thread's elements side by side, not 16 lanes apart, 510 / 281; 32 channels a workgroup, not 64, 355 / 293; two
+// states a lane, not four, 329 / 272; 16 channels 457 / 337.
 // ---------------------------------------------------------------------------------------------
 
 constexpr int kBlock = 16;
@@ -351,6 +360,10 @@ inline int segments_of(const ScanArgs& a, int least) {
   while (sh < 30 && (((long long)a.T >> sh) * tiles > 2560 || mean >> sh > 64)) sh++;
   return mean > 1LL << sh ? sh : 0;
 }
+// Both sides (us, 4,096 channels of 16 states, 1 / 2 / 3 sequences of 2,048 tokens; 128 workgroups a sequence): whole 137 / 142
+// / 185 against segments 79 / 152 / 207; gradient 557 / 564 / 665 against 237 / 426 / 606.  A prompt of 512 / 2,048 / 16,384
+// tokens beside 64 single ones: whole 53 / 180 / 1,340, segments 52 / 138 / 624; 70 prompts of 128, none of which is cut, 205
+// and 212.  Gradient of six sequences of 1 to 1,147 tokens, 1,536 channels of 32 states: 456 and 256.
 constexpr int kLeastForward = 256, kLeastBackward = 512;
 
 constexpr size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
