@@ -108,10 +108,10 @@ int scan_args(const stepq_scan_desc* d, ScanArgs* a) {
     return fail(STEPQ_ERR_UNSUPPORTED, "d_state must be 8, 16, 32 or 64 (got %d)", d->d_state);
   if (d->softplus != 0 && d->softplus != 1) return fail(STEPQ_ERR_INVALID_ARG, "softplus must be 0 or 1");
   STEPQ_TRY(sequences(d->n_seqs, d->n_tokens, d->cu_seqlens));
-  // threads of a launch, below 2^32: four states each of every sequence, an element each of dB and dC
-  const long long tiles = (d->channels / d->n_groups * (long long)d->d_state + 255) / 256 * d->n_groups;
-  const long long wide = ((d->channels / d->n_groups + 31LL) / 32) * d->n_groups;  // 32 channels by 8 waves
-  if (tiles * d->n_seqs * 64 + 256 > UINT_MAX || wide * d->n_seqs * 512 > UINT_MAX || 2LL * d->n_groups * d->d_state * d->n_tokens + 256 > UINT_MAX)
+  // threads of a launch, below 2^32: 32 channels by 8 waves of every sequence and of segments, which are no more than
+  // the sequences again where those are many; an element each of dB and dC
+  const long long wide = ((d->channels / d->n_groups + 31LL) / 32) * d->n_groups;
+  if (wide * d->n_seqs * 1024 > UINT_MAX || 2LL * d->n_groups * d->d_state * d->n_tokens + 256 > UINT_MAX)
     return fail(STEPQ_ERR_INVALID_ARG, "n_tokens (%d), n_seqs (%d) and channels (%d) exceed the launch grid", d->n_tokens,
                 d->n_seqs, d->channels);
   const long long unit = d->dtype == STEPQ_DTYPE_F32 ? 4 : 8, gn = (long long)d->n_groups * d->d_state;
