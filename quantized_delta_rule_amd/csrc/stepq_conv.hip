@@ -7,7 +7,7 @@
 // 4.9 TB/s (a copy reaches 5.05); the gradient of 8,192 x 8,192 89 us for its 403 MB, 4.5 TB/s, and 5 for the last sums; 70
 // single tokens x 10,240 7.5 us.  Eight channels a lane forward (16 bytes), four backward, where five sums and two windows
 // a channel are held.  Four rows in flight, not one: 158 -> 138 us and 112 -> 107.  Pieces of 32 tokens forward and 64
-// backward (64 / 128: 152 and 99 us; backward 32: 107): shorter ones read more rows twice, longer ones fill fewer CUs.
+// backward there (64 / 128: 152 and 99 us; backward 32: 107): shorter ones read more rows twice, longer ones fill fewer CUs.
 #include "stepq_layer.h"
 
 namespace stepq {
@@ -15,8 +15,7 @@ namespace {
 
 using namespace lay;
 
-constexpr int kShF = 5, kShB = 6;          // tokens of a piece: 2^kShF forward, 2^kShB backward
-constexpr int kAhead = 4;                  // rows read at once
+constexpr int kAhead = 4;  // rows read at once
 template <int DT>
 constexpr int kSize = DT == kF32 ? 4 : 2;
 
@@ -28,7 +27,6 @@ struct Part {
 };
 
 // False where the wave has nothing to do.  One lane a sequence raises the flags.
-template <int SH>
 __device__ __forceinline__ bool part_of(const ConvArgs& A, long long j, bool report, int lane, Part& P) {
   int a, b;
   if (report && j < A.N) {
@@ -36,13 +34,13 @@ __device__ __forceinline__ bool part_of(const ConvArgs& A, long long j, bool rep
     seq_slot(A, (int)j, ok, lane == 0);
   }
   long long idx;
-  if (!piece(A, SH, j, lane, P.s, idx)) return false;
+  if (!piece(A, A.sh, j, lane, P.s, idx)) return false;
   const bool ok = seq_range(A, P.s, a, b);
   P.slot = seq_slot(A, P.s, ok, false);
   P.t0 = a;
   P.len = b - a;
-  P.p = idx << SH;
-  P.end = P.p + (1 << SH) < P.len ? P.p + (1 << SH) : P.len;
+  P.p = idx << A.sh;
+  P.end = P.p + (1 << A.sh) < P.len ? P.p + (1 << A.sh) : P.len;
   P.first = idx == 0;
   return P.slot >= 0 && (P.p < P.len || P.first);
 }
@@ -71,7 +69,7 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
   const int cb = blockIdx.x % blocks;
   const long long j = (long long)(blockIdx.x / blocks) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Part P;
-  if (!part_of<kShF>(A, j, cb == 0, lane, P)) return;
+  if (!part_of(A, j, cb == 0, lane, P)) return;
   const int c = (cb * 64 + lane) * V;
   if (c >= A.C) return;
   float w[W][V], b[V], x[W][V];  // x: the last W inputs
@@ -162,7 +160,7 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
     for (int i = 0; i < W; i++) dw[i][v] = 0;
   }
   Part P;
-  if (part_of<kShB>(A, j, cb == 0, lane, P) && c < A.C) {
+  if (part_of(A, j, cb == 0, lane, P) && c < A.C) {
     float w[W][V], b[V], x[W][V], du[W][V];
     weights<W, V>(A, c, w, b);
     const long long so = (long long)P.s * (W - 1) * A.C + c;
@@ -282,10 +280,26 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
 
 constexpr int kFwdV = 8, kBwdV = 4;
 
+long long channel_blocks(const ConvArgs& a, bool back) {
+  const int wide = 64 * (back ? kBwdV : kFwdV);
+  return (a.C + wide - 1) / wide;
+}
+
+// Tokens of a piece (2^n): long pieces where they are waves enough, short ones where a call would be a few long chains.  us of
+// calls, long against short pieces: gradient 2,657 tokens x 120 channels 42 and 18, 2,933 x 4,752 (1,400 waves) 50 and 30,
+// 8,192 x 2,048 (1,100) 49 and 35, 8,192 x 8,192 (4,100) 97 and 104; forward 14 and 7, 22 and 18, 22 and 19, 53 and 55.
+constexpr long long kWaves = 2048;
+int piece_of(const ConvArgs& a, bool back) {
+  const int big = back ? 6 : 5, small = back ? 4 : 3;
+  return pieces(a, big) * channel_blocks(a, back) >= kWaves ? big : small;
+}
+
 template <int DT, int W>
-hipError_t launch(const ConvArgs& a, bool back, hipStream_t s) {
-  const int V = back ? kBwdV : kFwdV, blocks = (a.C + 64 * V - 1) / (64 * V);
-  const long long groups = (pieces(a, back ? kShB : kShF) + 3) / 4;
+hipError_t launch(const ConvArgs& given, bool back, hipStream_t s) {
+  ConvArgs a = given;
+  a.sh = piece_of(a, back);
+  const int blocks = (int)channel_blocks(a, back);
+  const long long groups = (pieces(a, a.sh) + 3) / 4;
   const dim3 grid((unsigned)(groups * blocks)), block(256);
   if (back) hipLaunchKernelGGL((k_conv_grad<DT, W, kBwdV>), grid, block, 0, s, a, blocks);
   else hipLaunchKernelGGL((k_conv<DT, W, kFwdV>), grid, block, 0, s, a, blocks);
@@ -307,12 +321,12 @@ hipError_t by_type(const ConvArgs& a, bool back, hipStream_t s) {
 hipError_t launch_conv(const ConvArgs& a, hipStream_t s) { return a.N <= 0 ? hipSuccess : by_type(a, false, s); }
 
 size_t conv_backward_bytes(const ConvArgs& a) {
-  return (size_t)((pieces(a, kShB) + 3) / 4) * a.C * (a.W + 1) * sizeof(float);
+  return (size_t)((pieces(a, piece_of(a, true)) + 3) / 4) * a.C * (a.W + 1) * sizeof(float);
 }
 
 hipError_t launch_conv_backward(const ConvArgs& a, hipStream_t s) {
-  SumArgs m{a.ws, (int)((pieces(a, kShB) + 3) / 4), (long long)a.C * (a.W + 1), (long long)a.C * a.W, a.C, a.dw, a.db,
-            nullptr};
+  SumArgs m{a.ws, (int)((pieces(a, piece_of(a, true)) + 3) / 4), (long long)a.C * (a.W + 1), (long long)a.C * a.W, a.C, a.dw,
+            a.db, nullptr};
   if (a.N > 0) {
     if (hipError_t e = by_type(a, true, s)) return e;
   }

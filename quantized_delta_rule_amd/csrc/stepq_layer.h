@@ -19,6 +19,7 @@ struct ConvArgs {
   const int* slots;         // [N] or nullptr
   unsigned* status;
   long long xs, os;         // elements between tokens of x, and of out / d_out
+  int sh;                   // tokens of a piece: 2^sh (set by the launch)
   const void* x;
   const void* w;            // [C, W] pdtype
   const void* b;            // [C] or nullptr
