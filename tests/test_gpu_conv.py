@@ -193,3 +193,32 @@ def test_no_sequence(conv):
     conv.forward(x, w, torch.zeros(0, 64).cuda(), n_seqs=0)
     conv.backward(x, w, x, torch.zeros(0, 64).cuda(), dw, n_seqs=0)
     assert float(dw.abs().sum()) == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_long_pieces(conv, dtype):
+    """Calls of so many waves that pieces are long: offsets around their ends, against shifted products in binary64."""
+    lens, C, W = [31, 33, 64, 0, 65, 1, 2, 127, 4000, 129, 4100], 4096, 4
+    cu = R.offsets(lens)
+    x = {m: v.cuda() for m, v in R.conv_inputs(9, cu[-1], C, W, len(lens), dtype).items()}
+    leaf = {m: x[m].double().requires_grad_(True) for m in ("x", "w", "b", "S")}
+    outs, lasts = [], []
+    for n in range(len(lens)):
+        every = torch.cat([leaf["S"][n], leaf["x"][cu[n]:cu[n + 1]]])
+        u = leaf["b"] + sum(leaf["w"][:, j] * every[j:j + lens[n]] for j in range(W))
+        outs.append(u * torch.sigmoid(u))
+        lasts.append(every[lens[n]:])
+    want, wl = torch.cat(outs), torch.stack(lasts)
+    grads = torch.autograd.grad([want, wl], list(leaf.values()), [x["dy"].double(), x["dS"].double()])
+    off = torch.tensor(cu, dtype=torch.int32).cuda()
+    out, last = torch.empty_like(x["x"]), torch.empty_like(x["S"])
+    conv.forward(x["x"], x["w"], out, bias=x["b"], state_in=x["S"], state_out=last, cu_seqlens=off)
+    assert R.rel(out, want) <= FWD + HALF[dtype] and torch.equal(last.double(), wl.detach())
+    dx, dw, db, dS = torch.empty_like(x["x"]), torch.empty(C, W).cuda(), torch.empty(C).cuda(), torch.empty_like(x["S"])
+    conv.backward(x["x"], x["w"], x["dy"], dx, dw, bias=x["b"], dbias=db, state_in=x["S"], d_state_out=x["dS"], d_state_in=dS,
+                  cu_seqlens=off)
+    # sums of 8,552 tokens: pieces of 64, four of them, 34 rows: the chains are no longer than the tolerance counts
+    for got, g, tol in zip((dx, dw, db, dS), grads, (DX + HALF[dtype], DW, DW, DX + HALF[dtype])):
+        assert R.rel(got, g) <= tol
+    for n in range(len(lens)):
+        assert R.rel(dx[cu[n]:cu[n + 1]], grads[0][cu[n]:cu[n + 1]]) <= DX + HALF[dtype], n
