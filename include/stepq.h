@@ -449,8 +449,8 @@ typedef struct {
 /*
  *   x, residual, residual_out, z, out [n_rows, n_heads, d] (residual, residual_out and z may be NULL;
  *   residual_out has residual's stride), weight [d] or NULL (ones), scale [n_rows, n_heads] or [n_rows, n_heads,
- *   d / group] binary32 (8-bit outputs only).  out may be x, and residual_out may be residual or x, each with the
- *   other's type and stride (in place); no output may overlap anything else.
+ *   d / group] binary32 (8-bit outputs only).  out and residual_out may each be x, residual or z, with its type and
+ *   stride (in place); no output may overlap anything else.
  */
 int stepq_norm_forward(const stepq_norm_desc* desc, const void* x, const void* weight, const void* residual,
                        const void* z, void* out, float* scale, void* residual_out, void* stream);
@@ -459,7 +459,8 @@ int stepq_norm_forward(const stepq_norm_desc* desc, const void* x, const void* w
  * Gradient of the norm at h [n_rows, n_heads, d] (x's stride; the sum that the norm was taken of, that is x or
  * residual_out): from d_out (dtype, out_stride) and d_residual (NULL = zero; residual_stride: the gradient that
  * reaches h by the residual's own way) to dx [n_rows, n_heads, d] (packed; the gradient of x and of the residual alike),
- * dz (packed; goes with z) and dweight [d] (binary32, NULL = not wanted).  out_dtype is dtype, group 0.
+ * dz (packed; goes with z) and dweight [d] (binary32, NULL = not wanted).  out_dtype is dtype, group 0.  dx and dz
+ * may each be a packed h, d_out, z or d_residual (in place); no output may overlap anything else.
  */
 int stepq_norm_backward_workspace(const stepq_norm_desc* desc, size_t* bytes);
 int stepq_norm_backward(const stepq_norm_desc* desc, const void* h, const void* weight, const void* z,

@@ -63,6 +63,20 @@ int apart(const void* out, const char* what, const void* const* in, const char* 
   return STEPQ_OK;
 }
 
+// An output's rows in the place of an input's: each row's own threads read it before they write it, which is right only
+// where both have the same bytes for a row.
+struct Rows {
+  const void* p;
+  const char* name;
+  long long stride;
+};
+int rows_apart(const Rows& out, bool same_type, const Rows* in, int n) {
+  for (int i = 0; i < n; i++)
+    if (out.p && out.p == in[i].p && (!same_type || out.stride != in[i].stride))
+      return fail(STEPQ_ERR_INVALID_ARG, "%s must not overlap %s, or have its type and row stride", out.name, in[i].name);
+  return STEPQ_OK;
+}
+
 #define STEPQ_TRY(call) \
   if (int rc_ = (call)) return rc_
 
@@ -362,6 +376,12 @@ int stepq_norm_forward(const stepq_norm_desc* desc, const void* x, const void* w
   STEPQ_TRY(all_aligned(p, names, 5, 16));
   STEPQ_TRY(aligned(out, eight ? 8 : 16, "out"));
   STEPQ_TRY(aligned(scale, 4, "scale"));
+  const Rows in[] = {{x, "x", a.xs}, {residual, "residual", a.rs}, {z, "z", a.zs}};
+  if (a.R > 0) {
+    STEPQ_TRY(rows_apart({out, "out", a.os}, !eight, in, 3));
+    STEPQ_TRY(rows_apart({residual_out, "residual_out", a.rs}, true, in, 3));
+    STEPQ_TRY(apart(residual_out, "residual_out", p + 5, names + 5, 1));
+  }
   STEPQ_ON_DEVICE(desc->device);
   a.x = x;
   a.w = weight;
@@ -388,6 +408,13 @@ int stepq_norm_backward(const stepq_norm_desc* desc, const void* h, const void* 
   STEPQ_TRY(pointers(a.R > 0 && z, p + 3, names + 3, 1));
   STEPQ_TRY(all_aligned(p, names, 7, 16));
   STEPQ_TRY(aligned(dweight, 4, "dweight"));
+  const Rows in[] = {{h, "h", a.xs}, {d_out, "d_out", a.os}, {z, "z", a.zs}, {d_residual, "d_residual", a.rs}};
+  const long long packed = (long long)a.H * a.D;
+  if (a.R > 0) {
+    STEPQ_TRY(rows_apart({dx, "dx", packed}, true, in, 4));
+    STEPQ_TRY(rows_apart({dz, "dz", packed}, true, in, 4));
+    STEPQ_TRY(apart(dx, "dx", p + 3, names + 3, 1));
+  }
   STEPQ_TRY(seq_workspace(workspace, workspace_bytes, norm_backward_bytes(a)));
   STEPQ_ON_DEVICE(desc->device);
   a.x = h;

@@ -46,8 +46,8 @@ def forward(x, weight, out, *, eps=1e-6, residual=None, residual_out=None, z=Non
     """out = h / sqrt(mean(h^2) + eps) * weight * act(z), h = x + residual; residual_out = h, rounded once.
 
     weight None: ones.  gate: what z goes through, SILU or SIGMOID.  8-bit out: scale = max |y| / 448 (e4m3) or
-    / 127 (int8) of a row or of every `group` columns, out = y / scale to the nearest.  out may be x, residual_out may
-    be residual or x (in place)."""
+    / 127 (int8) of a row or of every `group` columns, out = y / scale to the nearest.  out and residual_out may
+    each be x, residual or z, with its type and strides (in place)."""
     dev, shape, R, H, d = _shape(x)
     t = x.dtype
     code = dtype_code(t)
@@ -105,7 +105,7 @@ def backward(h, weight, d_out, dx, dweight=None, *, eps=1e-6, z=None, dz=None, g
              workspace=None, stream=None):
     """Gradient of forward() at h (x, or x + residual as residual_out keeps it): from d_out and d_residual (the gradient
     that reaches h beside the norm; None = zero) into dx (packed; the gradient of x and of the residual alike), dz and
-    dweight (float32; None = not wanted), all overwritten."""
+    dweight (float32; None = not wanted), all overwritten.  dx and dz may each be a packed h, d_out, z or d_residual."""
     desc, dev, shape, p = _describe_grad(h, weight, d_out, eps, z, gate, d_residual)
     if dx is None:
         raise TypeError("dx must be a torch tensor")

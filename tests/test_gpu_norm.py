@@ -159,6 +159,24 @@ def test_in_place(norm):
     assert torch.equal(c, h) and torch.equal(a, out)
 
 
+@pytest.mark.parametrize("rows,d", [(3000, 72), (1500, 520), (1100, 4096), (1100, 8192), (600, 16384), (600, 20000)])
+def test_in_the_place_of_any_input(norm, rows, d):
+    """The same bits, whichever rows are overwritten: more rows than workgroups, so that rows are read ahead."""
+    g = {m: v.cuda() for m, v in inputs(d + 43, (rows, d), BF16).items()}
+    out, h, dx, dz = (torch.empty_like(g["x"]) for _ in range(4))
+    dw, dw1 = torch.empty(d).cuda(), torch.empty(d).cuda()
+    norm.forward(g["x"], g["w"], out, residual=g["res"], residual_out=h, z=g["z"])
+    norm.backward(h, g["w"], g["dy"], dx, dw, z=g["z"], dz=dz, d_residual=g["x"])
+    for a, b in (("x", "z"), ("res", "x"), ("z", "res")):
+        c = {m: g[m].clone() for m in ("x", "res", "z")}
+        norm.forward(c["x"], g["w"], c[a], residual=c["res"], residual_out=c[b], z=c["z"])
+        assert torch.equal(c[a], out) and torch.equal(c[b], h), (a, b)
+    for a, b in (("h", "dy"), ("dy", "h"), ("z", "x"), ("x", "z")):
+        c = {m: v.clone() for m, v in dict(g, h=h).items()}
+        norm.backward(c["h"], g["w"], c["dy"], c[a], dw1, z=c["z"], dz=c[b], d_residual=c["x"])
+        assert torch.equal(c[a], dx) and torch.equal(c[b], dz) and torch.equal(dw1, dw), (a, b)
+
+
 def test_strided_rows(norm):
     wide = torch.randn(40, 3, 256).to(BF16).cuda()
     x, z = wide[:, 0, :], wide[:, 2, :]

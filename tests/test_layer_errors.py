@@ -66,9 +66,9 @@ def scan_calls(L, d):
 
 def norm_calls(L, d):
     n = ctypes.c_size_t()
-    p, q = ctypes.byref(d), V(AT)
-    return [L.stepq_norm_forward(p, *[q] * 7, None), L.stepq_norm_backward_workspace(p, ctypes.byref(n)),
-            L.stepq_norm_backward(p, *[q] * 9, 1 << 40, None)]
+    p, q = ctypes.byref(d), MANY
+    return [L.stepq_norm_forward(p, *q[:7], None), L.stepq_norm_backward_workspace(p, ctypes.byref(n)),
+            L.stepq_norm_backward(p, *q[:9], 1 << 40, None)]
 
 
 SEQS = [
@@ -205,6 +205,41 @@ def test_outputs_in_the_place_of_inputs(L):
     for a, b in (("x", "dx"), ("d_out", "ddt"), ("z", "dz"), ("dx", "dz"), ("dt", "ddt"), ("S_in", "dS_in"), ("dS_out", "dS_in")):
         p = same(names.index(a), names.index(b), 21)
         refused(L, L.stepq_scan_backward(s, *p, 1 << 40, None), INVALID, f"{b} must not overlap {a}")
+
+
+def test_norm_rows_in_the_place_of_others(L):
+    """The norm works in place where a row of both has the same bytes, and is refused where workgroups would write
+    rows that others still read."""
+    def norm(kw, a, b):
+        names = ["x", "weight", "residual", "z", "out", "scale", "residual_out"]
+        p = list(MANY[:7])
+        p[names.index(b)] = p[names.index(a)]
+        return L.stepq_norm_forward(ctypes.byref(norm_desc(**kw)), *p, None)
+
+    for a in ("x", "residual", "z"):
+        for b, own in (("out", "out"), ("residual_out", "residual")):
+            if (a, b) != ("residual", "residual_out"):
+                refused(L, norm({f"{own}_stride": 512}, a, b), INVALID, f"{b} must not overlap {a}")
+                refused(L, norm({f"{a}_stride": 512}, a, b), INVALID, f"{b} must not overlap {a}")
+            if not torch.cuda.is_available():
+                refused(L, norm({}, a, b), INVALID, "device 0 not available")
+                refused(L, norm({f"{own}_stride": 512, f"{a}_stride": 512}, a, b), INVALID, "device 0 not available")
+        refused(L, norm(dict(out_dtype=4), a, "out"), INVALID, f"out must not overlap {a}")
+    refused(L, norm({}, "out", "residual_out"), INVALID, "residual_out must not overlap out")
+    names = ["h", "weight", "z", "d_out", "d_residual", "dx", "dweight", "dz"]
+    strides = dict(h="x_stride", z="z_stride", d_out="out_stride", d_residual="residual_stride")
+    for b in ("dx", "dz"):
+        for a, st in strides.items():
+            p = list(MANY[:9])
+            p[names.index(b)] = p[names.index(a)]
+            refused(L, L.stepq_norm_backward(ctypes.byref(norm_desc(**{st: 512})), *p, 1 << 40, None), INVALID,
+                    f"{b} must not overlap {a}")
+            if not torch.cuda.is_available():
+                refused(L, L.stepq_norm_backward(ctypes.byref(norm_desc()), *p, 1 << 40, None), INVALID,
+                        "device 0 not available")
+    p = list(MANY[:9])
+    p[names.index("dz")] = p[names.index("dx")]
+    refused(L, L.stepq_norm_backward(ctypes.byref(norm_desc()), *p, 1 << 40, None), INVALID, "dx must not overlap dz")
 
 
 def test_good_calls_fail_only_at_the_device(L):
