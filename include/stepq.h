@@ -430,8 +430,8 @@ int stepq_scan_backward(const stepq_scan_desc* desc, const void* x, const void* 
  * (STEPQ_ACT_SILU) or sigmoid(z) (STEPQ_ACT_SIGMOID).
  *   dtype        type of x, residual, residual_out, z (F32, BF16, F16);  param_dtype that of weight.
  *   out_dtype    dtype, or E4M3 or I8: eight bits with scales: scale = max |y| / 448 (E4M3) or / 127 (I8) over
- *                a head's row (group = 0) or every `group` (64 or 128; d a multiple) of its columns, out = y / scale to
- *                the nearest (ties to even); a group of zeros has scale 1.  The scale is at least the smallest
+ *                a head's row (group = 0) or every `group` (64 or 128; d a multiple) of its columns, out = y / scale, a
+ *                binary32 quotient, to the nearest (ties to even); a group of zeros has scale 1.  The scale is at least the smallest
  *                normal binary32.  A y that is NaN takes no part in the maximum: its code is NaN (E4M3) or 0 (I8).
  *   n_rows       rows of n_heads * d elements, n_heads x n_rows below 2^31;  d a multiple of 8, at most 32768.
  *   strides      elements between rows, 0 = packed; multiples of 16 bytes (out's of 8 bytes with 8 bits), below

@@ -41,14 +41,15 @@ __device__ __forceinline__ long long at_row(const NormArgs& A, long long i, long
   return t * stride + (i - t * A.H) * A.D;
 }
 
-// Codes of eight values times 1 / scale.
-__device__ __forceinline__ void store_codes(int odt, void* out, long long i, const float* y, float inv) {
+// Codes of eight values y / scale.  A quotient, not a product with 1 / scale: that is off by up to 1.5 units in the last place,
+// and of the values that near a tie between two codes some would fall to the other side.
+__device__ __forceinline__ void store_codes(int odt, void* out, long long i, const float* y, float scale) {
   int w[2];
   if (odt == kE4M3) {
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const float u = y[j] * inv;
+      const float u = y[j] / scale;
       v[j] = u == u ? fminf(fmaxf(u, -448.0f), 448.0f) : u;
     }
 #pragma unroll
@@ -62,7 +63,7 @@ __device__ __forceinline__ void store_codes(int odt, void* out, long long i, con
       w[k] = 0;
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        const float u = y[4 * k + j] * inv, q = rintf(fminf(fmaxf(u, -127.0f), 127.0f));
+        const float u = y[4 * k + j] / scale, q = rintf(fminf(fmaxf(u, -127.0f), 127.0f));
         w[k] |= ((u == u ? (int)q : 0) & 255) << (8 * j);
       }
     }
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormArgs A) {
     const float scale = top > 0 ? fmaxf(top / most, 1.17549435e-38f) : 1.0f;
     if (c >= A.D || !live) continue;
     if (A.group == 0 ? c == 0 : c % A.group == 0) A.scale[A.group ? row * (A.D / A.group) + c / A.group : row] = scale;
-    store_codes(A.odtype, A.out, oo + c, h[k], 1.0f / scale);
+    store_codes(A.odtype, A.out, oo + c, h[k], scale);
   }
 }
 

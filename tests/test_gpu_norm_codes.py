@@ -1,0 +1,55 @@
+"""The norm's eight-bit codes are the quotients y / scale, rounded to binary32 and then to the nearest code (ties to even), to
+the bit: y is what the same call gives as binary32, the scale what the call writes."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+KINDS = {torch.float8_e4m3fn: 448.0, torch.int8: 127.0}
+
+
+@pytest.fixture(scope="module")
+def norm():
+    from quantized_delta_rule_amd import norm
+    return norm
+
+
+def codes_of(y, scale, group, kind):
+    """On the CPU, whose binary32 quotient is correctly rounded."""
+    v = (y.unflatten(-1, (-1, group or y.shape[-1])) / scale.reshape(*y.shape[:-1], -1, 1)).flatten(-2)
+    return v.to(kind) if kind == torch.float8_e4m3fn else v.round().to(kind)
+
+
+def check(norm, kind, x, w, group=0, **more):
+    y, codes = torch.empty(x.shape, device="cuda"), torch.empty(x.shape, dtype=kind, device="cuda")
+    scale = torch.empty(x.shape[:-1] + ((x.shape[-1] // group,) if group else ()), device="cuda")
+    norm.forward(x, w, y, **more)
+    norm.forward(x, w, codes, scale=scale, group=group, **more)
+    top = y.cpu().unflatten(-1, (-1, group or x.shape[-1])).abs().amax(-1).reshape(scale.shape)
+    assert torch.equal(scale.cpu(), torch.where(top > 0, top / KINDS[kind], torch.ones_like(top)))
+    want = codes_of(y.cpu(), scale.cpu(), group, kind)
+    assert int((codes.cpu().view(torch.int8) != want.view(torch.int8)).sum()) == 0
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+def test_quotients_at_ties(norm, kind):
+    """Rows whose every element is half-way between two codes, but for the norm's roundings."""
+    if kind == torch.int8:
+        ties = torch.arange(-126, 126).float() + 0.5
+    else:
+        ties = torch.tensor([(8 + m + 0.5) * 2.0 ** (e - 3) for e in range(-6, 8) for m in range(8)])
+        ties = torch.cat([ties, -ties])
+    d = 512
+    loud = 2.0 ** (8 * torch.rand(4000, 1, generator=torch.Generator().manual_seed(1)) - 4)
+    row = torch.zeros(d)
+    row[:len(ties)], row[-1] = ties, KINDS[kind]
+    check(norm, kind, (row * loud).cuda(), None, eps=1e-5)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+@pytest.mark.parametrize("rows,d,group", [(1000, 4096, 0), (1000, 4096, 128), (400, 1000, 0), (37, 8192, 64), (9, 20480, 0)])
+def test_quotients(norm, kind, rows, d, group):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, r, w = (torch.randn(*s, generator=g, device="cuda") for s in ((rows, d), (rows, d), (d,)))
+    check(norm, kind, x, w, group, residual=r)
+    check(norm, kind, x, None, group, z=r)
