@@ -38,7 +38,7 @@ def rows(t, name, dtype, shape, device):
         return t.data_ptr(), 0
     if st[0] < inner:
         raise ValueError(f"{name}: rows must not overlap (strides {list(st)})")
-    return t.data_ptr(), st[0]
+    return t.data_ptr(), 0 if st[0] == inner else st[0]
 
 
 def dense(t, name, dtype, shape, device):
