@@ -98,6 +98,11 @@ struct NormArgs {
   float* ws;
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+// Threads of that launch, which have to stay below 2^32: 8 to 64 a row of up to 512 columns, in workgroups of 256.
+constexpr long long norm_threads(long long rows, int D) {
+  const int wide = D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : D <= 512 ? 64 : D <= 8192 ? 256 : 1024;
+  return wide < 256 ? (rows * wide + 255) / 256 * 256 : rows * wide;
+}
 size_t norm_backward_bytes(const NormArgs& a);
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s);
 

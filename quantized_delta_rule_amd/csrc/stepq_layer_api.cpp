@@ -170,7 +170,7 @@ int scan_inputs(ScanArgs* a, const void* x, const void* dt, const float* A, cons
   return STEPQ_OK;
 }
 
-int norm_args(const stepq_norm_desc* d, NormArgs* a) {
+int norm_args(const stepq_norm_desc* d, bool forward, NormArgs* a) {
   if (!d) return fail(STEPQ_ERR_INVALID_ARG, "desc is NULL");
   if (!row_type(d->dtype)) return fail(STEPQ_ERR_INVALID_ARG, "dtype must be STEPQ_DTYPE_F32, _BF16 or _F16");
   if (!row_type(d->param_dtype))
@@ -188,7 +188,8 @@ int norm_args(const stepq_norm_desc* d, NormArgs* a) {
   if (d->group && (!eight || (d->group != 64 && d->group != 128) || d->d % d->group))
     return fail(STEPQ_ERR_INVALID_ARG, "group must be 0, or with 8 bits 64 or 128 and divide d (got %d)", d->group);
   if (!(d->eps >= 0) || d->eps > 1e30f) return fail(STEPQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  if (d->d > 512 && (long long)d->n_rows * d->n_heads * (d->d > 8192 ? 1024 : 256) > UINT_MAX)
+  // the gradient's workgroups go over any number of rows, but rows above 512 columns have one limit both ways
+  if ((forward || d->d > 512) && norm_threads((long long)d->n_rows * d->n_heads, d->d) > UINT_MAX)
     return fail(STEPQ_ERR_INVALID_ARG, "n_rows (%d) x n_heads (%d) exceeds the launch grid", d->n_rows, d->n_heads);
   const long long unit = d->dtype == STEPQ_DTYPE_F32 ? 4 : 8, all = (long long)d->n_heads * d->d;
   *a = NormArgs{};
@@ -209,7 +210,7 @@ int norm_args(const stepq_norm_desc* d, NormArgs* a) {
 }
 
 int norm_grad_args(const stepq_norm_desc* d, NormArgs* a) {
-  STEPQ_TRY(norm_args(d, a));
+  STEPQ_TRY(norm_args(d, false, a));
   if (d->out_dtype != d->dtype) return fail(STEPQ_ERR_INVALID_ARG, "the gradient's out_dtype must be dtype");
   return STEPQ_OK;
 }
@@ -366,7 +367,7 @@ int stepq_scan_backward(const stepq_scan_desc* desc, const void* x, const void* 
 int stepq_norm_forward(const stepq_norm_desc* desc, const void* x, const void* weight, const void* residual,
                        const void* z, void* out, float* scale, void* residual_out, void* stream) {
   NormArgs a;
-  STEPQ_TRY(norm_args(desc, &a));
+  STEPQ_TRY(norm_args(desc, true, &a));
   const bool eight = a.odtype != a.dtype;
   const void* p[] = {x, weight, residual, z, residual_out, out};
   const char* names[] = {"x", "weight", "residual", "z", "residual_out", "out"};

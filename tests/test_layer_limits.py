@@ -1,0 +1,33 @@
+"""Launch limits and workspaces of the layer calls at their borders: refused with a reason before a device is looked for."""
+import ctypes
+
+import pytest
+
+from test_layer_errors import INVALID, MANY, L, norm_desc, refused  # noqa: F401
+
+ROWS = [(8, 2 ** 29 - 32), (64, 2 ** 29 - 32), (72, 2 ** 28 - 16), (128, 2 ** 28 - 16), (136, 2 ** 27 - 8), (256, 2 ** 27 - 8),
+        (264, 2 ** 26 - 4), (512, 2 ** 26 - 4), (520, 2 ** 24 - 1), (8192, 2 ** 24 - 1), (8200, 2 ** 22 - 1), (32768, 2 ** 22 - 1)]
+
+
+def good(L, rc):  # noqa: F811
+    """Accepted: without a GPU such a call gets as far as looking for one, and with one this is not asked."""
+    refused(L, rc, INVALID, "device 0 not available")
+
+
+@pytest.mark.parametrize("d,most", ROWS)
+def test_rows_of_the_norm(L, d, most):  # noqa: F811
+    torch = pytest.importorskip("torch")
+    n = ctypes.c_size_t()
+    for heads in (1, 4):
+        for out in (1, 3):
+            over = ctypes.byref(norm_desc(n_rows=most // heads + 1, n_heads=heads, d=d, out_dtype=out))
+            refused(L, L.stepq_norm_forward(over, *MANY[:7], None), INVALID, "launch grid")
+            if not torch.cuda.is_available():
+                fits = ctypes.byref(norm_desc(n_rows=most // heads, n_heads=heads, d=d, out_dtype=out))
+                good(L, L.stepq_norm_forward(fits, *MANY[:7], None))
+        over = ctypes.byref(norm_desc(n_rows=most // heads + 1, n_heads=heads, d=d))
+        rc = L.stepq_norm_backward_workspace(over, ctypes.byref(n))
+        if d > 512:
+            refused(L, rc, INVALID, "launch grid")
+        else:
+            assert rc == 0
