@@ -382,7 +382,7 @@ int stepq_conv_backward(const stepq_conv_desc* desc, const void* x, const void* 
  * channel c reads group g = c / (channels / n_groups) of B and C; without z its factor is one, without D its
  * term is missing.
  *   dtype      type of x, dt, B, C, z, out and their gradients; A, D, dt_bias and states are binary32.
- *   channels   a multiple of 8 n_groups;  d_state 8, 16, 32 or 64.
+ *   channels   a multiple of 8 n_groups;  d_state 8, 16, 32 or 64; the gradient takes channels x (d_state + 2) up to 2^28 - 64.
  * Workspaces: forward none, or some states for each segment of long sequences; backward about n_tokens * channels *
  * d_state / 4 bytes (the states before every 16 tokens) and as much again for the tiles' parts of dB and dC.
  */

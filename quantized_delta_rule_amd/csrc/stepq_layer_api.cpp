@@ -149,6 +149,14 @@ int scan_args(const stepq_scan_desc* d, ScanArgs* a) {
   return STEPQ_OK;
 }
 
+int scan_grad_args(const stepq_scan_desc* d, ScanArgs* a) {
+  STEPQ_TRY(scan_args(d, a));
+  // the last sums: 16 threads a column of dA | dD | ddt_bias, in workgroups of 1,024
+  if (((long long)a->C * (a->n + 2) + 63) / 64 * 1024 > UINT_MAX)
+    return fail(STEPQ_ERR_INVALID_ARG, "channels (%d) x d_state (%d) exceed the gradient's launch grid", a->C, a->n);
+  return STEPQ_OK;
+}
+
 int scan_inputs(ScanArgs* a, const void* x, const void* dt, const float* A, const void* B, const void* C,
                 const float* D, const float* bias, const void* z, const float* S_in, const void* out) {
   const void* p[] = {x, dt, B, C, out, A, z, S_in};
@@ -295,7 +303,7 @@ int stepq_scan_forward_workspace(const stepq_scan_desc* desc, size_t* bytes) {
 }
 
 int stepq_scan_backward_workspace(const stepq_scan_desc* desc, size_t* bytes) {
-  return bytes_of(desc, bytes, scan_args, scan_backward_bytes);
+  return bytes_of(desc, bytes, scan_grad_args, scan_backward_bytes);
 }
 
 int stepq_scan_forward(const stepq_scan_desc* desc, const void* x, const void* dt, const float* A, const void* B,
@@ -326,7 +334,7 @@ int stepq_scan_backward(const stepq_scan_desc* desc, const void* x, const void* 
                         float* dD, float* ddt_bias, void* dz, float* dS_in, void* workspace, size_t workspace_bytes,
                         void* stream) {
   ScanArgs a;
-  STEPQ_TRY(scan_args(desc, &a));
+  STEPQ_TRY(scan_grad_args(desc, &a));
   STEPQ_TRY(scan_inputs(&a, x, dt, A, B, C, D, dt_bias, z, S_in, d_out));
   const void* p[] = {dx, ddt, dB, dC, dA, dz, dS_out, dS_in};
   const char* names[] = {"dx", "ddt", "dB", "dC", "dA", "dz", "dS_out", "dS_in"};

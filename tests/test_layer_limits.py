@@ -31,3 +31,21 @@ def test_rows_of_the_norm(L, d, most):  # noqa: F811
             refused(L, rc, INVALID, "launch grid")
         else:
             assert rc == 0
+
+
+@pytest.mark.parametrize("n", [8, 16, 32, 64])
+def test_columns_of_the_scans_last_sums(L, n):  # noqa: F811
+    from test_layer_errors import scan_desc
+    size = ctypes.c_size_t()
+    most = (2 ** 28 - 64) // (n + 2) // 8 * 8
+    if most + 8 >= 2 ** 24:
+        most = 2 ** 24 - 16  # other limits come first: every number of channels has its gradient
+    for ch in (most, most + 8):
+        d = ctypes.byref(scan_desc(channels=ch, n_groups=1, d_state=n, n_seqs=1, n_tokens=1))
+        assert L.stepq_scan_forward_workspace(d, ctypes.byref(size)) == 0
+        rc = L.stepq_scan_backward_workspace(d, ctypes.byref(size))
+        if ch > most and most < 2 ** 24 - 16:
+            refused(L, rc, INVALID, "gradient's launch grid")
+            refused(L, L.stepq_scan_backward(d, *MANY[:21], 1 << 50, None), INVALID, "gradient's launch grid")
+        else:
+            assert rc == 0
