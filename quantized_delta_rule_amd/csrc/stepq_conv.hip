@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256) void k_conv(ConvArgs A, int blocks) {
         float u = b[v];
 #pragma unroll
         for (int i = 0; i < W; i++) u = fmaf(w[i][v], x[i][v], u);
-        y[v] = act_of(A.act, u);
+        y[v] = act_of<DT>(A.act, u);
       }
       storev<DT, V>(po + (t0 + r) * ao, 0, y);
 #pragma unroll
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(256) void k_conv_grad(ConvArgs A, int blocks) {
           for (int i = 0; i < W; i++) u = fmaf(w[i][v], x[i][v], u);
           float d = dy[v];
           if (A.act == kSilu) {
-            const float s = sigmoid(u);
+            const float s = sigmoid<DT>(u);
             d *= fmaf(u * s, 1.0f - s, s);
           }
           du[W - 1][v] = d;

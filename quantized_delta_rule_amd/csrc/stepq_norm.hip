@@ -114,7 +114,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm(NormArgs A) {
     for (int j = 0; j < 8; j++) {
       h[k][j] *= rms;
       if (A.w) h[k][j] *= w[j];
-      if (A.z) h[k][j] *= act_of(A.gate, z[k][j]);
+      if (A.z) h[k][j] *= act_of<DT>(A.gate, z[k][j]);
       top = fmaxf(top, fabsf(h[k][j]));
     }
     if (A.odtype == DT && live) store8<DT>(A.out, oo + c, h[k]);
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A)
       for (int j = 0; j < 8; j++) {
         h[k][j] *= rms;
         if (A.z) {
-          const float v = z[k][j], s = sigmoid(v);
+          const float v = z[k][j], s = sigmoid<DT>(v);
           const float slope = A.gate == kSilu ? fmaf(v * s, 1.0f - s, s) : s * (1.0f - s);
           dz[j] = p[k][j] * h[k][j] * w[j] * slope;
           p[k][j] *= A.gate == kSilu ? v * s : s;

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void k_scan_tokens(ScanArgs A, int tiles) {
 #pragma unroll
     for (int k = 0; k < K; k++) {
       const float x = rx[k][0], z = rz[k][0];
-      const float D = step_of(A.softplus, rd[k][0] + bias[k]), dx = D * x;
+      const float D = step_of<DT>(A.softplus, rd[k][0] + bias[k]), dx = D * x;
       float y = 0;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256) void k_scan_tokens(ScanArgs A, int tiles) {
 #pragma unroll
       for (int m = 1; m < LN; m *= 2) y += __shfl_xor(y, m);
       if (A.D) y = fmaf(skip[k], x, y);
-      if (A.z) y *= z * sigmoid(z);
+      if (A.z) y *= z * sigmoid<DT>(z);
       if (live[k] && part == 0) storen<DT, 1>(A.out, t * A.os + c[k], &y);
     }
   }

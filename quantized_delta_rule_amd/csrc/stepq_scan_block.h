@@ -255,7 +255,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
     for (int i = 0; i < E; i++) D[i] = rd[i] + bias[i];
     if (A.softplus) {
 #pragma unroll
-      for (int i = 0; i < E; i++) D[i] = step_of(1, D[i]);
+      for (int i = 0; i < E; i++) D[i] = step_of<DT>(1, D[i]);
     }
 #pragma unroll
     for (int i = 0; i < E; i++) {
@@ -279,7 +279,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
     for (int i = 0; i < E; i++) y[i] = fmaf(skip[i], x0[i], y[i]);
     if (A.z) {
 #pragma unroll
-      for (int i = 0; i < E; i++) y[i] *= z0[i] * sigmoid(z0[i]);
+      for (int i = 0; i < E; i++) y[i] *= z0[i] * sigmoid<DT>(z0[i]);
     }
     if (k * kBlock + tok < count && mine) storev<DT, E>(op + (unsigned)(tok * ao + co * size), 0, y);
     op += (long long)ao * kBlock;

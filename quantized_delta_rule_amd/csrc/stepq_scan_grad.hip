@@ -255,12 +255,12 @@ __global__ __launch_bounds__(64 * NW) void k_scan_back(ScanArgs A, Space S) {
     for (int i = 0; i < E; i++) D0[i] = rd[i] + bias[i], slope0[i] = 1, e0[i] = ru[i];
     if (A.softplus) {
 #pragma unroll
-      for (int i = 0; i < E; i++) D0[i] = step_of(1, D0[i], slope0[i]);
+      for (int i = 0; i < E; i++) D0[i] = step_of<DT>(1, D0[i], slope0[i]);
     }
     if (A.z) {
 #pragma unroll
       for (int i = 0; i < E; i++) {
-        s0[i] = sigmoid(z0[i]);
+        s0[i] = sigmoid<DT>(z0[i]);
         e0[i] *= z0[i] * s0[i];
       }
     }
