@@ -167,12 +167,16 @@ __device__ __forceinline__ void storev(void* p, long long i, const float* x) {
 }
 
 // E neighbouring elements as they lie in memory: kept until they are used, so that their load is not waited for before.
+// Rows are 16-byte aligned, so a read of 32 bytes may assume no more than that.
 template <int DT, int E>
 struct Raw {
   typedef typename std::conditional<DT == kF32, float, unsigned short>::type T;
   typedef T V __attribute__((ext_vector_type(E)));
-  typename std::conditional<E == 1, T, V>::type v;
-  __device__ __forceinline__ void load(const void* p, long long at = 0) { v = *(const decltype(v)*)((const char*)p + at); }
+  typedef typename std::conditional<E == 1, T, V>::type Held;
+  typedef Held InMemory __attribute__((aligned(E * sizeof(T) < 16 ? E * sizeof(T) : 16)));
+  static_assert(alignof(InMemory) <= 16);
+  Held v;
+  __device__ __forceinline__ void load(const void* p, long long at = 0) { v = *(const InMemory*)((const char*)p + at); }
   __device__ __forceinline__ float operator[](int i) const {
     T x;
     if constexpr (E == 1) x = v;

@@ -39,3 +39,42 @@ def test_residual_of_any_kind():
             out = torch.empty_like(x)
             norm.forward(x, None, out, residual=left, residual_out=right)
             assert torch.equal(out, want) and torch.equal(right.as_subclass(torch.Tensor), h), (a, b)
+
+
+def odd(t, dtype=torch.float32):
+    """t's rows as a part of wider ones, 16 bytes past a multiple of 32 in every other row."""
+    wide = torch.zeros(t.shape[0], t.shape[1] + 12, dtype=dtype, device=t.device)
+    part = wide[:, 4:4 + t.shape[1]]
+    assert (part.data_ptr() + part.stride(0) * 4) % 32 in (0, 16) and part.stride(0) * 4 % 32 == 16
+    part.copy_(t)
+    return part
+
+
+@pytest.mark.gpu
+def test_binary32_rows_aligned_to_16_bytes_only():
+    from quantized_delta_rule_amd import conv, norm, scan
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, r, z, dy = (torch.randn(50, 520, generator=g, device="cuda") for _ in range(4))
+    w, b = torch.randn(520, 4, generator=g, device="cuda"), torch.randn(520, generator=g, device="cuda")
+    new = torch.empty_like
+    cu = torch.tensor([0, 1, 20, 50], dtype=torch.int32, device="cuda")
+    one, two = new(x), odd(x)
+    conv.forward(x, w, one, bias=b, cu_seqlens=cu)
+    conv.forward(odd(x), w, two, bias=b, cu_seqlens=cu)
+    assert torch.equal(one, two)
+    got = [(new(x), new(w), new(b)) for _ in range(2)]
+    conv.backward(x, w, dy, got[0][0], got[0][1], bias=b, dbias=got[0][2], cu_seqlens=cu)
+    conv.backward(odd(x), w, odd(dy), got[1][0], got[1][1], bias=b, dbias=got[1][2], cu_seqlens=cu)
+    assert all(torch.equal(p, q) for p, q in zip(*got))
+    h = (new(x), odd(x))
+    norm.forward(x, b, one, residual=r, residual_out=h[0], z=z)
+    norm.forward(odd(x), b, two, residual=odd(r), residual_out=h[1], z=odd(z))
+    assert torch.equal(one, two) and torch.equal(*h)
+    got = [(new(x), new(b), new(x)) for _ in range(2)]
+    norm.backward(x, b, dy, got[0][0], got[0][1], z=z, dz=got[0][2], d_residual=r)
+    norm.backward(odd(x), b, odd(dy), got[1][0], got[1][1], z=odd(z), dz=got[1][2], d_residual=odd(r))
+    assert all(torch.equal(p, q) for p, q in zip(*got))
+    A, B = -torch.rand(520, 16, generator=g, device="cuda"), torch.randn(50, 16, generator=g, device="cuda")
+    scan.forward(x, z, A, B.unflatten(1, (1, 16)), B.unflatten(1, (1, 16)), one, z=r, cu_seqlens=cu)
+    scan.forward(odd(x), odd(z), A, odd(B).unflatten(1, (1, 16)), odd(B).unflatten(1, (1, 16)), two, z=odd(r), cu_seqlens=cu)
+    assert torch.equal(one, two)
