@@ -461,7 +461,7 @@ int stepq_norm_forward(const stepq_norm_desc* desc, const void* x, const void* w
  * Gradient of the norm at h [n_rows, n_heads, d] (x's stride; the sum that the norm was taken of, that is x or
  * residual_out): from d_out (dtype, out_stride) and d_residual (NULL = zero; residual_stride: the gradient that
  * reaches h by the residual's own way) to dx [n_rows, n_heads, d] (packed; the gradient of x and of the residual alike),
- * dz (packed; goes with z) and dweight [d] (binary32, NULL = not wanted).  out_dtype is dtype, group 0.  dx and dz
+ * dz (packed; goes with z) and dweight [d] (binary32, NULL = not wanted, and no workspace).  out_dtype is dtype, group 0.  dx and dz
  * may each be a packed h, d_out, z or d_residual (in place); no output may overlap anything else.
  */
 int stepq_norm_backward_workspace(const stepq_norm_desc* desc, size_t* bytes);

@@ -424,7 +424,7 @@ int stepq_norm_backward(const stepq_norm_desc* desc, const void* h, const void* 
     STEPQ_TRY(rows_apart({dz, "dz", packed}, true, in, 4));
     STEPQ_TRY(apart(dx, "dx", p + 3, names + 3, 1));
   }
-  STEPQ_TRY(seq_workspace(workspace, workspace_bytes, norm_backward_bytes(a)));
+  STEPQ_TRY(seq_workspace(workspace, workspace_bytes, dweight ? norm_backward_bytes(a) : 0));
   STEPQ_ON_DEVICE(desc->device);
   a.x = h;
   a.w = weight;

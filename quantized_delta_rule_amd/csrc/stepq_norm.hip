@@ -266,54 +266,56 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void k_norm_grad(NormArgs A)
 // Workgroups of the gradient: four a CU where a workgroup's rows are short, two where they fill its registers and
 // each adds a longer row of partial sums (us of 512 and 1,024 workgroups: 8,192 rows of 2,048 35 and 29, 262,144
 // of 128 50 and 41; 8,192 of 4,096 45 and 49, 4,096 of 8,192 47 and 54).
-constexpr long long kGroups = 1024;
-long long grad_groups(const NormArgs& a, int rows) {
-  const long long sets = (a.R + rows - 1) / rows, most = a.D <= 2048 ? kGroups : kGroups / 2;
+long long grad_groups(const NormArgs& a) {
+  const int rows = a.D <= 64 ? 32 : a.D <= 128 ? 16 : a.D <= 256 ? 8 : a.D <= 512 ? 4 : 1;  // of a workgroup, as by_size gives them
+  const long long sets = (a.R + rows - 1) / rows, most = a.D <= 2048 ? 1024 : 512;
   return sets < most ? sets : most;
 }
 
-template <int DT, int TPR, int K>
-hipError_t launch(const NormArgs& a, bool back, hipStream_t s) {
+template <int DT, bool BACK, int TPR, int K>
+hipError_t launch(const NormArgs& a, hipStream_t s) {
   constexpr int THREADS = TPR > 256 ? TPR : 256, ROWS = THREADS / TPR;
-  if (back) {
-    const long long groups = grad_groups(a, ROWS);
+  if constexpr (BACK) {
+    const long long groups = grad_groups(a);
     hipLaunchKernelGGL((k_norm_grad<DT, TPR, K>), dim3((unsigned)groups), dim3(THREADS), 0, s, a);
     if (hipError_t e = hipGetLastError()) return e;
     if (!a.dw) return hipSuccess;
     SumArgs m{a.ws, (int)groups, a.D, a.D, 0, a.dw, nullptr, nullptr};
     return launch_sum(m, s);
+  } else {
+    hipLaunchKernelGGL((k_norm<DT, TPR, K>), dim3((unsigned)((a.R + ROWS - 1) / ROWS)), dim3(THREADS), 0, s, a);
+    return hipGetLastError();
   }
-  hipLaunchKernelGGL((k_norm<DT, TPR, K>), dim3((unsigned)((a.R + ROWS - 1) / ROWS)), dim3(THREADS), 0, s, a);
-  return hipGetLastError();
 }
 
-template <int DT>
-hipError_t by_size(const NormArgs& a, bool back, hipStream_t s) {
+template <int DT, bool BACK>
+hipError_t by_size(const NormArgs& a, hipStream_t s) {
   const int D = a.D;
-  if (D <= 64) return launch<DT, 8, 1>(a, back, s);
-  if (D <= 128) return launch<DT, 16, 1>(a, back, s);
-  if (D <= 256) return launch<DT, 32, 1>(a, back, s);
-  if (D <= 512) return launch<DT, 64, 1>(a, back, s);
-  if (D <= 2048) return launch<DT, 256, 1>(a, back, s);
-  if (D <= 4096) return launch<DT, 256, 2>(a, back, s);
-  if (D <= 8192) return launch<DT, 256, 4>(a, back, s);
-  if (D <= 16384) return back ? launch<DT, 512, 4>(a, true, s) : launch<DT, 1024, 2>(a, false, s);
-  return launch<DT, 1024, 4>(a, back, s);
+  if (D <= 64) return launch<DT, BACK, 8, 1>(a, s);
+  if (D <= 128) return launch<DT, BACK, 16, 1>(a, s);
+  if (D <= 256) return launch<DT, BACK, 32, 1>(a, s);
+  if (D <= 512) return launch<DT, BACK, 64, 1>(a, s);
+  if (D <= 2048) return launch<DT, BACK, 256, 1>(a, s);
+  if (D <= 4096) return launch<DT, BACK, 256, 2>(a, s);
+  if (D <= 8192) return launch<DT, BACK, 256, 4>(a, s);
+  if (D <= 16384) return launch<DT, BACK, BACK ? 512 : 1024, BACK ? 4 : 2>(a, s);
+  return launch<DT, BACK, 1024, 4>(a, s);
 }
 
-hipError_t by_type(const NormArgs& a, bool back, hipStream_t s) {
-  return a.dtype == kF32 ? by_size<kF32>(a, back, s)
-                         : a.dtype == kBF16 ? by_size<kBF16>(a, back, s) : by_size<kF16>(a, back, s);
+template <bool BACK>
+hipError_t by_type(const NormArgs& a, hipStream_t s) {
+  return a.dtype == kF32 ? by_size<kF32, BACK>(a, s)
+                         : a.dtype == kBF16 ? by_size<kBF16, BACK>(a, s) : by_size<kF16, BACK>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_norm(const NormArgs& a, hipStream_t s) { return a.R <= 0 ? hipSuccess : by_type(a, false, s); }
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) { return a.R <= 0 ? hipSuccess : by_type<false>(a, s); }
 
-size_t norm_backward_bytes(const NormArgs& a) { return a.R > 0 ? (size_t)kGroups * a.D * sizeof(float) : 0; }
+size_t norm_backward_bytes(const NormArgs& a) { return (size_t)grad_groups(a) * a.D * sizeof(float); }
 
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
-  if (a.R > 0) return by_type(a, true, s);
+  if (a.R > 0) return by_type<true>(a, s);
   SumArgs m{nullptr, 0, a.D, a.D, 0, a.dw, nullptr, nullptr};
   return a.dw ? launch_sum(m, s) : hipSuccess;
 }

@@ -96,7 +96,7 @@ def _describe_grad(h, weight, d_out, eps, z, gate, d_residual):
 
 
 def backward_workspace(h, weight, d_out, *, eps=1e-6, z=None, gate=SILU, d_residual=None):
-    """Bytes of workspace that backward() with these arguments takes."""
+    """Bytes of workspace that backward() with these arguments and a dweight takes (without one: none)."""
     d = _describe_grad(h, weight, d_out, eps, z, gate, d_residual)[0]
     return need(lib().stepq_norm_backward_workspace, "norm_backward_workspace", ctypes.byref(d))
 
@@ -114,6 +114,6 @@ def backward(h, weight, d_out, dx, dweight=None, *, eps=1e-6, z=None, dz=None, g
     gx, gz = dense(dx, "dx", h.dtype, shape, dev), dense(dz, "dz", h.dtype, shape, dev)
     gw = dense(dweight, "dweight", torch.float32, (shape[-1],), dev)
     d = ctypes.byref(desc)
-    ws, size, keep = workspace_of(workspace, need(lib().stepq_norm_backward_workspace, "norm_backward_workspace", d), dev,
-                                  stream)
+    room = 0 if dweight is None else need(lib().stepq_norm_backward_workspace, "norm_backward_workspace", d)
+    ws, size, keep = workspace_of(workspace, room, dev, stream)
     _check(lib().stepq_norm_backward(d, *p, gx, gw, gz, ws, size, stream_of(stream, dev)), "norm_backward")

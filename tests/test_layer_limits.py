@@ -49,3 +49,19 @@ def test_columns_of_the_scans_last_sums(L, n):  # noqa: F811
             refused(L, L.stepq_scan_backward(d, *MANY[:21], 1 << 50, None), INVALID, "gradient's launch grid")
         else:
             assert rc == 0
+
+
+def test_workspace_of_the_norms_gradient(L):  # noqa: F811
+    """A row of partial sums for each workgroup that writes one, no more; none where dweight is not wanted."""
+    torch = pytest.importorskip("torch")
+    n = ctypes.c_size_t()
+    for rows, d, groups in ((0, 64, 0), (1, 64, 1), (32, 64, 1), (33, 64, 2), (8192, 128, 512), (100000, 128, 1024), (5, 512, 2),
+                            (7, 1024, 7), (2000, 2048, 1024), (2000, 2056, 512), (8192, 4096, 512), (600, 32768, 512), (9, 32768, 9)):
+        desc = ctypes.byref(norm_desc(n_rows=rows, n_heads=1, d=d))
+        assert L.stepq_norm_backward_workspace(desc, ctypes.byref(n)) == 0 and n.value == groups * d * 4, (rows, d)
+        if rows:
+            p = list(MANY[:8])
+            refused(L, L.stepq_norm_backward(desc, *p, MANY[9], n.value - 1, None), INVALID, "workspace")
+            p[6] = None
+            if not torch.cuda.is_available():
+                good(L, L.stepq_norm_backward(desc, *p, None, 0, None))
