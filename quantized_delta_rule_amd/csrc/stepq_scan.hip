@@ -104,14 +104,13 @@ hipError_t tokens(const ScanArgs& a, hipStream_t s) {
 template <int DT, int NS, int NW>
 hipError_t blocks(const ScanArgs& a, hipStream_t s) {
   char* end;
-  const int sh = segments_of(a, kLeastForward);
-  const Segments q = lay_segments(a, sh, a.ws, &end);
+  const Segments q = lay_segments(a, segments_of(a, kLeastForward), a.ws, &end);
   const long long per = (long long)q.tiles * a.G;
-  if (!sh) {
+  if (!q.sh) {
     hipLaunchKernelGGL((k_scan_run<DT, NS, 32, NW, 0>), dim3((unsigned)(per * a.N)), dim3(64 * NW), 0, s, a, q);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)(per * pieces(a, sh)));
+  const dim3 grid((unsigned)(per * pieces(a, q.sh)));
   hipLaunchKernelGGL((k_scan_run<DT, NS, 32, NW, 1>), grid, dim3(64 * NW), 0, s, a, q);
   if (hipError_t e = hipGetLastError()) return e;
   hipLaunchKernelGGL((k_scan_run<DT, NS, 32, NW, 2>), grid, dim3(64 * NW), 0, s, a, q);

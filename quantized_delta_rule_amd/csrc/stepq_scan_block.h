@@ -41,6 +41,7 @@ __device__ __forceinline__ void unrolled(F&& f) {
 struct Segments {
   int tiles;    // of CH channels, in a group
   int sh;
+  long long over;  // sequences longer than this are cut, the others run whole (in their first segment's place)
   float* last;  // [segments, C, n]: the first of a sequence from its state, the others from zero
   float* steps; // [segments, C]
   float* first; // [N, C, n]: the first states of sequences of several segments (S_out may be S_in)
@@ -100,29 +101,58 @@ __device__ __forceinline__ void put_states(float* p, const float* h) {
   for (int i = 0; i < NS; i += W) storen<kF32, W>(p, i, h + i);
 }
 
+// Segments are numbered by sequence first: segment 0 of sequence s is number s, so that the workgroups of sequences that are not
+// cut lie side by side as they would without segments (the four sequences of 2,048 tokens x 2,048 channels that take 142 us whole
+// take 238 where their workgroups lie apart: two meet on a CU, none on others).  The later ones follow: those of
+// sequence s from number N + (cu[s] >> sh) on, which no two sequences share, since a sequence has (len - 1) >> sh of them.
+// Sequence and segment of the later number e; false where no sequence begins before it.  The whole wave asks for one e.
+__device__ __forceinline__ bool later(const ScanArgs& A, int sh, long long e, int lane, int& s, long long& idx) {
+  if (!A.cu) {
+    const long long more = (A.T / A.N - 1) >> sh;  // of each sequence; no call has e where it is zero
+    s = (int)(e / more);
+    idx = e - s * more + 1;
+    return true;
+  }
+  long long lo = 0, n = A.N;
+  do {  // 64 sequences at once, as `piece` does
+    const long long step = (n + 63) >> 6, at = lo + lane * step;
+    const int k = __popcll(__ballot(lane * step < n && A.cu[at] >> sh <= e));
+    if (k == 0) return false;
+    lo += (k - 1) * step;
+    n = n - (k - 1) * step < step ? n - (k - 1) * step : step;
+  } while (n > 1);
+  s = __builtin_amdgcn_readfirstlane((int)lo);
+  idx = e - (A.cu[s] >> sh) + 1;
+  return true;
+}
+
 // Segment j, or sequence j where there are none: its sequence, place, rows and channels.  False: nothing to do.
 struct Place {
   int s, slot, count;     // sequence, state index, tokens
   long long idx, len, p;  // segment of the sequence, the sequence's length, position in it
   long long row0;         // first row
+  long long more;         // number of the sequence's segment k > 0, less k
   bool ends;              // the sequence's last segment
 };
-__device__ __forceinline__ bool place(const ScanArgs& A, int sh, long long j, bool report, int lane, Place& Q) {
+__device__ __forceinline__ bool place(const ScanArgs& A, int sh, long long over, long long j, bool report, int lane, Place& Q) {
   int a, b;
   if (report && j < A.N) {
     const bool ok = seq_range(A, (int)j, a, b);
     seq_slot(A, (int)j, ok, lane == 0);
   }
   Q.idx = 0;
-  if (!sh) Q.s = (int)j;
-  else if (!piece(A, sh, j, lane, Q.s, Q.idx)) return false;
+  if (!sh || j < A.N) Q.s = (int)j;
+  else if (!later(A, sh, j - A.N, lane, Q.s, Q.idx)) return false;
   const bool valid = seq_range(A, Q.s, a, b);
   Q.slot = seq_slot(A, Q.s, valid, false);
   Q.len = b - a;
-  Q.p = sh ? Q.idx << sh : 0;
-  Q.ends = !sh || Q.p + (1LL << sh) >= Q.len;
+  const bool cut = sh && Q.len > over;
+  if (!cut && Q.idx > 0) return false;
+  Q.p = cut ? Q.idx << sh : 0;
+  Q.ends = !cut || Q.p + (1LL << sh) >= Q.len;
   Q.count = (int)(Q.ends ? Q.len - Q.p : 1LL << sh);
   Q.row0 = a + Q.p;
+  Q.more = A.N - 1 + (A.cu ? (long long)a >> sh : Q.s * ((Q.len - 1) >> sh));
   return Q.slot >= 0 && (Q.p < Q.len || Q.idx == 0) && Q.len >= A.split;
 }
 
@@ -156,7 +186,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   const int tg = unit % per, g = tg / Q.tiles, tile = tg - g * Q.tiles;
   const int sh = PASS == 0 ? 0 : Q.sh;
   Place W;
-  if (!place(A, sh, j, (PASS < 2 || (PASS == 3 && !sh)) && tg == 0 && threadIdx.x < 64, lane, W)) return;
+  if (!place(A, sh, Q.over, j, (PASS < 2 || (PASS == 3 && !sh)) && tg == 0 && threadIdx.x < 64, lane, W)) return;
   const int count = W.count, s = W.s;
   const long long idx = W.idx;
   const bool ends = W.ends;
@@ -173,7 +203,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   if (PASS < 2 || !sh || (idx == 0 && ends)) {  // a sequence of one segment is its own workgroup's alone
     if (A.S_in && idx == 0) get_states<NS>(A.S_in + so, h);
   } else if (idx > 0) {
-    get_states<NS>(Q.last + ((j - idx) * A.C + c) * n + part * NS, h);
+    get_states<NS>(Q.last + ((long long)s * A.C + c) * n + part * NS, h);
   } else {
     get_states<NS>(Q.first + ((long long)s * A.C + c) * n + part * NS, h);
   }
@@ -183,7 +213,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   if (PASS >= 2) {
 #pragma unroll 4
     for (long long k = 1; k < idx; k++) {
-      const long long o = (j - idx + k) * A.C + c;
+      const long long o = (W.more + k) * A.C + c;
       const float D = Q.steps[o];
       float e[NS];
       get_states<NS>(Q.last + o * n + part * NS, e);
@@ -296,7 +326,7 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
       parts[k & 1][part][T][cl] = y;
     }
   };
-  const int blocks = (count + kBlock - 1) / kBlock;
+  const int blocks = __builtin_amdgcn_readfirstlane((count + kBlock - 1) / kBlock);  // (one value of the wave)
   const long long kept0 = PASS == 3 ? first_block(A, W) : 0;
   if (blocks > 0) {
     fetch(0);
@@ -344,35 +374,50 @@ __global__ __launch_bounds__(64 * NW) void k_scan_run(ScanArgs A, Segments Q) {
   }
 }
 
-// Segments (0: none).  Where workgroups of 32 channels of whole sequences would be fewer than `least`: about ten
-// workgroups a CU, but no more than 64 of a sequence of mean length (each looks at all before it), of at least 64 tokens.
-// Where they are enough, but lengths differ and one may be eight times the mean, or 512 tokens, and more: segments of
-// that length, so that one long prompt beside single tokens or short ones does not run as one chain.
-inline int segments_of(const ScanArgs& a, int least) {
-  const long long tiles = (a.Cg + 31) / 32 * a.G, mean = a.N > 0 ? a.T / a.N : 0;
-  if (a.N <= 0) return 0;
-  if (tiles * a.N >= least) {
-    int sh = 9;
-    while (1LL << sh < 8 * mean) sh++;
-    return a.cu && (long long)a.T - a.N > 1LL << sh ? sh : 0;
+// Which sequences are cut, and how.  Where workgroups of 32 channels of whole sequences would be fewer than `least`, all of
+// more than a segment: about ten workgroups of segments a CU, but no more than 64 segments of a sequence (each looks at all
+// before it), of at least 64 tokens.  Otherwise those that would run long after the rest has ended.  Lengths are on the device; known
+// here are their mean and what one of them may have (all tokens but one for each other sequence).  The rest ends after
+// about `mean` tokens or, where CUs are full, what two workgroups a CU take for all tokens: longer by half and of more
+// than 1,024 tokens is cut.  A call whose sequences turn out alike pays a pass that finds nothing to do.
+struct Cut {
+  int sh;          // segments of 2^sh tokens (0: none)
+  long long over;  // of sequences longer than this
+};
+inline Cut segments_of(const ScanArgs& a, int least) {
+  if (a.N <= 0) return Cut{0, 0};
+  const long long tiles = (a.Cg + 31) / 32 * a.G, mean = a.T / a.N, longest = a.cu ? (long long)a.T - a.N + 1 : mean;
+  auto length = [&](long long most, long long of) {
+    int sh = 6;
+    while (sh < 30 && (((long long)a.T >> sh) * tiles > most || of >> sh > 64)) sh++;
+    return sh;
+  };
+  if (tiles * a.N < least) {
+    const int sh = length(2560, mean);
+    if (mean > 1LL << sh) return Cut{sh, 1LL << sh};
   }
-  int sh = 6;
-  while (sh < 30 && (((long long)a.T >> sh) * tiles > 2560 || mean >> sh > 64)) sh++;
-  return mean > 1LL << sh ? sh : 0;
+  const int sh = length(tiles * a.N > 2560 ? tiles * a.N : 2560, longest);
+  const long long full = a.T * tiles / 512, rest = mean > full ? mean : full;
+  long long over = rest + rest / 2 > 1024 ? rest + rest / 2 : 1024;
+  if (over < 1LL << sh) over = 1LL << sh;
+  return longest > over ? Cut{sh, over} : Cut{0, 0};
 }
-// Both sides (us, 4,096 channels of 16 states, 1 / 2 / 3 sequences of 2,048 tokens; 128 workgroups a sequence): whole 137 / 142
-// / 185 against segments 79 / 152 / 207; gradient 557 / 564 / 665 against 237 / 426 / 606.  A prompt of 512 / 2,048 / 16,384
-// tokens beside 64 single ones: whole 53 / 180 / 1,340, segments 52 / 138 / 624; 70 prompts of 128, none of which is cut, 205
-// and 212.  Gradient of six sequences of 1 to 1,147 tokens, 1,536 channels of 32 states: 456 and 256.
+// Both sides, us, 16 states, bf16 (whole or cut by an even rule on the mean, against this one).  One to three sequences of 2,048
+// tokens x 4,096 channels, 128 workgroups each: whole 137 / 142 / 185, all cut 79 / 152 / 207; gradient 557 / 564 / 665 and 237 /
+// 426 / 606.  Uneven: {1, 16,384} x 4,096 1,256 and 500; {7 of 1, 14,000} x 4,096 1,078 and 440, gradient 3,177 and 1,304; {3 of 1,
+// 16,384} x 2,048 1,119 and 253; {60 of 1, 3,000} x 128 199 and 23, gradient 674 and 58; {200 of 1, 12,000} x 32 787 and 45, 2,643 and
+// 124; {64 of 1, 2,048} x 4,096 140 and 114, 402 and 311.  Alike: 8 of 2,048 x 4,096 308 and 313, gradient 1,126 and 1,135; 70 of
+// 128 181 and 177, 616 and 593; 4 of 2,048 x 2,048 143 and 148, 395 and 376; 4 of 350 x 2,048 28.5 and 32.5; 60 of 50 x 128 12 and
+// 16, gradient 30 and 37: a pass that finds nothing to cut costs 4 to 8 us, so that calls of up to 1,024 tokens go without.
 constexpr int kLeastForward = 256, kLeastBackward = 512;
 
 constexpr size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace of the segments at `ws`, up to `end`.
-inline Segments lay_segments(const ScanArgs& a, int sh, char* ws, char** end) {
-  Segments q{(a.Cg + 31) / 32, sh, nullptr, nullptr, nullptr, nullptr};
-  if (sh) {
-    const size_t m = (size_t)pieces(a, sh);
+inline Segments lay_segments(const ScanArgs& a, Cut cut, char* ws, char** end) {
+  Segments q{(a.Cg + 31) / 32, cut.sh, cut.over, nullptr, nullptr, nullptr, nullptr};
+  if (cut.sh) {
+    const size_t m = (size_t)pieces(a, cut.sh);
     q.last = (float*)ws;
     q.steps = (float*)(ws += up(m * a.C * a.n * 4));
     q.first = (float*)(ws += up(m * a.C * 4));
