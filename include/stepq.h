@@ -383,8 +383,11 @@ int stepq_conv_backward(const stepq_conv_desc* desc, const void* x, const void* 
  * term is missing.
  *   dtype      type of x, dt, B, C, z, out and their gradients; A, D, dt_bias and states are binary32.
  *   channels   a multiple of 8 n_groups;  d_state 8, 16, 32 or 64; the gradient takes channels x (d_state + 2) up to 2^28 - 64.
- * Workspaces: forward none, or some states for each segment of long sequences; backward about n_tokens * channels *
- * d_state / 4 bytes (the states before every 16 tokens) and as much again for the tiles' parts of dB and dC.
+ * Workspaces: forward none or, where sequences may be cut into segments, states of each; backward up to channels * d_state
+ * (n_tokens / 2 + 9 n_seqs) bytes, with the channels of a group rounded up to 32 (by token: the states before every 16
+ * tokens, and as much for the tiles' parts of dB and dC; by sequence: the states before its last tokens, its parts of dA,
+ * dD and ddt_bias).  Where sequences may be cut, either call takes up to 27 channels * d_state * n_seqs bytes more, or
+ * 13 channels * d_state * n_seqs + 1.2 MB * d_state if that is larger.
  */
 typedef struct {
   int dtype;

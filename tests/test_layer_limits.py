@@ -65,3 +65,22 @@ def test_workspace_of_the_norms_gradient(L):  # noqa: F811
             p[6] = None
             if not torch.cuda.is_available():
                 good(L, L.stepq_norm_backward(desc, *p, None, 0, None))
+
+
+def test_workspaces_of_the_scan(L):  # noqa: F811
+    """No more than the interface tells, for many short sequences, narrow groups and long sequences alike."""
+    import random
+    from test_layer_errors import scan_desc
+    rng, size = random.Random(5), ctypes.c_size_t()
+    calls = [(8192, 8192, 4096, 1, 16), (16384, 512, 4096, 512, 16), (16384, 1, 4096, 1, 16), (270000, 2, 8192, 1, 16), (0, 3, 64, 1, 8),
+             (1, 1, 8, 1, 64), (4000, 200, 8, 1, 64)]
+    for _ in range(400):
+        G, N = rng.choice([1, 1, 2, 16, 64]), int(10 ** rng.uniform(0, 3.6))
+        calls.append((int(10 ** rng.uniform(0, 5)), N, 8 * G * rng.randint(1, 40), G, rng.choice([8, 16, 32, 64])))
+    for T, N, ch, G, n in calls:
+        d = ctypes.byref(scan_desc(channels=ch, n_groups=G, d_state=n, n_seqs=N, n_tokens=T, cu_seqlens=4096))
+        wide = G * ((ch // G + 31) // 32 * 32)
+        cut = 13 * wide * n * N + max(14 * wide * n * N, 1.2e6 * n)
+        assert L.stepq_scan_forward_workspace(d, ctypes.byref(size)) == 0 and size.value <= cut, (T, N, ch, G, n)
+        assert L.stepq_scan_backward_workspace(d, ctypes.byref(size)) == 0
+        assert size.value <= wide * n * (T / 2 + 9 * N) + cut + 4096, (T, N, ch, G, n)
