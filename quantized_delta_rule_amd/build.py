@@ -68,15 +68,18 @@ def build(verbose: bool = False) -> str:
 
 
 KERNEL_SOURCES = ("stepq_k128_gdn.hip", "stepq_k128_kda.hip", "stepq_k64.hip")
+LAYER_SOURCES = ("stepq_conv.hip", "stepq_scan.hip", "stepq_scan_grad.hip", "stepq_norm.hip",
+                 "stepq_layer_sum.hip")
 
 
-def kernel_resources() -> dict:
-    """Compiles the step kernels' units for the device only and returns the compiler's resource
+def kernel_resources(sources=None) -> dict:
+    """Compiles these units (None: the step kernels') for the device only and returns the compiler's resource
     report per kernel: {mangled name: {"VGPRs", "ScratchSize", "Occupancy", "VGPRs Spill",
     "SGPRs Spill", "LDS Size"}} (integers)."""
     import re
     import tempfile
     from concurrent.futures import ThreadPoolExecutor
+    sources = KERNEL_SOURCES if sources is None else sources
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     flags = [f for f in HIPCC_FLAGS if f not in ("-shared", "-fPIC")]
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -85,8 +88,8 @@ def kernel_resources() -> dict:
             return _run([hipcc, *flags, *inc, "--cuda-device-only", "-c",
                          "-Rpass-analysis=kernel-resource-usage", os.path.join(CSRC, src),
                          "-o", os.path.join(td, src + ".o")])
-        with ThreadPoolExecutor(len(KERNEL_SOURCES)) as ex:
-            text = "\n".join(ex.map(one, KERNEL_SOURCES))
+        with ThreadPoolExecutor(len(sources)) as ex:
+            text = "\n".join(ex.map(one, sources))
     out, cur = {}, None
     for line in text.splitlines():
         m = re.search(r"remark: Function Name: (\S+)", line)
