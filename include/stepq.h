@@ -436,6 +436,7 @@ int stepq_scan_backward(const stepq_scan_desc* desc, const void* x, const void* 
  *                a head's row (group = 0) or every `group` (64 or 128; d a multiple) of its columns, out = y / scale, a
  *                binary32 quotient, to the nearest (ties to even); a group of zeros has scale 1.  The scale is at least the smallest
  *                normal binary32.  A y that is NaN takes no part in the maximum: its code is NaN (E4M3) or 0 (I8).
+ *                A row with an infinity has 1 / sqrt(inf) = 0: its finite columns are zero, the infinite ones NaN.
  *   n_rows       rows of n_heads * d elements, n_heads x n_rows below 2^31 and, for the launch grid, at most 2^29 - 32 (d to
  *                64), 2^28 - 16 (to 128), 2^27 - 8 (to 256), 2^26 - 4 (to 512), 2^24 - 1 (to 8192) or 2^22 - 1; the
  *                gradient only the last two.  d a multiple of 8, at most 32768.

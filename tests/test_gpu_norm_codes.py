@@ -53,3 +53,23 @@ def test_quotients(norm, kind, rows, d, group):
     x, r, w = (torch.randn(*s, generator=g, device="cuda") for s in ((rows, d), (rows, d), (d,)))
     check(norm, kind, x, w, group, residual=r)
     check(norm, kind, x, None, group, z=r)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("d", [64, 640, 4096])
+def test_rows_with_an_infinity(norm, d, dtype):
+    """1 / sqrt(inf) is zero: so are the finite columns, and the infinite ones NaN (zero in int8); scales are one."""
+    x, w = torch.randn(5, d, generator=torch.Generator().manual_seed(3)).to(dtype).cuda(), torch.ones(d).cuda()
+    x[1, 7], x[3, 0], x[3, d - 1] = float("inf"), -float("inf"), float("inf")
+    at = {1: [7], 3: [0, d - 1]}
+    for kind in (dtype, torch.float8_e4m3fn, torch.int8):
+        out, scale = torch.empty(5, d, dtype=kind, device="cuda"), None if kind == dtype else torch.empty(5, device="cuda")
+        norm.forward(x, w, out, scale=scale)
+        got = out.float().cpu()
+        for row, cols in at.items():
+            assert scale is None or float(scale[row]) == 1.0
+            bad = torch.zeros(d, dtype=torch.bool)
+            bad[cols] = True
+            assert bool((got[row][~bad] == 0).all())
+            assert bool((got[row][bad] == 0).all() if kind == torch.int8 else torch.isnan(got[row][bad]).all())
+        assert bool(torch.isfinite(got[[0, 2, 4]]).all()) and bool((got[[0, 2, 4]].abs().amax(-1) > 0).all())
