@@ -26,7 +26,8 @@ def check(norm, kind, x, w, group=0, **more):
     norm.forward(x, w, y, **more)
     norm.forward(x, w, codes, scale=scale, group=group, **more)
     top = y.cpu().unflatten(-1, (-1, group or x.shape[-1])).abs().amax(-1).reshape(scale.shape)
-    assert torch.equal(scale.cpu(), torch.where(top > 0, top / KINDS[kind], torch.ones_like(top)))
+    least = torch.tensor(2.0 ** -126)  # of a scale
+    assert torch.equal(scale.cpu(), torch.where(top > 0, torch.maximum(top / KINDS[kind], least), torch.ones_like(top)))
     want = codes_of(y.cpu(), scale.cpu(), group, kind)
     assert int((codes.cpu().view(torch.int8) != want.view(torch.int8)).sum()) == 0
 
@@ -73,3 +74,19 @@ def test_rows_with_an_infinity(norm, d, dtype):
             assert bool((got[row][~bad] == 0).all())
             assert bool((got[row][bad] == 0).all() if kind == torch.int8 else torch.isnan(got[row][bad]).all())
         assert bool(torch.isfinite(got[[0, 2, 4]]).all()) and bool((got[[0, 2, 4]].abs().amax(-1) > 0).all())
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=str)
+def test_quotients_by_scales_of_every_size(norm, kind):
+    """Rows whose scales go from the smallest normal binary32 to its largest, and an infinite one."""
+    d = 512
+    x = torch.randn(2000, d, generator=torch.Generator().manual_seed(4)).cuda()
+    w = torch.ones(d, device="cuda")
+    for power in (-126, -120, -100, -95, -91, -88, -60, 60, 100, 118):
+        check(norm, kind, x, w * 2.0 ** power)
+    w[5] = float("inf")  # finite values over an infinite scale are zero, infinite ones NaN (zero in int8)
+    codes, scale = torch.empty(2000, d, dtype=kind, device="cuda"), torch.empty(2000, device="cuda")
+    norm.forward(x, w, codes, scale=scale)
+    got = codes.float().cpu()
+    assert bool(torch.isinf(scale).all()) and float(got[:, :5].abs().max()) == 0 and float(got[:, 6:].abs().max()) == 0
+    assert bool((got[:, 5] == 0).all() if kind == torch.int8 else torch.isnan(got[:, 5]).all())
