@@ -5,8 +5,10 @@
 // A row stays in registers from its load to its store, eight neighbouring columns a lane: 8 to 64 lanes a row (to 512
 // columns), or a workgroup of 256 (to 8,192) or 1,024 (to 32,768; 512 for the gradient to 16,384).  Bound by HBM, some ten
 // operations an element: 16,381 x 48 rows of 128 with a gate, bf16, 120 us, 5.0 TB/s (a copy reaches 5.05); the gradient of
-// 8,192 rows of 4,096 with the residual's 44 us for its 268 MB and 5 for the last sums (without reading the next row
-// ahead 69); 70 rows of 4,096 with the residual and e4m3 out 5.3 us.  The gradient of rows above 16,384 spills registers
+// 8,192 rows of 4,096 with the residual's 44 us for its 268 MB, some of them cached, and 5 for the last sums (without
+// reading the next row ahead 69); 70 rows of 4,096 with the residual and e4m3 out 5.5 us.  16,384 rows with the residual,
+// own type / e4m3 out, us: of 768 28 / 34, 1,024 30 / 36, 1,536 37 / 42, 2,048 47 / 49, 4,096 100 / 97: a workgroup of 256 holds one
+// row, and one of 768 uses 96 of its threads.  The gradient of rows above 16,384 spills registers
 // (1,024 of 32,768: 219 us, 0.9 TB/s).
 #include "stepq_layer.h"
 

@@ -19,10 +19,10 @@ using namespace lay;
 //
 // Bound by vector issue: a state and token take an exponential (two slots), the argument's product, two multiply-adds and a
 // product, six slots; steps, gates and the parts' sums make it 9.7 (counted: 163 M slots of 64 lanes for 16,381 tokens x
-// 4,096 channels x 16 states).  One sequence of 16,384 x 2,048 runs both its passes, 118 and 168 us, at 98% of the issue of
-// CUs that this load holds at 2.0 GHz; eight ragged prompts of 16,381 x 4,096 take 327 us, 87% of the issue while
-// a CU is busy, the rest is that prompts of 1 to 3,698 tokens are unequal.  What the layout is worth there (us, 16,381 x
-// 4,096 / 16,384 x 2,048): B and C through scalar loads 876 / 443 (their wait stops every LDS read too), row broadcasts 581 /
+// 4,096 channels x 16 states).  Eight ragged prompts of 16,381 x 4,096 take 337 us, 1.9 GHz of full issue on every SIMD
+// (85% of the issue while a CU is busy); one sequence of 16,384 x 2,048 takes 254 us for its 142 M slots, 2.2 GHz of it (98%, the two
+// passes 116 and 168 us under a tracer, where CUs run at 2.0 GHz): slots bind, not the prompts' unequal lengths.  What the
+// layout was worth when it was chosen (us, 16,381 x 4,096 / 16,384 x 2,048): B and C through scalar loads 876 / 443 (their wait stops every LDS read too), row broadcasts 581 /
 // 310; a thread's elements side by side, not 16 lanes apart, 510 / 281; 32 channels a workgroup, not 64, 355 / 293; two
 // states a lane, not four, 329 / 272; 16 channels 457 / 337.
 // ---------------------------------------------------------------------------------------------

@@ -9,10 +9,13 @@
 //
 // Bound by vector issue: five slots of 64 lanes a state and token to run it again, nine back, 1.5 for the sums over channels
 // that dB and dC are, 1 for those over states; with the rest 25.8 (counted: 216 M for 8,192 tokens x 4,096 channels
-// x 16 states).  There the states' pass takes 136-150 us, the way back 500-540 (82% of the issue at the 2.0 GHz that this
-// load runs at), the tiles' sums 23.  Sums over channels: two steps across lanes that also deal four values out to
-// four lanes each (six instructions for four values, 16 a plain tree would take), the rest through LDS.  One block of
-// instructions for what crosses lanes, ordered so that no wait states are needed inside: 683 -> 647 us.
+// x 16 states).  There the states' pass takes 136-150 us, the way back 500-540 (78% of the issue while a CU is busy), the tiles'
+// sums 23: 626 us in all.  That call has 512 workgroups, two a CU, so two waves a SIMD, where 16 states leave room for three of 16-bit
+// rows (165 registers, 48 KB of LDS); 32 states leave room for two, of binary32 rows for one (256 registers and some accumulation
+// registers: 3,001 tokens x 1,536 channels 306 us against 229 of 16-bit rows).  Sums over channels: two steps across
+// lanes that also deal four values out to four lanes each (six instructions for four values, 16 a plain tree would
+// take), the rest through LDS.  One block of instructions for what crosses lanes, ordered so that no wait states are needed
+// inside: 683 -> 647 us.
 #include "stepq_scan_block.h"
 
 namespace stepq {
