@@ -68,3 +68,40 @@ def test_slots_gaps_and_skipped_sequences(scan):  # noqa: F811
     assert int(status) == 0 and R.rel(out[6:2450], o[6:2450]) <= TOL and R.rel(pool[slots[:4]], s) <= TOL
     assert torch.equal(pool[[1, 3, 5]].cpu(), x["S"][[1, 3, 5]]) and torch.equal(pool[2].cpu(), x["S"][2])
     assert bool((out[:6] == 3).all()) and bool((out[2450:] == 3).all())
+
+
+def test_one_graph_for_all_lengths(scan):  # noqa: F811
+    """Captured calls read their offsets at each replay: even, uneven, empty and skipped sequences, against eager calls bit for bit."""
+    T, N, ch = 4000, 4, 512
+    x = R.scan_inputs(64, T, ch, 64, 8, N, BF16)
+    g = {m: dev(v) for m, v in x.items()}
+    cu = torch.tensor([0, 1000, 2000, 3000, T], dtype=torch.int32).cuda()
+    args = [g[m] for m in ("x", "dt", "A", "B", "C")]
+
+    def call(to, cu):
+        scan.forward(*args, to["out"], D=g["D"], dt_bias=g["bias"], z=g["z"], state_in=g["S"], state_out=to["S1"], cu_seqlens=cu)
+        scan.backward(*args, g["dy"], to["x"], to["dt"], to["A"], to["B"], to["C"], D=g["D"], dD=to["D"], dt_bias=g["bias"],
+                      ddt_bias=to["bias"], z=g["z"], dz=to["z"], state_in=g["S"], d_state_out=g["dS"], d_state_in=to["S"], cu_seqlens=cu)
+
+    def fresh():
+        return {m: torch.zeros_like(g[{"out": "x", "S1": "S"}.get(m, m)]) for m in
+                ("out", "S1", "x", "dt", "A", "B", "C", "D", "bias", "z", "S")}
+    kept = fresh()
+    call(kept, cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(kept, cu)
+    for lens in ([1000] * 4, [1, 3997, 1, 1], [2000, 0, 0, 2000], [3000, 17, 983, 0], [0, 0, 0, 4000], [500, 1500, 700, 1300]):
+        now = torch.tensor(R.offsets(lens), dtype=torch.int32).cuda()
+        cu.copy_(now)
+        for v in kept.values():
+            v.zero_()
+        graph.replay()
+        eager = fresh()
+        call(eager, now)
+        torch.cuda.synchronize()
+        for m, v in eager.items():
+            assert torch.equal(kept[m], v), (lens, m)
+    o, s = forward_want(x, R.offsets([500, 1500, 700, 1300]))
+    assert R.rel(kept["out"], o) <= TOL + HALF[BF16] and R.rel(kept["S1"], s) <= TOL
